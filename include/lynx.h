@@ -395,6 +395,99 @@ int lynx_decode_attn_int4(const void* q_bf16, int B, int T, int Hq, int Hkv, int
 int lynx_attn_merge(const float* o_a, const float* lse_a, const float* o_b, const float* lse_b,
                     int64_t rows, int head_dim, float* o, float* lse, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around attention in one step of a serving loop: pages and slots
+ * for the step's new tokens (lynx_assign_pages), their queries, keys and values
+ * (lynx_qkv_append), and the verification of drafted tokens
+ * (lynx_verify_drafts).  Integer arrays and probabilities need only the
+ * alignment of their elements here; other buffers 16 bytes as everywhere.
+ */
+
+/* Pages, positions and slots of the new tokens of a ragged batch, from the
+ * requests' lengths, on the GPU (nothing is read back).
+ *   ctx_len     [B] int32: tokens of each request already in its pages
+ *   new_len     [B] int32: new tokens of each request in this step (0 allowed)
+ *   page_table  [B][Hkv][max_pages] int32, updated in place: entries of fresh
+ *               pages are written, no other
+ *   free_pages  [n_free] int32: page ids to take, from the front (4-byte
+ *               aligned: the rest of an earlier call's list may be passed)
+ *   n_rows      rows of positions and slots; the batch's rows are packed from
+ *               row 0, request after request
+ *   cu_new      [B + 1] int32: first row of each request, then the row behind
+ *               the last (values past n_rows are given as n_rows)
+ *   positions   [n_rows] int32: the row's position in its request
+ *   slots       [n_rows][Hkv] int64: page id * 256 + position % 256
+ *   ctx_out     [B] int32: ctx_len + new_len of each granted request, ctx_len
+ *               of a refused one (not ctx_len itself: other CTAs read that)
+ *   n_taken     [1] int32: ids taken from free_pages
+ * Request b has ceil(ctx / 256) pages a head and needs ceil((ctx + new) / 256);
+ * the missing ones take Hkv ids each (page by page, head 0 first) in request
+ * order.  A request whose new tokens do not fit (a length below 0 or past
+ * max_pages * 256: device error word 3; rows past n_rows) is refused and
+ * takes no pages.  A request that the free list is too short for is refused
+ * too, and so is every later one that needs a page: ids are dealt by running
+ * sum, so that the outcome does not depend on what later requests ask for.
+ * Rows of refused requests and rows behind the last request get position -1
+ * and slot -1, which lynx_qkv_append skips.  Limits: max_pages * 256 < 2^31,
+ * n_rows <= 2^30. */
+int lynx_assign_pages(const int32_t* ctx_len, const int32_t* new_len, int B, int Hkv, int32_t* page_table,
+                      int max_pages, const int32_t* free_pages, int n_free, int n_rows, int32_t* cu_new,
+                      int32_t* positions, int64_t* slots, int32_t* ctx_out, int32_t* n_taken, void* stream);
+
+/* The new tokens' queries, keys and values on their way to attention: RMS norm
+ * of each query and key head, rotation by the token's position, and keys and
+ * values written to their slots of BF16 page pools.
+ *   qkv_bf16    rows of Hq query heads, Hkv key heads and Hkv value heads of 128
+ *               BF16 each; row r begins at r * row_stride elements (>= (Hq + 2
+ *               Hkv) * 128, a multiple of 8)
+ *   q_weight, k_weight   [128] float32 norm weights (NULL: no norm):
+ *               y = x / sqrt(mean(x^2) + norm_eps) * weight
+ *   cos_sin     [max_pos][rot_dim] float32: the rot_dim / 2 cosines of a
+ *               position, then its rot_dim / 2 sines (16-byte aligned)
+ *   rot_dim     channels rotated, a multiple of 16 in 0..128 (0: none; cos_sin
+ *               may be NULL); pair i is channels (i, i + rot_dim / 2), or
+ *               (2i, 2i + 1) with interleaved = 1;
+ *               (a, b) <- (a cos_i - b sin_i, b cos_i + a sin_i)
+ *   positions   [n_rows] int32; a row with a negative position is skipped: its
+ *               q_out row and its slots stay as they were
+ *   slots       [n_rows][Hkv] int64: page id * 256 + token; negative: not written.
+ *               No two rows may name one slot.
+ *   q_out       [n_rows][Hq][128] BF16
+ *   k_pages, v_pages   pools [n_pool_pages][128][256] BF16, written at the slots
+ * Arithmetic in float32, rounded to BF16 once; values are copied.  A position
+ * past max_pos - 1 sets device error word 4 and the row is skipped; a slot past
+ * the pool sets word 5 and is not written.  q_out must not overlap qkv. */
+int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
+                    const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
+                    int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
+                    void* k_pages, void* v_pages, int64_t n_pool_pages, void* stream);
+
+/* Verification of drafted tokens against the target model's probabilities
+ * (paper §4.3), from given random numbers.
+ *   p           target probabilities: row (b, t) of V values at b * p_stride_b +
+ *               t * p_stride_t elements, t = 0..T (row t is the distribution that
+ *               draft t is tested against, row T the one behind the last draft)
+ *   q           draft probabilities, rows t = 0..T-1 alike; NULL: every draft was
+ *               certain (greedy drafts)
+ *   prob_dtype  LYNX_OUT_F32 or LYNX_OUT_BF16, of p and q
+ *   draft       [B][T] int32;  n_draft [B] int32 (NULL: T each; clamped to 0..T)
+ *   u           [B][T + 1] float32 in [0, 1): u[b][i] tests draft i, u[b][T] draws
+ *               the next token
+ *   tokens      [B][T + 1] int32: the accepted drafts, the next token, then -1
+ *   n_accept    [B] int32: accepted drafts
+ * Draft i is accepted while u_i * q_i(x_i) < p_i(x_i) (float32 product; an id
+ * outside 0..V-1 is not).  With n drafts accepted, the next token is drawn from
+ * max(0, p_n - q_n) (float32 difference; the drafted id's weight is 0 where q is
+ * NULL) if draft n was rejected, from p_n if n = n_draft; if the difference has no
+ * weight at all, from p_n too, and if that has none, the token is -1.  Weights
+ * are held as whole multiples of 2^-40 (at most 1, rounded down; NaN and negative
+ * values 0), so that their sums are exact: with W their sum, the token is the
+ * lowest k whose running sum exceeds floor(W * floor(u * 2^24) / 2^24).
+ * Limits: 1 <= T <= 64, V <= 2^20. */
+int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, const void* q, int64_t q_stride_b,
+                       int64_t q_stride_t, int prob_dtype, int B, int T, int V, const int32_t* draft,
+                       const int32_t* n_draft, const float* u, int32_t* tokens, int32_t* n_accept, void* stream);
+
 /* Workspace bytes needed by lynx_decode_attn / lynx_decode_attn_bf16 for the
  * given shape on the current device (0 for invalid shapes). */
 size_t lynx_decode_attn_workspace_size(int B, int T, int Hq, int Hkv, int head_dim, int max_pages);

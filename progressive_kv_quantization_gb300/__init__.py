@@ -24,6 +24,9 @@ from .lynx import (  # noqa: F401
     lynx_device_status,
     lynx_encode_pages,
     lynx_quantize_magnitudes,
+    lynx_assign_pages,
+    lynx_qkv_append,
+    lynx_verify_drafts,
     lynx_reconstruct,
     load,
 )

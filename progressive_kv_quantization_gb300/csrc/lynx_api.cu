@@ -33,6 +33,8 @@ int cuda_fail(cudaError_t e, const char* where) {
 }
 
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+// not on a multiple of its element's size (NULL is)
+bool off_type(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) != 0; }
 
 int check_params(const lynx_params_t* p) {
   if (p == nullptr) return fail(LYNX_ERR_INVALID_ARG, "params is NULL");
@@ -711,6 +713,114 @@ int lynx_decode_attn_bf16(const void* q_bf16, int B, int T, int Hq, int Hkv, int
                        100.0f, 1e-6f, stream);
 }
 
+int lynx_assign_pages(const int32_t* ctx_len, const int32_t* new_len, int B, int Hkv, int32_t* page_table,
+                      int max_pages, const int32_t* free_pages, int n_free, int n_rows, int32_t* cu_new,
+                      int32_t* positions, int64_t* slots, int32_t* ctx_out, int32_t* n_taken, void* stream) {
+  g_last_error[0] = '\0';
+  if (B < 1 || Hkv < 1 || max_pages < 1 || n_free < 0 || n_rows < 0)
+    return fail(LYNX_ERR_INVALID_ARG, "B=%d Hkv=%d max_pages=%d must be >= 1, n_free=%d n_rows=%d >= 0", B, Hkv,
+                max_pages, n_free, n_rows);
+  if ((int64_t)max_pages * kP > 0x7fffffff) return fail(LYNX_ERR_UNSUPPORTED, "max_pages too large");
+  if (n_rows > 1 << 30 || (int64_t)Hkv * 128 > 0x7fffffff)
+    return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%d, Hkv=%d too large", n_rows, Hkv);
+  if (!ctx_len || !new_len || !page_table || !cu_new || !ctx_out || !n_taken || (n_free > 0 && !free_pages) ||
+      (n_rows > 0 && (!positions || !slots)))
+    return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
+  if (off_type(ctx_len, 4) || off_type(new_len, 4) || off_type(page_table, 4) || off_type(free_pages, 4) ||
+      off_type(cu_new, 4) || off_type(positions, 4) || off_type(slots, 8) || off_type(ctx_out, 4) ||
+      off_type(n_taken, 4))
+    return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
+  if (ctx_out == ctx_len || ctx_out == new_len)
+    return fail(LYNX_ERR_INVALID_ARG, "ctx_out must not be ctx_len or new_len");
+  int* status = device_status_ptr();
+  if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
+  const AssignArgs a{ctx_len, new_len, page_table, free_pages, cu_new, positions, slots, ctx_out,
+                     n_taken, status,  B,          Hkv,        max_pages, n_free, n_rows};
+  cudaError_t e = launch_assign_pages(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lynx_assign_pages launch");
+  return LYNX_OK;
+}
+
+int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
+                    const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
+                    int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
+                    void* k_pages, void* v_pages, int64_t n_pool_pages, void* stream) {
+  g_last_error[0] = '\0';
+  if (n_rows < 0 || Hq < 1 || Hkv < 1)
+    return fail(LYNX_ERR_INVALID_ARG, "n_rows=%lld Hq=%d Hkv=%d", (long long)n_rows, Hq, Hkv);
+  if (head_dim != kH) return fail(LYNX_ERR_UNSUPPORTED, "head_dim=%d (need 128)", head_dim);
+  if (row_stride < ((int64_t)Hq + 2 * (int64_t)Hkv) * kH)
+    return fail(LYNX_ERR_INVALID_ARG, "row_stride=%lld < (Hq + 2 Hkv) * 128", (long long)row_stride);
+  if (rot_dim < 0 || rot_dim > kH || rot_dim % 16 != 0)
+    return fail(LYNX_ERR_UNSUPPORTED, "rot_dim=%d (need a multiple of 16 in 0..128)", rot_dim);
+  if (interleaved != 0 && interleaved != 1) return fail(LYNX_ERR_INVALID_ARG, "interleaved=%d", interleaved);
+  if ((q_weight || k_weight) && !(norm_eps >= 0.0f && norm_eps <= 1.0f))
+    return fail(LYNX_ERR_UNSUPPORTED, "norm_eps=%g outside [0, 1]", (double)norm_eps);
+  if (n_rows == 0) return LYNX_OK;
+  if (n_pool_pages < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool_pages);
+  if (rot_dim > 0 && (max_pos < 1 || !cos_sin))
+    return fail(LYNX_ERR_INVALID_ARG, "rot_dim=%d needs a table of cosines and sines", rot_dim);
+  if (!qkv_bf16 || !positions || !slots || !q_out || !k_pages || !v_pages)
+    return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
+  if (misaligned(qkv_bf16) || misaligned(q_out) || misaligned(k_pages) || misaligned(v_pages) ||
+      (cos_sin && misaligned(cos_sin)) || row_stride % 8 != 0)
+    return fail(LYNX_ERR_ALIGNMENT, "rows of qkv, q_out, the pools and cos_sin must be 16-byte aligned");
+  if (off_type(q_weight, 4) || off_type(k_weight, 4) || off_type(positions, 4) || off_type(slots, 8))
+    return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
+  if (n_rows > 1 << 30 || (int64_t)Hq + Hkv > 65535)
+    return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%lld, Hq=%d, Hkv=%d too large", (long long)n_rows, Hq, Hkv);
+  if (n_pool_pages > ((int64_t)1 << 40)) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages too large");
+  int* status = device_status_ptr();
+  if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
+  AppendArgs a{};
+  a.qkv = static_cast<const uint16_t*>(qkv_bf16);
+  a.row_stride = row_stride;
+  a.n_rows = n_rows;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.norm_eps = norm_eps;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.n_pool = n_pool_pages;
+  a.status = status;
+  cudaError_t e = launch_qkv_append(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lynx_qkv_append launch");
+  return LYNX_OK;
+}
+
+int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, const void* q, int64_t q_stride_b,
+                       int64_t q_stride_t, int prob_dtype, int B, int T, int V, const int32_t* draft,
+                       const int32_t* n_draft, const float* u, int32_t* tokens, int32_t* n_accept, void* stream) {
+  g_last_error[0] = '\0';
+  if (B < 1 || T < 1 || V < 1) return fail(LYNX_ERR_INVALID_ARG, "B=%d T=%d V=%d must be >= 1", B, T, V);
+  // the Lynx paper (§6.1) drafts at most 64 tokens
+  if (T > 64) return fail(LYNX_ERR_UNSUPPORTED, "T=%d > 64", T);
+  if (V > kVerifyMaxVocab) return fail(LYNX_ERR_UNSUPPORTED, "V=%d > %d", V, kVerifyMaxVocab);
+  if (B > 1 << 24) return fail(LYNX_ERR_UNSUPPORTED, "B=%d too large", B);
+  if (prob_dtype != LYNX_OUT_BF16 && prob_dtype != LYNX_OUT_F32)
+    return fail(LYNX_ERR_INVALID_ARG, "prob_dtype=%d (need 0 = BF16 or 1 = F32)", prob_dtype);
+  if (!p || !draft || !u || !tokens || !n_accept) return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
+  if (p_stride_t < V || p_stride_b < 0 || (q && (q_stride_t < V || q_stride_b < 0)))
+    return fail(LYNX_ERR_INVALID_ARG, "strides must hold a row of V probabilities");
+  const int size = prob_dtype == LYNX_OUT_F32 ? 4 : 2;
+  if (off_type(p, size) || off_type(q, size) || off_type(draft, 4) || off_type(n_draft, 4) || off_type(u, 4) ||
+      off_type(tokens, 4) || off_type(n_accept, 4))
+    return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
+  const VerifyArgs a{p, q, p_stride_b, p_stride_t, q_stride_b, q_stride_t, draft, n_draft, u, tokens, n_accept, B, T, V};
+  cudaError_t e = launch_verify_drafts(a, prob_dtype == LYNX_OUT_BF16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lynx_verify_drafts launch");
+  return LYNX_OK;
+}
+
 int lynx_test_inject_wait_timeout(int n_calls) {
   g_last_error[0] = '\0';
   if (n_calls < 0) return fail(LYNX_ERR_INVALID_ARG, "n_calls=%d < 0", n_calls);
@@ -729,7 +839,9 @@ int lynx_device_status(void) {
     const int zero = 0;
     cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
     return fail(LYNX_ERR_DEVICE, "device error word = %d (1: a bounded wait gave up, "
-                "2: page id outside the pool, 3: ctx_len outside 0..max_pages*256)", v);
+                "2: page id outside the pool, 3: ctx_len outside 0..max_pages*256, "
+                "4: position outside the table of cosines and sines, 5: slot outside the pool, "
+                "6: cu_q not the bounds of a ragged batch)", v);
   }
   return LYNX_OK;
 }

@@ -206,4 +206,56 @@ cudaError_t launch_decode(const DecodeArgs& a, int mode, const LutTables* lut, c
 cudaError_t launch_attn_merge(const float* oa, const float* la, const float* ob, const float* lb,
                               int64_t rows, float* o, float* lse, cudaStream_t s);
 
+// ---- the operators around attention in a serving step
+
+struct AssignArgs {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  int32_t* page_table;
+  const int32_t* free_pages;
+  int32_t* cu_new;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* ctx_out;
+  int32_t* n_taken;
+  int* status;
+  int B, Hkv, max_pages, n_free, n_rows;
+};
+cudaError_t launch_assign_pages(const AssignArgs& a, cudaStream_t s);
+
+struct AppendArgs {
+  const uint16_t* qkv;
+  int64_t row_stride;    // elements
+  int64_t n_rows;
+  int Hq, Hkv;
+  const float* q_weight;   // NULL: no norm
+  const float* k_weight;
+  float norm_eps;
+  const float* cos_sin;    // [max_pos][rot]: rot / 2 cosines, then rot / 2 sines
+  int max_pos, rot, interleaved;
+  const int32_t* positions;
+  const int64_t* slots;
+  uint16_t* q_out;
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  int64_t n_pool;
+  int* status;
+  int heads_per_job, q_jobs;   // set by the launcher
+};
+cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s);
+
+constexpr int kVerifyMaxVocab = 1 << 20;
+struct VerifyArgs {
+  const void* p;
+  const void* q;   // NULL: each draft had probability 1
+  int64_t p_stride_b, p_stride_t, q_stride_b, q_stride_t;   // elements
+  const int32_t* draft;
+  const int32_t* n_draft;   // NULL: T for every request
+  const float* u;
+  int32_t* tokens;
+  int32_t* n_accept;
+  int B, T, V;
+};
+cudaError_t launch_verify_drafts(const VerifyArgs& a, bool bf16, cudaStream_t s);
+
 }  // namespace lynx

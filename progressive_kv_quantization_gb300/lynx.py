@@ -79,6 +79,11 @@ SIGNATURES = {
     "lynx_reconstruct_variant": (_I32, [_VP, _VP, _I64, _I32, _PP, _VP, _I32, _VP]),
     "lynx_decode_attn_int4": (_I32, [_VP, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _I64, _VP, _I32,
                                      _VP, _PP, _F32, _I32, _VP, _VP, _VP, _SZ, _VP]),
+    "lynx_assign_pages": (_I32, [_VP, _VP, _I32, _I32, _VP, _I32, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "lynx_qkv_append": (_I32, [_VP, _I64, _I64, _I32, _I32, _I32, _VP, _VP, _F32, _VP, _I32, _I32, _I32, _VP, _VP,
+                               _VP, _VP, _VP, _I64, _VP]),
+    "lynx_verify_drafts": (_I32, [_VP, _I64, _I64, _VP, _I64, _I64, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP,
+                                  _VP, _VP]),
     "lynx_decode_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "lynx_device_status": (_I32, []),
     "lynx_test_inject_wait_timeout": (_I32, [_I32]),
@@ -499,6 +504,144 @@ def lynx_attn_merge(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
     _check(load().lynx_attn_merge(_ptr(o_a), _ptr(lse_a), _ptr(o_b), _ptr(lse_b), lse_a.numel(),
                                   o_a.shape[-1], _ptr(out), _ptr(lse), _stream(stream)), "lynx_attn_merge")
     return out, lse
+
+
+class _On:
+    """Checks the tensors of a call (type, shape, all on the first one's device) and
+    makes that device current for the launch."""
+
+    __slots__ = ("device", "before")
+
+    def __init__(self, first, name):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise LynxError(f"{name} must live on a CUDA device")
+        self.device = first.device
+
+    def need(self, t, dtype, shape, name):
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+            raise LynxError(f"{name} must be a contiguous {dtype} tensor")
+        if t.shape != shape:
+            raise LynxError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.device != self.device:
+            raise LynxError(f"{name} must live on {self.device}")
+        return t
+
+    def make(self, t, dtype, shape, name):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        return self.need(t, dtype, shape, name)
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+
+def lynx_assign_pages(ctx_len, new_len, page_table, free_pages, n_rows: int, cu_new=None, positions=None, slots=None,
+                      ctx_out=None, n_taken=None, stream=None):
+    """Pages, positions and slots of a step's new tokens from the requests'
+    lengths: ctx_len, new_len int32 [B], page_table int32 [B, Hkv, max_pages]
+    (fresh pages' entries are written in place, with ids from the front of
+    free_pages int32 [n_free]).  Returns (cu_new i32 [B + 1], positions i32
+    [n_rows], slots i64 [n_rows, Hkv], ctx_out i32 [B], n_taken i32 [1]); rows of
+    requests that did not fit and rows behind the last request hold -1."""
+    on = _On(page_table, "page_table")
+    if page_table.dim() != 3:
+        raise LynxError("page_table must be [B, Hkv, max_pages]")
+    B, Hkv, max_pages = page_table.shape
+    n_rows = int(n_rows)
+    if n_rows < 0:
+        raise LynxError("n_rows must not be negative")
+    on.need(page_table, torch.int32, page_table.shape, "page_table")
+    on.need(ctx_len, torch.int32, (B,), "ctx_len")
+    on.need(new_len, torch.int32, (B,), "new_len")
+    n_free = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
+    on.need(free_pages, torch.int32, (n_free,), "free_pages")
+    cu_new = on.make(cu_new, torch.int32, (B + 1,), "cu_new")
+    positions = on.make(positions, torch.int32, (n_rows,), "positions")
+    slots = on.make(slots, torch.int64, (n_rows, Hkv), "slots")
+    ctx_out = on.make(ctx_out, torch.int32, (B,), "ctx_out")
+    n_taken = on.make(n_taken, torch.int32, (1,), "n_taken")
+    with on:
+        _check(load().lynx_assign_pages(_ptr(ctx_len), _ptr(new_len), B, Hkv, _ptr(page_table), max_pages,
+                                        _ptr(free_pages), n_free, n_rows, _ptr(cu_new), _ptr(positions), _ptr(slots),
+                                        _ptr(ctx_out), _ptr(n_taken), _stream(stream, on.device)),
+               "lynx_assign_pages")
+    return cu_new, positions, slots, ctx_out, n_taken
+
+
+def lynx_qkv_append(qkv, n_q_heads: int, n_kv_heads: int, cos_sin, positions, slots, k_pages, v_pages, q_weight=None,
+                    k_weight=None, norm_eps: float = 1e-6, interleaved=False, q_out=None, stream=None):
+    """RMS norm (float32 weights [128]; None: no norm) and rotation (cos_sin float32
+    [max_pos, rot_dim], the cosines of a position before its sines; None: no
+    rotation) of the query and key heads of qkv bf16 [n_rows, >= (Hq + 2 Hkv) *
+    128] (rows may be strided), the queries to q_out [n_rows, Hq, 128], the keys
+    and values to slots int64 [n_rows, Hkv] of the pools k_pages / v_pages bf16
+    [n, 128, 256].  Rows with a negative position are skipped.  Returns q_out."""
+    on = _On(qkv, "qkv")
+    Hq, Hkv = int(n_q_heads), int(n_kv_heads)
+    if qkv.dtype != torch.bfloat16 or qkv.dim() != 2 or (qkv.shape[1] > 1 and qkv.stride(1) != 1):
+        raise LynxError("qkv must be a bfloat16 tensor [n_rows, channels] with contiguous channels")
+    n_rows = qkv.shape[0]
+    if Hq < 1 or Hkv < 1 or qkv.shape[1] < (Hq + 2 * Hkv) * H:
+        raise LynxError("each row of qkv must hold (n_q_heads + 2 n_kv_heads) * 128 channels")
+    stride = qkv.stride(0) if n_rows > 1 else (Hq + 2 * Hkv) * H
+    max_pos = rot = 0
+    if cos_sin is not None:
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise LynxError("cos_sin must be a float32 tensor [max_pos, rot_dim]")
+        max_pos, rot = cos_sin.shape
+        on.need(cos_sin, torch.float32, cos_sin.shape, "cos_sin")
+    on.need(positions, torch.int32, (n_rows,), "positions")
+    on.need(slots, torch.int64, (n_rows, Hkv), "slots")
+    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            on.need(w, torch.float32, (H,), nm)
+    n_pool = k_pages.shape[0] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3 else 0
+    on.need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages")
+    on.need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages")
+    q_out = on.make(q_out, torch.bfloat16, (n_rows, Hq, H), "q_out")
+    with on:
+        _check(load().lynx_qkv_append(_ptr(qkv), n_rows, stride, Hq, Hkv, H, _ptr(q_weight), _ptr(k_weight),
+                                      float(norm_eps), _ptr(cos_sin), max_pos, rot, int(bool(interleaved)),
+                                      _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), n_pool,
+                                      _stream(stream, on.device)), "lynx_qkv_append")
+    return q_out
+
+
+def lynx_verify_drafts(p, q, draft, u, n_draft=None, tokens=None, n_accept=None, stream=None):
+    """Verification of drafted tokens from given random numbers: target
+    probabilities p [B, T + 1, V] and draft probabilities q [B, T, V] (float32 or
+    bfloat16, rows may be strided; q None: greedy drafts), draft int32 [B, T], u
+    float32 [B, T + 1], n_draft int32 [B] (None: T each).  Returns (tokens int32
+    [B, T + 1]: the accepted drafts, the next token, -1 behind it; n_accept int32
+    [B])."""
+    on = _On(p, "p")
+    code = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}.get(p.dtype)
+    if code is None or p.dim() != 3 or p.shape[1] < 2 or (p.shape[2] > 1 and p.stride(2) != 1):
+        raise LynxError("p must be a float32 or bfloat16 tensor [B, T + 1, V] with contiguous rows")
+    B, T, V = p.shape[0], p.shape[1] - 1, p.shape[2]
+    qs = (0, 0)
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dtype != p.dtype or q.shape != (B, T, V) or q.device != on.device or (
+                V > 1 and q.stride(2) != 1):
+            raise LynxError("q must be a tensor [B, T, V] of p's type with contiguous rows, on p's device")
+        qs = (q.stride(0) if B > 1 else 0, q.stride(1) if T > 1 else V)
+    on.need(draft, torch.int32, (B, T), "draft")
+    on.need(u, torch.float32, (B, T + 1), "u")
+    if n_draft is not None:
+        on.need(n_draft, torch.int32, (B,), "n_draft")
+    tokens = on.make(tokens, torch.int32, (B, T + 1), "tokens")
+    n_accept = on.make(n_accept, torch.int32, (B,), "n_accept")
+    with on:
+        _check(load().lynx_verify_drafts(_ptr(p), p.stride(0) if B > 1 else 0, p.stride(1), _ptr(q), qs[0], qs[1], code,
+                                         B, T, V, _ptr(draft), _ptr(n_draft), _ptr(u), _ptr(tokens), _ptr(n_accept),
+                                         _stream(stream, on.device)), "lynx_verify_drafts")
+    return tokens, n_accept
 
 
 def lynx_device_status():

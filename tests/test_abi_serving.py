@@ -1,0 +1,72 @@
+"""Argument checks of the serving-step entry points, without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from progressive_kv_quantization_gb300 import lynx as L
+
+
+@pytest.fixture
+def a(lynx_lib):
+    buf = ctypes.create_string_buffer(64)
+    p = ctypes.c_void_p((ctypes.addressof(buf) + 15) & ~15)
+    p.buf = buf
+    return p
+
+
+def test_assign_pages_argument_checks(lynx_lib, a):
+    b = ctypes.c_void_p(a.value + 8)
+
+    def call(ctx=a, new=a, B=1, Hkv=1, table=a, mp=1, free=a, nf=1, rows=1, cu=a, pos=a, slots=a, out=b, taken=a):
+        return lynx_lib.lynx_assign_pages(ctx, new, B, Hkv, table, mp, free, nf, rows, cu, pos, slots, out, taken, None)
+    for kw in (dict(B=0), dict(Hkv=0), dict(mp=0), dict(nf=-1), dict(rows=-1), dict(ctx=None), dict(new=None),
+               dict(table=None), dict(free=None), dict(cu=None), dict(pos=None), dict(slots=None), dict(out=None),
+               dict(taken=None), dict(out=a)):
+        assert call(**kw) == -1, kw
+    assert call(mp=1 << 23) == -2 and call(rows=(1 << 30) + 1) == -2 and call(Hkv=1 << 24) == -2
+    for name in ("ctx", "new", "table", "free", "cu", "pos", "out", "taken"):
+        assert call(**{name: ctypes.c_void_p(a.value + 2)}) == -3, name
+    assert call(slots=ctypes.c_void_p(a.value + 4)) == -3
+
+
+def test_qkv_append_argument_checks(lynx_lib, a):
+    def call(qkv=a, n=1, stride=384, Hq=1, Hkv=1, D=128, wq=None, wk=None, eps=1e-6, cs=a, mp=4, rot=128, il=0, pos=a,
+             slots=a, q=a, k=a, v=a, pool=1):
+        return lynx_lib.lynx_qkv_append(qkv, n, stride, Hq, Hkv, D, wq, wk, eps, cs, mp, rot, il, pos, slots, q, k, v,
+                                        pool, None)
+    for kw in (dict(n=-1), dict(Hq=0), dict(Hkv=0), dict(stride=383), dict(il=2), dict(pool=0), dict(cs=None),
+               dict(mp=0), dict(qkv=None), dict(pos=None), dict(slots=None), dict(q=None), dict(k=None), dict(v=None)):
+        assert call(**kw) == -1, kw
+    for kw in (dict(D=64), dict(rot=8), dict(rot=144), dict(rot=-16), dict(wq=a, eps=-1.0), dict(wk=a, eps=float("nan")),
+               dict(Hq=65535, stride=1 << 24)):
+        assert call(**kw) == -2, kw
+    for name in ("qkv", "cs", "q", "k", "v"):
+        assert call(**{name: ctypes.c_void_p(a.value + 8)}) == -3, name
+    assert call(stride=388) == -3
+    assert call(pos=ctypes.c_void_p(a.value + 2)) == -3 and call(slots=ctypes.c_void_p(a.value + 4)) == -3
+    assert call(n=0, qkv=None, pos=None, slots=None, q=None, k=None, v=None, cs=None) == 0
+
+
+def test_verify_drafts_argument_checks(lynx_lib, a):
+    def call(p=a, pb=20, pt=10, q=a, qb=10, qt=10, dt=1, B=1, T=1, V=10, d=a, nd=None, u=a, tok=a, n=a):
+        return lynx_lib.lynx_verify_drafts(p, pb, pt, q, qb, qt, dt, B, T, V, d, nd, u, tok, n, None)
+    for kw in (dict(B=0), dict(T=0), dict(V=0), dict(dt=2), dict(p=None), dict(d=None), dict(u=None), dict(tok=None),
+               dict(n=None), dict(pt=9), dict(qt=9), dict(pb=-1), dict(qb=-1)):
+        assert call(**kw) == -1, kw
+    assert call(T=65) == -2 and call(V=(1 << 20) + 1, pt=1 << 21, qt=1 << 21) == -2 and call(B=(1 << 24) + 1) == -2
+    for name in ("p", "q", "d", "nd", "u", "tok", "n"):
+        assert call(**{name: ctypes.c_void_p(a.value + 2)}) == -3, name
+    assert call(dt=0, p=ctypes.c_void_p(a.value + 1)) == -3
+
+
+def test_bindings_refuse_host_tensors():
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(L.LynxError, match="CUDA"):
+        L.lynx_assign_pages(i, i, torch.zeros(1, 1, 1, dtype=torch.int32), i, 1)
+    x = torch.zeros(1, 384, dtype=torch.bfloat16)
+    pages = torch.zeros(1, 128, 256, dtype=torch.bfloat16)
+    with pytest.raises(L.LynxError, match="CUDA"):
+        L.lynx_qkv_append(x, 1, 1, None, i, torch.zeros(1, 1, dtype=torch.int64), pages, pages)
+    with pytest.raises(L.LynxError, match="CUDA"):
+        L.lynx_verify_drafts(torch.zeros(1, 2, 4), None, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 2))
