@@ -398,8 +398,8 @@ int lynx_attn_merge(const float* o_a, const float* lse_a, const float* o_b, cons
 /* ---------------------------------------------------------------------------
  * The operators around attention in one step of a serving loop: pages and slots
  * for the step's new tokens (lynx_assign_pages), their queries, keys and values
- * (lynx_qkv_append), and the verification of drafted tokens
- * (lynx_verify_drafts).  Integer arrays and probabilities need only the
+ * (lynx_qkv_append), their attention to the paged cache (lynx_chunk_attn_bf16),
+ * and the verification of drafted tokens (lynx_verify_drafts).  Integer arrays and probabilities need only the
  * alignment of their elements here; other buffers 16 bytes as everywhere.
  */
 
@@ -462,6 +462,41 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
                     int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
                     void* k_pages, void* v_pages, int64_t n_pool_pages, void* stream);
 
+/* Attention of a ragged batch of chunks of new tokens over BF16 pages: chunked
+ * prefill, batches that mix prompts with decoding requests, or one token a
+ * request.  The chunks' own keys and values are in the pages already (as
+ * lynx_qkv_append leaves them).
+ *   q_bf16      [n_rows][Hq][128] BF16, rows row_stride elements apart (>= Hq * 128,
+ *               a multiple of 8).  Query head hq attends KV head hq / (Hq / Hkv).
+ *   cu_q        [B + 1] int32: request b's T_b = cu_q[b + 1] - cu_q[b] rows begin at
+ *               row cu_q[b] (0 rows allowed).  A request whose bounds do not lie in
+ *               order within 0..n_rows is left out and sets device error word 6.
+ *   k_pages, v_pages   pools [n_pool_pages][128][256] BF16;  page_table
+ *               [B][Hkv][max_pages] int32 and ctx_len [B] int32 (all keys of the
+ *               request, the chunk's among them) as lynx_decode_attn
+ *   causal      1: token i of request b sees keys 0 .. ctx_len[b] - T_b + i; a row
+ *               that sees none outputs zeros and lse = -inf.  0: all ctx_len[b] keys.
+ *   out         [n_rows][Hq][128], BF16 (LYNX_OUT_BF16) or float32 (LYNX_OUT_F32,
+ *               as lynx_attn_merge takes it);  lse [n_rows][Hq] float32 (NULL to
+ *               skip).  Rows behind the last request are left as they are.
+ *   workspace   device scratch of lynx_chunk_attn_workspace_size() bytes, clobbered.
+ *               Calls that may overlap (other streams, other captured graphs) need
+ *               one each.
+ * Scores and sums in float32; the probabilities are rounded to BF16 for the
+ * product with the values (their sum is not), an error of about 2^-9 / sqrt(keys
+ * that matter) of the output, at most 2^-8.  Keys and values of positions below
+ * ctx_len must be finite; positions past it in the last page may hold anything.
+ * Limits: Hq % Hkv == 0, B <= 65535, n_rows * Hq / Hkv <= 2^30, n_pool_pages <
+ * 2^24. */
+int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq,
+                         int Hkv, int head_dim, const void* k_pages, const void* v_pages, int64_t n_pool_pages,
+                         const int32_t* page_table, int max_pages, const int32_t* ctx_len, float sm_scale, int causal,
+                         void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lynx_chunk_attn_bf16 for n_rows rows on the current device
+ * (0 for invalid shapes). */
+size_t lynx_chunk_attn_workspace_size(int64_t n_rows, int B, int Hq, int Hkv, int head_dim);
+
 /* Verification of drafted tokens against the target model's probabilities
  * (paper §4.3), from given random numbers.
  *   p           target probabilities: row (b, t) of V values at b * p_stride_b +
@@ -494,9 +529,10 @@ size_t lynx_decode_attn_workspace_size(int B, int T, int Hq, int Hkv, int head_d
 
 /* Test hook (not for production use; off by default): the next n_calls calls
  * of lynx_decode_attn, lynx_decode_attn_bf16, lynx_decode_attn_int4,
- * lynx_decode_attn_uniform, lynx_reconstruct or lynx_encode_tokens made from
- * this host thread run with a fault planted on the host side of the launch:
- * every CTA never issues the copy of its first V page (decode), of its first
+ * lynx_decode_attn_uniform, lynx_chunk_attn_bf16, lynx_reconstruct or
+ * lynx_encode_tokens made from this host thread run with a fault planted on the host side of the launch:
+ * every CTA never issues the copy of its first V page (decode; its first V tile
+ * in lynx_chunk_attn_bf16), of its first
  * page (reconstruct) or of its first item (the token encoder's TMA-staged
  * kernel; an input that admits no tensor map takes the other kernel, which
  * has no waits, and the call runs normally), and every bounded wait of those

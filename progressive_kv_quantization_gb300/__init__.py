@@ -27,6 +27,8 @@ from .lynx import (  # noqa: F401
     lynx_assign_pages,
     lynx_qkv_append,
     lynx_verify_drafts,
+    lynx_chunk_attn_bf16,
+    lynx_chunk_attn_workspace_size,
     lynx_reconstruct,
     load,
 )

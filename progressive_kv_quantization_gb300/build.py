@@ -21,7 +21,8 @@ LIB = os.path.join(BUILD, "liblynx.so")
 
 SOURCES = ["lynx_api.cu", "encode.cu", "reconstruct.cu", "decode_attn.cu", "decode_quant.cu", "decode_tc.cu",
            "decode_narrow.cu", "decode_draft.cu", "decode_bf16.cu",
-           "decode_noalloc.cu", "assign_pages.cu", "qkv_append.cu", "verify_drafts.cu"]
+           "decode_noalloc.cu", "assign_pages.cu", "qkv_append.cu", "verify_drafts.cu",
+           "chunk_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

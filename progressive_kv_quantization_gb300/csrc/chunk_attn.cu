@@ -1,0 +1,793 @@
+// Attention of ragged chunks of new tokens over BF16 pages on the 5th-generation
+// tensor cores (lynx_chunk_attn_bf16): chunked prefill, mixed batches, and single
+// tokens.
+//
+//   S = Q K^T,  P = 2^(S c - m),  O = (sum P V) / (sum P),  c = sm_scale log2(e)
+//   lse = (m + log2 sum P) ln 2
+//
+// Tile.  The query rows of a request that share a KV head are its tokens times
+// the G = Hq / Hkv heads of the group (row = token G + head): a tile is 256 of
+// them, two groups of 128, against 128 keys at a time.  A page is stored
+// channel-major, so a K half page [128 channels][128 tokens] is the MN-major B
+// operand of S = Q K^T and a V half page the K-major B operand of O = P V as they
+// lie: nothing is transposed.
+//
+// Warps.  0-3 and 4-7: softmax of the two groups, one row a thread; 8: issues
+// every tcgen05.mma; 9: TMA of K and V tiles through a ring.  S and O of both
+// groups live in tensor memory (4 x 128 columns).  P overwrites S as BF16 and is
+// the A operand of O += P V from there.  While one group does its softmax the
+// tensor core works for the other.
+//
+// Softmax in one pass over the keys.  The running maximum moves only where a
+// score leads it by more than 8 in log2 units, so that O is rescaled (a round
+// trip through registers) on few tiles; P is at most 2^8.  Row sums are taken
+// of the float32 probabilities.  P is rounded to BF16 for the matrix product
+// (kind::f16 wants V's type): a relative 2^-9 a term, unbiased, about the size of
+// the BF16 output's own rounding once summed.
+//
+// Work split.  The tiles of all requests and heads stand on one line, each as
+// long as its estimated cost; the line is cut into equal parts, one a CTA, one
+// CTA an SM.  A tile that a cut goes through is computed in parts that leave
+// their unnormalised O, m and sum in the workspace, and chunk_combine_kernel
+// joins them; so a long chunk, a ragged batch and a single token over a long
+// context all fill the machine, and the result does not depend on timing.
+//
+// Keys past ctx_len in the last page take no part: their scores are replaced, and
+// their V rows are zeroed in shared memory (0 x NaN would be NaN).
+
+#include "lynx_internal.cuh"
+#include "tma_ptx.cuh"
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+namespace lynx {
+namespace {
+
+constexpr int kGroupRows = 128;
+constexpr int kTileRows = 2 * kGroupRows;
+constexpr int kTileKeys = 128;
+constexpr int kBox = 16384;                    // TMA box: 64 tokens x 128 channels
+constexpr int kSlot = 2 * kBox;                // one K or V tile
+constexpr int kSlots = 5;
+constexpr int kQBytes = 2 * kBox;              // a group's queries: two halves [128 rows][64 channels]
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kMaxItems = 24;
+constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
+constexpr float kLazyLog2 = 8.0f;
+
+constexpr int kOffQ = 0;
+constexpr int kOffRing = kOffQ + 2 * kQBytes;
+constexpr int kOffBar = kOffRing + kSlots * kSlot;
+constexpr int kNumBars = 2 * kSlots + 9;
+constexpr int kOffItems = kOffBar + 8 * kNumBars;
+constexpr int kItemInts = 10;
+constexpr int kOffScan = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
+constexpr int kOffMisc = kOffScan + 16 * 8;
+constexpr int kSmem = kOffMisc + 96;
+constexpr int kSmemAlloc = kSmem + 1024;
+static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
+
+// one tile, or the part of one, of a CTA
+struct Item {
+  int b, h, q_base, row0, rows, T, ctx, k0, k1, kind;
+};
+enum Kind { kDirect = 0, kPartA = 1, kPartB = 2, kNothing = 3 };
+static_assert(sizeof(Item) == kItemInts * 4, "Item");
+
+// what a CTA tells the combine: its part of a tile that an earlier CTA began
+// (a_*), and the tile that it began and did not end (b_*)
+struct Header {
+  int a_state;    // 0: nothing, 1: a part in slot 2 c, 2: the whole tile, already written out
+  int a_ends;     // the tile ends in this CTA
+  int b_open;     // 0: no such tile
+  int b_state;    // as a_state, slot 2 c + 1
+  int h, q_base, row0, rows;
+};
+
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// shared-memory operand, 128-byte swizzle.  K-major: rows of 128 bytes along K,
+// 8-row groups 1024 bytes apart.  MN-major: rows of 64 values along MN, 8-row
+// (K) groups 1024 bytes apart, the next 64 along MN one TMA box on.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(kBox >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// float32 accumulators, BF16 operands, 128 x 128; the B operand K-major or MN-major
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
+constexpr uint32_t kIdescMn = kIdesc | (1u << 16);
+
+#define LYNX_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
+#define LYNX_I8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+// 32 columns of the thread's tensor-memory row
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : LYNX_R8(v, 0), LYNX_R8(v, 8), LYNX_R8(v, 16), LYNX_R8(v, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::LYNX_I8(v, 0),
+      LYNX_I8(v, 8), LYNX_I8(v, 16), LYNX_I8(v, 24), "r"(addr)
+      : "memory");
+}
+// the loaded registers hold their values only behind the wait: pass them through it
+#define LYNX_P8(v, o) "+r"(v[o]), "+r"(v[o + 1]), "+r"(v[o + 2]), "+r"(v[o + 3]), "+r"(v[o + 4]), "+r"(v[o + 5]), "+r"(v[o + 6]), "+r"(v[o + 7])
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : LYNX_P8(v, 0), LYNX_P8(v, 8), LYNX_P8(v, 16), LYNX_P8(v, 24)
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_hold32(uint32_t* v) {
+  asm volatile("" : LYNX_P8(v, 0), LYNX_P8(v, 8), LYNX_P8(v, 16), LYNX_P8(v, 24) : : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st_() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// ------------------------------------------------------------------ work split
+
+// A request's tiles on the cost line of one head, in 1/256 keys: tile m costs
+// its keys (those before the chunk plus 256 / G more with every tile under a
+// causal mask) and 256 keys for its start and end.
+struct Request {
+  int q_base, T, ctx, tiles;
+  long long base, step;
+  __device__ long long at(int m) const { return m * base + step * ((long long)m * (m + 1) / 2); }
+  __device__ int tile_of(long long x) const {   // the tile that holds x, at(0) <= x < at(tiles)
+    int lo = 0, hi = tiles;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (at(mid) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+};
+
+__device__ __forceinline__ Request load_request(const ChunkArgs& a, int b) {
+  Request r{0, 0, 0, 0, 0, 0};
+  if (b >= a.B) return r;
+  const int lo = a.cu_q[b], hi = a.cu_q[b + 1];
+  const int ctx = a.ctx_len[b];
+  const int max_keys = a.max_pages * kP;
+  if (ctx < 0 || ctx > max_keys) atomicExch(a.status, 3);
+  if (lo < 0 || hi < lo || hi > a.n_rows) {
+    atomicExch(a.status, 6);
+    return r;
+  }
+  r.q_base = lo;
+  r.T = hi - lo;
+  r.ctx = min(max(ctx, 0), max_keys);
+  r.tiles = (r.T * a.G + kTileRows - 1) / kTileRows;
+  r.base = (long long)((a.causal ? max(r.ctx - r.T, 0) : r.ctx) + 256) << 8;
+  r.step = a.causal ? 65536 / a.G : 0;
+  return r;
+}
+
+// keys that the rows of a token see
+__device__ __forceinline__ int visible(const ChunkArgs& a, int ctx, int T, int token) {
+  return a.causal ? max(ctx - T + token + 1, 0) : ctx;
+}
+
+template <typename V>
+__device__ __forceinline__ V block_scan(V v, V* s_scan, V* total) {   // inclusive; all threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) s_scan[warp] = v;
+  __syncthreads();
+  V before = 0, all = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const V u = s_scan[w];
+    if (w < warp) before += u;
+    all += u;
+  }
+  __syncthreads();
+  *total = all;
+  return v + before;
+}
+
+// ------------------------------------------------------------------ kernel
+
+__global__ void __launch_bounds__(kThreads, 1)
+chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = blockIdx.x;
+
+  Item* items = reinterpret_cast<Item*>(smem + kOffItems);
+  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
+  long long* s_next = reinterpret_cast<long long*>(smem + kOffMisc);
+  Header* s_hdr = reinterpret_cast<Header*>(smem + kOffMisc + 16);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc + 64);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 68);
+
+  const uint32_t bar0 = base + kOffBar;
+  auto kv_full = [&](int s) { return bar0 + 8 * s; };
+  auto kv_empty = [&](int s) { return bar0 + 8 * (kSlots + s); };
+  const uint32_t bars = bar0 + 8 * 2 * kSlots;
+  auto q_full = [&](int g) { return bars + 8 * g; };
+  auto s_full = [&](int g) { return bars + 8 * (2 + g); };
+  auto p_full = [&](int g) { return bars + 8 * (4 + g); };
+  auto o_done = [&](int g) { return bars + 8 * (6 + g); };
+  const uint32_t drained = bars + 8 * 8;   // used once, by a CTA that gives up
+
+  if (tid == 0) {
+    for (int s = 0; s < 2 * kSlots; ++s) mbar_init(bar0 + 8 * s, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(q_full(g), kGroupRows);
+      mbar_init(s_full(g), 1);
+      mbar_init(p_full(g), kGroupRows);
+      mbar_init(o_done(g), 1);
+    }
+    mbar_init(drained, 1);
+    *s_hdr = Header{0, 0, 0, 0, 0, 0, 0, 0};
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  // every access to global memory follows this wait
+  wait_prerequisite_grids();
+
+  // the line's length, and this CTA's part [x0, x1) of it
+  Request req = load_request(a, tid);
+  long long Wh = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    const Request r = b0 == 0 ? req : load_request(a, b0 + tid);
+    long long sum;
+    block_scan(r.at(r.tiles), s_scan, &sum);
+    Wh += sum;
+  }
+  const long long W = Wh * a.Hkv;
+  const long long n_cta = max(1ll, min((long long)gridDim.x, W / ((long long)a.min_keys << 8)));
+  auto cut = [&](long long i) { return W / n_cta * i + W % n_cta * i / n_cta; };
+  long long x0 = c < n_cta ? cut(c) : W;
+  const long long x1 = c < n_cta ? cut(c + 1) : W;
+
+  const unsigned long long wait_ns = a.wait_ns;
+  auto give_up = [&]() {
+    atomicExch(a.status, 1);
+    *s_abort = 1;
+  };
+  // counters of each role, running over all items
+  uint32_t n_kv_ring = 0;     // K and V tiles through the ring (producer; MMA warp)
+  uint32_t n_tile_g = 0;      // S tiles of this thread's group (softmax)
+  uint32_t mma_items[2] = {0, 0}, mma_tiles[2] = {0, 0};
+  bool failed = false;
+
+  while (x0 < x1) {
+    // ---- the items of this head's segment, at most kMaxItems
+    const long long h = x0 / Wh;
+    const long long seg0 = x0 - h * Wh, seg1 = min(x1 - h * Wh, Wh);
+    long long before = 0;
+    int n_items = 0;
+    if (tid == 0) *s_next = h * Wh + seg1;
+    for (int b0 = 0; b0 < a.B && before < seg1; b0 += kThreads) {
+      const Request r = b0 == 0 ? req : load_request(a, b0 + tid);
+      long long sum;
+      const long long len = r.at(r.tiles);
+      const long long p = before + block_scan(len, s_scan, &sum) - len;
+      const long long lo = max(seg0 - p, 0ll), hi = min(seg1 - p, len);
+      int m0 = 0, m1 = -1;
+      if (lo < hi) {
+        m0 = r.tile_of(lo);
+        m1 = r.tile_of(hi - 1);
+      }
+      int all;
+      int at = n_items + block_scan(m1 - m0 + 1, reinterpret_cast<int*>(s_scan), &all) - (m1 - m0 + 1);
+      for (int m = m0; m <= m1; ++m, ++at) {
+        if (at >= kMaxItems) {
+          if (at == kMaxItems) *s_next = h * Wh + p + r.at(m);
+          break;
+        }
+        const int last = min(r.T - 1, (int)(((long long)kTileRows * (m + 1) - 1) / a.G));
+        const int n_kv = (visible(a, r.ctx, r.T, last) + kTileKeys - 1) / kTileKeys;
+        const long long from = r.at(m), cost = r.at(m + 1) - from;
+        const bool starts = lo <= from, ends = hi >= from + cost;
+        Item it;
+        it.b = b0 + tid;
+        it.h = (int)h;
+        it.q_base = r.q_base;
+        it.row0 = m * kTileRows;
+        it.rows = min(kTileRows, r.T * a.G - it.row0);
+        it.T = r.T;
+        it.ctx = r.ctx;
+        it.k0 = starts ? 0 : (int)((lo - from) * n_kv / cost);
+        it.k1 = ends ? n_kv : (int)((hi - from) * n_kv / cost);
+        const bool whole = it.k0 == 0 && it.k1 == n_kv && (n_kv > 0 || starts);
+        it.kind = whole ? kDirect : it.k0 == it.k1 ? kNothing : starts ? kPartB : kPartA;
+        items[at] = it;
+        const int state = n_kv > 0 && whole ? 2 : it.k1 > it.k0 ? 1 : 0;
+        if (!starts) {
+          s_hdr->a_state = state;
+          s_hdr->a_ends = ends;
+        } else if (!ends && n_kv > 0) {
+          s_hdr->b_open = 1;
+          s_hdr->b_state = state;
+          s_hdr->h = it.h;
+          s_hdr->q_base = it.q_base;
+          s_hdr->row0 = it.row0;
+          s_hdr->rows = it.rows;
+        }
+      }
+      n_items += all;
+      before += sum;
+    }
+    __syncthreads();
+    n_items = min(n_items, kMaxItems);
+    x0 = *s_next;
+
+    if (warp == kTmaWarp) {
+      // ================= producer: K and V tiles in the order of use
+      if (lane == 0) {
+        for (int i = 0; i < n_items && !failed; ++i) {
+          const Item it = items[i];
+          if (it.kind == kNothing || it.k0 == it.k1) continue;
+          const int32_t* row = a.page_table + ((int64_t)it.b * a.Hkv + it.h) * a.max_pages;
+          int next_id = row[it.k0 >> 1];
+          int64_t id = 0;
+          for (int k = it.k0; k < it.k1 && !failed; ++k) {
+            if (k == it.k0 || !(k & 1)) {
+              id = next_id;
+              if (((k >> 1) + 1) * 2 < it.k1) next_id = row[(k >> 1) + 1];
+              if (id < 0 || id >= a.n_pool) {
+                atomicExch(a.status, 2);
+                id = 0;
+              }
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const int s = n_kv_ring % kSlots;
+              if (n_kv_ring >= kSlots && !mbar_wait(kv_empty(s), (n_kv_ring / kSlots - 1) & 1, wait_ns)) {
+                give_up();
+                failed = true;
+                break;
+              }
+              if (a.inject && n_kv_ring == 1) {   // test hook: the first V tile never arrives
+                ++n_kv_ring;
+                continue;
+              }
+              const uint32_t dst = base + kOffRing + s * kSlot;
+              mbar_expect_tx(kv_full(s), kSlot);
+              tma_tile_g2s(dst, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys, (int)(id * kH), kv_full(s));
+              tma_tile_g2s(dst + kBox, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys + 64, (int)(id * kH), kv_full(s));
+              ++n_kv_ring;
+            }
+          }
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ================= tensor-core warp
+      for (int i = 0; i < n_items && !failed; ++i) {
+        const Item it = items[i];
+        if (it.kind == kNothing || it.k0 == it.k1) continue;
+        const int groups = it.rows > kGroupRows ? 2 : 1;
+        const int n = it.k1 - it.k0;
+        // S of group g against the K tile in slot s
+        auto qk = [&](int g, int s) {
+          if (lane == 0) {
+            const uint32_t q = base + kOffQ + g * kQBytes, k = base + kOffRing + s * kSlot;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ss(tmem + g * 128, desc_k(q + (ks >> 2) * kBox + (ks & 3) * 32), desc_mn(k + ks * 2048), kIdescMn, ks > 0);
+            tc_commit(s_full(g));
+          }
+          __syncwarp();
+        };
+        auto wait_kv = [&](uint32_t u) {
+          if (!mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns)) failed = true;
+          failed = __any_sync(0xffffffffu, failed);
+          return !failed;
+        };
+        if (!wait_kv(n_kv_ring)) break;
+        for (int g = 0; g < groups; ++g) {
+          if (!mbar_wait(q_full(g), mma_items[g] & 1, wait_ns)) failed = true;
+          ++mma_items[g];
+        }
+        failed = __any_sync(0xffffffffu, failed);
+        if (failed) break;
+        tc_fence_after();
+        for (int g = 0; g < groups; ++g) qk(g, n_kv_ring % kSlots);
+        if (lane == 0) tc_commit(kv_empty(n_kv_ring % kSlots));
+        for (int j = 0; j < n; ++j) {
+          const uint32_t uv = n_kv_ring + 2 * j + 1, uk = uv + 1;
+          const int sv = uv % kSlots, sk = uk % kSlots;
+          if (!wait_kv(uv)) break;
+          const int tail = it.ctx - (it.k0 + j) * kTileKeys;   // valid keys of the tile
+          if (tail < kTileKeys) {
+            // zero the V rows of the tokens past the context: 16-byte pieces of
+            // 8 tokens, the one that the context ends in value by value
+            uint8_t* v = smem + kOffRing + sv * kSlot;
+            for (int x = lane; x < kH * 16; x += 32) {
+              const int ch = x >> 4, piece = x & 15;
+              const int left = tail - piece * 8;
+              if (left >= 8) continue;
+              uint8_t* at = v + (piece >> 3) * kBox + ch * 128 + (((piece & 7) ^ (ch & 7)) << 4);
+              if (left <= 0) {
+                *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                for (int e = left; e < 8; ++e) reinterpret_cast<uint16_t*>(at)[e] = 0;
+              }
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+          if (j + 1 < n && !wait_kv(uk)) break;
+          for (int g = 0; g < groups; ++g) {
+            if (!mbar_wait(p_full(g), mma_tiles[g] & 1, wait_ns)) failed = true;
+            ++mma_tiles[g];
+            failed = __any_sync(0xffffffffu, failed);
+            if (failed) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint32_t v = base + kOffRing + sv * kSlot;
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                mma_ts(tmem + 256 + g * 128, tmem + g * 128 + ks * 8, desc_k(v + (ks >> 2) * kBox + (ks & 3) * 32), kIdesc,
+                       j > 0 || ks > 0);
+              tc_commit(o_done(g));
+            }
+            __syncwarp();
+            if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sv));
+            if (j + 1 < n) {
+              qk(g, sk);
+              if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sk));
+            }
+          }
+          if (failed) break;
+        }
+        n_kv_ring += 2 * n;
+      }
+      if (failed && lane == 0) give_up();
+    } else {
+      // ================= softmax: group g, one row a thread
+      const int g = warp >> 2;
+      const int r = (warp & 3) * 32 + lane;               // row of the group, tensor-memory lane
+      const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
+      for (int i = 0; i < n_items && !failed; ++i) {
+        const Item it = items[i];
+        if (it.kind == kNothing || it.rows <= g * kGroupRows) continue;
+        const int row = it.row0 + g * kGroupRows + r;
+        const bool real = g * kGroupRows + r < it.rows;
+        const int token = row / a.G, hq = it.h * a.G + row - token * a.G;
+        const int64_t out_row = ((int64_t)(it.q_base + token)) * a.Hq + hq;
+        float m = -CUDART_INF_F, l = 0.0f;
+        const int n = it.k1 - it.k0;
+        if (n > 0) {
+          // the row's queries to shared memory, 16-byte pieces swizzled
+          uint8_t* q = smem + kOffQ + g * kQBytes + r * 128;
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(it.q_base + token) * a.q_stride + hq * kH);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (real) v = src[x];
+            *reinterpret_cast<uint4*>(q + (x >> 3) * kBox + (((x & 7) ^ (r & 7)) << 4)) = v;
+          }
+          fence_proxy_async();
+          mbar_arrive(q_full(g));
+          // rows past the tile's last hold zero queries: whatever they sum up is not written
+          const int seen = real ? visible(a, it.ctx, it.T, token) : 0x7fffffff;
+          const float sc = a.scale_log2;
+          for (int j = 0; j < n; ++j) {
+            if (!mbar_wait(s_full(g), n_tile_g & 1, wait_ns)) failed = true;
+            failed = __any_sync(0xffffffffu, failed);
+            if (failed) break;
+            tc_fence_after();
+            uint32_t s[128];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tmem_ld32(t_s + 32 * x, s + 32 * x);
+            tmem_wait_ld32(s);
+            tmem_hold32(s + 32);
+            tmem_hold32(s + 64);
+            tmem_hold32(s + 96);
+            const int left = seen - (it.k0 + j) * kTileKeys;
+            if (__any_sync(0xffffffffu, left < kTileKeys)) {
+#pragma unroll
+              for (int x = 0; x < 128; ++x)
+                if (x >= left) s[x] = 0xFF800000u;   // -inf
+            }
+            float mx[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
+#pragma unroll
+            for (int x = 4; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
+              const float m_new = fmaxf(m, top);
+              const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - m_new);
+              if (j > 0) {   // rescale O, once the product before has been added to it
+                if (!mbar_wait(o_done(g), (n_tile_g - 1) & 1, wait_ns)) failed = true;
+                failed = __any_sync(0xffffffffu, failed);
+                if (failed) break;
+                tc_fence_after();
+                const float fo = m == -CUDART_INF_F ? 1.0f : f;   // O is 0 there
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  uint32_t o[32];
+                  tmem_ld32(t_o + 32 * x, o);
+                  tmem_wait_ld32(o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+                  tmem_st32(t_o + 32 * x, o);
+                }
+              }
+              l *= f;
+              m = m_new;
+            }
+            const float ref = m == -CUDART_INF_F ? 0.0f : -m;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t p[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float p0 = ex2(fmaf(__uint_as_float(s[64 * x + 2 * e]), sc, ref));
+                const float p1 = ex2(fmaf(__uint_as_float(s[64 * x + 2 * e + 1]), sc, ref));
+                sum[e & 3] += p0 + p1;
+                p[e] = bf16x2(p0, p1);
+              }
+              tmem_st32(t_s + 32 * x, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st_();
+            tc_fence_before();
+            mbar_arrive(p_full(g));
+            ++n_tile_g;
+          }
+          if (!failed && !mbar_wait(o_done(g), (n_tile_g - 1) & 1, wait_ns)) failed = true;
+          failed = __any_sync(0xffffffffu, failed);
+          if (failed) break;
+          tc_fence_after();
+        }
+        // ---- the row's output, or its part
+        const bool part = it.kind != kDirect;
+        const float scale = part ? 1.0f : l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
+        float* ws = nullptr;
+        if (part) {
+          float* slot = a.ws_o + (int64_t)(2 * c + (it.kind == kPartB)) * a.slot_rows * (kH + 2);
+          const int rr = g * kGroupRows + r;
+          ws = slot + rr * kH;
+          if (real) {
+            slot[a.slot_rows * kH + 2 * rr] = m;
+            slot[a.slot_rows * kH + 2 * rr + 1] = l;
+          }
+        } else if (real && a.lse) {
+          a.lse[out_row] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(t_o + 32 * x, o);
+            tmem_wait_ld32(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+          if (real && (part || a.out_f32)) {
+            uint4* dst = reinterpret_cast<uint4*>(part ? ws : static_cast<float*>(a.out) + out_row * kH) + 8 * x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else if (real) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * kH) + 4 * x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = bf16x2(__uint_as_float(o[8 * e + 2 * y]), __uint_as_float(o[8 * e + 2 * y + 1]));
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before();   // O has been read before the next item's first product
+      }
+      if (failed && lane == 0) give_up();
+    }
+    __syncthreads();
+    if (*s_abort) break;
+  }
+
+  allow_dependent_launch();
+  if (*s_abort) {
+    // the copies and products in flight end before the memory they use is given up
+    if (warp == kTmaWarp && lane == 0) {
+      for (uint32_t u = n_kv_ring > kSlots ? n_kv_ring - kSlots : 0; u < n_kv_ring; ++u)
+        if (!(a.inject && u == 1)) mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns);
+    }
+    if (warp == kMmaWarp) {
+      if (lane == 0) {
+        tc_commit(drained);
+        mbar_wait(drained, 0, wait_ns);
+      }
+      __syncwarp();
+    }
+  }
+  if (tid == 0) reinterpret_cast<Header*>(a.ws_hdr)[c] = *s_abort ? Header{0, 0, 0, 0, 0, 0, 0, 0} : *s_hdr;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ join of the parts
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+
+// CTA (c, y) joins the tile that CTA c of the kernel above began and did not
+// end: rows y kJoinWarps + warp, + gridDim.y kJoinWarps, ...; a warp a row.
+// With m* the largest of the parts' m: O = sum 2^(m_i - m*) O_i / sum 2^(m_i - m*) l_i.
+__global__ void __launch_bounds__(kJoinThreads)
+chunk_combine_kernel(const ChunkArgs a) {
+  __shared__ int s_slot[2 * kMaxCtas];
+  __shared__ int s_n;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_prerequisite_grids();
+  const Header* hdr = reinterpret_cast<const Header*>(a.ws_hdr);
+  const Header hd = hdr[c];
+  if (!hd.b_open || hd.b_state == 2) return;
+  if (warp == 0) {
+    int n = 0;
+    if (hd.b_state == 1) {
+      if (lane == 0) s_slot[0] = 2 * c + 1;
+      n = 1;
+    }
+    // the CTAs behind, up to the one where the tile ends
+    for (int d0 = c + 1; d0 < a.n_cta; d0 += 32) {
+      const int d = d0 + lane;
+      int state = 0, ends = 0;
+      if (d < a.n_cta) {
+        state = hdr[d].a_state;
+        ends = hdr[d].a_ends;
+      }
+      const unsigned e = __ballot_sync(0xffffffffu, ends != 0);
+      const unsigned within = e ? (e & -e) | ((e & -e) - 1) : 0xffffffffu;
+      const unsigned valid = __ballot_sync(0xffffffffu, state == 1) & within;
+      if (__ballot_sync(0xffffffffu, state == 2) & within) {   // one CTA had it all and wrote it out
+        n = 0;
+        break;
+      }
+      if (valid >> lane & 1) s_slot[n + __popc(valid & ((1u << lane) - 1))] = 2 * d;
+      n += __popc(valid);
+      if (e) break;
+    }
+    if (lane == 0) s_n = n;
+  }
+  __syncthreads();
+  const int n = s_n;
+  if (n == 0) return;
+  const int64_t stride = (int64_t)a.slot_rows * (kH + 2);
+  for (int r = blockIdx.y * kJoinWarps + warp; r < hd.rows; r += gridDim.y * kJoinWarps) {
+    const float* ml = a.ws_o + (int64_t)a.slot_rows * kH + 2 * r;
+    float m = -CUDART_INF_F;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[s_slot[i] * stride]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* slot = a.ws_o + s_slot[i] * stride;
+      const float2 st = *reinterpret_cast<const float2*>(slot + (int64_t)a.slot_rows * kH + 2 * r);
+      const float4 o = *reinterpret_cast<const float4*>(slot + r * kH + 4 * lane);
+      const float f = st.x == -CUDART_INF_F ? (st.y == st.y ? 0.0f : 1.0f) : ex2(st.x - m);   // a NaN sum stays
+      l = fmaf(f, st.y, l);
+      acc.x = fmaf(f, o.x, acc.x);
+      acc.y = fmaf(f, o.y, acc.y);
+      acc.z = fmaf(f, o.z, acc.z);
+      acc.w = fmaf(f, o.w, acc.w);
+    }
+    const float scale = l > 0.0f ? 1.0f / l : l;
+    const int row = hd.row0 + r;
+    const int token = row / a.G;
+    const int64_t out_row = (int64_t)(hd.q_base + token) * a.Hq + hd.h * a.G + row - token * a.G;
+    acc.x *= scale;
+    acc.y *= scale;
+    acc.z *= scale;
+    acc.w *= scale;
+    if (a.out_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * kH + 4 * lane) = acc;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * kH + 4 * lane) =
+          make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
+    if (lane == 0 && a.lse) a.lse[out_row] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace
+
+int chunk_ctas() {
+  const int n = device_sm_count();
+  return n < kMaxCtas ? n : kMaxCtas;
+}
+
+// partial rows per slot: those of a tile, or all that the batch has
+int chunk_slot_rows(int64_t n_rows, int G) {
+  const int64_t rows = (n_rows * G + 1) & ~(int64_t)1;
+  return rows < kTileRows ? (int)rows : kTileRows;
+}
+
+size_t chunk_ws_bytes(int64_t n_rows, int G) {
+  return (size_t)kMaxCtas * sizeof(Header) + (size_t)2 * chunk_ctas() * chunk_slot_rows(n_rows, G) * (kH + 2) * 4;
+}
+
+cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {
+  static bool configured[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
+  if (n_pool_too_large(a.n_pool)) return cudaErrorInvalidValue;
+  CUtensorMap tk, tv;
+  if (!bf16_page_map(&tk, a.k_pages, a.n_pool) || !bf16_page_map(&tv, a.v_pages, a.n_pool))
+    return cudaErrorInvalidValue;
+  a.n_cta = chunk_ctas();
+  a.slot_rows = chunk_slot_rows(a.n_rows, a.G);
+  a.ws_hdr = workspace;
+  a.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * sizeof(Header));
+  // two tiles of keys are the least that is worth a CTA's start and end (counted as two more)
+  a.min_keys = 512;
+  cudaError_t e = launch_programmatic(chunk_attn_kernel, dim3(a.n_cta), dim3(kThreads), kSmemAlloc, s, a, tk, tv);
+  if (e != cudaSuccess) return e;
+  const int slices = (a.slot_rows + kJoinWarps - 1) / kJoinWarps;
+  return launch_programmatic(chunk_combine_kernel, dim3(a.n_cta, slices < 8 ? slices : 8), dim3(kJoinThreads), 0, s, a);
+}
+
+}  // namespace lynx

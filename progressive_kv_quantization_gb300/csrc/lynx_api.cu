@@ -797,6 +797,91 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
   return LYNX_OK;
 }
 
+namespace {
+
+int check_chunk_shape(int64_t n_rows, int B, int Hq, int Hkv, int head_dim) {
+  if (n_rows < 0 || B < 1 || Hq < 1 || Hkv < 1)
+    return fail(LYNX_ERR_INVALID_ARG, "n_rows=%lld must be >= 0, B=%d Hq=%d Hkv=%d >= 1", (long long)n_rows, B, Hq,
+                Hkv);
+  if (head_dim != kH) return fail(LYNX_ERR_UNSUPPORTED, "head_dim=%d (need 128)", head_dim);
+  if (Hq % Hkv != 0) return fail(LYNX_ERR_INVALID_ARG, "Hq=%d not a multiple of Hkv=%d", Hq, Hkv);
+  if (Hq > 65536 || B > 65535 || n_rows > 0x40000000 / (Hq / Hkv))
+    return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%lld, Hq=%d or B=%d too large", (long long)n_rows, Hq, B);
+  return LYNX_OK;
+}
+
+}  // namespace
+
+size_t lynx_chunk_attn_workspace_size(int64_t n_rows, int B, int Hq, int Hkv, int head_dim) {
+  if (check_chunk_shape(n_rows, B, Hq, Hkv, head_dim) != LYNX_OK) return 0;
+  return chunk_ws_bytes(n_rows, Hq / Hkv);
+}
+
+int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq,
+                         int Hkv, int head_dim, const void* k_pages, const void* v_pages, int64_t n_pool_pages,
+                         const int32_t* page_table, int max_pages, const int32_t* ctx_len, float sm_scale, int causal,
+                         void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_chunk_shape(n_rows, B, Hq, Hkv, head_dim);
+  if (st != LYNX_OK) return st;
+  if (max_pages < 1) return fail(LYNX_ERR_INVALID_ARG, "max_pages=%d must be >= 1", max_pages);
+  if ((int64_t)max_pages * kP > 0x7fffff00) return fail(LYNX_ERR_UNSUPPORTED, "max_pages too large");
+  if (row_stride < (int64_t)Hq * kH)
+    return fail(LYNX_ERR_INVALID_ARG, "row_stride=%lld < Hq * 128", (long long)row_stride);
+  if (out_dtype != LYNX_OUT_BF16 && out_dtype != LYNX_OUT_F32)
+    return fail(LYNX_ERR_INVALID_ARG, "out_dtype=%d (need 0 = BF16 or 1 = F32)", out_dtype);
+  if (causal != 0 && causal != 1) return fail(LYNX_ERR_INVALID_ARG, "causal=%d", causal);
+  if (!(sm_scale > 0.0f) || !isfinite(sm_scale))
+    return fail(LYNX_ERR_INVALID_ARG, "sm_scale=%g must be finite and > 0", (double)sm_scale);
+  if (n_rows == 0) return LYNX_OK;
+  if (!q_bf16 || !cu_q || !k_pages || !v_pages || !page_table || !ctx_len || !out)
+    return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
+  if (n_pool_pages < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool_pages);
+  if (n_pool_too_large(n_pool_pages))
+    return fail(LYNX_ERR_UNSUPPORTED, "n_pool_pages=%lld too large", (long long)n_pool_pages);
+  if (misaligned(q_bf16) || misaligned(k_pages) || misaligned(v_pages) || misaligned(out) || misaligned(workspace) ||
+      row_stride % 8 != 0)
+    return fail(LYNX_ERR_ALIGNMENT, "rows of q, the pools, out and the workspace must be 16-byte aligned");
+  if (off_type(cu_q, 4) || off_type(page_table, 4) || off_type(ctx_len, 4) || off_type(lse, 4))
+    return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
+  const size_t need = chunk_ws_bytes(n_rows, Hq / Hkv);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(LYNX_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                workspace ? workspace_bytes : (size_t)0);
+  int* status = device_status_ptr();
+  if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
+  ChunkArgs a{};
+  a.q = static_cast<const uint16_t*>(q_bf16);
+  a.q_stride = row_stride;
+  a.n_rows = n_rows;
+  a.cu_q = cu_q;
+  a.ctx_len = ctx_len;
+  a.page_table = page_table;
+  a.k_pages = static_cast<const uint16_t*>(k_pages);
+  a.v_pages = static_cast<const uint16_t*>(v_pages);
+  a.n_pool = n_pool_pages;
+  a.out = out;
+  a.lse = lse;
+  a.out_f32 = out_dtype == LYNX_OUT_F32;
+  a.status = status;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.max_pages = max_pages;
+  a.causal = causal;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.wait_ns = kDefaultWaitNs;
+  if (g_inject_calls > 0) {   // test hook, off unless armed
+    --g_inject_calls;
+    a.inject = 1;
+    a.wait_ns = 1000000ull;
+  }
+  cudaError_t e = launch_chunk_attn(a, workspace, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lynx_chunk_attn_bf16 launch");
+  return LYNX_OK;
+}
+
 int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, const void* q, int64_t q_stride_b,
                        int64_t q_stride_t, int prob_dtype, int B, int T, int V, const int32_t* draft,
                        const int32_t* n_draft, const float* u, int32_t* tokens, int32_t* n_accept, void* stream) {

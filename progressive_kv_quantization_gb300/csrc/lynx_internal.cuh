@@ -258,4 +258,30 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify_drafts(const VerifyArgs& a, bool bf16, cudaStream_t s);
 
+struct ChunkArgs {
+  const uint16_t* q;
+  int64_t q_stride;      // elements between rows
+  int64_t n_rows;
+  const int32_t* cu_q;
+  const int32_t* ctx_len;
+  const int32_t* page_table;
+  const uint16_t* k_pages;
+  const uint16_t* v_pages;
+  int64_t n_pool;
+  void* out;
+  float* lse;            // NULL to skip
+  int out_f32;
+  int* status;
+  int B, Hq, Hkv, G, max_pages, causal;
+  float scale_log2;
+  unsigned long long wait_ns;   // as DecodeArgs
+  int inject;                   // test hook: every CTA's first V tile is never copied
+  // set by the launcher
+  int n_cta, slot_rows, min_keys;
+  void* ws_hdr;
+  float* ws_o;
+};
+size_t chunk_ws_bytes(int64_t n_rows, int G);
+cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s);
+
 }  // namespace lynx

@@ -82,6 +82,9 @@ SIGNATURES = {
     "lynx_assign_pages": (_I32, [_VP, _VP, _I32, _I32, _VP, _I32, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP]),
     "lynx_qkv_append": (_I32, [_VP, _I64, _I64, _I32, _I32, _I32, _VP, _VP, _F32, _VP, _I32, _I32, _I32, _VP, _VP,
                                _VP, _VP, _VP, _I64, _VP]),
+    "lynx_chunk_attn_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
+    "lynx_chunk_attn_bf16": (_I32, [_VP, _I64, _I64, _VP, _I32, _I32, _I32, _I32, _VP, _VP, _I64, _VP, _I32, _VP,
+                                    _F32, _I32, _VP, _I32, _VP, _VP, _SZ, _VP]),
     "lynx_verify_drafts": (_I32, [_VP, _I64, _I64, _VP, _I64, _I64, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP,
                                   _VP, _VP]),
     "lynx_decode_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
@@ -611,6 +614,55 @@ def lynx_qkv_append(qkv, n_q_heads: int, n_kv_heads: int, cos_sin, positions, sl
                                       _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), n_pool,
                                       _stream(stream, on.device)), "lynx_qkv_append")
     return q_out
+
+
+def lynx_chunk_attn_workspace_size(n_rows, B, Hq, Hkv, head_dim) -> int:
+    return int(load().lynx_chunk_attn_workspace_size(n_rows, B, Hq, Hkv, head_dim))
+
+
+def lynx_chunk_attn_bf16(q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_heads: int, sm_scale=None, causal=True,
+                         out=None, lse=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """Attention of a ragged batch of chunks of new tokens over BF16 page pools
+    (their own keys and values already in the pages): q bf16 [n_rows, Hq, 128]
+    (rows may be strided), request b's rows cu_q[b] .. cu_q[b + 1] - 1 (int32
+    [B + 1]), page_table int32 [B, Hkv, max_pages], ctx_len int32 [B] (all keys,
+    the chunk's among them).  Returns (out [n_rows, Hq, 128] of out's type or
+    out_dtype, bfloat16 or float32; lse f32 [n_rows, Hq]); rows behind the last
+    request are left as they are."""
+    on = _On(q, "q")
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != H or q.stride(2) != 1 or (
+            q.shape[1] > 1 and q.stride(1) != H):
+        raise LynxError("q must be a bfloat16 tensor [n_rows, Hq, 128] with contiguous rows")
+    n_rows, Hq, _ = q.shape
+    stride = q.stride(0) if n_rows > 1 else Hq * H
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 3 or page_table.shape[1] != n_kv_heads:
+        raise LynxError("page_table must be [B, Hkv, max_pages]")
+    B, Hkv, max_pages = page_table.shape
+    on.need(page_table, torch.int32, page_table.shape, "page_table")
+    on.need(cu_q, torch.int32, (B + 1,), "cu_q")
+    on.need(ctx_len, torch.int32, (B,), "ctx_len")
+    n_pool = k_pages.shape[0] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3 else 0
+    on.need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages")
+    on.need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages")
+    dtype = out.dtype if isinstance(out, torch.Tensor) else out_dtype
+    code = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}.get(dtype)
+    if code is None:
+        raise LynxError("out_dtype must be torch.bfloat16 or torch.float32")
+    out = on.make(out, dtype, (n_rows, Hq, H), "out")
+    lse = on.make(lse, torch.float32, (n_rows, Hq), "lse")
+    if workspace is None:
+        ws_bytes = lynx_chunk_attn_workspace_size(n_rows, B, Hq, Hkv, H)
+        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=on.device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != on.device or not workspace.is_contiguous():
+        raise LynxError(f"workspace must be a contiguous tensor on {on.device}")
+    scale = float(sm_scale) if sm_scale is not None else 1.0 / math.sqrt(H)
+    with on:
+        _check(load().lynx_chunk_attn_bf16(_ptr(q), n_rows, stride, _ptr(cu_q), B, Hq, Hkv, H, _ptr(k_pages),
+                                           _ptr(v_pages), n_pool, _ptr(page_table), max_pages, _ptr(ctx_len), scale,
+                                           int(bool(causal)), _ptr(out), code, _ptr(lse), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), _stream(stream, on.device)),
+               "lynx_chunk_attn_bf16")
+    return out, lse
 
 
 def lynx_verify_drafts(p, q, draft, u, n_draft=None, tokens=None, n_accept=None, stream=None):

@@ -48,6 +48,29 @@ def test_qkv_append_argument_checks(lynx_lib, a):
     assert call(n=0, qkv=None, pos=None, slots=None, q=None, k=None, v=None, cs=None) == 0
 
 
+def test_chunk_attn_argument_checks(lynx_lib, a):
+    size = lynx_lib.lynx_chunk_attn_workspace_size(1, 1, 4, 2, 128)
+
+    def call(q=a, n=1, stride=512, cu=a, B=1, Hq=4, Hkv=2, D=128, k=a, v=a, pool=1, table=a, mp=1, ctx=a, scale=0.1,
+             causal=1, out=a, dt=0, lse=a, ws=a, wsb=size):
+        return lynx_lib.lynx_chunk_attn_bf16(q, n, stride, cu, B, Hq, Hkv, D, k, v, pool, table, mp, ctx, scale, causal,
+                                             out, dt, lse, ws, wsb, None)
+    for kw in (dict(n=-1), dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Hq=3, Hkv=2), dict(mp=0), dict(stride=511),
+               dict(dt=2), dict(causal=2), dict(scale=0.0), dict(scale=float("inf")), dict(q=None), dict(cu=None),
+               dict(k=None), dict(v=None), dict(table=None), dict(ctx=None), dict(out=None), dict(pool=0)):
+        assert call(**kw) == -1, kw
+    for kw in (dict(D=64), dict(mp=1 << 23), dict(n=1 << 30), dict(B=65536), dict(pool=1 << 24)):
+        assert call(**kw) == -2, kw
+    for name in ("q", "k", "v", "out", "ws"):
+        assert call(**{name: ctypes.c_void_p(a.value + 8)}) == -3, name
+    for name in ("cu", "table", "ctx", "lse"):
+        assert call(**{name: ctypes.c_void_p(a.value + 2)}) == -3, name
+    assert call(stride=516) == -3
+    assert call(ws=None) == -4 and call(wsb=size - 1) == -4
+    assert call(n=0, q=None, cu=None, k=None, v=None, table=None, ctx=None, out=None, ws=None) == 0
+    assert size > 0 and lynx_lib.lynx_chunk_attn_workspace_size(1, 1, 4, 3, 128) == 0
+
+
 def test_verify_drafts_argument_checks(lynx_lib, a):
     def call(p=a, pb=20, pt=10, q=a, qb=10, qt=10, dt=1, B=1, T=1, V=10, d=a, nd=None, u=a, tok=a, n=a):
         return lynx_lib.lynx_verify_drafts(p, pb, pt, q, qb, qt, dt, B, T, V, d, nd, u, tok, n, None)

@@ -1,0 +1,348 @@
+"""GPU parity of lynx_chunk_attn_bf16 with the float64 oracle: ragged batches,
+one token to several tiles, odd lengths, group sizes that do not divide the
+tile, rows that see no key, strided queries, garbage past the context, splits
+of long contexts, and the paths around them."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as sv
+from progressive_kv_quantization_gb300 import lynx as L
+
+pytestmark = pytest.mark.gpu
+D = 128
+LSE_TOL = 2.0 ** -11
+
+
+def batch(new, ctx, Hq, Hkv, seed, pad=0, k_scale=1.0, max_pages=None, extra_stride=0):
+    """Random batch on the device; ctx holds all keys.  Pages in shuffled order, and
+    everything past a request's context (and unused table entries) is garbage."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    B = len(new)
+    n_rows = sum(new) + pad
+    pages = [-(-c // 256) for c in ctx]
+    max_pages = max_pages or max(max(pages), 1)
+    n_pool = sum(pages) * Hkv + 2
+    order = torch.randperm(n_pool, generator=torch.Generator().manual_seed(seed)).int()
+    table = torch.full((B, Hkv, max_pages), 2 ** 30, dtype=torch.int32)      # unused entries: far outside the pool
+    at = 0
+    for b in range(B):
+        table[b, :, :pages[b]] = order[at:at + Hkv * pages[b]].view(Hkv, pages[b])
+        at += Hkv * pages[b]
+    k = (torch.randn(n_pool, D, 256, generator=g, device="cuda") * k_scale).bfloat16()
+    v = (torch.randn(n_pool, D, 256, generator=g, device="cuda")
+         + torch.randn(1, D, 1, generator=g, device="cuda")).bfloat16()
+    for b in range(B):
+        if ctx[b] % 256:
+            ids = table[b, :, pages[b] - 1].long().cuda()
+            k[ids, :, ctx[b] % 256:] = float("nan")
+            v[ids, :, ctx[b] % 256:] = float("inf")
+    q = torch.randn(n_rows, Hq * D + extra_stride, generator=g, device="cuda").bfloat16()[:, :Hq * D]
+    q = q.unflatten(1, (Hq, D))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    cu = i32([sum(new[:b]) for b in range(B + 1)])
+    return dict(q=q, cu=cu, k=k, v=v, table=table.cuda(), ctx=i32(list(ctx)), Hkv=Hkv)
+
+
+def oracle(x, causal, scale=1 / math.sqrt(D)):
+    f = lambda t: t.double().cpu().numpy()
+    table = x["table"].cpu().numpy().astype(np.int64)
+    with np.errstate(invalid="ignore"):
+        return sv.chunk_attention(f(x["q"]), x["cu"].cpu().numpy(), f(x["k"]), f(x["v"]), table, x["ctx"].cpu().numpy(),
+                                  x["Hkv"], scale, causal)
+
+
+def call(x, causal, **kw):
+    return L.lynx_chunk_attn_bf16(x["q"], x["cu"], x["k"], x["v"], x["table"], x["ctx"], x["Hkv"], causal=causal, **kw)
+
+
+def check(x, causal, out, lse, v_max=None, scale=1 / math.sqrt(D), ref=None):
+    """|out - ref| <= sum_j p_j |v_j| (2^-9 for P's rounding to BF16, doubled for
+    what float32 adds: scores off by LSE_TOL at worst, the exponential by 2 ulp,
+    sums in any order) + half a BF16 step of the value; sum_j p_j |v_j| is at most
+    the largest |v|."""
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    ro, rl = oracle(x, causal, scale) if ref is None else ref
+    g, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    rows = ~np.isnan(rl)
+    v = x["v"].float()
+    vm = float(v[torch.isfinite(v)].abs().max())
+    half = 2.0 ** -8 if out.dtype == torch.bfloat16 else 0.0
+    lim = 2.0 ** -8 * vm + half * np.abs(ro)
+    err = np.abs(g - ro)
+    assert np.all(err[rows] <= lim[rows]), f"output off by {np.nanmax(err)}"
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(gl) & rows, empty)
+    assert np.all(g[empty] == 0)
+    fin = rows & ~empty
+    # scores: exact products, 128 float32 additions of partial sums of at most
+    # scale * sum |q k| < 30, each off by 2^-23 at worst: 128 * 2^-23 * 30 < 2^-11
+    assert np.all(np.abs(gl[fin] - rl[fin]) <= LSE_TOL + 2.0 ** -20 * np.abs(rl[fin])), np.max(np.abs(gl[fin] - rl[fin]))
+    # over all: the mean square error of P's rounding is far smaller than its bound
+    big = fin & (np.abs(ro).max(-1) > 0)
+    if big.sum() > 4:
+        rel = np.linalg.norm(err[big]) / np.linalg.norm(ro[big])
+        assert rel < 2.0 ** -7, f"relative error {rel}"
+    return g
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv", [
+    ([1], [1], 1, 1), ([1], [300], 4, 1), ([5], [5], 8, 2), ([17], [1000], 8, 2), ([64], [64], 4, 1),
+    ([65], [191], 4, 2), ([128], [128], 3, 1), ([300], [300], 5, 1), ([256], [2000], 2, 2), ([33], [129], 12, 3),
+    ([200], [1111], 10, 2), ([1], [4096], 16, 2), ([1000], [1500], 1, 1), ([90], [500], 16, 1)])
+def test_one_request(cuda_device, new, ctx, Hq, Hkv, causal):
+    x = batch(new, ctx, Hq, Hkv, sum(new) + ctx[0])
+    check(x, causal, *call(x, causal))
+    check(x, causal, *call(x, causal, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv,pad", [
+    ([3, 0, 200, 1, 64], [10, 40, 513, 700, 64], 4, 2, 0),
+    ([1] * 40, [1 + 37 * i for i in range(40)], 8, 2, 3),
+    ([0, 0, 5], [0, 3, 5], 2, 1, 9),
+    ([130, 1, 131, 2, 132], [1300, 1, 131, 900, 2000], 6, 2, 1),
+    ([0], [100], 2, 1, 0), ([0], [100], 2, 1, 5)])
+def test_ragged_batches_leave_rows_behind(cuda_device, new, ctx, Hq, Hkv, pad, causal):
+    x = batch(new, ctx, Hq, Hkv, len(new) + pad, pad=pad)
+    out = torch.full((sum(new) + pad, Hq, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((sum(new) + pad, Hq), 4.0, device="cuda")
+    call(x, causal, out=out, lse=lse)
+    check(x, causal, out, lse)
+    assert (out[sum(new):] == 3).all() and (lse[sum(new):] == 4).all()
+
+
+def test_many_requests_of_one_token(cuda_device):
+    """More requests than a CTA has threads, and more items than its list holds."""
+    rng = np.random.default_rng(0)
+    ctx = [int(c) for c in rng.integers(0, 300, 700)]
+    x = batch([1] * 700, ctx, 2, 2, 5)
+    check(x, True, *call(x, True))
+    x = batch([1] * 5000, [int(c) for c in rng.integers(1, 60, 5000)], 1, 1, 6)
+    check(x, True, *call(x, True))
+
+
+def test_rows_that_see_no_key(cuda_device):
+    # more new tokens than keys: the first rows see none
+    x = batch([300, 5], [100, 0], 4, 2, 8)
+    out, lse = call(x, True)
+    g = check(x, True, out, lse)
+    assert (g[:200] == 0).all() and torch.isneginf(lse[:200]).all()
+    assert (g[300:] == 0).all() and torch.isneginf(lse[300:]).all()
+    check(x, False, *call(x, False))
+
+
+@pytest.mark.parametrize("k_scale,scale", [(1.0, 1 / math.sqrt(D)), (8.0, 1 / math.sqrt(D)), (1.0, 2.0 ** -14),
+                                           (30.0, 0.2)])
+def test_score_ranges(cuda_device, k_scale, scale):
+    """Flat scores to nearly one-hot rows: the running maximum never moves, or often."""
+    x = batch([100, 30], [1500, 900], 4, 2, 11, k_scale=k_scale)
+    out, lse = call(x, True, sm_scale=scale)
+    ro, rl = oracle(x, True, scale)
+    torch.cuda.synchronize()
+    g, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    # scores of up to `top`, a float32 sum of 128 exact products each: absolute
+    # error 128 * 2^-24 * top; a probability is off by the factor e^that
+    top = float(np.abs(rl).max()) + 10
+    ds = 128 * 2.0 ** -24 * top * 2
+    vm = float(x["v"].float()[torch.isfinite(x["v"].float())].abs().max())
+    assert np.all(np.abs(g - ro) <= (2.0 ** -8 + 2 * ds) * vm + 2.0 ** -8 * np.abs(ro))
+    assert np.all(np.abs(gl - rl) <= ds + 2.0 ** -20 * np.abs(rl))
+
+
+@pytest.mark.parametrize("order", ["up", "down"])
+def test_running_maximum_moves_on_every_tile(cuda_device, order):
+    """Keys whose scores grow (or fall) by far more than the lag from tile to tile."""
+    Hq, Hkv, n, T = 4, 1, 2048, 20
+    x = batch([T], [n], Hq, Hkv, 12)
+    q = x["q"]
+    q[:, :, 0] = 8.0
+    ramp = torch.arange(n, device="cuda").float() * (0.5 if order == "up" else -0.5)
+    ids = x["table"][0, 0].long()
+    kk = x["k"][ids].clone()
+    kk[:, 0, :] = ramp.view(-1, 256).bfloat16()
+    x["k"][ids] = kk
+    out, lse = call(x, True)
+    ro, rl = oracle(x, True)
+    torch.cuda.synchronize()
+    top = float(np.abs(rl).max())
+    ds = 128 * 2.0 ** -24 * top * 2
+    vm = float(x["v"].float()[torch.isfinite(x["v"].float())].abs().max())
+    assert np.all(np.abs(out.double().cpu().numpy() - ro) <= (2.0 ** -8 + 2 * ds) * vm + 2.0 ** -8 * np.abs(ro))
+    assert np.all(np.abs(lse.double().cpu().numpy() - rl) <= ds + 2.0 ** -20 * np.abs(rl))
+
+
+def test_strided_queries_and_wide_tables(cuda_device):
+    x = batch([70, 9], [600, 300], 4, 2, 13, max_pages=9, extra_stride=5 * 128)
+    assert x["q"].stride(0) == 9 * 128
+    check(x, True, *call(x, True))
+
+
+def test_long_context_split_over_the_machine(cuda_device):
+    """One token, and a few, over 50,000 keys: every CTA takes a part of the tile."""
+    for new in ([1], [3, 40]):
+        ctx = [50001, 20000][:len(new)]
+        x = batch(new, ctx, 8, 2, 14)
+        a = call(x, True)
+        check(x, True, *a)
+        b = call(x, True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])      # the split does not depend on timing
+
+
+def test_large_prefill_sampled_rows(cuda_device):
+    """4,096 tokens over 9,000 keys with 16 heads: sampled rows against the oracle."""
+    new, ctx, Hq, Hkv = [4096], [9000], 16, 4
+    x = batch(new, ctx, Hq, Hkv, 15)
+    out, lse = call(x, True)
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    rng = np.random.default_rng(0)
+    ids = x["table"][0].long()
+    for t in [0, 1, 63, 64, 4095, *rng.integers(0, 4096, 40)]:
+        h = int(rng.integers(0, Hq))
+        n = 9000 - 4096 + int(t) + 1
+        k = x["k"][ids[h // 4]].permute(0, 2, 1).reshape(-1, D)[:n].double()
+        v = x["v"][ids[h // 4]].permute(0, 2, 1).reshape(-1, D)[:n].double()
+        s = k @ x["q"][int(t), h].double() / math.sqrt(D)
+        o = torch.softmax(s, 0) @ v
+        assert abs(float(torch.logsumexp(s, 0)) - float(lse[int(t), h])) < LSE_TOL
+        lim = 2.0 ** -8 * float(v.abs().max()) + 2.0 ** -8 * o.abs()
+        assert bool(((out[int(t), h].double() - o).abs() <= lim).all())
+
+
+def test_bad_page_ids_lengths_and_bounds_are_reported(cuda_device):
+    x = batch([4, 4], [300, 300], 2, 1, 16)
+    good = call(x, True)
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    y = dict(x, table=x["table"].clone())
+    y["table"][0, 0, 1] = -5
+    call(y, True)
+    with pytest.raises(L.LynxError, match="= 2"):
+        L.lynx_device_status()
+    y = dict(x, ctx=torch.tensor([300, 513], dtype=torch.int32, device="cuda"))
+    call(y, True)
+    with pytest.raises(L.LynxError, match="= 3"):
+        L.lynx_device_status()
+    y = dict(x, cu=torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda"))
+    out, _ = call(y, True)
+    with pytest.raises(L.LynxError, match="= 6"):
+        L.lynx_device_status()
+    assert torch.equal(out[:4], good[0][:4])          # the request with good bounds is computed
+    again = call(x, True)
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    assert torch.equal(again[0], good[0])
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_context_recovers(cuda_device):
+    x = batch([300, 2], [1200, 900], 4, 2, 17)
+    good = call(x, True)
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    assert L.load().lynx_test_inject_wait_timeout(1) == 0
+    call(x, True)
+    with pytest.raises(L.LynxError, match="= 1"):
+        L.lynx_device_status()
+    for _ in range(2):
+        out, lse = call(x, True)
+        torch.cuda.synchronize()
+        L.lynx_device_status()
+        assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+
+
+def test_captured_graph_with_other_lengths(cuda_device):
+    new, ctx = [40, 1, 90], [700, 300, 100]
+    x = batch(new, ctx, 4, 2, 18, pad=30)
+    out = torch.zeros(161, 4, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(161, 4, device="cuda")
+    ws = torch.empty(L.lynx_chunk_attn_workspace_size(161, 3, 4, 2, D), dtype=torch.uint8, device="cuda")
+    call(x, True, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(x, True, out=out, lse=lse, workspace=ws)
+    for new in ([40, 1, 90], [1, 1, 1], [0, 150, 7], [100, 0, 0]):
+        x["cu"].copy_(torch.tensor([0, new[0], new[0] + new[1], sum(new)]))
+        g.replay()
+        a = (out.clone(), lse.clone())
+        check(x, True, *a)
+
+
+def test_back_to_back_calls_share_a_workspace(cuda_device):
+    """Calls in one stream, one behind the other, with one workspace."""
+    xs = [batch([1, 30], [9000, 2000], 8, 2, 19), batch([64], [8000], 4, 4, 20), batch([1] * 5, [3000] * 5, 16, 2, 21)]
+    ws = torch.empty(max(L.lynx_chunk_attn_workspace_size(x["q"].shape[0], len(x["ctx"]), x["q"].shape[1], x["Hkv"], D)
+                         for x in xs), dtype=torch.uint8, device="cuda")
+    single = [call(x, True) for x in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [call(x, True, workspace=ws) for x in xs]
+        torch.cuda.synchronize()
+        for a, b in zip(single, outs):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_streams_with_a_workspace_each(cuda_device):
+    x, y = batch([200], [3000], 8, 2, 22), batch([1] * 9, [5000] * 9, 8, 2, 23)
+    a, b = call(x, True), call(y, True)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        a2, b2 = call(x, True, stream=s1), call(y, True, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], a2[0]) and torch.equal(b[0], b2[0])
+
+
+def test_workspace_and_guard_bands(cuda_device):
+    """Nothing is written outside the outputs and the workspace."""
+    x = batch([37, 1], [5000, 700], 8, 2, 24)
+    n = 38
+    size = L.lynx_chunk_attn_workspace_size(n, 2, 8, 2, D)
+    ws = torch.full((size + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((n + 2, 8, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n + 2, 8), 7.0, device="cuda")
+    call(x, True, out=out[1:n + 1], lse=lse[1:n + 1], workspace=ws[256:256 + size])
+    check(x, True, out[1:n + 1], lse[1:n + 1])
+    assert (ws[:256] == 0x5A).all() and (ws[256 + size:] == 0x5A).all()
+    for t in (out, lse):
+        assert (t[0] == 7).all() and (t[n + 1] == 7).all()
+    with pytest.raises(L.LynxError, match="workspace"):
+        call(x, True, workspace=ws[256:256 + size - 16])
+
+
+def test_agrees_with_the_decode_kernel(cuda_device):
+    """A batch of single tokens equals lynx_decode_attn_bf16 within both roundings."""
+    B, Hq, Hkv = 6, 8, 2
+    x = batch([1] * B, [700, 256, 1, 1300, 2048, 511], Hq, Hkv, 25)
+    x["k"] = torch.nan_to_num(x["k"], 0, 0, 0)
+    x["v"] = torch.nan_to_num(x["v"], 0, 0, 0)
+    o, l = call(x, True, out_dtype=torch.float32)
+    table = x["table"].clamp(max=x["k"].shape[0] - 1)
+    od, ld = L.lynx_decode_attn_bf16(x["q"].view(B, 1, Hq, D), x["k"], x["v"], table, x["ctx"], Hkv)
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    vm = float(x["v"].float().abs().max())
+    assert float((o.view_as(od) - od).abs().max()) <= 2.0 ** -8 * vm
+    assert float((l.view_as(ld) - ld).abs().max()) <= LSE_TOL
+
+
+def test_context_offsets_pass_32_bits(cuda_device):
+    """Pages whose first element lies past 2^31 elements of the pool (9 GB each)."""
+    n_pool = 70000
+    k = torch.zeros(n_pool, D, 256, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros(n_pool, D, 256, dtype=torch.bfloat16, device="cuda")
+    x = batch([5], [600], 2, 1, 26)
+    for i, p in enumerate((69999, 65537, 66000)):
+        src = int(x["table"][0, 0, i])
+        k[p], v[p] = x["k"][src], x["v"][src]
+    table = torch.tensor([[[69999, 65537, 66000]]], dtype=torch.int32, device="cuda")
+    a = call(x, True)
+    b = L.lynx_chunk_attn_bf16(x["q"], x["cu"], k, v, table, x["ctx"], 1)
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
