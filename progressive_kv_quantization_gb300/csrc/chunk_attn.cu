@@ -52,7 +52,8 @@ constexpr int kSlot = 2 * kBox;                // one K or V tile
 constexpr int kSlots = 5;
 constexpr int kQBytes = 2 * kBox;              // a group's queries: two halves [128 rows][64 channels]
 constexpr int kMmaWarp = 8, kTmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;                  // warps 10 and 11 only fill their warpgroup
+constexpr int kRegsSoftmax = 208, kRegsOther = 80;   // of 168 each at launch: 256 x 208 + 128 x 80 <= 384 x 168
 constexpr int kMaxItems = 24;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
 constexpr float kLazyLog2 = 8.0f;
@@ -64,7 +65,7 @@ constexpr int kNumBars = 2 * kSlots + 9;
 constexpr int kOffItems = kOffBar + 8 * kNumBars;
 constexpr int kItemInts = 10;
 constexpr int kOffScan = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
-constexpr int kOffMisc = kOffScan + 16 * 8;
+constexpr int kOffMisc = kOffScan + 16 * 8;   // 12 warps' sums
 constexpr int kSmem = kOffMisc + 96;
 constexpr int kSmemAlloc = kSmem + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
@@ -154,6 +155,34 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -203,6 +232,9 @@ __device__ __forceinline__ int visible(const ChunkArgs& a, int ctx, int T, int t
   return a.causal ? max(ctx - T + token + 1, 0) : ctx;
 }
 
+// the two sides of the kernel meet here from their own loops
+__device__ __forceinline__ void sync_all() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
 template <typename V>
 __device__ __forceinline__ V block_scan(V v, V* s_scan, V* total) {   // inclusive; all threads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -212,14 +244,14 @@ __device__ __forceinline__ V block_scan(V v, V* s_scan, V* total) {   // inclusi
     if (lane >= o) v += u;
   }
   if (lane == 31) s_scan[warp] = v;
-  __syncthreads();
+  sync_all();
   V before = 0, all = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     const V u = s_scan[w];
     if (w < warp) before += u;
     all += u;
   }
-  __syncthreads();
+  sync_all();
   *total = all;
   return v + before;
 }
@@ -277,10 +309,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   wait_prerequisite_grids();
 
   // the line's length, and this CTA's part [x0, x1) of it
-  Request req = load_request(a, tid);
   long long Wh = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const Request r = b0 == 0 ? req : load_request(a, b0 + tid);
+    const Request r = load_request(a, b0 + tid);
     long long sum;
     block_scan(r.at(r.tiles), s_scan, &sum);
     Wh += sum;
@@ -302,15 +333,15 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   uint32_t mma_items[2] = {0, 0}, mma_tiles[2] = {0, 0};
   bool failed = false;
 
-  while (x0 < x1) {
-    // ---- the items of this head's segment, at most kMaxItems
+  // the items of the current head's segment, at most kMaxItems, into shared memory; moves x0 on
+  auto next_items = [&]() {
     const long long h = x0 / Wh;
     const long long seg0 = x0 - h * Wh, seg1 = min(x1 - h * Wh, Wh);
     long long before = 0;
     int n_items = 0;
     if (tid == 0) *s_next = h * Wh + seg1;
     for (int b0 = 0; b0 < a.B && before < seg1; b0 += kThreads) {
-      const Request r = b0 == 0 ? req : load_request(a, b0 + tid);
+      const Request r = load_request(a, b0 + tid);
       long long sum;
       const long long len = r.at(r.tiles);
       const long long p = before + block_scan(len, s_scan, &sum) - len;
@@ -360,133 +391,146 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       n_items += all;
       before += sum;
     }
-    __syncthreads();
+    sync_all();
     n_items = min(n_items, kMaxItems);
     x0 = *s_next;
+    return n_items;
+  };
 
-    if (warp == kTmaWarp) {
-      // ================= producer: K and V tiles in the order of use
-      if (lane == 0) {
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    while (x0 < x1) {
+      const int n_items = next_items();
+      if (warp == kTmaWarp) {
+        // ================= producer: K and V tiles in the order of use
+        if (lane == 0) {
+          for (int i = 0; i < n_items && !failed; ++i) {
+            const Item it = items[i];
+            if (it.kind == kNothing || it.k0 == it.k1) continue;
+            const int32_t* row = a.page_table + ((int64_t)it.b * a.Hkv + it.h) * a.max_pages;
+            int next_id = row[it.k0 >> 1];
+            int64_t id = 0;
+            for (int k = it.k0; k < it.k1 && !failed; ++k) {
+              if (k == it.k0 || !(k & 1)) {
+                id = next_id;
+                if (((k >> 1) + 1) * 2 < it.k1) next_id = row[(k >> 1) + 1];
+                if (id < 0 || id >= a.n_pool) {
+                  atomicExch(a.status, 2);
+                  id = 0;
+                }
+              }
+#pragma unroll
+              for (int kv = 0; kv < 2; ++kv) {
+                const int s = n_kv_ring % kSlots;
+                if (n_kv_ring >= kSlots && !mbar_wait(kv_empty(s), (n_kv_ring / kSlots - 1) & 1, wait_ns)) {
+                  give_up();
+                  failed = true;
+                  break;
+                }
+                if (a.inject && n_kv_ring == 1) {   // test hook: the first V tile never arrives
+                  ++n_kv_ring;
+                  continue;
+                }
+                const uint32_t dst = base + kOffRing + s * kSlot;
+                mbar_expect_tx(kv_full(s), kSlot);
+                tma_tile_g2s(dst, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys, (int)(id * kH), kv_full(s));
+                tma_tile_g2s(dst + kBox, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys + 64, (int)(id * kH), kv_full(s));
+                ++n_kv_ring;
+              }
+            }
+          }
+        }
+      } else if (warp == kMmaWarp) {
+        // ================= tensor-core warp
         for (int i = 0; i < n_items && !failed; ++i) {
           const Item it = items[i];
           if (it.kind == kNothing || it.k0 == it.k1) continue;
-          const int32_t* row = a.page_table + ((int64_t)it.b * a.Hkv + it.h) * a.max_pages;
-          int next_id = row[it.k0 >> 1];
-          int64_t id = 0;
-          for (int k = it.k0; k < it.k1 && !failed; ++k) {
-            if (k == it.k0 || !(k & 1)) {
-              id = next_id;
-              if (((k >> 1) + 1) * 2 < it.k1) next_id = row[(k >> 1) + 1];
-              if (id < 0 || id >= a.n_pool) {
-                atomicExch(a.status, 2);
-                id = 0;
-              }
-            }
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              const int s = n_kv_ring % kSlots;
-              if (n_kv_ring >= kSlots && !mbar_wait(kv_empty(s), (n_kv_ring / kSlots - 1) & 1, wait_ns)) {
-                give_up();
-                failed = true;
-                break;
-              }
-              if (a.inject && n_kv_ring == 1) {   // test hook: the first V tile never arrives
-                ++n_kv_ring;
-                continue;
-              }
-              const uint32_t dst = base + kOffRing + s * kSlot;
-              mbar_expect_tx(kv_full(s), kSlot);
-              tma_tile_g2s(dst, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys, (int)(id * kH), kv_full(s));
-              tma_tile_g2s(dst + kBox, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys + 64, (int)(id * kH), kv_full(s));
-              ++n_kv_ring;
-            }
-          }
-        }
-      }
-    } else if (warp == kMmaWarp) {
-      // ================= tensor-core warp
-      for (int i = 0; i < n_items && !failed; ++i) {
-        const Item it = items[i];
-        if (it.kind == kNothing || it.k0 == it.k1) continue;
-        const int groups = it.rows > kGroupRows ? 2 : 1;
-        const int n = it.k1 - it.k0;
-        // S of group g against the K tile in slot s
-        auto qk = [&](int g, int s) {
-          if (lane == 0) {
-            const uint32_t q = base + kOffQ + g * kQBytes, k = base + kOffRing + s * kSlot;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_ss(tmem + g * 128, desc_k(q + (ks >> 2) * kBox + (ks & 3) * 32), desc_mn(k + ks * 2048), kIdescMn, ks > 0);
-            tc_commit(s_full(g));
-          }
-          __syncwarp();
-        };
-        auto wait_kv = [&](uint32_t u) {
-          if (!mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns)) failed = true;
-          failed = __any_sync(0xffffffffu, failed);
-          return !failed;
-        };
-        if (!wait_kv(n_kv_ring)) break;
-        for (int g = 0; g < groups; ++g) {
-          if (!mbar_wait(q_full(g), mma_items[g] & 1, wait_ns)) failed = true;
-          ++mma_items[g];
-        }
-        failed = __any_sync(0xffffffffu, failed);
-        if (failed) break;
-        tc_fence_after();
-        for (int g = 0; g < groups; ++g) qk(g, n_kv_ring % kSlots);
-        if (lane == 0) tc_commit(kv_empty(n_kv_ring % kSlots));
-        for (int j = 0; j < n; ++j) {
-          const uint32_t uv = n_kv_ring + 2 * j + 1, uk = uv + 1;
-          const int sv = uv % kSlots, sk = uk % kSlots;
-          if (!wait_kv(uv)) break;
-          const int tail = it.ctx - (it.k0 + j) * kTileKeys;   // valid keys of the tile
-          if (tail < kTileKeys) {
-            // zero the V rows of the tokens past the context: 16-byte pieces of
-            // 8 tokens, the one that the context ends in value by value
-            uint8_t* v = smem + kOffRing + sv * kSlot;
-            for (int x = lane; x < kH * 16; x += 32) {
-              const int ch = x >> 4, piece = x & 15;
-              const int left = tail - piece * 8;
-              if (left >= 8) continue;
-              uint8_t* at = v + (piece >> 3) * kBox + ch * 128 + (((piece & 7) ^ (ch & 7)) << 4);
-              if (left <= 0) {
-                *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                for (int e = left; e < 8; ++e) reinterpret_cast<uint16_t*>(at)[e] = 0;
-              }
-            }
-            fence_proxy_async();
-            __syncwarp();
-          }
-          if (j + 1 < n && !wait_kv(uk)) break;
-          for (int g = 0; g < groups; ++g) {
-            if (!mbar_wait(p_full(g), mma_tiles[g] & 1, wait_ns)) failed = true;
-            ++mma_tiles[g];
-            failed = __any_sync(0xffffffffu, failed);
-            if (failed) break;
-            tc_fence_after();
+          const int groups = it.rows > kGroupRows ? 2 : 1;
+          const int n = it.k1 - it.k0;
+          // S of group g against the K tile in slot s
+          auto qk = [&](int g, int s) {
             if (lane == 0) {
-              const uint32_t v = base + kOffRing + sv * kSlot;
+              const uint32_t q = base + kOffQ + g * kQBytes, k = base + kOffRing + s * kSlot;
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
-                mma_ts(tmem + 256 + g * 128, tmem + g * 128 + ks * 8, desc_k(v + (ks >> 2) * kBox + (ks & 3) * 32), kIdesc,
-                       j > 0 || ks > 0);
-              tc_commit(o_done(g));
+                mma_ss(tmem + g * 128, desc_k(q + (ks >> 2) * kBox + (ks & 3) * 32), desc_mn(k + ks * 2048), kIdescMn, ks > 0);
+              tc_commit(s_full(g));
             }
             __syncwarp();
-            if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sv));
-            if (j + 1 < n) {
-              qk(g, sk);
-              if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sk));
-            }
+          };
+          auto wait_kv = [&](uint32_t u) {
+            if (!mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns)) failed = true;
+            failed = __any_sync(0xffffffffu, failed);
+            return !failed;
+          };
+          if (!wait_kv(n_kv_ring)) break;
+          for (int g = 0; g < groups; ++g) {
+            if (!mbar_wait(q_full(g), mma_items[g] & 1, wait_ns)) failed = true;
+            ++mma_items[g];
           }
+          failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
+          tc_fence_after();
+          for (int g = 0; g < groups; ++g) qk(g, n_kv_ring % kSlots);
+          if (lane == 0) tc_commit(kv_empty(n_kv_ring % kSlots));
+          for (int j = 0; j < n; ++j) {
+            const uint32_t uv = n_kv_ring + 2 * j + 1, uk = uv + 1;
+            const int sv = uv % kSlots, sk = uk % kSlots;
+            if (!wait_kv(uv)) break;
+            const int tail = it.ctx - (it.k0 + j) * kTileKeys;   // valid keys of the tile
+            if (tail < kTileKeys) {
+              // zero the V rows of the tokens past the context: 16-byte pieces of
+              // 8 tokens, the one that the context ends in value by value
+              uint8_t* v = smem + kOffRing + sv * kSlot;
+              for (int x = lane; x < kH * 16; x += 32) {
+                const int ch = x >> 4, piece = x & 15;
+                const int left = tail - piece * 8;
+                if (left >= 8) continue;
+                uint8_t* at = v + (piece >> 3) * kBox + ch * 128 + (((piece & 7) ^ (ch & 7)) << 4);
+                if (left <= 0) {
+                  *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  for (int e = left; e < 8; ++e) reinterpret_cast<uint16_t*>(at)[e] = 0;
+                }
+              }
+              fence_proxy_async();
+              __syncwarp();
+            }
+            if (j + 1 < n && !wait_kv(uk)) break;
+            for (int g = 0; g < groups; ++g) {
+              if (!mbar_wait(p_full(g), mma_tiles[g] & 1, wait_ns)) failed = true;
+              ++mma_tiles[g];
+              failed = __any_sync(0xffffffffu, failed);
+              if (failed) break;
+              tc_fence_after();
+              if (lane == 0) {
+                const uint32_t v = base + kOffRing + sv * kSlot;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  mma_ts(tmem + 256 + g * 128, tmem + g * 128 + ks * 8, desc_k(v + (ks >> 2) * kBox + (ks & 3) * 32), kIdesc,
+                         j > 0 || ks > 0);
+                tc_commit(o_done(g));
+              }
+              __syncwarp();
+              if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sv));
+              if (j + 1 < n) {
+                qk(g, sk);
+                if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sk));
+              }
+            }
+            if (failed) break;
+          }
+          n_kv_ring += 2 * n;
         }
-        n_kv_ring += 2 * n;
+        if (failed && lane == 0) give_up();
       }
-      if (failed && lane == 0) give_up();
-    } else {
+      sync_all();
+      if (*s_abort) break;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    while (x0 < x1) {
+      const int n_items = next_items();
       // ================= softmax: group g, one row a thread
       const int g = warp >> 2;
       const int r = (warp & 3) * 32 + lane;               // row of the group, tensor-memory lane
@@ -534,12 +578,13 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               for (int x = 0; x < 128; ++x)
                 if (x >= left) s[x] = 0xFF800000u;   // -inf
             }
-            float mx[4];
+            float mx[8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) mx[x] = __uint_as_float(s[x]);
+            for (int x = 0; x < 8; ++x) mx[x] = fmaxf(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
 #pragma unroll
-            for (int x = 4; x < 128; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            for (int x = 8; x < 64; ++x)
+              mx[x & 7] = max3(mx[x & 7], __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+            const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
             if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
               const float m_new = fmaxf(m, top);
               const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - m_new);
@@ -563,20 +608,26 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               m = m_new;
             }
             const float ref = m == -CUDART_INF_F ? 0.0f : -m;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint64_t sc2 = pair(__float_as_uint(sc), __float_as_uint(sc));
+            const uint64_t ref2 = pair(__float_as_uint(ref), __float_as_uint(ref));
+            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               uint32_t p[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float p0 = ex2(fmaf(__uint_as_float(s[64 * x + 2 * e]), sc, ref));
-                const float p1 = ex2(fmaf(__uint_as_float(s[64 * x + 2 * e + 1]), sc, ref));
-                sum[e & 3] += p0 + p1;
+                float p0, p1;
+                unpair(fma2(pair(s[64 * x + 2 * e], s[64 * x + 2 * e + 1]), sc2, ref2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum[e & 3] = add2(sum[e & 3], pair(__float_as_uint(p0), __float_as_uint(p1)));
                 p[e] = bf16x2(p0, p1);
               }
               tmem_st32(t_s + 32 * x, p);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            float l0, l1;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+            l += l0 + l1;
             tmem_wait_st_();
             tc_fence_before();
             mbar_arrive(p_full(g));
@@ -633,9 +684,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         tc_fence_before();   // O has been read before the next item's first product
       }
       if (failed && lane == 0) give_up();
+      sync_all();
+      if (*s_abort) break;
     }
-    __syncthreads();
-    if (*s_abort) break;
   }
 
   allow_dependent_launch();
