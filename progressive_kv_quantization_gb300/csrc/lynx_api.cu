@@ -767,7 +767,8 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
     return fail(LYNX_ERR_ALIGNMENT, "rows of qkv, q_out, the pools and cos_sin must be 16-byte aligned");
   if (off_type(q_weight, 4) || off_type(k_weight, 4) || off_type(positions, 4) || off_type(slots, 8))
     return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
-  if (n_rows > 1 << 30 || (int64_t)Hq + Hkv > 65535)
+  if (n_rows > 1 << 30 || (int64_t)Hq + 8 * (int64_t)Hkv > 65535 ||
+      (n_rows / 32 + 1) * ((int64_t)Hq + 8 * (int64_t)Hkv) > 0x7fffffff)
     return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%lld, Hq=%d, Hkv=%d too large", (long long)n_rows, Hq, Hkv);
   if (n_pool_pages > ((int64_t)1 << 40)) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages too large");
   int* status = device_status_ptr();

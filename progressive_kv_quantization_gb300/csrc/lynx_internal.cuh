@@ -240,7 +240,7 @@ struct AppendArgs {
   uint16_t* v_pages;
   int64_t n_pool;
   int* status;
-  int heads_per_job, q_jobs;   // set by the launcher
+  int heads_per_job, q_jobs, kv_parts, whole_rows;   // set by the launcher
 };
 cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s);
 

@@ -37,11 +37,50 @@ constexpr int kRun = 512;                          // values per run, 16 a lane
 __device__ __forceinline__ float prob(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float prob(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
 
-// whole multiples of 2^-40 of a weight, 0 for NaN
-__device__ __forceinline__ unsigned long long units(float w) {
-  w = fminf(fmaxf(w, 0.0f), 1.0f);
-  return __float2ull_rz(w * 1099511627776.0f);
-}
+// Sums of weights in whole multiples of 2^-40 (NaN and negative weights 0, at
+// most 1 each).  A weight's two 20-bit halves come from float additions rounded
+// down onto numbers whose last place is 2^-20 and 2^-40: the bits that the sum
+// holds above those of 8 and 2^-17 are the whole multiples.  (The conversion
+// float -> uint64 is far slower: 39.5 us for 32 rows of 151,936 with it.)  Up to
+// 2^11 weights fit the 32-bit sums.
+struct Units {
+  uint32_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(float w) {
+    w = __saturatef(w);
+    const float h = __fadd_rd(w, 8.0f);
+    const float rest = w - (h - 8.0f);                    // exact, below 2^-20
+    hi += __float_as_uint(h) - 0x41000000u;               // bits of 8
+    lo += __float_as_uint(__fadd_rd(rest, 0x1p-17f)) - 0x37000000u;   // bits of 2^-17
+  }
+  __device__ __forceinline__ unsigned long long value() const { return ((unsigned long long)hi << 20) + lo; }
+};
+
+// 16 bytes of a row as floats
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int n = 4;
+  float v[4];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int n = 8;
+  float v[8];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -50,7 +89,7 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 verify_drafts_kernel(const VerifyArgs a) {
   extern __shared__ unsigned long long s_run[];    // sums of this CTA's runs
   __shared__ unsigned s_ok[2];
@@ -65,16 +104,17 @@ verify_drafts_kernel(const VerifyArgs a) {
   const T* q = a.q ? static_cast<const T*>(a.q) + (int64_t)b * a.q_stride_b : nullptr;
   const float* u = a.u + (int64_t)b * (a.T + 1);
   const int32_t* draft = a.draft + (int64_t)b * a.T;
+  // read ahead of their first use: the request's counts and numbers arrive together
+  const float u_last = u[a.T];
   const int n_draft = a.n_draft ? min(max(a.n_draft[b], 0), a.T) : a.T;
 
   if (tid < 64) {
     bool ok = false;
-    if (tid < n_draft) {
-      const int x = draft[tid];
-      if (x >= 0 && x < a.V) {
-        const float qx = q ? prob(q + tid * a.q_stride_t, x) : 1.0f;
-        ok = __fmul_rn(u[tid], qx) < prob(p + tid * a.p_stride_t, x);
-      }
+    const int x = tid < a.T ? draft[tid] : -1;
+    const float ux = tid < a.T ? u[tid] : 0.0f;
+    if (x >= 0 && x < a.V) {
+      const float qx = q ? prob(q + tid * a.q_stride_t, x) : 1.0f;
+      ok = __fmul_rn(ux, qx) < prob(p + tid * a.p_stride_t, x) && tid < n_draft;
     }
     const unsigned m = __ballot_sync(0xffffffffu, ok);
     if (lane == 0) s_ok[warp] = m;
@@ -100,17 +140,41 @@ verify_drafts_kernel(const VerifyArgs a) {
       if (drafted) w = __fsub_rn(w, prob(drafted, i));
       if (i == out) w = 0.0f;
     }
-    return units(w);
+    return w;
   };
+  // both rows on 16-byte boundaries: whole runs are read 16 bytes a lane
+  const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0 &&
+                    (!drafted || (reinterpret_cast<uintptr_t>(drafted) & 15) == 0);
   for (int attempt = 0; attempt < 2; ++attempt) {
     unsigned long long mine = 0;
     for (int r = r0 + warp; r < r1; r += kWarps) {
-      unsigned long long v = 0;
-      const int64_t i0 = (int64_t)r * kRun + lane;
+      const int64_t i0 = (int64_t)r * kRun;
+      Units sum;
+      if (wide && i0 + kRun <= a.V) {
+        constexpr int kVec = Vec<T>::n, kLoads = kRun / 32 / kVec;
+        Vec<T> x[kLoads], y[kLoads];
+        const bool minus = residual && drafted;
 #pragma unroll
-      for (int k = 0; k < kRun / 32; ++k)
-        if (i0 + 32 * k < a.V) v += weight(i0 + 32 * k);
-      v = warp_sum(v);
+        for (int k = 0; k < kLoads; ++k) x[k].load(row + i0 + (k * 32 + lane) * kVec);
+        if (minus) {
+#pragma unroll
+          for (int k = 0; k < kLoads; ++k) y[k].load(drafted + i0 + (k * 32 + lane) * kVec);
+        }
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            float w = x[k].v[e];
+            if (minus) w = __fsub_rn(w, y[k].v[e]);
+            if (residual && i0 + (k * 32 + lane) * kVec + e == out) w = 0.0f;
+            sum.add(w);
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kRun / 32; ++k)
+          if (i0 + 32 * k + lane < a.V) sum.add(weight(i0 + 32 * k + lane));
+      }
+      const unsigned long long v = warp_sum(sum.value());
       if (lane == 0) s_run[r - r0] = v;
       mine += v;
     }
@@ -122,16 +186,16 @@ verify_drafts_kernel(const VerifyArgs a) {
       s_sum = v;
     }
     cluster.sync();
-    total = before = 0;
-    for (int c = 0; c < C; ++c) {
-      const unsigned long long v = *cluster.map_shared_rank(&s_sum, c);
-      if (c < rank) before += v;
-      total += v;
-    }
-    cluster.sync();   // s_sum may change, or this CTA leave, only when all have read it
+    // one CTA's sum a lane (C <= 32)
+    const unsigned long long part = lane < C ? *cluster.map_shared_rank(&s_sum, lane) : 0;
+    total = warp_sum(part);
+    before = warp_sum(lane < rank ? part : 0);
     if (total > 0 || !residual || !rejected) break;
     residual = false;
+    cluster.sync();   // s_sum changes only when all have read it
   }
+  // a CTA leaves only when all have read its sum
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   int32_t* tokens = a.tokens + (int64_t)b * (a.T + 1);
   if (rank == 0) {
@@ -142,47 +206,65 @@ verify_drafts_kernel(const VerifyArgs a) {
       if (total == 0) tokens[n] = -1;
     }
   }
-  if (total == 0) return;
-  const float uf = u[a.T];
-  const long long step = min(max((long long)(uf * 16777216.0f), 0ll), (1ll << 24) - 1);   // NaN: 0
-  const unsigned long long limit =
-      (total >> 24) * (unsigned long long)step + (((total & 0xFFFFFFull) * (unsigned long long)step) >> 24);
-  if (warp != 0 || limit < before || limit >= before + s_sum) return;
+  // ---- the CTA that holds the limit looks for the token; its first warp
+  auto find = [&]() {
+    if (total == 0) return;
+    const long long step = min(max((long long)(u_last * 16777216.0f), 0ll), (1ll << 24) - 1);   // NaN: 0
+    const unsigned long long limit =
+        (total >> 24) * (unsigned long long)step + (((total & 0xFFFFFFull) * (unsigned long long)step) >> 24);
+    if (warp != 0 || limit < before || limit >= before + s_sum) return;
 
-  // the run that holds the limit: 32 runs at a time
-  unsigned long long at = before;
-  int found = r1 - 1;
-  for (int base = 0; base < r1 - r0; base += 32) {
-    unsigned long long v = base + lane < r1 - r0 ? s_run[base + lane] : 0, incl = v;
+    // the run that holds the limit: 32 runs at a time
+    unsigned long long at = before;
+    int found = r1 - 1;
+    for (int base = 0; base < r1 - r0; base += 32) {
+      unsigned long long v = base + lane < r1 - r0 ? s_run[base + lane] : 0, incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, at + incl > limit);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        found = r0 + base + l;
+        at += __shfl_sync(0xffffffffu, incl - v, l);
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    // 16 values a lane, one behind the other: the lane, then its value
+    constexpr int kOwn = kRun / 32;
+    const int64_t i0 = (int64_t)found * kRun + lane * kOwn;
+    float w[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) w[k] = i0 + k < a.V ? weight(i0 + k) : 0.0f;
+    Units own;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) own.add(w[k]);
+    unsigned long long incl = own.value();
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, at + incl > limit);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      found = r0 + base + l;
-      at += __shfl_sync(0xffffffffu, incl - v, l);
-      break;
-    }
-    at += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  for (int k = 0; k < kRun / 32; ++k) {
-    const int64_t i = (int64_t)found * kRun + 32 * k + lane;
-    unsigned long long incl = i < a.V ? weight(i) : 0;
+    if (hit && lane == __ffs(hit) - 1) {
+      at += incl - own.value();
+      int k = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      for (int e = 0; e < kOwn; ++e) {
+        Units one;
+        one.add(w[e]);
+        at += one.value();
+        k += at <= limit;
+      }
+      tokens[n] = (int32_t)(i0 + k);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, at + incl > limit);
-    if (hit) {
-      if (lane == 0) tokens[n] = (int32_t)((int64_t)found * kRun + 32 * k + __ffs(hit) - 1);
-      return;
-    }
-    at += __shfl_sync(0xffffffffu, incl, 31);
-  }
+  };
+  find();
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <typename T>

@@ -23,6 +23,7 @@ H, P, C = 128, 256, 32
 PLANE_BYTES = H * P // 2
 META_FLOATS = 2 * H + 2 * H * (P // C)
 OUT_BF16, OUT_F32 = 0, 1
+_SCALE = 1.0 / math.sqrt(H)
 
 
 class LynxError(RuntimeError):
@@ -511,37 +512,45 @@ def lynx_attn_merge(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
 
 class _On:
     """Checks the tensors of a call (type, shape, all on the first one's device) and
-    makes that device current for the launch."""
+    launches with that device current."""
 
-    __slots__ = ("device", "before")
+    __slots__ = ("device", "index")
 
     def __init__(self, first, name):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise LynxError(f"{name} must live on a CUDA device")
         self.device = first.device
+        self.index = self.device.index
 
     def need(self, t, dtype, shape, name):
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+        """t's address, if it is what it has to be"""
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous():
             raise LynxError(f"{name} must be a contiguous {dtype} tensor")
         if t.shape != shape:
             raise LynxError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.device != self.device:
+        if t.get_device() != self.index:
             raise LynxError(f"{name} must live on {self.device}")
-        return t
+        return t.data_ptr()
 
     def make(self, t, dtype, shape, name):
         if t is None:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        return self.need(t, dtype, shape, name)
+        self.need(t, dtype, shape, name)
+        return t
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.device)
+    def call(self, name, stream, *args):
+        fn = getattr(_lib or load(), name)
+        before = _current_device()
+        if before == self.index:
+            status = fn(*args, stream.cuda_stream if stream is not None else _stream(None, self.device))
+        else:
+            with torch.cuda.device(self.index):
+                status = fn(*args, _stream(stream, self.device))
+        if status != 0:
+            _check(status, name)
 
-    def __exit__(self, *exc):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.before)
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def lynx_assign_pages(ctx_len, new_len, page_table, free_pages, n_rows: int, cu_new=None, positions=None, slots=None,
@@ -555,25 +564,21 @@ def lynx_assign_pages(ctx_len, new_len, page_table, free_pages, n_rows: int, cu_
     on = _On(page_table, "page_table")
     if page_table.dim() != 3:
         raise LynxError("page_table must be [B, Hkv, max_pages]")
-    B, Hkv, max_pages = page_table.shape
-    n_rows = int(n_rows)
+    shape = page_table.shape
+    B, Hkv, max_pages = shape
     if n_rows < 0:
         raise LynxError("n_rows must not be negative")
-    on.need(page_table, torch.int32, page_table.shape, "page_table")
-    on.need(ctx_len, torch.int32, (B,), "ctx_len")
-    on.need(new_len, torch.int32, (B,), "new_len")
-    n_free = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
-    on.need(free_pages, torch.int32, (n_free,), "free_pages")
-    cu_new = on.make(cu_new, torch.int32, (B + 1,), "cu_new")
-    positions = on.make(positions, torch.int32, (n_rows,), "positions")
+    i32, need = torch.int32, on.need
+    cu_new = on.make(cu_new, i32, (B + 1,), "cu_new")
+    positions = on.make(positions, i32, (n_rows,), "positions")
     slots = on.make(slots, torch.int64, (n_rows, Hkv), "slots")
-    ctx_out = on.make(ctx_out, torch.int32, (B,), "ctx_out")
-    n_taken = on.make(n_taken, torch.int32, (1,), "n_taken")
-    with on:
-        _check(load().lynx_assign_pages(_ptr(ctx_len), _ptr(new_len), B, Hkv, _ptr(page_table), max_pages,
-                                        _ptr(free_pages), n_free, n_rows, _ptr(cu_new), _ptr(positions), _ptr(slots),
-                                        _ptr(ctx_out), _ptr(n_taken), _stream(stream, on.device)),
-               "lynx_assign_pages")
+    ctx_out = on.make(ctx_out, i32, (B,), "ctx_out")
+    n_taken = on.make(n_taken, i32, (1,), "n_taken")
+    n_free = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
+    on.call("lynx_assign_pages", stream, need(ctx_len, i32, (B,), "ctx_len"), need(new_len, i32, (B,), "new_len"), B,
+            Hkv, need(page_table, i32, shape, "page_table"), max_pages,
+            need(free_pages, i32, (n_free,), "free_pages"), n_free, n_rows, cu_new.data_ptr(), positions.data_ptr(),
+            slots.data_ptr(), ctx_out.data_ptr(), n_taken.data_ptr())
     return cu_new, positions, slots, ctx_out, n_taken
 
 
@@ -586,33 +591,30 @@ def lynx_qkv_append(qkv, n_q_heads: int, n_kv_heads: int, cos_sin, positions, sl
     and values to slots int64 [n_rows, Hkv] of the pools k_pages / v_pages bf16
     [n, 128, 256].  Rows with a negative position are skipped.  Returns q_out."""
     on = _On(qkv, "qkv")
-    Hq, Hkv = int(n_q_heads), int(n_kv_heads)
-    if qkv.dtype != torch.bfloat16 or qkv.dim() != 2 or (qkv.shape[1] > 1 and qkv.stride(1) != 1):
+    Hq, Hkv, need = n_q_heads, n_kv_heads, on.need
+    if qkv.dtype is not torch.bfloat16 or qkv.dim() != 2 or (qkv.shape[1] > 1 and qkv.stride(1) != 1):
         raise LynxError("qkv must be a bfloat16 tensor [n_rows, channels] with contiguous channels")
-    n_rows = qkv.shape[0]
-    if Hq < 1 or Hkv < 1 or qkv.shape[1] < (Hq + 2 * Hkv) * H:
+    n_rows, width = qkv.shape
+    if Hq < 1 or Hkv < 1 or width < (Hq + 2 * Hkv) * H:
         raise LynxError("each row of qkv must hold (n_q_heads + 2 n_kv_heads) * 128 channels")
     stride = qkv.stride(0) if n_rows > 1 else (Hq + 2 * Hkv) * H
-    max_pos = rot = 0
+    max_pos = rot = table = wq = wk = None
     if cos_sin is not None:
         if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
             raise LynxError("cos_sin must be a float32 tensor [max_pos, rot_dim]")
         max_pos, rot = cos_sin.shape
-        on.need(cos_sin, torch.float32, cos_sin.shape, "cos_sin")
-    on.need(positions, torch.int32, (n_rows,), "positions")
-    on.need(slots, torch.int64, (n_rows, Hkv), "slots")
-    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            on.need(w, torch.float32, (H,), nm)
+        table = need(cos_sin, torch.float32, cos_sin.shape, "cos_sin")
+    if q_weight is not None:
+        wq = need(q_weight, torch.float32, (H,), "q_weight")
+    if k_weight is not None:
+        wk = need(k_weight, torch.float32, (H,), "k_weight")
     n_pool = k_pages.shape[0] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3 else 0
-    on.need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages")
-    on.need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages")
     q_out = on.make(q_out, torch.bfloat16, (n_rows, Hq, H), "q_out")
-    with on:
-        _check(load().lynx_qkv_append(_ptr(qkv), n_rows, stride, Hq, Hkv, H, _ptr(q_weight), _ptr(k_weight),
-                                      float(norm_eps), _ptr(cos_sin), max_pos, rot, int(bool(interleaved)),
-                                      _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), n_pool,
-                                      _stream(stream, on.device)), "lynx_qkv_append")
+    on.call("lynx_qkv_append", stream, qkv.data_ptr(), n_rows, stride, Hq, Hkv, H, wq, wk, norm_eps, table,
+            max_pos or 0, rot or 0, 1 if interleaved else 0, need(positions, torch.int32, (n_rows,), "positions"),
+            need(slots, torch.int64, (n_rows, Hkv), "slots"), q_out.data_ptr(),
+            need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages"),
+            need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages"), n_pool)
     return q_out
 
 
@@ -630,23 +632,19 @@ def lynx_chunk_attn_bf16(q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_he
     out_dtype, bfloat16 or float32; lse f32 [n_rows, Hq]); rows behind the last
     request are left as they are."""
     on = _On(q, "q")
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != H or q.stride(2) != 1 or (
+    need, i32 = on.need, torch.int32
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or q.shape[2] != H or q.stride(2) != 1 or (
             q.shape[1] > 1 and q.stride(1) != H):
         raise LynxError("q must be a bfloat16 tensor [n_rows, Hq, 128] with contiguous rows")
     n_rows, Hq, _ = q.shape
     stride = q.stride(0) if n_rows > 1 else Hq * H
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 3 or page_table.shape[1] != n_kv_heads:
         raise LynxError("page_table must be [B, Hkv, max_pages]")
-    B, Hkv, max_pages = page_table.shape
-    on.need(page_table, torch.int32, page_table.shape, "page_table")
-    on.need(cu_q, torch.int32, (B + 1,), "cu_q")
-    on.need(ctx_len, torch.int32, (B,), "ctx_len")
+    shape = page_table.shape
+    B, Hkv, max_pages = shape
     n_pool = k_pages.shape[0] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3 else 0
-    on.need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages")
-    on.need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages")
     dtype = out.dtype if isinstance(out, torch.Tensor) else out_dtype
-    code = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}.get(dtype)
-    if code is None:
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise LynxError("out_dtype must be torch.bfloat16 or torch.float32")
     out = on.make(out, dtype, (n_rows, Hq, H), "out")
     lse = on.make(lse, torch.float32, (n_rows, Hq), "lse")
@@ -655,13 +653,13 @@ def lynx_chunk_attn_bf16(q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_he
         workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=on.device)
     elif not isinstance(workspace, torch.Tensor) or workspace.device != on.device or not workspace.is_contiguous():
         raise LynxError(f"workspace must be a contiguous tensor on {on.device}")
-    scale = float(sm_scale) if sm_scale is not None else 1.0 / math.sqrt(H)
-    with on:
-        _check(load().lynx_chunk_attn_bf16(_ptr(q), n_rows, stride, _ptr(cu_q), B, Hq, Hkv, H, _ptr(k_pages),
-                                           _ptr(v_pages), n_pool, _ptr(page_table), max_pages, _ptr(ctx_len), scale,
-                                           int(bool(causal)), _ptr(out), code, _ptr(lse), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), _stream(stream, on.device)),
-               "lynx_chunk_attn_bf16")
+    on.call("lynx_chunk_attn_bf16", stream, q.data_ptr(), n_rows, stride, need(cu_q, i32, (B + 1,), "cu_q"), B, Hq, Hkv,
+            H, need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages"),
+            need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages"), n_pool,
+            need(page_table, i32, shape, "page_table"), max_pages, need(ctx_len, i32, (B,), "ctx_len"),
+            sm_scale if sm_scale is not None else _SCALE, 1 if causal else 0, out.data_ptr(),
+            OUT_BF16 if dtype is torch.bfloat16 else OUT_F32, lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return out, lse
 
 
@@ -673,26 +671,25 @@ def lynx_verify_drafts(p, q, draft, u, n_draft=None, tokens=None, n_accept=None,
     [B, T + 1]: the accepted drafts, the next token, -1 behind it; n_accept int32
     [B])."""
     on = _On(p, "p")
-    code = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}.get(p.dtype)
-    if code is None or p.dim() != 3 or p.shape[1] < 2 or (p.shape[2] > 1 and p.stride(2) != 1):
+    need, i32, dtype, shape = on.need, torch.int32, p.dtype, p.shape
+    if (dtype is not torch.float32 and dtype is not torch.bfloat16) or len(shape) != 3 or shape[1] < 2 or (
+            shape[2] > 1 and p.stride(2) != 1):
         raise LynxError("p must be a float32 or bfloat16 tensor [B, T + 1, V] with contiguous rows")
-    B, T, V = p.shape[0], p.shape[1] - 1, p.shape[2]
-    qs = (0, 0)
+    B, T, V = shape[0], shape[1] - 1, shape[2]
+    pb, pt, _ = p.stride()
+    q_at, qb, qt = None, 0, V
     if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dtype != p.dtype or q.shape != (B, T, V) or q.device != on.device or (
-                V > 1 and q.stride(2) != 1):
+        if not isinstance(q, torch.Tensor) or q.dtype is not dtype or q.shape != (B, T, V) or (
+                q.get_device() != on.index) or (V > 1 and q.stride(2) != 1):
             raise LynxError("q must be a tensor [B, T, V] of p's type with contiguous rows, on p's device")
-        qs = (q.stride(0) if B > 1 else 0, q.stride(1) if T > 1 else V)
-    on.need(draft, torch.int32, (B, T), "draft")
-    on.need(u, torch.float32, (B, T + 1), "u")
-    if n_draft is not None:
-        on.need(n_draft, torch.int32, (B,), "n_draft")
-    tokens = on.make(tokens, torch.int32, (B, T + 1), "tokens")
-    n_accept = on.make(n_accept, torch.int32, (B,), "n_accept")
-    with on:
-        _check(load().lynx_verify_drafts(_ptr(p), p.stride(0) if B > 1 else 0, p.stride(1), _ptr(q), qs[0], qs[1], code,
-                                         B, T, V, _ptr(draft), _ptr(n_draft), _ptr(u), _ptr(tokens), _ptr(n_accept),
-                                         _stream(stream, on.device)), "lynx_verify_drafts")
+        q_at = q.data_ptr()
+        qb, qt = q.stride(0) if B > 1 else 0, q.stride(1) if T > 1 else V
+    tokens = on.make(tokens, i32, (B, T + 1), "tokens")
+    n_accept = on.make(n_accept, i32, (B,), "n_accept")
+    on.call("lynx_verify_drafts", stream, p.data_ptr(), pb if B > 1 else 0, pt, q_at, qb, qt,
+            OUT_F32 if dtype is torch.float32 else OUT_BF16, B, T, V, need(draft, i32, (B, T), "draft"),
+            None if n_draft is None else need(n_draft, i32, (B,), "n_draft"),
+            need(u, torch.float32, (B, T + 1), "u"), tokens.data_ptr(), n_accept.data_ptr())
     return tokens, n_accept
 
 
