@@ -107,6 +107,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// one lane of a whole warp, the same one every time
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// a value that all lanes of the warp share
+template <typename V>
+__device__ __forceinline__ V uni(V v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
 // shared-memory operand, 128-byte swizzle.  K-major: rows of 128 bytes along K,
 // 8-row groups 1024 bytes apart.  MN-major: rows of 64 values along MN, 8-row
 // (K) groups 1024 bytes apart, the next 64 along MN one TMA box on.
@@ -441,22 +452,26 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           }
         }
       } else if (warp == kMmaWarp) {
-        // ================= tensor-core warp
+        // ================= tensor-core warp.  Everything that the products' operands
+        // are made of is the same in all lanes and known to be (uni), and one
+        // elected lane issues: the compiler keeps descriptors in uniform registers
+        // then.  66 clocks a product of 128 x 128 x 16 against 79 under lane == 0;
+        // the tensor core takes 64.
+        const uint32_t tm = uni(tmem);
+        const uint64_t q_desc = desc_k(uni(base) + kOffQ), k_desc = desc_mn(uni(base) + kOffRing);
+        const uint64_t v_desc = desc_k(uni(base) + kOffRing);
         for (int i = 0; i < n_items && !failed; ++i) {
-          const Item it = items[i];
-          if (it.kind == kNothing || it.k0 == it.k1) continue;
-          const int groups = it.rows > kGroupRows ? 2 : 1;
-          const int n = it.k1 - it.k0;
-          // S of group g against the K tile in slot s
-          auto qk = [&](int g, int s) {
-            if (lane == 0) {
-              const uint32_t q = base + kOffQ + g * kQBytes, k = base + kOffRing + s * kSlot;
+          const int n = uni(items[i].k1 - items[i].k0);
+          const int groups = uni(items[i].rows) > kGroupRows ? 2 : 1;
+          const int keys = uni(items[i].ctx - items[i].k0 * kTileKeys);   // from the first tile on
+          if (uni(items[i].kind) == kNothing || n == 0) continue;
+          // S of group g against the K tile in slot s; by the elected lane
+          auto qk = [&](int g, uint32_t s) {
+            const uint64_t q = q_desc + g * (kQBytes >> 4), k = k_desc + (uint64_t)(s * (kSlot >> 4));
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                mma_ss(tmem + g * 128, desc_k(q + (ks >> 2) * kBox + (ks & 3) * 32), desc_mn(k + ks * 2048), kIdescMn, ks > 0);
-              tc_commit(s_full(g));
-            }
-            __syncwarp();
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ss(tm + g * 128, q + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, k + ks * 128, kIdescMn, ks > 0);
+            tc_commit(s_full(g));
           };
           auto wait_kv = [&](uint32_t u) {
             if (!mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns)) failed = true;
@@ -471,13 +486,17 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
           tc_fence_after();
-          for (int g = 0; g < groups; ++g) qk(g, n_kv_ring % kSlots);
-          if (lane == 0) tc_commit(kv_empty(n_kv_ring % kSlots));
+          const uint32_t s0 = uni(n_kv_ring % kSlots);
+          if (elected()) {
+            for (int g = 0; g < groups; ++g) qk(g, s0);
+            tc_commit(kv_empty(s0));
+          }
+          __syncwarp();
           for (int j = 0; j < n; ++j) {
             const uint32_t uv = n_kv_ring + 2 * j + 1, uk = uv + 1;
-            const int sv = uv % kSlots, sk = uk % kSlots;
+            const uint32_t sv = uni(uv % kSlots), sk = uni(uk % kSlots);
             if (!wait_kv(uv)) break;
-            const int tail = it.ctx - (it.k0 + j) * kTileKeys;   // valid keys of the tile
+            const int tail = keys - j * kTileKeys;   // valid keys of the tile
             if (tail < kTileKeys) {
               // zero the V rows of the tokens past the context: 16-byte pieces of
               // 8 tokens, the one that the context ends in value by value
@@ -503,20 +522,20 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               failed = __any_sync(0xffffffffu, failed);
               if (failed) break;
               tc_fence_after();
-              if (lane == 0) {
-                const uint32_t v = base + kOffRing + sv * kSlot;
+              if (elected()) {
+                const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                  mma_ts(tmem + 256 + g * 128, tmem + g * 128 + ks * 8, desc_k(v + (ks >> 2) * kBox + (ks & 3) * 32), kIdesc,
+                  mma_ts(tm + 256 + g * 128, tm + g * 128 + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc,
                          j > 0 || ks > 0);
                 tc_commit(o_done(g));
+                if (g == groups - 1) tc_commit(kv_empty(sv));
+                if (j + 1 < n) {
+                  qk(g, sk);
+                  if (g == groups - 1) tc_commit(kv_empty(sk));
+                }
               }
               __syncwarp();
-              if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sv));
-              if (j + 1 < n) {
-                qk(g, sk);
-                if (g == groups - 1 && lane == 0) tc_commit(kv_empty(sk));
-              }
             }
             if (failed) break;
           }
@@ -697,10 +716,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         if (!(a.inject && u == 1)) mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns);
     }
     if (warp == kMmaWarp) {
-      if (lane == 0) {
-        tc_commit(drained);
-        mbar_wait(drained, 0, wait_ns);
-      }
+      if (elected()) tc_commit(drained);
+      __syncwarp();
+      mbar_wait(drained, 0, wait_ns);
       __syncwarp();
     }
   }
