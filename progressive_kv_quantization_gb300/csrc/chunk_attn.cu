@@ -113,6 +113,8 @@ __device__ __forceinline__ bool elected() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+// mask of the first n of two packed 16-bit values
+__device__ __forceinline__ uint32_t keep2(int n) { return n >= 2 ? 0xFFFFFFFFu : n == 1 ? 0x0000FFFFu : 0u; }
 // a value that all lanes of the warp share
 template <typename V>
 __device__ __forceinline__ V uni(V v) {
@@ -197,6 +199,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// 32 bytes: a whole sector at once, if the address is a multiple of 32
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, int wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), LYNX_I8(v, 0) : "memory");
+  } else {
+    uint4* d = static_cast<uint4*>(p);
+    d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // ------------------------------------------------------------------ work split
@@ -320,9 +333,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   wait_prerequisite_grids();
 
   // the line's length, and this CTA's part [x0, x1) of it
+  const Request req = load_request(a, tid);   // used again for the first list
   long long Wh = 0;
   for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const Request r = load_request(a, b0 + tid);
+    const Request r = b0 == 0 ? req : load_request(a, b0 + tid);
     long long sum;
     block_scan(r.at(r.tiles), s_scan, &sum);
     Wh += sum;
@@ -345,14 +359,14 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   bool failed = false;
 
   // the items of the current head's segment, at most kMaxItems, into shared memory; moves x0 on
-  auto next_items = [&]() {
+  auto next_items = [&](bool first) {
     const long long h = x0 / Wh;
     const long long seg0 = x0 - h * Wh, seg1 = min(x1 - h * Wh, Wh);
     long long before = 0;
     int n_items = 0;
     if (tid == 0) *s_next = h * Wh + seg1;
     for (int b0 = 0; b0 < a.B && before < seg1; b0 += kThreads) {
-      const Request r = load_request(a, b0 + tid);
+      const Request r = first && b0 == 0 ? req : load_request(a, b0 + tid);
       long long sum;
       const long long len = r.at(r.tiles);
       const long long p = before + block_scan(len, s_scan, &sum) - len;
@@ -408,10 +422,11 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     return n_items;
   };
 
+  int n_items = x0 < x1 ? next_items(true) : 0;
+  bool more = n_items > 0;
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    while (x0 < x1) {
-      const int n_items = next_items();
+    while (more) {
       if (warp == kTmaWarp) {
         // ================= producer: K and V tiles in the order of use
         if (lane == 0) {
@@ -497,19 +512,28 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             const uint32_t sv = uni(uv % kSlots), sk = uni(uk % kSlots);
             if (!wait_kv(uv)) break;
             const int tail = keys - j * kTileKeys;   // valid keys of the tile
-            if (tail < kTileKeys) {
-              // zero the V rows of the tokens past the context: 16-byte pieces of
-              // 8 tokens, the one that the context ends in value by value
-              uint8_t* v = smem + kOffRing + sv * kSlot;
-              for (int x = lane; x < kH * 16; x += 32) {
-                const int ch = x >> 4, piece = x & 15;
-                const int left = tail - piece * 8;
-                if (left >= 8) continue;
-                uint8_t* at = v + (piece >> 3) * kBox + ch * 128 + (((piece & 7) ^ (ch & 7)) << 4);
-                if (left <= 0) {
-                  *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                  for (int e = left; e < 8; ++e) reinterpret_cast<uint16_t*>(at)[e] = 0;
+            const int steps = uni(min(8, (tail + 15) >> 4));   // products of 16 keys that hold valid ones
+            if (tail < steps * 16) {
+              // zero the V rows of the last product's tokens past the context: 16-byte
+              // pieces of 8 tokens, the one that the context ends in value by value
+#pragma unroll
+              for (int x = 0; x < kH / 32; ++x) {
+                const int ch = 32 * x + lane;
+                uint8_t* v = smem + kOffRing + sv * kSlot + ch * 128;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int piece = 2 * steps - 2 + y, left = tail - piece * 8;
+                  uint4* at = reinterpret_cast<uint4*>(v + (piece >> 3) * kBox + (((piece & 7) ^ (ch & 7)) << 4));
+                  if (left <= 0) {
+                    *at = make_uint4(0u, 0u, 0u, 0u);
+                  } else if (left < 8) {
+                    uint4 w = *at;
+                    w.x &= keep2(left);
+                    w.y &= keep2(left - 2);
+                    w.z &= keep2(left - 4);
+                    w.w &= keep2(left - 6);
+                    *at = w;
+                  }
                 }
               }
               fence_proxy_async();
@@ -526,8 +550,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
                 const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                  mma_ts(tm + 256 + g * 128, tm + g * 128 + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc,
-                         j > 0 || ks > 0);
+                  if (ks < steps)
+                    mma_ts(tm + 256 + g * 128, tm + g * 128 + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc,
+                           j > 0 || ks > 0);
                 tc_commit(o_done(g));
                 if (g == groups - 1) tc_commit(kv_empty(sv));
                 if (j + 1 < n) {
@@ -544,20 +569,51 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         if (failed && lane == 0) give_up();
       }
       sync_all();
-      if (*s_abort) break;
+      more = !*s_abort && x0 < x1;
+      if (more) n_items = next_items(false);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    while (x0 < x1) {
-      const int n_items = next_items();
+    while (more) {
       // ================= softmax: group g, one row a thread
       const int g = warp >> 2;
       const int r = (warp & 3) * 32 + lane;               // row of the group, tensor-memory lane
       const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
-      for (int i = 0; i < n_items && !failed; ++i) {
+      auto next_active = [&](int i) {   // the next item that this group has rows of
+        while (i < n_items && (items[i].kind == kNothing || items[i].rows <= g * kGroupRows)) ++i;
+        return i;
+      };
+      // this thread's row of an item's queries, as 16-byte pieces
+      auto query_row = [&](const Item& it) -> const uint4* {
+        const int row = it.row0 + g * kGroupRows + r, token = row / a.G;
+        if (g * kGroupRows + r >= it.rows || it.k0 == it.k1) return nullptr;
+        return reinterpret_cast<const uint4*>(a.q + (int64_t)(it.q_base + token) * a.q_stride +
+                                              (it.h * a.G + row - token * a.G) * kH);
+      };
+      // an item's queries to shared memory, swizzled; the products that read the
+      // item's before have all been seen to be done
+      auto load_queries = [&](const Item& it) {
+        if (it.k0 == it.k1) return;
+        const uint4* src = query_row(it);
+        uint8_t* q = smem + kOffQ + g * kQBytes + r * 128;
+        uint4 v[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = src ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) *reinterpret_cast<uint4*>(q + (x >> 3) * kBox + (((x & 7) ^ (r & 7)) << 4)) = v[x];
+        fence_proxy_async();
+        mbar_arrive(q_full(g));
+      };
+      int i = next_active(0);
+      if (i < n_items) load_queries(items[i]);
+      while (i < n_items && !failed) {
         const Item it = items[i];
-        if (it.kind == kNothing || it.rows <= g * kGroupRows) continue;
+        i = next_active(i + 1);
+        if (i < n_items) {   // on their way to L2 meanwhile
+          const uint4* src = query_row(items[i]);
+          if (src) asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(src));
+        }
         const int row = it.row0 + g * kGroupRows + r;
         const bool real = g * kGroupRows + r < it.rows;
         const int token = row / a.G, hq = it.h * a.G + row - token * a.G;
@@ -565,17 +621,6 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         float m = -CUDART_INF_F, l = 0.0f;
         const int n = it.k1 - it.k0;
         if (n > 0) {
-          // the row's queries to shared memory, 16-byte pieces swizzled
-          uint8_t* q = smem + kOffQ + g * kQBytes + r * 128;
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(it.q_base + token) * a.q_stride + hq * kH);
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (real) v = src[x];
-            *reinterpret_cast<uint4*>(q + (x >> 3) * kBox + (((x & 7) ^ (r & 7)) << 4)) = v;
-          }
-          fence_proxy_async();
-          mbar_arrive(q_full(g));
           // rows past the tile's last hold zero queries: whatever they sum up is not written
           const int seen = real ? visible(a, it.ctx, it.T, token) : 0x7fffffff;
           const float sc = a.scale_log2;
@@ -652,23 +697,23 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             mbar_arrive(p_full(g));
             ++n_tile_g;
           }
-          if (!failed && !mbar_wait(o_done(g), (n_tile_g - 1) & 1, wait_ns)) failed = true;
+          if (failed) break;
+          // the next item's first product runs while this one's output is written
+          if (i < n_items) load_queries(items[i]);
+          if (!mbar_wait(o_done(g), (n_tile_g - 1) & 1, wait_ns)) failed = true;
           failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
           tc_fence_after();
+        } else if (i < n_items) {
+          load_queries(items[i]);
         }
         // ---- the row's output, or its part
         const bool part = it.kind != kDirect;
-        const float scale = part ? 1.0f : l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays
-        float* ws = nullptr;
+        const float scale = part ? 1.0f : l > 0.0f ? 1.0f / l : l;   // 0 for a row without keys, NaN stays
+        const int rr = g * kGroupRows + r;
+        float* slot = a.ws_o + (int64_t)(2 * c + (it.kind == kPartB)) * a.slot_rows * (kH + 2);
         if (part) {
-          float* slot = a.ws_o + (int64_t)(2 * c + (it.kind == kPartB)) * a.slot_rows * (kH + 2);
-          const int rr = g * kGroupRows + r;
-          ws = slot + rr * kH;
-          if (real) {
-            slot[a.slot_rows * kH + 2 * rr] = m;
-            slot[a.slot_rows * kH + 2 * rr + 1] = l;
-          }
+          if (real) *reinterpret_cast<float2*>(slot + a.slot_rows * kH + 2 * rr) = make_float2(m, l);
         } else if (real && a.lse) {
           a.lse[out_row] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
         }
@@ -684,27 +729,31 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
-          if (real && (part || a.out_f32)) {
-            uint4* dst = reinterpret_cast<uint4*>(part ? ws : static_cast<float*>(a.out) + out_row * kH) + 8 * x;
+          if (part) {   // [four channels][row]: a warp's stores are contiguous
+            if (real) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else if (real) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_row * kH) + 4 * x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = bf16x2(__uint_as_float(o[8 * e + 2 * y]), __uint_as_float(o[8 * e + 2 * y + 1]));
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(slot + ((8 * x + e) * a.slot_rows + rr) * 4) =
+                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
+          } else if (real && a.out_f32) {
+            float* dst = static_cast<float*>(a.out) + out_row * kH + 32 * x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store32(dst + 8 * e, o + 8 * e, a.out_wide);
+          } else if (real) {
+            uint16_t* dst = static_cast<uint16_t*>(a.out) + out_row * kH + 32 * x;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            store32(dst, o, a.out_wide);
+            store32(dst + 16, o + 8, a.out_wide);
           }
         }
         tc_fence_before();   // O has been read before the next item's first product
       }
       if (failed && lane == 0) give_up();
       sync_all();
-      if (*s_abort) break;
+      more = !*s_abort && x0 < x1;
+      if (more) n_items = next_items(false);
     }
   }
 
@@ -734,11 +783,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 // ------------------------------------------------------------------ join of the parts
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
 
-// CTA (c, y) joins the tile that CTA c of the kernel above began and did not
-// end: rows y kJoinWarps + warp, + gridDim.y kJoinWarps, ...; a warp a row.
-// With m* the largest of the parts' m: O = sum 2^(m_i - m*) O_i / sum 2^(m_i - m*) l_i.
+// CTA (c, y) joins rows 32 y .. of the tile that CTA c of the kernel above began
+// and did not end; a row a lane, 16 channels a warp.  With m* the largest of the
+// parts' m: O = sum 2^(m_i - m*) O_i / sum 2^(m_i - m*) l_i.
 __global__ void __launch_bounds__(kJoinThreads)
 chunk_combine_kernel(const ChunkArgs a) {
   __shared__ int s_slot[2 * kMaxCtas];
@@ -747,7 +795,7 @@ chunk_combine_kernel(const ChunkArgs a) {
   wait_prerequisite_grids();
   const Header* hdr = reinterpret_cast<const Header*>(a.ws_hdr);
   const Header hd = hdr[c];
-  if (!hd.b_open || hd.b_state == 2) return;
+  if (!hd.b_open || hd.b_state == 2 || (int)blockIdx.y * 32 >= hd.rows) return;
   if (warp == 0) {
     int n = 0;
     if (hd.b_state == 1) {
@@ -776,44 +824,51 @@ chunk_combine_kernel(const ChunkArgs a) {
     if (lane == 0) s_n = n;
   }
   __syncthreads();
-  const int n = s_n;
-  if (n == 0) return;
+  const int n = s_n, r = blockIdx.y * 32 + lane;
+  if (n == 0 || r >= hd.rows) return;
   const int64_t stride = (int64_t)a.slot_rows * (kH + 2);
-  for (int r = blockIdx.y * kJoinWarps + warp; r < hd.rows; r += gridDim.y * kJoinWarps) {
-    const float* ml = a.ws_o + (int64_t)a.slot_rows * kH + 2 * r;
-    float m = -CUDART_INF_F;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[s_slot[i] * stride]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
+  const float* ml = a.ws_o + (int64_t)a.slot_rows * kH + 2 * r;
+  const float* po = a.ws_o + (int64_t)(4 * warp * a.slot_rows + r) * 4;
+  float m = -CUDART_INF_F;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* slot = a.ws_o + s_slot[i] * stride;
-      const float2 st = *reinterpret_cast<const float2*>(slot + (int64_t)a.slot_rows * kH + 2 * r);
-      const float4 o = *reinterpret_cast<const float4*>(slot + r * kH + 4 * lane);
-      const float f = st.x == -CUDART_INF_F ? (st.y == st.y ? 0.0f : 1.0f) : ex2(st.x - m);   // a NaN sum stays
-      l = fmaf(f, st.y, l);
-      acc.x = fmaf(f, o.x, acc.x);
-      acc.y = fmaf(f, o.y, acc.y);
-      acc.z = fmaf(f, o.z, acc.z);
-      acc.w = fmaf(f, o.w, acc.w);
+  for (int i = 0; i < n; ++i) m = fmaxf(m, ml[s_slot[i] * stride]);
+  float acc[16], l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const int64_t at = s_slot[i] * stride;
+    const float2 st = *reinterpret_cast<const float2*>(ml + at);
+    float4 o[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] = *reinterpret_cast<const float4*>(po + at + (int64_t)x * a.slot_rows * 4);
+    const float f = st.x == -CUDART_INF_F ? (st.y == st.y ? 0.0f : 1.0f) : ex2(st.x - m);   // a NaN sum stays
+    l = fmaf(f, st.y, l);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      acc[4 * x] = fmaf(f, o[x].x, acc[4 * x]);
+      acc[4 * x + 1] = fmaf(f, o[x].y, acc[4 * x + 1]);
+      acc[4 * x + 2] = fmaf(f, o[x].z, acc[4 * x + 2]);
+      acc[4 * x + 3] = fmaf(f, o[x].w, acc[4 * x + 3]);
     }
-    const float scale = l > 0.0f ? 1.0f / l : l;
-    const int row = hd.row0 + r;
-    const int token = row / a.G;
-    const int64_t out_row = (int64_t)(hd.q_base + token) * a.Hq + hd.h * a.G + row - token * a.G;
-    acc.x *= scale;
-    acc.y *= scale;
-    acc.z *= scale;
-    acc.w *= scale;
-    if (a.out_f32)
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out_row * kH + 4 * lane) = acc;
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out_row * kH + 4 * lane) =
-          make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
-    if (lane == 0 && a.lse) a.lse[out_row] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
   }
+  const float scale = l > 0.0f ? 1.0f / l : l;
+  const int row = hd.row0 + r;
+  const int token = row / a.G;
+  const int64_t out_row = (int64_t)(hd.q_base + token) * a.Hq + hd.h * a.G + row - token * a.G;
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(acc[e] * scale);
+  if (a.out_f32) {
+    float* dst = static_cast<float*>(a.out) + out_row * kH + 16 * warp;
+    store32(dst, w, a.out_wide);
+    store32(dst + 8, w + 8, a.out_wide);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = bf16x2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+    store32(static_cast<uint16_t*>(a.out) + out_row * kH + 16 * warp, w, a.out_wide);
+  }
+  if (warp == 0 && a.lse) a.lse[out_row] = l == 0.0f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace
@@ -848,6 +903,7 @@ cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {
   if (!bf16_page_map(&tk, a.k_pages, a.n_pool) || !bf16_page_map(&tv, a.v_pages, a.n_pool))
     return cudaErrorInvalidValue;
   a.n_cta = chunk_ctas();
+  a.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   a.slot_rows = chunk_slot_rows(a.n_rows, a.G);
   a.ws_hdr = workspace;
   a.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * sizeof(Header));
@@ -855,8 +911,7 @@ cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {
   a.min_keys = 512;
   cudaError_t e = launch_programmatic(chunk_attn_kernel, dim3(a.n_cta), dim3(kThreads), kSmemAlloc, s, a, tk, tv);
   if (e != cudaSuccess) return e;
-  const int slices = (a.slot_rows + kJoinWarps - 1) / kJoinWarps;
-  return launch_programmatic(chunk_combine_kernel, dim3(a.n_cta, slices < 8 ? slices : 8), dim3(kJoinThreads), 0, s, a);
+  return launch_programmatic(chunk_combine_kernel, dim3(a.n_cta, (a.slot_rows + 31) / 32), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace lynx

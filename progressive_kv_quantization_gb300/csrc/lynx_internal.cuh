@@ -278,6 +278,7 @@ struct ChunkArgs {
   int inject;                   // test hook: every CTA's first V tile is never copied
   // set by the launcher
   int n_cta, slot_rows, min_keys;
+  int out_wide;                 // out is 32-byte aligned
   void* ws_hdr;
   float* ws_o;
 };
