@@ -57,6 +57,7 @@ constexpr int kRegsSoftmax = 208, kRegsOther = 80;   // of 168 each at launch: 2
 constexpr int kMaxItems = 24;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
 constexpr float kLazyLog2 = 8.0f;
+constexpr int kMinKeysLog2 = 8;                // least cost of a CTA's part of the work, in keys
 
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + 2 * kQBytes;
@@ -66,7 +67,7 @@ constexpr int kOffItems = kOffBar + 8 * kNumBars;
 constexpr int kItemInts = 10;
 constexpr int kOffScan = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
 constexpr int kOffMisc = kOffScan + 16 * 8;   // 12 warps' sums
-constexpr int kSmem = kOffMisc + 96;
+constexpr int kSmem = kOffMisc + 96;   // next (8), header (32, at 16), tmem and abort (at 64), cut (16, at 72)
 constexpr int kSmemAlloc = kSmem + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
 
@@ -293,7 +294,8 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 
   Item* items = reinterpret_cast<Item*>(smem + kOffItems);
   long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
-  long long* s_next = reinterpret_cast<long long*>(smem + kOffMisc);
+  long long* s_next = reinterpret_cast<long long*>(smem + kOffMisc);   // where the next list begins
+  const long long* s_cut = s_next + 9;                                 // this CTA's end, the line's length of a head
   Header* s_hdr = reinterpret_cast<Header*>(smem + kOffMisc + 16);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc + 64);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 68);
@@ -342,10 +344,18 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     Wh += sum;
   }
   const long long W = Wh * a.Hkv;
-  const long long n_cta = max(1ll, min((long long)gridDim.x, W / ((long long)a.min_keys << 8)));
-  auto cut = [&](long long i) { return W / n_cta * i + W % n_cta * i / n_cta; };
-  long long x0 = c < n_cta ? cut(c) : W;
-  const long long x1 = c < n_cta ? cut(c + 1) : W;
+  // (64-bit divisions would take as long as all the rest of this)
+  const unsigned n_cta = (unsigned)max(1ll, min((long long)gridDim.x, W >> (kMinKeysLog2 + 8)));
+  const unsigned share = 0xFFFFFFFFu / n_cta;
+  auto cut = [&](unsigned i) {
+    return i >= n_cta ? W : (long long)__umul64hi((unsigned long long)W, (unsigned long long)(i * share) << 32);
+  };
+  if (tid == 0) {
+    s_next[0] = cut(c);
+    s_next[9] = cut(c + 1);
+    s_next[10] = Wh;
+  }
+  __syncthreads();
 
   const unsigned long long wait_ns = a.wait_ns;
   auto give_up = [&]() {
@@ -358,9 +368,16 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   uint32_t mma_items[2] = {0, 0}, mma_tiles[2] = {0, 0};
   bool failed = false;
 
-  // the items of the current head's segment, at most kMaxItems, into shared memory; moves x0 on
+  // the items of the current head's segment, at most kMaxItems, into shared
+  // memory; 0 at the end.  (All that it keeps lies in shared memory, not in the
+  // registers of the softmax.)
   auto next_items = [&](bool first) {
-    const long long h = x0 / Wh;
+    const long long x0 = *s_next, x1 = s_cut[0], Wh = s_cut[1];
+    if (x0 >= x1) return 0;
+    sync_all();   // everyone has read x0
+    long long h = (long long)(__ll2float_rn(x0) / __ll2float_rn(Wh));   // off by one at most
+    h -= h * Wh > x0;
+    h += (h + 1) * Wh <= x0;
     const long long seg0 = x0 - h * Wh, seg1 = min(x1 - h * Wh, Wh);
     long long before = 0;
     int n_items = 0;
@@ -395,8 +412,12 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         it.rows = min(kTileRows, r.T * a.G - it.row0);
         it.T = r.T;
         it.ctx = r.ctx;
-        it.k0 = starts ? 0 : (int)((lo - from) * n_kv / cost);
-        it.k1 = ends ? n_kv : (int)((hi - from) * n_kv / cost);
+        // where a cut falls among the tile's keys: the same function on both of its sides, not decreasing
+        auto key_tile = [&](long long x) {
+          return min(n_kv, (int)(__ll2float_rn(x - from) * (float)n_kv / __ll2float_rn(cost)));
+        };
+        it.k0 = starts ? 0 : key_tile(lo);
+        it.k1 = ends ? n_kv : key_tile(hi);
         const bool whole = it.k0 == 0 && it.k1 == n_kv && (n_kv > 0 || starts);
         it.kind = whole ? kDirect : it.k0 == it.k1 ? kNothing : starts ? kPartB : kPartA;
         items[at] = it;
@@ -417,16 +438,13 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       before += sum;
     }
     sync_all();
-    n_items = min(n_items, kMaxItems);
-    x0 = *s_next;
-    return n_items;
+    return min(n_items, kMaxItems);
   };
 
-  int n_items = x0 < x1 ? next_items(true) : 0;
-  bool more = n_items > 0;
+  int n_items = next_items(true);
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    while (more) {
+    while (n_items > 0) {
       if (warp == kTmaWarp) {
         // ================= producer: K and V tiles in the order of use
         if (lane == 0) {
@@ -548,11 +566,16 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               tc_fence_after();
               if (elected()) {
                 const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
+                if (steps == 8) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                  if (ks < steps)
+                  for (int ks = 0; ks < 8; ++ks)
                     mma_ts(tm + 256 + g * 128, tm + g * 128 + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc,
                            j > 0 || ks > 0);
+                } else {
+                  for (int ks = 0; ks < steps; ++ks)
+                    mma_ts(tm + 256 + g * 128, tm + g * 128 + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc,
+                           j > 0 || ks > 0);
+                }
                 tc_commit(o_done(g));
                 if (g == groups - 1) tc_commit(kv_empty(sv));
                 if (j + 1 < n) {
@@ -569,12 +592,11 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         if (failed && lane == 0) give_up();
       }
       sync_all();
-      more = !*s_abort && x0 < x1;
-      if (more) n_items = next_items(false);
+      n_items = *s_abort ? 0 : next_items(false);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    while (more) {
+    while (n_items > 0) {
       // ================= softmax: group g, one row a thread
       const int g = warp >> 2;
       const int r = (warp & 3) * 32 + lane;               // row of the group, tensor-memory lane
@@ -608,7 +630,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       int i = next_active(0);
       if (i < n_items) load_queries(items[i]);
       while (i < n_items && !failed) {
-        const Item it = items[i];
+        const Item& it = items[i];
         i = next_active(i + 1);
         if (i < n_items) {   // on their way to L2 meanwhile
           const uint4* src = query_row(items[i]);
@@ -752,8 +774,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       }
       if (failed && lane == 0) give_up();
       sync_all();
-      more = !*s_abort && x0 < x1;
-      if (more) n_items = next_items(false);
+      n_items = *s_abort ? 0 : next_items(false);
     }
   }
 
@@ -907,8 +928,6 @@ cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {
   a.slot_rows = chunk_slot_rows(a.n_rows, a.G);
   a.ws_hdr = workspace;
   a.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * sizeof(Header));
-  // two tiles of keys are the least that is worth a CTA's start and end (counted as two more)
-  a.min_keys = 512;
   cudaError_t e = launch_programmatic(chunk_attn_kernel, dim3(a.n_cta), dim3(kThreads), kSmemAlloc, s, a, tk, tv);
   if (e != cudaSuccess) return e;
   return launch_programmatic(chunk_combine_kernel, dim3(a.n_cta, (a.slot_rows + 31) / 32), dim3(kJoinThreads), 0, s, a);

@@ -277,7 +277,7 @@ struct ChunkArgs {
   unsigned long long wait_ns;   // as DecodeArgs
   int inject;                   // test hook: every CTA's first V tile is never copied
   // set by the launcher
-  int n_cta, slot_rows, min_keys;
+  int n_cta, slot_rows;
   int out_wide;                 // out is 32-byte aligned
   void* ws_hdr;
   float* ws_o;

@@ -232,7 +232,12 @@ def test_bad_page_ids_lengths_and_bounds_are_reported(cuda_device):
     out, _ = call(y, True)
     with pytest.raises(L.LynxError, match="= 6"):
         L.lynx_device_status()
-    assert torch.equal(out[:4], good[0][:4])          # the request with good bounds is computed
+    # The request with good bounds is computed.  (Not the same bits: how its keys are
+    # cut into parts depends on the batch.  Both results are within check()'s bound
+    # of the definition.)
+    vm = float(x["v"].float()[torch.isfinite(x["v"].float())].abs().max())
+    ro = oracle(x, True)[0][:4]
+    assert np.all(np.abs(out[:4].double().cpu().numpy() - ro) <= 2.0 ** -8 * vm + 2.0 ** -8 * np.abs(ro))
     again = call(x, True)
     torch.cuda.synchronize()
     L.lynx_device_status()
