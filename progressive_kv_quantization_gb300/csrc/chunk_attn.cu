@@ -51,8 +51,8 @@ constexpr int kBox = 16384;                    // TMA box: 64 tokens x 128 chann
 constexpr int kSlot = 2 * kBox;                // one K or V tile
 constexpr int kSlots = 5;
 constexpr int kQBytes = 2 * kBox;              // a group's queries: two halves [128 rows][64 channels]
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
-constexpr int kThreads = 384;                  // warps 10 and 11 only fill their warpgroup
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kListWarp = 10;
+constexpr int kThreads = 384;                  // warp 11 only fills its warpgroup
 constexpr int kRegsSoftmax = 208, kRegsOther = 80;   // of 168 each at launch: 256 x 208 + 128 x 80 <= 384 x 168
 constexpr int kMaxItems = 24;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
@@ -65,9 +65,8 @@ constexpr int kOffBar = kOffRing + kSlots * kSlot;
 constexpr int kNumBars = 2 * kSlots + 9;
 constexpr int kOffItems = kOffBar + 8 * kNumBars;
 constexpr int kItemInts = 10;
-constexpr int kOffScan = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
-constexpr int kOffMisc = kOffScan + 16 * 8;   // 12 warps' sums
-constexpr int kSmem = kOffMisc + 96;   // next (8), header (32, at 16), tmem and abort (at 64), cut (16, at 72)
+constexpr int kOffMisc = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
+constexpr int kSmem = kOffMisc + 80;   // number of items, header (32, at 16), tensor memory, abort flag (at 64)
 constexpr int kSmemAlloc = kSmem + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
 
@@ -257,28 +256,126 @@ __device__ __forceinline__ int visible(const ChunkArgs& a, int ctx, int T, int t
   return a.causal ? max(ctx - T + token + 1, 0) : ctx;
 }
 
-// the two sides of the kernel meet here from their own loops
+// all warps meet here from their own loops
 __device__ __forceinline__ void sync_all() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 template <typename V>
-__device__ __forceinline__ V block_scan(V v, V* s_scan, V* total) {   // inclusive; all threads
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ V warp_scan(V v) {   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const V u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+    if ((threadIdx.x & 31) >= o) v += u;
   }
-  if (lane == 31) s_scan[warp] = v;
-  sync_all();
-  V before = 0, all = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const V u = s_scan[w];
-    if (w < warp) before += u;
-    all += u;
+  return v;
+}
+
+// The list warp: measures the line, finds this CTA's part of it and hands out
+// the part's items, the tiles of one head at a time and at most kMaxItems.
+// Requests are taken 32 at a time, one a lane, the next ones on their way.  (One
+// warp and one place in the code: the list's instructions are fetched once, which
+// is most of the time that a short list takes.)
+__device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, volatile int* s_n_items, Header* s_hdr,
+                                           const volatile int* s_abort) {
+  const int lane = threadIdx.x & 31;
+  long long Wh = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const Request r = load_request(a, b0 + lane);
+    Wh += __shfl_sync(0xffffffffu, warp_scan(r.at(r.tiles)), 31);
   }
+  const long long W = Wh * a.Hkv;
+  // CTAs that get a part (64-bit divisions would take as long as the rest of this)
+  unsigned n_cta = (unsigned)max(1ll, min((long long)gridDim.x, W >> (kMinKeysLog2 + 8)));
+  // A multiple of the heads, where that leaves no more than 1/32 of the CTAs idle
+  // or they are not all used anyway: then each head has its own CTAs.
+  const unsigned heads = (unsigned)a.Hkv, over = n_cta % heads;
+  const bool by_head = n_cta >= heads && (n_cta < gridDim.x || over * 32 <= gridDim.x);
+  if (by_head) n_cta -= over;
+  const unsigned per = by_head ? n_cta / heads : n_cta, share = 0xFFFFFFFFu / per;
+  auto cut = [&](unsigned i) {   // where CTA i begins
+    if (i >= n_cta) return W;
+    const unsigned whole = i / per;
+    const unsigned long long len = by_head ? Wh : W;
+    return (long long)(whole * len + __umul64hi(len, (unsigned long long)((i - whole * per) * share) << 32));
+  };
+  long long x0 = cut(blockIdx.x);
+  const long long x1 = cut(blockIdx.x + 1);
+  while (x0 < x1) {
+    long long h = (long long)(__ll2float_rn(x0) / __ll2float_rn(Wh));   // off by one at most
+    h -= h * Wh > x0;
+    h += (h + 1) * Wh <= x0;
+    const long long seg0 = x0 - h * Wh, seg1 = min(x1 - h * Wh, Wh);
+    long long before = 0, next = h * Wh + seg1;
+    int n_items = 0;
+    for (int b0 = 0; b0 < a.B && before < seg1; b0 += 32) {
+      const Request r = load_request(a, b0 + lane);
+      const long long len = r.at(r.tiles);
+      const long long end = before + warp_scan(len), p = end - len;
+      before = __shfl_sync(0xffffffffu, end, 31);
+      if (before <= seg0) continue;
+      const long long lo = max(seg0 - p, 0ll), hi = min(seg1 - p, len);
+      int m0 = 0, m1 = -1;
+      if (lo < hi) {
+        m0 = r.tile_of(lo);
+        m1 = r.tile_of(hi - 1);
+      }
+      int at = n_items + warp_scan(m1 - m0 + 1);
+      n_items = __shfl_sync(0xffffffffu, at, 31);
+      at -= m1 - m0 + 1;
+      long long stop = next;
+      for (int m = m0; m <= m1; ++m, ++at) {
+        if (at >= kMaxItems) {
+          if (at == kMaxItems) stop = h * Wh + p + r.at(m);
+          break;
+        }
+        const int last = min(r.T - 1, (int)(((long long)kTileRows * (m + 1) - 1) / a.G));
+        const int n_kv = (visible(a, r.ctx, r.T, last) + kTileKeys - 1) / kTileKeys;
+        const long long from = r.at(m), cost = r.at(m + 1) - from;
+        const bool starts = lo <= from, ends = hi >= from + cost;
+        Item it;
+        it.b = b0 + lane;
+        it.h = (int)h;
+        it.q_base = r.q_base;
+        it.row0 = m * kTileRows;
+        it.rows = min(kTileRows, r.T * a.G - it.row0);
+        it.T = r.T;
+        it.ctx = r.ctx;
+        // where a cut falls among the tile's keys: the same function on both of its sides, not decreasing
+        auto key_tile = [&](long long x) {
+          return min(n_kv, (int)(__ll2float_rn(x - from) * (float)n_kv / __ll2float_rn(cost)));
+        };
+        it.k0 = starts ? 0 : key_tile(lo);
+        it.k1 = ends ? n_kv : key_tile(hi);
+        const bool whole = it.k0 == 0 && it.k1 == n_kv && (n_kv > 0 || starts);
+        it.kind = whole ? kDirect : it.k0 == it.k1 ? kNothing : starts ? kPartB : kPartA;
+        items[at] = it;
+        const int state = n_kv > 0 && whole ? 2 : it.k1 > it.k0 ? 1 : 0;
+        if (!starts) {
+          s_hdr->a_state = state;
+          s_hdr->a_ends = ends;
+        } else if (!ends && n_kv > 0) {
+          s_hdr->b_open = 1;
+          s_hdr->b_state = state;
+          s_hdr->h = it.h;
+          s_hdr->q_base = it.q_base;
+          s_hdr->row0 = it.row0;
+          s_hdr->rows = it.rows;
+        }
+      }
+      // the lane that ran out of room knows where the next list begins
+      const unsigned cutter = __ballot_sync(0xffffffffu, stop != next);
+      if (cutter) next = __shfl_sync(0xffffffffu, stop, __ffs(cutter) - 1);
+      if (n_items > kMaxItems) break;
+    }
+    x0 = next;
+    if (lane == 0) *s_n_items = min(n_items, kMaxItems);
+    __syncwarp();
+    sync_all();   // the list is there
+    sync_all();   // and done with
+    if (*s_abort) return;
+  }
+  if (lane == 0) *s_n_items = 0;
+  __syncwarp();
   sync_all();
-  *total = all;
-  return v + before;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -293,9 +390,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   const int c = blockIdx.x;
 
   Item* items = reinterpret_cast<Item*>(smem + kOffItems);
-  long long* s_scan = reinterpret_cast<long long*>(smem + kOffScan);
-  long long* s_next = reinterpret_cast<long long*>(smem + kOffMisc);   // where the next list begins
-  const long long* s_cut = s_next + 9;                                 // this CTA's end, the line's length of a head
+  volatile int* s_n_items = reinterpret_cast<volatile int*>(smem + kOffMisc);
   Header* s_hdr = reinterpret_cast<Header*>(smem + kOffMisc + 16);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc + 64);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 68);
@@ -334,29 +429,6 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   // every access to global memory follows this wait
   wait_prerequisite_grids();
 
-  // the line's length, and this CTA's part [x0, x1) of it
-  const Request req = load_request(a, tid);   // used again for the first list
-  long long Wh = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-    const Request r = b0 == 0 ? req : load_request(a, b0 + tid);
-    long long sum;
-    block_scan(r.at(r.tiles), s_scan, &sum);
-    Wh += sum;
-  }
-  const long long W = Wh * a.Hkv;
-  // (64-bit divisions would take as long as all the rest of this)
-  const unsigned n_cta = (unsigned)max(1ll, min((long long)gridDim.x, W >> (kMinKeysLog2 + 8)));
-  const unsigned share = 0xFFFFFFFFu / n_cta;
-  auto cut = [&](unsigned i) {
-    return i >= n_cta ? W : (long long)__umul64hi((unsigned long long)W, (unsigned long long)(i * share) << 32);
-  };
-  if (tid == 0) {
-    s_next[0] = cut(c);
-    s_next[9] = cut(c + 1);
-    s_next[10] = Wh;
-  }
-  __syncthreads();
-
   const unsigned long long wait_ns = a.wait_ns;
   auto give_up = [&]() {
     atomicExch(a.status, 1);
@@ -368,83 +440,23 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   uint32_t mma_items[2] = {0, 0}, mma_tiles[2] = {0, 0};
   bool failed = false;
 
-  // the items of the current head's segment, at most kMaxItems, into shared
-  // memory; 0 at the end.  (All that it keeps lies in shared memory, not in the
-  // registers of the softmax.)
-  auto next_items = [&](bool first) {
-    const long long x0 = *s_next, x1 = s_cut[0], Wh = s_cut[1];
-    if (x0 >= x1) return 0;
-    sync_all();   // everyone has read x0
-    long long h = (long long)(__ll2float_rn(x0) / __ll2float_rn(Wh));   // off by one at most
-    h -= h * Wh > x0;
-    h += (h + 1) * Wh <= x0;
-    const long long seg0 = x0 - h * Wh, seg1 = min(x1 - h * Wh, Wh);
-    long long before = 0;
-    int n_items = 0;
-    if (tid == 0) *s_next = h * Wh + seg1;
-    for (int b0 = 0; b0 < a.B && before < seg1; b0 += kThreads) {
-      const Request r = first && b0 == 0 ? req : load_request(a, b0 + tid);
-      long long sum;
-      const long long len = r.at(r.tiles);
-      const long long p = before + block_scan(len, s_scan, &sum) - len;
-      const long long lo = max(seg0 - p, 0ll), hi = min(seg1 - p, len);
-      int m0 = 0, m1 = -1;
-      if (lo < hi) {
-        m0 = r.tile_of(lo);
-        m1 = r.tile_of(hi - 1);
-      }
-      int all;
-      int at = n_items + block_scan(m1 - m0 + 1, reinterpret_cast<int*>(s_scan), &all) - (m1 - m0 + 1);
-      for (int m = m0; m <= m1; ++m, ++at) {
-        if (at >= kMaxItems) {
-          if (at == kMaxItems) *s_next = h * Wh + p + r.at(m);
-          break;
-        }
-        const int last = min(r.T - 1, (int)(((long long)kTileRows * (m + 1) - 1) / a.G));
-        const int n_kv = (visible(a, r.ctx, r.T, last) + kTileKeys - 1) / kTileKeys;
-        const long long from = r.at(m), cost = r.at(m + 1) - from;
-        const bool starts = lo <= from, ends = hi >= from + cost;
-        Item it;
-        it.b = b0 + tid;
-        it.h = (int)h;
-        it.q_base = r.q_base;
-        it.row0 = m * kTileRows;
-        it.rows = min(kTileRows, r.T * a.G - it.row0);
-        it.T = r.T;
-        it.ctx = r.ctx;
-        // where a cut falls among the tile's keys: the same function on both of its sides, not decreasing
-        auto key_tile = [&](long long x) {
-          return min(n_kv, (int)(__ll2float_rn(x - from) * (float)n_kv / __ll2float_rn(cost)));
-        };
-        it.k0 = starts ? 0 : key_tile(lo);
-        it.k1 = ends ? n_kv : key_tile(hi);
-        const bool whole = it.k0 == 0 && it.k1 == n_kv && (n_kv > 0 || starts);
-        it.kind = whole ? kDirect : it.k0 == it.k1 ? kNothing : starts ? kPartB : kPartA;
-        items[at] = it;
-        const int state = n_kv > 0 && whole ? 2 : it.k1 > it.k0 ? 1 : 0;
-        if (!starts) {
-          s_hdr->a_state = state;
-          s_hdr->a_ends = ends;
-        } else if (!ends && n_kv > 0) {
-          s_hdr->b_open = 1;
-          s_hdr->b_state = state;
-          s_hdr->h = it.h;
-          s_hdr->q_base = it.q_base;
-          s_hdr->row0 = it.row0;
-          s_hdr->rows = it.rows;
-        }
-      }
-      n_items += all;
-      before += sum;
-    }
+  // Every role goes through the lists of items that the list warp makes, and
+  // meets the others in front of and behind each.
+  auto next_list = [&]() {
     sync_all();
-    return min(n_items, kMaxItems);
+    return *s_n_items;
+  };
+  auto list_done = [&]() {   // false: a wait has run out somewhere
+    sync_all();
+    return *s_abort == 0;
   };
 
-  int n_items = next_items(true);
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    while (n_items > 0) {
+    if (warp == kListWarp) {
+      make_lists(a, items, s_n_items, s_hdr, s_abort);
+    } else {
+    while (const int n_items = next_list()) {
       if (warp == kTmaWarp) {
         // ================= producer: K and V tiles in the order of use
         if (lane == 0) {
@@ -591,12 +603,12 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         }
         if (failed && lane == 0) give_up();
       }
-      sync_all();
-      n_items = *s_abort ? 0 : next_items(false);
+      if (!list_done()) break;
+    }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    while (n_items > 0) {
+    while (const int n_items = next_list()) {
       // ================= softmax: group g, one row a thread
       const int g = warp >> 2;
       const int r = (warp & 3) * 32 + lane;               // row of the group, tensor-memory lane
@@ -773,8 +785,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         tc_fence_before();   // O has been read before the next item's first product
       }
       if (failed && lane == 0) give_up();
-      sync_all();
-      n_items = *s_abort ? 0 : next_items(false);
+      if (!list_done()) break;
     }
   }
 
