@@ -12,8 +12,9 @@
 // operand of S = Q K^T and a V half page the K-major B operand of O = P V as they
 // lie: nothing is transposed.
 //
-// Warps.  0-3 and 4-7: softmax of the two groups, one row a thread; 8: issues
-// every tcgen05.mma; 9: TMA of K and V tiles through a ring.  S and O of both
+// Warps.  0-3 and 4-7: softmax of the two groups, one row a thread; 8 and 11:
+// issue the groups' tcgen05.mma; 9: TMA of K and V tiles through a ring; 10: the
+// lists of tiles.  S and O of both
 // groups live in tensor memory (4 x 128 columns).  P overwrites S as BF16 and is
 // the A operand of O += P V from there.  While one group does its softmax the
 // tensor core works for the other.
@@ -51,8 +52,8 @@ constexpr int kBox = 16384;                    // TMA box: 64 tokens x 128 chann
 constexpr int kSlot = 2 * kBox;                // one K or V tile
 constexpr int kSlots = 5;
 constexpr int kQBytes = 2 * kBox;              // a group's queries: two halves [128 rows][64 channels]
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kListWarp = 10;
-constexpr int kThreads = 384;                  // warp 11 only fills its warpgroup
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kListWarp = 10, kMmaWarp1 = 11;
+constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 80;   // of 168 each at launch: 256 x 208 + 128 x 80 <= 384 x 168
 constexpr int kMaxItems = 24;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
@@ -406,14 +407,17 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   const uint32_t drained = bars + 8 * 8;   // used once, by a CTA that gives up
 
   if (tid == 0) {
-    for (int s = 0; s < 2 * kSlots; ++s) mbar_init(bar0 + 8 * s, 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(kv_full(s), 1);
+      mbar_init(kv_empty(s), 2);   // both groups
+    }
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_full(g), kGroupRows);
       mbar_init(s_full(g), 1);
       mbar_init(p_full(g), kGroupRows);
       mbar_init(o_done(g), 1);
     }
-    mbar_init(drained, 1);
+    mbar_init(drained, 2);
     *s_hdr = Header{0, 0, 0, 0, 0, 0, 0, 0};
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -437,7 +441,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   // counters of each role, running over all items
   uint32_t n_kv_ring = 0;     // K and V tiles through the ring (producer; MMA warp)
   uint32_t n_tile_g = 0;      // S tiles of this thread's group (softmax)
-  uint32_t mma_items[2] = {0, 0}, mma_tiles[2] = {0, 0};
+  uint32_t mma_items = 0, mma_tiles = 0;   // of the tensor-core warp's group
   bool failed = false;
 
   // Every role goes through the lists of items that the list warp makes, and
@@ -496,56 +500,66 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             }
           }
         }
-      } else if (warp == kMmaWarp) {
-        // ================= tensor-core warp.  Everything that the products' operands
-        // are made of is the same in all lanes and known to be (uni), and one
-        // elected lane issues: the compiler keeps descriptors in uniform registers
-        // then.  66 clocks a product of 128 x 128 x 16 against 79 under lane == 0;
-        // the tensor core takes 64.
-        const uint32_t tm = uni(tmem);
-        const uint64_t q_desc = desc_k(uni(base) + kOffQ), k_desc = desc_mn(uni(base) + kOffRing);
-        const uint64_t v_desc = desc_k(uni(base) + kOffRing);
+      } else {
+        // ================= tensor-core warp of group g: while it waits, the other
+        // group's products run.  Everything that the products' operands are made of
+        // is the same in all lanes and known to be (uni), and one elected lane
+        // issues: the compiler keeps descriptors in uniform registers then.  66
+        // clocks a product of 128 x 128 x 16 against 79 under lane == 0; the tensor
+        // core takes 64.
+        const int g = warp == kMmaWarp ? 0 : 1;
+        const uint32_t t_s = uni(tmem) + g * 128, t_o = uni(tmem) + 256 + g * 128;
+        const uint64_t q_desc = desc_k(uni(base) + kOffQ + g * kQBytes);
+        const uint64_t k_desc = desc_mn(uni(base) + kOffRing), v_desc = desc_k(uni(base) + kOffRing);
         for (int i = 0; i < n_items && !failed; ++i) {
           const int n = uni(items[i].k1 - items[i].k0);
-          const int groups = uni(items[i].rows) > kGroupRows ? 2 : 1;
+          const bool both = uni(items[i].rows) > kGroupRows;
           const int keys = uni(items[i].ctx - items[i].k0 * kTileKeys);   // from the first tile on
           if (uni(items[i].kind) == kNothing || n == 0) continue;
-          // S of group g against the K tile in slot s; by the elected lane
-          auto qk = [&](int g, uint32_t s) {
-            const uint64_t q = q_desc + g * (kQBytes >> 4), k = k_desc + (uint64_t)(s * (kSlot >> 4));
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_ss(tm + g * 128, q + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, k + ks * 128, kIdescMn, ks > 0);
-            tc_commit(s_full(g));
-          };
-          auto wait_kv = [&](uint32_t u) {
-            if (!mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns)) failed = true;
+          const uint32_t u0 = n_kv_ring;
+          n_kv_ring += 2 * n;
+          auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (!mbar_wait(bar, parity, wait_ns)) failed = true;
             failed = __any_sync(0xffffffffu, failed);
             return !failed;
           };
-          if (!wait_kv(n_kv_ring)) break;
-          for (int g = 0; g < groups; ++g) {
-            if (!mbar_wait(q_full(g), mma_items[g] & 1, wait_ns)) failed = true;
-            ++mma_items[g];
+          if (g == 1 && !both) {
+            // The first group is alone.  The slots are taken and given back all the
+            // same: a warp that ran ahead of the ring could not tell a phase of a
+            // slot's barrier from the one before the last.
+            for (uint32_t u = u0; u != n_kv_ring; ++u) {
+              if (!wait(kv_full(u % kSlots), (u / kSlots) & 1)) break;
+              if (lane == 0) mbar_arrive(kv_empty(u % kSlots));
+            }
+            continue;
           }
-          failed = __any_sync(0xffffffffu, failed);
-          if (failed) break;
+          // S of the K tile in slot s; by the elected lane
+          auto qk = [&](uint32_t s) {
+            const uint64_t k = k_desc + (uint64_t)(s * (kSlot >> 4));
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ss(t_s, q_desc + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, k + ks * 128, kIdescMn, ks > 0);
+            tc_commit(s_full(g));
+          };
+          if (!wait(kv_full(u0 % kSlots), (u0 / kSlots) & 1) || !wait(q_full(g), mma_items & 1)) break;
+          ++mma_items;
           tc_fence_after();
-          const uint32_t s0 = uni(n_kv_ring % kSlots);
+          const uint32_t s0 = uni(u0 % kSlots);
           if (elected()) {
-            for (int g = 0; g < groups; ++g) qk(g, s0);
+            qk(s0);
             tc_commit(kv_empty(s0));
           }
           __syncwarp();
           for (int j = 0; j < n; ++j) {
-            const uint32_t uv = n_kv_ring + 2 * j + 1, uk = uv + 1;
+            const uint32_t uv = u0 + 2 * j + 1, uk = uv + 1;
             const uint32_t sv = uni(uv % kSlots), sk = uni(uk % kSlots);
-            if (!wait_kv(uv)) break;
+            if (!wait(kv_full(sv), (uv / kSlots) & 1)) break;
             const int tail = keys - j * kTileKeys;   // valid keys of the tile
             const int steps = uni(min(8, (tail + 15) >> 4));   // products of 16 keys that hold valid ones
             if (tail < steps * 16) {
-              // zero the V rows of the last product's tokens past the context: 16-byte
-              // pieces of 8 tokens, the one that the context ends in value by value
+              // Zero the V rows of the last product's tokens past the context: 16-byte
+              // pieces of 8 tokens, the one that the context ends in value by value.
+              // (Both groups' warps do so; they write the same.)
 #pragma unroll
               for (int x = 0; x < kH / 32; ++x) {
                 const int ch = 32 * x + lane;
@@ -569,37 +583,29 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               fence_proxy_async();
               __syncwarp();
             }
-            if (j + 1 < n && !wait_kv(uk)) break;
-            for (int g = 0; g < groups; ++g) {
-              if (!mbar_wait(p_full(g), mma_tiles[g] & 1, wait_ns)) failed = true;
-              ++mma_tiles[g];
-              failed = __any_sync(0xffffffffu, failed);
-              if (failed) break;
-              tc_fence_after();
-              if (elected()) {
-                const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
-                if (steps == 8) {
+            if (j + 1 < n && !wait(kv_full(sk), (uk / kSlots) & 1)) break;
+            if (!wait(p_full(g), mma_tiles & 1)) break;
+            ++mma_tiles;
+            tc_fence_after();
+            if (elected()) {
+              const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
+              if (steps == 8) {
 #pragma unroll
-                  for (int ks = 0; ks < 8; ++ks)
-                    mma_ts(tm + 256 + g * 128, tm + g * 128 + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc,
-                           j > 0 || ks > 0);
-                } else {
-                  for (int ks = 0; ks < steps; ++ks)
-                    mma_ts(tm + 256 + g * 128, tm + g * 128 + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc,
-                           j > 0 || ks > 0);
-                }
-                tc_commit(o_done(g));
-                if (g == groups - 1) tc_commit(kv_empty(sv));
-                if (j + 1 < n) {
-                  qk(g, sk);
-                  if (g == groups - 1) tc_commit(kv_empty(sk));
-                }
+                for (int ks = 0; ks < 8; ++ks)
+                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, j > 0 || ks > 0);
+              } else {
+                for (int ks = 0; ks < steps; ++ks)
+                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, j > 0 || ks > 0);
               }
-              __syncwarp();
+              tc_commit(o_done(g));
+              tc_commit(kv_empty(sv));
+              if (j + 1 < n) {
+                qk(sk);
+                tc_commit(kv_empty(sk));
+              }
             }
-            if (failed) break;
+            __syncwarp();
           }
-          n_kv_ring += 2 * n;
         }
         if (failed && lane == 0) give_up();
       }
@@ -796,7 +802,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       for (uint32_t u = n_kv_ring > kSlots ? n_kv_ring - kSlots : 0; u < n_kv_ring; ++u)
         if (!(a.inject && u == 1)) mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns);
     }
-    if (warp == kMmaWarp) {
+    if (warp == kMmaWarp || warp == kMmaWarp1) {
       if (elected()) tc_commit(drained);
       __syncwarp();
       mbar_wait(drained, 0, wait_ns);

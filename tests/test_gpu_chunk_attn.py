@@ -126,6 +126,16 @@ def test_many_requests_of_one_token(cuda_device):
     check(x, True, *call(x, True))
 
 
+def test_requests_of_one_group_between_requests_of_two(cuda_device):
+    """Tiles of up to 128 rows between tiles of 256, many tiles of keys each: both
+    groups of rows keep step with the ring of key and value tiles."""
+    for new, ctx, Hq, Hkv in (([1, 300, 1, 200, 1], [3000, 3000, 2500, 2000, 900], 8, 1),
+                              ([1, 1, 1, 129, 2, 513], [9000, 100, 4000, 5000, 6000, 1000], 2, 2),
+                              ([64, 1, 65, 1, 66], [4000, 4000, 4000, 4000, 4000], 6, 2)):
+        x = batch(new, ctx, Hq, Hkv, sum(new))
+        check(x, True, *call(x, True))
+
+
 def test_rows_that_see_no_key(cuda_device):
     # more new tokens than keys: the first rows see none
     x = batch([300, 5], [100, 0], 4, 2, 8)
