@@ -1,15 +1,18 @@
-"""Builds the in-tree CUDA library ``_build/liblynx.so`` for sm_103a with nvcc.
+"""Builds the in-tree CUDA library ``_build/liblynx.so`` for sm_103a with nvcc,
+and ``_build/lynx_binding.so``, the native part of the Python binding.
 
 Each .cu file compiles to an object in parallel; the objects link into one
 shared library with the CUDA runtime linked statically, so the library needs
-only the NVIDIA driver at run time.  Rebuilds only when a source or header is
-newer than the library.
+only the NVIDIA driver at run time.  The binding (one C++ file against torch's
+headers) links to that library.  Rebuilds only when a source or header is newer
+than the libraries.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "liblynx.so")
+BINDING = os.path.join(BUILD, "lynx_binding.so")
 
 SOURCES = ["lynx_api.cu", "encode.cu", "reconstruct.cu", "decode_attn.cu", "decode_quant.cu", "decode_tc.cu",
            "decode_narrow.cu", "decode_draft.cu", "decode_bf16.cu",
@@ -38,14 +42,15 @@ def nvcc() -> str:
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files.append(os.path.join(CSRC, "binding.cpp"))
     files.append(os.path.join(INCLUDE, "lynx.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -67,14 +72,37 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(r.stdout, r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        import torch   # its headers
+        inc = os.path.join(os.path.dirname(torch.__file__), "include")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
+        obj = os.path.join(BUILD, "binding.o")
+        dirs = [INCLUDE, sysconfig.get_paths()["include"], inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[f"-I{d}" for d in dirs], "-c",
+               os.path.join(CSRC, "binding.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding_obj, torch_lib = binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # torch's libraries are in the process when the binding is imported
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, binding_obj, "-L", BUILD, "-l:liblynx.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 

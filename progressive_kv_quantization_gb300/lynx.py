@@ -4,12 +4,15 @@ Argument marshalling only: every function checks tensor types, allocates the
 outputs the caller did not pass (torch device memory), and calls the entry
 point of the same name in ``_build/liblynx.so`` on the current CUDA stream.
 There is no fallback: if the library is missing or a call fails, a
-``LynxError`` is raised.
+``LynxError`` is raised.  The entry points of a serving step, whose kernels can
+be shorter than ctypes and checks in Python, do the same in the native module
+``_build/lynx_binding.so`` (csrc/binding.cpp).
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 from dataclasses import dataclass
@@ -23,7 +26,6 @@ H, P, C = 128, 256, 32
 PLANE_BYTES = H * P // 2
 META_FLOATS = 2 * H + 2 * H * (P // C)
 OUT_BF16, OUT_F32 = 0, 1
-_SCALE = 1.0 / math.sqrt(H)
 
 
 class LynxError(RuntimeError):
@@ -510,47 +512,23 @@ def lynx_attn_merge(o_a, lse_a, o_b, lse_b, out=None, lse=None, stream=None):
     return out, lse
 
 
-class _On:
-    """Checks the tensors of a call (type, shape, all on the first one's device) and
-    launches with that device current."""
-
-    __slots__ = ("device", "index")
-
-    def __init__(self, first, name):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise LynxError(f"{name} must live on a CUDA device")
-        self.device = first.device
-        self.index = self.device.index
-
-    def need(self, t, dtype, shape, name):
-        """t's address, if it is what it has to be"""
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous():
-            raise LynxError(f"{name} must be a contiguous {dtype} tensor")
-        if t.shape != shape:
-            raise LynxError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-        if t.get_device() != self.index:
-            raise LynxError(f"{name} must live on {self.device}")
-        return t.data_ptr()
-
-    def make(self, t, dtype, shape, name):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        self.need(t, dtype, shape, name)
-        return t
-
-    def call(self, name, stream, *args):
-        fn = getattr(_lib or load(), name)
-        before = _current_device()
-        if before == self.index:
-            status = fn(*args, stream.cuda_stream if stream is not None else _stream(None, self.device))
-        else:
-            with torch.cuda.device(self.index):
-                status = fn(*args, _stream(stream, self.device))
-        if status != 0:
-            _check(status, name)
+_binding = None
 
 
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+def _native():
+    """The native part of the binding, loaded at its first use."""
+    global _binding
+    load()
+    path = os.path.join(_HERE, "_build", "lynx_binding.so")
+    if not os.path.exists(path):
+        raise LynxError(f"{path} is missing: build the CUDA library first "
+                        "(python -m progressive_kv_quantization_gb300.build)")
+    spec = importlib.util.spec_from_file_location("lynx_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.set_error(LynxError)
+    _binding = module
+    return module
 
 
 def lynx_assign_pages(ctx_len, new_len, page_table, free_pages, n_rows: int, cu_new=None, positions=None, slots=None,
@@ -561,25 +539,8 @@ def lynx_assign_pages(ctx_len, new_len, page_table, free_pages, n_rows: int, cu_
     free_pages int32 [n_free]).  Returns (cu_new i32 [B + 1], positions i32
     [n_rows], slots i64 [n_rows, Hkv], ctx_out i32 [B], n_taken i32 [1]); rows of
     requests that did not fit and rows behind the last request hold -1."""
-    on = _On(page_table, "page_table")
-    if page_table.dim() != 3:
-        raise LynxError("page_table must be [B, Hkv, max_pages]")
-    shape = page_table.shape
-    B, Hkv, max_pages = shape
-    if n_rows < 0:
-        raise LynxError("n_rows must not be negative")
-    i32, need = torch.int32, on.need
-    cu_new = on.make(cu_new, i32, (B + 1,), "cu_new")
-    positions = on.make(positions, i32, (n_rows,), "positions")
-    slots = on.make(slots, torch.int64, (n_rows, Hkv), "slots")
-    ctx_out = on.make(ctx_out, i32, (B,), "ctx_out")
-    n_taken = on.make(n_taken, i32, (1,), "n_taken")
-    n_free = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
-    on.call("lynx_assign_pages", stream, need(ctx_len, i32, (B,), "ctx_len"), need(new_len, i32, (B,), "new_len"), B,
-            Hkv, need(page_table, i32, shape, "page_table"), max_pages,
-            need(free_pages, i32, (n_free,), "free_pages"), n_free, n_rows, cu_new.data_ptr(), positions.data_ptr(),
-            slots.data_ptr(), ctx_out.data_ptr(), n_taken.data_ptr())
-    return cu_new, positions, slots, ctx_out, n_taken
+    return (_binding or _native()).assign_pages(ctx_len, new_len, page_table, free_pages, n_rows, cu_new, positions,
+                                                slots, ctx_out, n_taken, stream and stream.cuda_stream)
 
 
 def lynx_qkv_append(qkv, n_q_heads: int, n_kv_heads: int, cos_sin, positions, slots, k_pages, v_pages, q_weight=None,
@@ -590,32 +551,9 @@ def lynx_qkv_append(qkv, n_q_heads: int, n_kv_heads: int, cos_sin, positions, sl
     128] (rows may be strided), the queries to q_out [n_rows, Hq, 128], the keys
     and values to slots int64 [n_rows, Hkv] of the pools k_pages / v_pages bf16
     [n, 128, 256].  Rows with a negative position are skipped.  Returns q_out."""
-    on = _On(qkv, "qkv")
-    Hq, Hkv, need = n_q_heads, n_kv_heads, on.need
-    if qkv.dtype is not torch.bfloat16 or qkv.dim() != 2 or (qkv.shape[1] > 1 and qkv.stride(1) != 1):
-        raise LynxError("qkv must be a bfloat16 tensor [n_rows, channels] with contiguous channels")
-    n_rows, width = qkv.shape
-    if Hq < 1 or Hkv < 1 or width < (Hq + 2 * Hkv) * H:
-        raise LynxError("each row of qkv must hold (n_q_heads + 2 n_kv_heads) * 128 channels")
-    stride = qkv.stride(0) if n_rows > 1 else (Hq + 2 * Hkv) * H
-    max_pos = rot = table = wq = wk = None
-    if cos_sin is not None:
-        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
-            raise LynxError("cos_sin must be a float32 tensor [max_pos, rot_dim]")
-        max_pos, rot = cos_sin.shape
-        table = need(cos_sin, torch.float32, cos_sin.shape, "cos_sin")
-    if q_weight is not None:
-        wq = need(q_weight, torch.float32, (H,), "q_weight")
-    if k_weight is not None:
-        wk = need(k_weight, torch.float32, (H,), "k_weight")
-    n_pool = k_pages.shape[0] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3 else 0
-    q_out = on.make(q_out, torch.bfloat16, (n_rows, Hq, H), "q_out")
-    on.call("lynx_qkv_append", stream, qkv.data_ptr(), n_rows, stride, Hq, Hkv, H, wq, wk, norm_eps, table,
-            max_pos or 0, rot or 0, 1 if interleaved else 0, need(positions, torch.int32, (n_rows,), "positions"),
-            need(slots, torch.int64, (n_rows, Hkv), "slots"), q_out.data_ptr(),
-            need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages"),
-            need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages"), n_pool)
-    return q_out
+    return (_binding or _native()).qkv_append(qkv, n_q_heads, n_kv_heads, cos_sin, positions, slots, k_pages, v_pages,
+                                              q_weight, k_weight, norm_eps, interleaved, q_out,
+                                              stream and stream.cuda_stream)
 
 
 def lynx_chunk_attn_workspace_size(n_rows, B, Hq, Hkv, head_dim) -> int:
@@ -631,36 +569,11 @@ def lynx_chunk_attn_bf16(q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_he
     the chunk's among them).  Returns (out [n_rows, Hq, 128] of out's type or
     out_dtype, bfloat16 or float32; lse f32 [n_rows, Hq]); rows behind the last
     request are left as they are."""
-    on = _On(q, "q")
-    need, i32 = on.need, torch.int32
-    if q.dtype is not torch.bfloat16 or q.dim() != 3 or q.shape[2] != H or q.stride(2) != 1 or (
-            q.shape[1] > 1 and q.stride(1) != H):
-        raise LynxError("q must be a bfloat16 tensor [n_rows, Hq, 128] with contiguous rows")
-    n_rows, Hq, _ = q.shape
-    stride = q.stride(0) if n_rows > 1 else Hq * H
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 3 or page_table.shape[1] != n_kv_heads:
-        raise LynxError("page_table must be [B, Hkv, max_pages]")
-    shape = page_table.shape
-    B, Hkv, max_pages = shape
-    n_pool = k_pages.shape[0] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3 else 0
-    dtype = out.dtype if isinstance(out, torch.Tensor) else out_dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise LynxError("out_dtype must be torch.bfloat16 or torch.float32")
-    out = on.make(out, dtype, (n_rows, Hq, H), "out")
-    lse = on.make(lse, torch.float32, (n_rows, Hq), "lse")
-    if workspace is None:
-        ws_bytes = lynx_chunk_attn_workspace_size(n_rows, B, Hq, Hkv, H)
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=on.device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != on.device or not workspace.is_contiguous():
-        raise LynxError(f"workspace must be a contiguous tensor on {on.device}")
-    on.call("lynx_chunk_attn_bf16", stream, q.data_ptr(), n_rows, stride, need(cu_q, i32, (B + 1,), "cu_q"), B, Hq, Hkv,
-            H, need(k_pages, torch.bfloat16, (n_pool, H, P), "k_pages"),
-            need(v_pages, torch.bfloat16, (n_pool, H, P), "v_pages"), n_pool,
-            need(page_table, i32, shape, "page_table"), max_pages, need(ctx_len, i32, (B,), "ctx_len"),
-            sm_scale if sm_scale is not None else _SCALE, 1 if causal else 0, out.data_ptr(),
-            OUT_BF16 if dtype is torch.bfloat16 else OUT_F32, lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
-    return out, lse
+    return (_binding or _native()).chunk_attn_bf16(q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_heads, sm_scale,
+                                                   causal, out, lse, out_dtype is torch.float32, workspace,
+                                                   stream and stream.cuda_stream)
 
 
 def lynx_verify_drafts(p, q, draft, u, n_draft=None, tokens=None, n_accept=None, stream=None):
@@ -670,27 +583,8 @@ def lynx_verify_drafts(p, q, draft, u, n_draft=None, tokens=None, n_accept=None,
     float32 [B, T + 1], n_draft int32 [B] (None: T each).  Returns (tokens int32
     [B, T + 1]: the accepted drafts, the next token, -1 behind it; n_accept int32
     [B])."""
-    on = _On(p, "p")
-    need, i32, dtype, shape = on.need, torch.int32, p.dtype, p.shape
-    if (dtype is not torch.float32 and dtype is not torch.bfloat16) or len(shape) != 3 or shape[1] < 2 or (
-            shape[2] > 1 and p.stride(2) != 1):
-        raise LynxError("p must be a float32 or bfloat16 tensor [B, T + 1, V] with contiguous rows")
-    B, T, V = shape[0], shape[1] - 1, shape[2]
-    pb, pt, _ = p.stride()
-    q_at, qb, qt = None, 0, V
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dtype is not dtype or q.shape != (B, T, V) or (
-                q.get_device() != on.index) or (V > 1 and q.stride(2) != 1):
-            raise LynxError("q must be a tensor [B, T, V] of p's type with contiguous rows, on p's device")
-        q_at = q.data_ptr()
-        qb, qt = q.stride(0) if B > 1 else 0, q.stride(1) if T > 1 else V
-    tokens = on.make(tokens, i32, (B, T + 1), "tokens")
-    n_accept = on.make(n_accept, i32, (B,), "n_accept")
-    on.call("lynx_verify_drafts", stream, p.data_ptr(), pb if B > 1 else 0, pt, q_at, qb, qt,
-            OUT_F32 if dtype is torch.float32 else OUT_BF16, B, T, V, need(draft, i32, (B, T), "draft"),
-            None if n_draft is None else need(n_draft, i32, (B,), "n_draft"),
-            need(u, torch.float32, (B, T + 1), "u"), tokens.data_ptr(), n_accept.data_ptr())
-    return tokens, n_accept
+    return (_binding or _native()).verify_drafts(p, q, draft, u, n_draft, tokens, n_accept,
+                                                 stream and stream.cuda_stream)
 
 
 def lynx_device_status():
