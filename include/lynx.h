@@ -429,7 +429,7 @@ int lynx_attn_merge(const float* o_a, const float* lse_a, const float* o_b, cons
  * sum, so that the outcome does not depend on what later requests ask for.
  * Rows of refused requests and rows behind the last request get position -1
  * and slot -1, which lynx_qkv_append skips.  Limits: max_pages * 256 < 2^31,
- * n_rows <= 2^30. */
+ * n_rows and n_free <= 2^30. */
 int lynx_assign_pages(const int32_t* ctx_len, const int32_t* new_len, int B, int Hkv, int32_t* page_table,
                       int max_pages, const int32_t* free_pages, int n_free, int n_rows, int32_t* cu_new,
                       int32_t* positions, int64_t* slots, int32_t* ctx_out, int32_t* n_taken, void* stream);

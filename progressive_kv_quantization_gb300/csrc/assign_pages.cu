@@ -27,18 +27,25 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 128;    // rows per CTA
+// Sums stop here: past every number of rows and of free ids (2^30 at most), and
+// two such numbers still add up within 32 bits.  Addition cut off at a bound is
+// associative, so the sums are the same in any order.
+constexpr int kMost = (1 << 30) + 1;
+static_assert(kThreads == 256, "eight steps of bisection");
+
+__device__ __forceinline__ int add(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kMost); }
 
 __global__ void __launch_bounds__(kThreads)
 assign_pages_kernel(const AssignArgs a) {
-  __shared__ long long s_rows[kThreads + 1];   // rows before request i of the group; [n]: behind the last
-  __shared__ long long s_free[kThreads];       // first free-list index of request i
+  __shared__ int s_rows[kThreads];   // rows before request i of the group
+  __shared__ int s_free[kThreads];   // first free-list index of request i
   __shared__ int s_ctx[kThreads];
-  __shared__ int s_held[kThreads];             // pages held; -1: refused
-  __shared__ long long s_warp[2][kThreads / 32];
-  __shared__ long long s_taken;
+  __shared__ int s_held[kThreads];   // pages held; -1: refused
+  __shared__ int2 s_warp[kThreads / 32];
+  __shared__ int s_taken;
   __shared__ int r_pos[kTile];                 // position of the tile's row; -1: none
   __shared__ int r_req[kTile];
-  __shared__ long long r_free[kTile];          // free-list index of the row's page, head 0; -1: in the table
+  __shared__ int r_free[kTile];                // free-list index of the row's page, head 0; -1: in the table
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row0 = blockIdx.x * kTile;
@@ -48,79 +55,82 @@ assign_pages_kernel(const AssignArgs a) {
 
   if (tid < kTile) r_pos[tid] = -1;
   if (tid == 0) s_taken = 0;
-  __syncthreads();
+  allow_dependent_launch();
+  wait_prerequisite_grids();
 
-  long long rows_before = 0, free_before = 0;   // over the groups behind us
+  int rows_before = 0, free_before = 0;   // over the groups behind us
   for (int b0 = 0; b0 < a.B && (first || rows_before < row1); b0 += kThreads) {
-    const int n = min(kThreads, a.B - b0);
     const int b = b0 + tid;
-    int ctx = 0, rows = 0;
-    bool valid = false;
-    if (tid < n) {
-      ctx = a.ctx_len[b];
-      rows = a.new_len[b];
-      valid = ctx >= 0 && rows >= 0 && (long long)ctx + rows <= max_keys;
-      if (!valid && first) atomicExch(a.status, 3);
-      rows = max(rows, 0);
-    }
-    // inclusive sums of the rows, then of the pages of the requests that can be granted
-    auto block_scan = [&](long long v, int which) {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      if (lane == 31) s_warp[which][warp] = v;
-      __syncthreads();
-      long long before = 0;
-      for (int w = 0; w < warp; ++w) before += s_warp[which][w];
-      return v + before;
-    };
-    const long long row_end = rows_before + block_scan(rows, 0);
-    valid = valid && row_end <= a.n_rows;
+    const bool in = b < a.B;
+    const int ctx = in ? a.ctx_len[b] : 0, asked = in ? a.new_len[b] : 0;
+    bool valid = in && ctx >= 0 && asked >= 0 && (long long)ctx + asked <= max_keys;
+    if (in && !valid && first) atomicExch(a.status, 3);
+    const int rows = min(max(asked, 0), kMost);
     const int held = (ctx + kP - 1) / kP;
     const int need = valid ? (ctx + rows + kP - 1) / kP - held : 0;
-    const long long free_end = free_before + block_scan((long long)need * a.Hkv, 1);
-    const bool granted = valid && (need == 0 || free_end <= a.n_free);
-    s_rows[tid] = row_end - rows;
-    if (tid == kThreads - 1) s_rows[kThreads] = row_end;
-    s_free[tid] = free_end - (long long)need * a.Hkv;
-    s_ctx[tid] = ctx;
-    s_held[tid] = granted ? held : -1;
-    if (first) {
-      if (tid < n) {
-        if (b == 0) a.cu_new[0] = 0;
-        a.cu_new[b + 1] = (int)min(row_end, (long long)a.n_rows);
-        a.ctx_out[b] = granted ? ctx + rows : ctx;
-        // the running sum of the granted requests does not decrease
-        if (granted && need > 0) atomicMax(&s_taken, free_end);
+    const int ids = (int)min((long long)need * a.Hkv, (long long)kMost);
+    // Inclusive sums of rows and ids, side by side.  The ids of a request whose
+    // rows do not fit count too: behind it no request with rows fits, so no sum
+    // that matters has them.
+    int row_end = rows, free_end = ids;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, row_end, o), v = __shfl_up_sync(0xffffffffu, free_end, o);
+      if (lane >= o) {
+        row_end = add(row_end, u);
+        free_end = add(free_end, v);
       }
     }
+    if (lane == 31) s_warp[warp] = make_int2(row_end, free_end);
     __syncthreads();
-    rows_before = s_rows[kThreads];
-    if (lane == 31) s_warp[0][warp] = free_end;
-    const long long lo = s_rows[0];
+    int rows_warp = rows_before, free_warp = free_before;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int2 u = s_warp[w];
+      rows_before = add(rows_before, u.x);
+      free_before = add(free_before, u.y);
+      if (w < warp) {
+        rows_warp = add(rows_warp, u.x);
+        free_warp = add(free_warp, u.y);
+      }
+    }
+    row_end = add(row_end, rows_warp);
+    free_end = add(free_end, free_warp);
+    valid = valid && row_end <= a.n_rows;
+    const bool granted = valid && (need == 0 || free_end <= a.n_free);
+    const int row_begin = row_end - rows;   // of no use where the sum has been cut off, and not used
+    s_rows[tid] = row_begin;
+    s_free[tid] = free_end - ids;
+    s_ctx[tid] = ctx;
+    s_held[tid] = granted ? held : -1;
+    if (first && in) {
+      if (b == 0) a.cu_new[0] = 0;
+      a.cu_new[b + 1] = min(row_end, a.n_rows);
+      a.ctx_out[b] = granted ? ctx + rows : ctx;
+      // the running sum of the granted requests does not decrease
+      if (granted && need > 0) atomicMax(&s_taken, free_end);
+    }
+    __syncthreads();
     // the tile's rows that lie in this group
-    if (tid < kTile && row0 + tid < row1 && row0 + tid >= lo && row0 + tid < rows_before) {
-      const int r = row0 + tid;
+    const int lo = s_rows[0], r = row0 + tid;
+    if (tid < kTile && r < row1 && r >= lo && r < rows_before) {
       int i = 0, j = kThreads;   // last request whose rows begin at or before r: those in front of it end there
-      while (j - i > 1) {
+#pragma unroll
+      for (int step = 0; step < 8; ++step) {   // log2 kThreads
         const int mid = (i + j) >> 1;
         if (s_rows[mid] <= r) i = mid; else j = mid;
       }
       if (s_held[i] >= 0) {
-        const int pos = s_ctx[i] + (int)(r - s_rows[i]);
+        const int pos = s_ctx[i] + r - s_rows[i];
         const int page = pos / kP;
         r_pos[tid] = pos;
         r_req[tid] = b0 + i;
-        r_free[tid] = page < s_held[i] ? -1 : s_free[i] + (long long)(page - s_held[i]) * a.Hkv;
+        r_free[tid] = page < s_held[i] ? -1 : s_free[i] + (page - s_held[i]) * a.Hkv;
       }
     }
     __syncthreads();
-    free_before = s_warp[0][kThreads / 32 - 1];
-    __syncthreads();
   }
-  if (first && tid == 0) a.n_taken[0] = (int)s_taken;
+  if (first && tid == 0) a.n_taken[0] = s_taken;
 
   if (tid < row1 - row0) a.positions[row0 + tid] = r_pos[tid];
   const int n_out = (row1 - row0) * a.Hkv;
@@ -131,7 +141,7 @@ assign_pages_kernel(const AssignArgs a) {
     if (pos >= 0) {
       const int page = pos / kP;
       int32_t* entry = a.page_table + ((int64_t)r_req[r] * a.Hkv + h) * a.max_pages + page;
-      const long long f = r_free[r];
+      const int f = r_free[r];
       const int id = f < 0 ? *entry : a.free_pages[f + h];
       if (f >= 0 && pos % kP == 0) *entry = id;
       slot = (int64_t)id * kP + pos % kP;
@@ -144,8 +154,7 @@ assign_pages_kernel(const AssignArgs a) {
 
 cudaError_t launch_assign_pages(const AssignArgs& a, cudaStream_t s) {
   const int grid = a.n_rows > kTile ? (a.n_rows + kTile - 1) / kTile : 1;
-  assign_pages_kernel<<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_programmatic(assign_pages_kernel, dim3(grid), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace lynx

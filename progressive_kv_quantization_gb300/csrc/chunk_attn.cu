@@ -639,7 +639,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         uint8_t* q = smem + kOffQ + g * kQBytes + r * 128;
         uint4 v[16];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = src ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < 16; ++x) v[x] = src ? src[x] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int x = 0; x < 16; ++x) *reinterpret_cast<uint4*>(q + (x >> 3) * kBox + (((x & 7) ^ (r & 7)) << 4)) = v[x];
         fence_proxy_async();

@@ -721,8 +721,8 @@ int lynx_assign_pages(const int32_t* ctx_len, const int32_t* new_len, int B, int
     return fail(LYNX_ERR_INVALID_ARG, "B=%d Hkv=%d max_pages=%d must be >= 1, n_free=%d n_rows=%d >= 0", B, Hkv,
                 max_pages, n_free, n_rows);
   if ((int64_t)max_pages * kP > 0x7fffffff) return fail(LYNX_ERR_UNSUPPORTED, "max_pages too large");
-  if (n_rows > 1 << 30 || (int64_t)Hkv * 128 > 0x7fffffff)
-    return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%d, Hkv=%d too large", n_rows, Hkv);
+  if (n_rows > 1 << 30 || n_free > 1 << 30 || (int64_t)Hkv * 128 > 0x7fffffff)
+    return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%d, n_free=%d or Hkv=%d too large", n_rows, n_free, Hkv);
   if (!ctx_len || !new_len || !page_table || !cu_new || !ctx_out || !n_taken || (n_free > 0 && !free_pages) ||
       (n_rows > 0 && (!positions || !slots)))
     return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");

@@ -6,7 +6,8 @@
 //   y = x rsqrt(mean_c x_c^2 + eps) w            (no norm without a weight)
 //   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin) for the pairs (a, b) of
 //   the first rot channels: (i, i + rot / 2), or (2i, 2i + 1) interleaved
-// All in float32, rounded once to BF16.
+// computed as rsqrt(..) (x_a (w_a cos) - x_b (w_b sin)), the brackets once for a
+// row and all its heads; float32, rounded once to BF16.
 //
 // A half-warp holds one head of one row, 8 channels (16 bytes) a lane; a pair's
 // other half is rot / 16 lanes away (a shuffle) or in the same lane.  A CTA
@@ -30,51 +31,33 @@ constexpr int kTile = 32;                  // rows per CTA
 constexpr int kBatch = 4;                  // query heads of a row read at once
 constexpr int kPitch = kH / 2 + 1;         // words per staged token: the reading lanes (one token each) hit all banks
 
-struct Head {
-  float v[8];
-};
-
-__device__ __forceinline__ Head unpack(const uint4& x) {
-  Head h;
+__device__ __forceinline__ void unpack(const uint4& x, float (&v)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    h.v[2 * i] = __uint_as_float(w[i] << 16);
-    h.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  return h;
-}
-__device__ __forceinline__ uint4 pack(const Head& h) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(h.v[2 * i], h.v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&p);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// the lane's 8 factors of a norm weight; all lanes of a warp call the norm together
-__device__ __forceinline__ void rms_norm(Head& h, const float (&w)[8], float eps) {
-  float ss = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(h.v[i], h.v[i], ss);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float r = rsqrtf(ss * (1.0f / kH) + eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h.v[i] = h.v[i] * r * w[i];
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// cosines and sines of the lane's 8 channels, sines signed: y = y cos + other sin
+// A row's rotation with the norm weight in it, for the lane's 8 channels: with x'
+// the pairs' other halves, y = rsqrt(..) (x c + x' s)
 struct Turn {
   float c[8], s[8];
 };
 
+// `row`: the position's cosines and sines; c0: the lane's first channel; o0: where
+// the other halves of its pairs begin
 template <bool INTERLEAVED>
-__device__ __forceinline__ Turn load_turn(const float* row, int rot, int lane16) {
+__device__ __forceinline__ Turn load_turn(const float* row, int rot, const float* weight, int c0, int o0) {
   Turn t;
-  const int half = rot >> 1, c0 = 8 * lane16;
+  const int half = rot >> 1;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     t.c[i] = 1.0f;
@@ -82,8 +65,8 @@ __device__ __forceinline__ Turn load_turn(const float* row, int rot, int lane16)
   }
   if (c0 < rot) {
     if (INTERLEAVED) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + c0 / 2));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + c0 / 2));
+      const float4 c = *reinterpret_cast<const float4*>(row + c0 / 2);
+      const float4 s = *reinterpret_cast<const float4*>(row + half + c0 / 2);
       const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -93,30 +76,58 @@ __device__ __forceinline__ Turn load_turn(const float* row, int rot, int lane16)
       }
     } else {
       const bool low = c0 < half;
-      const int i0 = low ? c0 : c0 - half;
+      const int i0 = low ? c0 : o0;
+      load8(row + i0, t.c);
+      load8(row + half + i0, t.s);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(row + i0 + 4 * q));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i0 + 4 * q));
-        const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
+      for (int i = 0; i < 8; ++i)
+        if (low) t.s[i] = -t.s[i];
+    }
+  }
+  if (weight) {
+    float w[8], o[8];
+    load8(weight + c0, w);
+    load8(weight + o0, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          t.c[4 * q + i] = cc[i];
-          t.s[4 * q + i] = low ? -sc[i] : sc[i];
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      t.c[i] *= w[i];
+      t.s[i] *= INTERLEAVED ? o[i ^ 1] : o[i];
     }
   }
   return t;
 }
 
+// One head; all lanes of a warp together.  The other halves come from lane
+// `partner` (packed), or are the lane's own.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate(Head& h, const Turn& t, int partner) {
-  Head o;
+__device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, int partner, bool norm, float eps) {
+  float a[8], o[8];
+  unpack(x, a);
+  if (INTERLEAVED) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o.v[i] = INTERLEAVED ? h.v[i ^ 1] : __shfl_sync(0xffffffffu, h.v[i], partner);
+    for (int i = 0; i < 8; ++i) o[i] = a[i ^ 1];
+  } else {
+    unpack(make_uint4(__shfl_sync(0xffffffffu, x.x, partner), __shfl_sync(0xffffffffu, x.y, partner),
+                      __shfl_sync(0xffffffffu, x.z, partner), __shfl_sync(0xffffffffu, x.w, partner)), o);
+  }
+  float r = 1.0f;
+  if (norm) {
+    float ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h.v[i] = fmaf(h.v[i], t.c[i], o.v[i] * t.s[i]);
+    for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss);
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+    r = rsqrtf(ss * (1.0f / kH) + eps);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y0 = fmaf(a[2 * i], t.c[2 * i], o[2 * i] * t.s[2 * i]) * r;
+    const float y1 = fmaf(a[2 * i + 1], t.c[2 * i + 1], o[2 * i + 1] * t.s[2 * i + 1]) * r;
+    const __nv_bfloat162 p = __floats2bfloat162_rn(y0, y1);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <bool INTERLEAVED>
@@ -130,79 +141,102 @@ qkv_append_kernel(const AppendArgs a) {
   const bool is_kv = job >= a.q_jobs;
   const int kv_head = is_kv ? (job - a.q_jobs) / a.kv_parts : 0;
   const int half = a.rot >> 1;
-  // the lane that holds the other halves of this lane's pairs
-  int partner = lane;
-  if (!INTERLEAVED && 8 * lane16 < a.rot) partner = 8 * lane16 < half ? lane + half / 8 : lane - half / 8;
-
+  // the lane that holds the other halves of this lane's pairs, and their channels
+  const int c0 = 8 * lane16;
+  int away = 0;
+  if (!INTERLEAVED && c0 < a.rot) away = c0 < half ? half : -half;
+  const int partner = lane + away / 8, o0 = c0 + away;
+  allow_dependent_launch();
+  wait_prerequisite_grids();
   const float* weight = is_kv ? a.k_weight : a.q_weight;
-  float w[8];
+  auto finish = [&](const uint4& x, const Turn& turn) {
+    return norm_rotate<INTERLEAVED>(x, turn, partner, weight != nullptr, a.norm_eps);
+  };
+  // position of a row that takes part, or -1
+  auto checked = [&](int pos) {
+    if (a.rot > 0 && pos >= a.max_pos) {
+      if (lane16 == 0) atomicExch(a.status, 4);
+      return -1;
+    }
+    return pos;
+  };
+  auto turn_at = [&](int pos) {
+    return load_turn<INTERLEAVED>(a.cos_sin + (int64_t)(pos < 0 ? 0 : pos) * a.rot, a.rot, weight, c0, o0);
+  };
+  // heads are read before their row's position is known (what is skipped is not written)
+  auto head_at = [&](int64_t row, int h) {
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (row < a.n_rows) x = *(reinterpret_cast<const uint4*>(a.qkv + row * a.row_stride + (int64_t)h * kH) + lane16);
+    return x;
+  };
+  constexpr int kSteps = kTile / kHalfWarps;   // rows of a half-warp
+  const int64_t row_hw = row0 + hw;
+  int pos[kSteps];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = weight ? weight[8 * lane16 + i] : 1.0f;
-
-  const int h0 = is_kv ? a.Hq + kv_head : job * a.heads_per_job;
-  const int h1 = is_kv ? h0 + 1 : min(h0 + a.heads_per_job, a.Hq);
-
-  int positions[kTile / kHalfWarps];
-#pragma unroll
-  for (int k = 0; k < kTile / kHalfWarps; ++k) {
-    const int64_t row = row0 + k * kHalfWarps + hw;
-    positions[k] = row < a.n_rows ? __ldg(a.positions + row) : -1;
+  for (int k = 0; k < kSteps; ++k) {
+    const int64_t row = row_hw + k * kHalfWarps;
+    pos[k] = row < a.n_rows ? a.positions[row] : -1;
   }
+
+  if (!is_kv) {
+    // ---- queries, kBatch heads at a time, the next ones on their way
+    const int h0 = job * a.heads_per_job, h1 = min(h0 + a.heads_per_job, a.Hq);
+    uint4 x[kBatch];
 #pragma unroll
-  for (int k = 0; k < kTile / kHalfWarps; ++k) {
-    const int t = k * kHalfWarps + hw;
-    const int64_t row = row0 + t;
-    const int pos = positions[k];
-    const bool far = pos >= a.max_pos && a.rot > 0;
-    if (far && lane16 == 0) atomicExch(a.status, 4);
-    const bool on = pos >= 0 && !far;
-    const Turn turn = load_turn<INTERLEAVED>(a.cos_sin + (int64_t)(on ? pos : 0) * a.rot, a.rot, lane16);
-    const uint4* src = reinterpret_cast<const uint4*>(a.qkv + (on ? row : 0) * a.row_stride) + lane16;
-    if (!is_kv) {
+    for (int i = 0; i < kBatch; ++i)
+      if (h0 + i < h1) x[i] = head_at(row_hw, h0 + i);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int64_t row = row_hw + k * kHalfWarps;
+      const int p = checked(pos[k]);
+      const Turn turn = turn_at(p);
       for (int h = h0; h < h1; h += kBatch) {
-        uint4 x[kBatch];
+        uint4 next[kBatch];
+        const bool last = h + kBatch >= h1;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (on && h + i < h1) x[i] = __ldg(src + (h + i) * (kH / 8));
+          const int hn = last ? h0 + i : h + kBatch + i;
+          if (hn < h1 && (!last || k + 1 < kSteps)) next[i] = head_at(last ? row + kHalfWarps : row, hn);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           if (h + i >= h1) break;
-          Head y = unpack(x[i]);
-          if (weight) rms_norm(y, w, a.norm_eps);
-          if (a.rot > 0) rotate<INTERLEAVED>(y, turn, partner);
-          if (on) *(reinterpret_cast<uint4*>(a.q_out + (row * a.Hq + h + i) * kH) + lane16) = pack(y);
+          const uint4 r = finish(x[i], turn);
+          if (p >= 0) *(reinterpret_cast<uint4*>(a.q_out + (row * a.Hq + h + i) * kH) + lane16) = r;
         }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) x[i] = next[i];
       }
-    } else {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u), v = x;
-      if (on) {
-        x = __ldg(src + h0 * (kH / 8));
-        v = __ldg(src + (h0 + a.Hkv) * (kH / 8));
-      }
-      Head y = unpack(x);
-      if (weight) rms_norm(y, w, a.norm_eps);
-      if (a.rot > 0) rotate<INTERLEAVED>(y, turn, partner);
-      const uint4 r = pack(y);
-      uint32_t* dk = s_kv[0] + t * kPitch + 4 * lane16;
-      uint32_t* dv = s_kv[1] + t * kPitch + 4 * lane16;
-      dk[0] = r.x; dk[1] = r.y; dk[2] = r.z; dk[3] = r.w;
-      dv[0] = v.x; dv[1] = v.y; dv[2] = v.z; dv[3] = v.w;
     }
+    return;
   }
-  if (!is_kv) return;
+
+  // ---- a KV head: keys and values to shared memory, then out by channel
+  uint4 xk[kSteps], xv[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    xk[k] = head_at(row_hw + k * kHalfWarps, a.Hq + kv_head);
+    xv[k] = head_at(row_hw + k * kHalfWarps, a.Hq + a.Hkv + kv_head);
+  }
+  const int64_t slot_row = row0 + lane;
+  const int slot_pos = slot_row < a.n_rows ? a.positions[slot_row] : -1;
+  int64_t slot = slot_row < a.n_rows ? a.slots[slot_row * a.Hkv + kv_head] : -1;
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int t = k * kHalfWarps + hw;
+    const uint4 r = finish(xk[k], turn_at(checked(pos[k])));
+    const uint4 v = xv[k];
+    uint32_t* dk = s_kv[0] + t * kPitch + 4 * lane16;
+    uint32_t* dv = s_kv[1] + t * kPitch + 4 * lane16;
+    dk[0] = r.x; dk[1] = r.y; dk[2] = r.z; dk[3] = r.w;
+    dv[0] = v.x; dv[1] = v.y; dv[2] = v.z; dv[3] = v.w;
+  }
   __syncthreads();
   // one token per lane, a pair of channels at a time
-  const int64_t row = row0 + lane;
-  int64_t slot = -1;
-  if (row < a.n_rows) {
-    const int pos = __ldg(a.positions + row);
-    if (pos >= 0 && (pos < a.max_pos || a.rot == 0)) slot = a.slots[row * a.Hkv + kv_head];
-    if (slot >= a.n_pool * kP) {
-      if (tid < 32) atomicExch(a.status, 5);
-      slot = -1;
-    }
+  if (slot_pos < 0 || (a.rot > 0 && slot_pos >= a.max_pos)) slot = -1;
+  if (slot >= a.n_pool * kP) {
+    if (tid < 32) atomicExch(a.status, 5);
+    slot = -1;
   }
   if (slot >= 0) {
     const int64_t at = (slot / kP) * kPageElems + slot % kP;
@@ -242,11 +276,8 @@ cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s) {
   // against 190.
   a.whole_rows = a.n_rows * (a.Hq + 2 * a.Hkv) * (4 * kH) > ((int64_t)100 << 20);
   const unsigned grid = (unsigned)(tiles * (a.q_jobs + a.Hkv * a.kv_parts));
-  if (a.interleaved)
-    qkv_append_kernel<true><<<grid, kThreads, 0, s>>>(a);
-  else
-    qkv_append_kernel<false><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_programmatic(a.interleaved ? qkv_append_kernel<true> : qkv_append_kernel<false>, dim3(grid),
+                             dim3(kThreads), 0, s, a);
 }
 
 }  // namespace lynx

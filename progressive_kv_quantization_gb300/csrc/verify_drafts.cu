@@ -63,7 +63,7 @@ struct Vec<float> {
   static constexpr int n = 4;
   float v[4];
   __device__ __forceinline__ void load(const float* p) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 x = *reinterpret_cast<const float4*>(p);
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
   }
 };
@@ -72,7 +72,7 @@ struct Vec<__nv_bfloat16> {
   static constexpr int n = 8;
   float v[8];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -104,6 +104,8 @@ verify_drafts_kernel(const VerifyArgs a) {
   const T* q = a.q ? static_cast<const T*>(a.q) + (int64_t)b * a.q_stride_b : nullptr;
   const float* u = a.u + (int64_t)b * (a.T + 1);
   const int32_t* draft = a.draft + (int64_t)b * a.T;
+  allow_dependent_launch();
+  wait_prerequisite_grids();
   // read ahead of their first use: the request's counts and numbers arrive together
   const float u_last = u[a.T];
   const int n_draft = a.n_draft ? min(max(a.n_draft[b], 0), a.T) : a.T;
@@ -277,13 +279,15 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)(((a.V + kRun - 1) / kRun + C - 1) / C) * 8;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T>, a);
 }
 

@@ -24,7 +24,7 @@ def test_assign_pages_argument_checks(lynx_lib, a):
                dict(table=None), dict(free=None), dict(cu=None), dict(pos=None), dict(slots=None), dict(out=None),
                dict(taken=None), dict(out=a)):
         assert call(**kw) == -1, kw
-    assert call(mp=1 << 23) == -2 and call(rows=(1 << 30) + 1) == -2 and call(Hkv=1 << 24) == -2
+    assert call(mp=1 << 23) == -2 and call(rows=(1 << 30) + 1) == -2 and call(nf=(1 << 30) + 1) == -2 and call(Hkv=1 << 24) == -2
     for name in ("ctx", "new", "table", "free", "cu", "pos", "out", "taken"):
         assert call(**{name: ctypes.c_void_p(a.value + 2)}) == -3, name
     assert call(slots=ctypes.c_void_p(a.value + 4)) == -3
