@@ -32,7 +32,9 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRun = 512;                          // values per run, 16 a lane
+constexpr int kRun = 256;                          // values per run, 8 a lane
+constexpr int kStages = 3;                         // runs of a warp in flight or in hand
+constexpr int kStageBytes = kStages * 4 * kThreads * 16;   // two pieces of each row a thread
 
 __device__ __forceinline__ float prob(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float prob(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
@@ -55,32 +57,18 @@ struct Units {
   __device__ __forceinline__ unsigned long long value() const { return ((unsigned long long)hi << 20) + lo; }
 };
 
-// 16 bytes of a row as floats
+// value e of 16 bytes of a row
 template <typename T>
-struct Vec;
-template <>
-struct Vec<float> {
-  static constexpr int n = 4;
-  float v[4];
-  __device__ __forceinline__ void load(const float* p) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-  }
-};
-template <>
-struct Vec<__nv_bfloat16> {
-  static constexpr int n = 8;
-  float v[8];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-};
+__device__ __forceinline__ float value(const uint4& x, int e) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if (sizeof(T) == 4) return __uint_as_float(w[e]);
+  return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+}
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -91,7 +79,10 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
 verify_drafts_kernel(const VerifyArgs a) {
-  extern __shared__ unsigned long long s_run[];    // sums of this CTA's runs
+  constexpr int kVec = 16 / sizeof(T), kLoads = kRun / 32 / kVec;
+  extern __shared__ __align__(16) uint8_t s_dyn[];
+  uint4* s_stage = reinterpret_cast<uint4*>(s_dyn);                                          // [stage][piece][thread]
+  unsigned long long* s_run = reinterpret_cast<unsigned long long*>(s_dyn + kStageBytes);    // sums of this CTA's runs
   __shared__ unsigned s_ok[2];
   __shared__ unsigned long long s_part[kWarps];
   __shared__ unsigned long long s_sum;             // of this CTA's part, read by the whole cluster
@@ -128,7 +119,8 @@ verify_drafts_kernel(const VerifyArgs a) {
   const T* row = p + n * a.p_stride_t;
   const T* drafted = rejected && q ? q + n * a.q_stride_t : nullptr;
   // without draft probabilities a rejected draft had all of its row's
-  const int out = rejected && !q ? draft[n] : -1;
+  const int drafted_id = rejected && !q ? draft[n] : -1;
+  const int out = drafted_id < a.V ? drafted_id : -1;
 
   // this CTA's runs
   const int n_runs = (a.V + kRun - 1) / kRun;
@@ -144,39 +136,63 @@ verify_drafts_kernel(const VerifyArgs a) {
     }
     return w;
   };
-  // both rows on 16-byte boundaries: whole runs are read 16 bytes a lane
+  // both rows on 16-byte boundaries
   const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0 &&
                     (!drafted || (reinterpret_cast<uintptr_t>(drafted) & 15) == 0);
   for (int attempt = 0; attempt < 2; ++attempt) {
     unsigned long long mine = 0;
-    for (int r = r0 + warp; r < r1; r += kWarps) {
-      const int64_t i0 = (int64_t)r * kRun;
+    const bool minus = residual && drafted;
+    // A thread's 16-byte pieces of the next kStages - 1 runs of its warp are on
+    // their way to its own places in shared memory while it sums this run's.
+    const int n_mine = r1 - r0 > warp ? (r1 - r0 - warp + kWarps - 1) / kWarps : 0;
+    auto staged = [&](int r) { return wide && (int64_t)(r + 1) * kRun <= a.V; };
+    auto fetch = [&](int k) {
+      const int r = r0 + warp + k * kWarps;
+      if (k < n_mine && staged(r)) {
+        uint4* dst = s_stage + (k % kStages) * 4 * kThreads + tid;
+        const int64_t i0 = (int64_t)r * kRun + lane * kVec;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+          copy_async16(dst + x * kThreads, row + i0 + x * 32 * kVec);
+          if (minus) copy_async16(dst + (2 + x) * kThreads, drafted + i0 + x * 32 * kVec);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(k);
+    for (int k = 0; k < n_mine; ++k) {
+      fetch(k + kStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      const int r = r0 + warp + k * kWarps;
       Units sum;
-      if (wide && i0 + kRun <= a.V) {
-        constexpr int kVec = Vec<T>::n, kLoads = kRun / 32 / kVec;
-        Vec<T> x[kLoads], y[kLoads];
-        const bool minus = residual && drafted;
+      if (staged(r)) {
+        const uint4* src = s_stage + (k % kStages) * 4 * kThreads + tid;
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k) x[k].load(row + i0 + (k * 32 + lane) * kVec);
-        if (minus) {
+        for (int x = 0; x < kLoads; ++x) {
+          const uint4 px = src[x * kThreads];
+          uint4 qx = make_uint4(0u, 0u, 0u, 0u);
+          if (minus) qx = src[(2 + x) * kThreads];
 #pragma unroll
-          for (int k = 0; k < kLoads; ++k) y[k].load(drafted + i0 + (k * 32 + lane) * kVec);
+          for (int e = 0; e < kVec; ++e) sum.add(__fsub_rn(value<T>(px, e), value<T>(qx, e)));   // w - 0 is w
+        }
+      } else {
+        const int64_t i0 = (int64_t)r * kRun + lane;
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = i0 + 32 * e < a.V ? prob(row, i0 + 32 * e) : 0.0f;
+          y[e] = minus && i0 + 32 * e < a.V ? prob(drafted, i0 + 32 * e) : 0.0f;
         }
 #pragma unroll
-        for (int k = 0; k < kLoads; ++k)
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            float w = x[k].v[e];
-            if (minus) w = __fsub_rn(w, y[k].v[e]);
-            if (residual && i0 + (k * 32 + lane) * kVec + e == out) w = 0.0f;
-            sum.add(w);
-          }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kRun / 32; ++k)
-          if (i0 + 32 * k + lane < a.V) sum.add(weight(i0 + 32 * k + lane));
+        for (int e = 0; e < 8; ++e) sum.add(__fsub_rn(x[e], y[e]));
       }
-      const unsigned long long v = warp_sum(sum.value());
+      unsigned long long v = warp_sum(sum.value());
+      if (residual && out >= 0 && out / kRun == r) {   // the certain draft's own weight
+        Units own;
+        own.add(prob(row, out));
+        v -= own.value();
+      }
       if (lane == 0) s_run[r - r0] = v;
       mine += v;
     }
@@ -235,7 +251,7 @@ verify_drafts_kernel(const VerifyArgs a) {
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
     }
-    // 16 values a lane, one behind the other: the lane, then its value
+    // 8 values a lane, one behind the other: the lane, then its value
     constexpr int kOwn = kRun / 32;
     const int64_t i0 = (int64_t)found * kRun + lane * kOwn;
     float w[kOwn];
@@ -277,7 +293,16 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.B * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)(((a.V + kRun - 1) / kRun + C - 1) / C) * 8;
+  cfg.dynamicSmemBytes = kStageBytes + (size_t)(((a.V + kRun - 1) / kRun + C - 1) / C) * 8;
+  static bool configured[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(verify_drafts_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kStageBytes + kVerifyMaxVocab / kRun * 8);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
