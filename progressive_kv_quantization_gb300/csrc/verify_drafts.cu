@@ -42,19 +42,44 @@ __device__ __forceinline__ float prob(const __nv_bfloat16* p, int64_t i) { retur
 // Sums of weights in whole multiples of 2^-40 (NaN and negative weights 0, at
 // most 1 each).  A weight's two 20-bit halves come from float additions rounded
 // down onto numbers whose last place is 2^-20 and 2^-40: the bits that the sum
-// holds above those of 8 and 2^-17 are the whole multiples.  (The conversion
-// float -> uint64 is far slower: 39.5 us for 32 rows of 151,936 with it.)  Up to
-// 2^11 weights fit the 32-bit sums.
+// holds above those of 8 and 2^-17 are the whole multiples.  Two weights at a
+// time, four instructions each; the conversion float -> uint64 took 39.5 us for
+// 32 rows of 151,936.  A run's halves fit 32 bits over a whole warp.
 struct Units {
   uint32_t hi = 0, lo = 0;
-  __device__ __forceinline__ void add(float w) {
-    w = __saturatef(w);
-    const float h = __fadd_rd(w, 8.0f);
-    const float rest = w - (h - 8.0f);                    // exact, below 2^-20
-    hi += __float_as_uint(h) - 0x41000000u;               // bits of 8
-    lo += __float_as_uint(__fadd_rd(rest, 0x1p-17f)) - 0x37000000u;   // bits of 2^-17
+  // max(0, p - q), at most 1, 0 for NaN
+  static __device__ __forceinline__ float weight(float p, float q) {
+    float w;
+    asm("sub.rn.sat.f32 %0, %1, %2;" : "=f"(w) : "f"(p), "f"(q));
+    return w;
   }
-  __device__ __forceinline__ unsigned long long value() const { return ((unsigned long long)hi << 20) + lo; }
+  static __device__ __forceinline__ uint64_t both(float v) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(v));
+    return d;
+  }
+  __device__ __forceinline__ void add2(float w0, float w1) {
+    uint64_t w, h, t, rest, l;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(w0), "f"(w1));
+    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(h) : "l"(w), "l"(both(8.0f)));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(h), "l"(both(-8.0f)));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rest) : "l"(t), "l"(both(-1.0f)), "l"(w));   // exact, below 2^-20
+    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(l) : "l"(rest), "l"(both(0x1p-17f)));
+    hi += (uint32_t)h + (uint32_t)(h >> 32) - 2u * 0x41000000u;   // bits of 8
+    lo += (uint32_t)l + (uint32_t)(l >> 32) - 2u * 0x37000000u;   // bits of 2^-17
+  }
+  static __device__ __forceinline__ unsigned long long join(uint32_t hi, uint32_t lo) {
+    return ((unsigned long long)hi << 20) + lo;
+  }
+  __device__ __forceinline__ unsigned long long value() const { return join(hi, lo); }
+  __device__ __forceinline__ unsigned long long over_warp() const {
+    return join(__reduce_add_sync(0xffffffffu, hi), __reduce_add_sync(0xffffffffu, lo));
+  }
+  static __device__ __forceinline__ unsigned long long of(float w) {
+    Units u;
+    u.add2(w, 0.0f);
+    return u.value();
+  }
 };
 
 // value e of 16 bytes of a row
@@ -129,12 +154,8 @@ verify_drafts_kernel(const VerifyArgs a) {
   bool residual = true;
   unsigned long long total = 0, before = 0;
   auto weight = [&](int64_t i) {
-    float w = prob(row, i);
-    if (residual) {
-      if (drafted) w = __fsub_rn(w, prob(drafted, i));
-      if (i == out) w = 0.0f;
-    }
-    return w;
+    const float w = Units::weight(prob(row, i), residual && drafted ? prob(drafted, i) : 0.0f);
+    return residual && i == out ? 0.0f : w;
   };
   // both rows on 16-byte boundaries
   const bool wide = (reinterpret_cast<uintptr_t>(row) & 15) == 0 &&
@@ -174,7 +195,8 @@ verify_drafts_kernel(const VerifyArgs a) {
           uint4 qx = make_uint4(0u, 0u, 0u, 0u);
           if (minus) qx = src[(2 + x) * kThreads];
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) sum.add(__fsub_rn(value<T>(px, e), value<T>(qx, e)));   // w - 0 is w
+          for (int e = 0; e < kVec; e += 2)   // w - 0 is w
+            sum.add2(Units::weight(value<T>(px, e), value<T>(qx, e)), Units::weight(value<T>(px, e + 1), value<T>(qx, e + 1)));
         }
       } else {
         const int64_t i0 = (int64_t)r * kRun + lane;
@@ -185,14 +207,10 @@ verify_drafts_kernel(const VerifyArgs a) {
           y[e] = minus && i0 + 32 * e < a.V ? prob(drafted, i0 + 32 * e) : 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum.add(__fsub_rn(x[e], y[e]));
+        for (int e = 0; e < 8; e += 2) sum.add2(Units::weight(x[e], y[e]), Units::weight(x[e + 1], y[e + 1]));
       }
-      unsigned long long v = warp_sum(sum.value());
-      if (residual && out >= 0 && out / kRun == r) {   // the certain draft's own weight
-        Units own;
-        own.add(prob(row, out));
-        v -= own.value();
-      }
+      unsigned long long v = sum.over_warp();
+      if (residual && out >= 0 && out / kRun == r) v -= Units::of(Units::weight(prob(row, out), 0.0f));   // the certain draft's
       if (lane == 0) s_run[r - r0] = v;
       mine += v;
     }
@@ -216,10 +234,10 @@ verify_drafts_kernel(const VerifyArgs a) {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   int32_t* tokens = a.tokens + (int64_t)b * (a.T + 1);
-  if (rank == 0) {
-    for (int i = tid; i <= a.T; i += kThreads)
+  if (rank == 0 && warp == 1) {   // the first warp looks for the token meanwhile
+    for (int i = lane; i <= a.T; i += 32)
       if (i != n) tokens[i] = i < n ? draft[i] : -1;
-    if (tid == 0) {
+    if (lane == 0) {
       a.n_accept[b] = n;
       if (total == 0) tokens[n] = -1;
     }
@@ -259,7 +277,7 @@ verify_drafts_kernel(const VerifyArgs a) {
     for (int k = 0; k < kOwn; ++k) w[k] = i0 + k < a.V ? weight(i0 + k) : 0.0f;
     Units own;
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) own.add(w[k]);
+    for (int k = 0; k < kOwn; k += 2) own.add2(w[k], w[k + 1]);
     unsigned long long incl = own.value();
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -272,9 +290,7 @@ verify_drafts_kernel(const VerifyArgs a) {
       int k = 0;
 #pragma unroll
       for (int e = 0; e < kOwn; ++e) {
-        Units one;
-        one.add(w[e]);
-        at += one.value();
+        at += Units::of(w[e]);
         k += at <= limit;
       }
       tokens[n] = (int32_t)(i0 + k);
