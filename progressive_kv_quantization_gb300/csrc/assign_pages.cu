@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 128;    // rows per CTA
+constexpr int kBatch = 4;
 // Sums stop here: past every number of rows and of free ids (2^30 at most), and
 // two such numbers still add up within 32 bits.  Addition cut off at a bound is
 // associative, so the sums are the same in any order.
@@ -133,20 +134,40 @@ assign_pages_kernel(const AssignArgs a) {
   if (first && tid == 0) a.n_taken[0] = s_taken;
 
   if (tid < row1 - row0) a.positions[row0 + tid] = r_pos[tid];
+  // slots, kBatch a thread at a time, so that their table entries are read together
   const int n_out = (row1 - row0) * a.Hkv;
-  for (int i = tid; i < n_out; i += kThreads) {
-    const int r = i / a.Hkv, h = i - r * a.Hkv;
-    const int pos = r_pos[r];
-    int64_t slot = -1;
-    if (pos >= 0) {
-      const int page = pos / kP;
-      int32_t* entry = a.page_table + ((int64_t)r_req[r] * a.Hkv + h) * a.max_pages + page;
-      const int f = r_free[r];
-      const int id = f < 0 ? *entry : a.free_pages[f + h];
-      if (f >= 0 && pos % kP == 0) *entry = id;
-      slot = (int64_t)id * kP + pos % kP;
+  const int dr = kThreads / a.Hkv, dh = kThreads - dr * a.Hkv;
+  int r = tid / a.Hkv, h = tid - r * a.Hkv;
+  for (int i0 = tid; i0 < n_out; i0 += kBatch * kThreads) {
+    int id[kBatch], pos[kBatch];
+    int32_t* fresh[kBatch];   // the entry of a page that begins here
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      pos[k] = -1;
+      id[k] = 0;
+      fresh[k] = nullptr;
+      if (i0 + k * kThreads < n_out) {
+        pos[k] = r_pos[r];
+        if (pos[k] >= 0) {
+          int32_t* entry = a.page_table + ((int64_t)r_req[r] * a.Hkv + h) * a.max_pages + pos[k] / kP;
+          const int f = r_free[r];
+          id[k] = f < 0 ? *entry : a.free_pages[f + h];
+          if (f >= 0 && pos[k] % kP == 0) fresh[k] = entry;
+        }
+      }
+      r += dr;
+      h += dh;
+      if (h >= a.Hkv) {
+        h -= a.Hkv;
+        ++r;
+      }
     }
-    a.slots[(int64_t)row0 * a.Hkv + i] = slot;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k * kThreads >= n_out) break;
+      if (fresh[k]) *fresh[k] = id[k];
+      a.slots[(int64_t)row0 * a.Hkv + i0 + k * kThreads] = pos[k] >= 0 ? (int64_t)id[k] * kP + pos[k] % kP : -1;
+    }
   }
 }
 

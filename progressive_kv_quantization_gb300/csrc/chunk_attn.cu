@@ -33,6 +33,12 @@
 // joins them; so a long chunk, a ragged batch and a single token over a long
 // context all fill the machine, and the result does not depend on timing.
 //
+// A list is gone through from its end.  Where a CTA's part is the end of one tile
+// and the beginning of the next, the CTAs of a head then all begin at key 0 and,
+// behind their second tile's part, all go on at the same distance from it: the
+// keys and values of a context that L2 does not hold are read from memory twice,
+// not once a tile (128 tiles over 131,072 keys: 6.4 GB in the other order).
+//
 // Keys past ctx_len in the last page take no part: their scores are replaced, and
 // their V rows are zeroed in shared memory (0 x NaN would be NaN).
 
@@ -362,6 +368,7 @@ __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, vola
           s_hdr->rows = it.rows;
         }
       }
+      __syncwarp();   // the lanes' loops end at different times
       // the lane that ran out of room knows where the next list begins
       const unsigned cutter = __ballot_sync(0xffffffffu, stop != next);
       if (cutter) next = __shfl_sync(0xffffffffu, stop, __ffs(cutter) - 1);
@@ -464,7 +471,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       if (warp == kTmaWarp) {
         // ================= producer: K and V tiles in the order of use
         if (lane == 0) {
-          for (int i = 0; i < n_items && !failed; ++i) {
+          for (int i = n_items - 1; i >= 0 && !failed; --i) {
             const Item it = items[i];
             if (it.kind == kNothing || it.k0 == it.k1) continue;
             const int32_t* row = a.page_table + ((int64_t)it.b * a.Hkv + it.h) * a.max_pages;
@@ -511,7 +518,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         const uint32_t t_s = uni(tmem) + g * 128, t_o = uni(tmem) + 256 + g * 128;
         const uint64_t q_desc = desc_k(uni(base) + kOffQ + g * kQBytes);
         const uint64_t k_desc = desc_mn(uni(base) + kOffRing), v_desc = desc_k(uni(base) + kOffRing);
-        for (int i = 0; i < n_items && !failed; ++i) {
+        for (int i = n_items - 1; i >= 0 && !failed; --i) {
           const int n = uni(items[i].k1 - items[i].k0);
           const bool both = uni(items[i].rows) > kGroupRows;
           const int keys = uni(items[i].ctx - items[i].k0 * kTileKeys);   // from the first tile on
@@ -620,8 +627,8 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       const int r = (warp & 3) * 32 + lane;               // row of the group, tensor-memory lane
       const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
-      auto next_active = [&](int i) {   // the next item that this group has rows of
-        while (i < n_items && (items[i].kind == kNothing || items[i].rows <= g * kGroupRows)) ++i;
+      auto next_active = [&](int i) {   // the next item that this group has rows of, -1 behind the last
+        while (i >= 0 && (items[i].kind == kNothing || items[i].rows <= g * kGroupRows)) --i;
         return i;
       };
       // this thread's row of an item's queries, as 16-byte pieces
@@ -645,12 +652,12 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         fence_proxy_async();
         mbar_arrive(q_full(g));
       };
-      int i = next_active(0);
-      if (i < n_items) load_queries(items[i]);
-      while (i < n_items && !failed) {
+      int i = next_active(n_items - 1);
+      if (i >= 0) load_queries(items[i]);
+      while (i >= 0 && !failed) {
         const Item& it = items[i];
-        i = next_active(i + 1);
-        if (i < n_items) {   // on their way to L2 meanwhile
+        i = next_active(i - 1);
+        if (i >= 0) {   // on their way to L2 meanwhile
           const uint4* src = query_row(items[i]);
           if (src) asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(src));
         }
@@ -739,12 +746,12 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           }
           if (failed) break;
           // the next item's first product runs while this one's output is written
-          if (i < n_items) load_queries(items[i]);
+          if (i >= 0) load_queries(items[i]);
           if (!mbar_wait(o_done(g), (n_tile_g - 1) & 1, wait_ns)) failed = true;
           failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
           tc_fence_after();
-        } else if (i < n_items) {
+        } else if (i >= 0) {
           load_queries(items[i]);
         }
         // ---- the row's output, or its part
