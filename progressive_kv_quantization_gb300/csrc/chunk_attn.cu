@@ -64,6 +64,7 @@ constexpr int kRegsSoftmax = 208, kRegsOther = 80;   // of 168 each at launch: 2
 constexpr int kMaxItems = 24;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
 constexpr float kLazyLog2 = 8.0f;
+constexpr int kBusyPolls = 4096;               // some 100 us
 constexpr int kMinKeysLog2 = 8;                // least cost of a CTA's part of the work, in keys
 
 constexpr int kOffQ = 0;
@@ -73,7 +74,7 @@ constexpr int kNumBars = 2 * kSlots + 9;
 constexpr int kOffItems = kOffBar + 8 * kNumBars;
 constexpr int kItemInts = 10;
 constexpr int kOffMisc = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
-constexpr int kSmem = kOffMisc + 80;   // number of items, header (32, at 16), tensor memory, abort flag (at 64)
+constexpr int kSmem = kOffMisc + 80;   // number of items, header (32, at 16), tensor memory, abort flag (at 64), busy flags
 constexpr int kSmemAlloc = kSmem + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
 
@@ -155,6 +156,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* v) {
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
       "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::LYNX_I8(v, 0),
       LYNX_I8(v, 8), LYNX_I8(v, 16), LYNX_I8(v, 24), "r"(addr)
+      : "memory");
+}
+// 16 columns, waited for
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : LYNX_R8(v, 0), LYNX_R8(v, 8)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::LYNX_I8(v, 0),
+      LYNX_I8(v, 8), "r"(addr)
       : "memory");
 }
 // the loaded registers hold their values only behind the wait: pass them through it
@@ -401,6 +418,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   volatile int* s_n_items = reinterpret_cast<volatile int*>(smem + kOffMisc);
   Header* s_hdr = reinterpret_cast<Header*>(smem + kOffMisc + 16);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc + 64);
+  volatile int* s_busy = reinterpret_cast<volatile int*>(smem + kOffMisc + 72);   // a group's products are being issued
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 68);
 
   const uint32_t bar0 = base + kOffBar;
@@ -427,6 +445,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     mbar_init(drained, 2);
     *s_hdr = Header{0, 0, 0, 0, 0, 0, 0, 0};
     *s_abort = 0;
+    s_busy[0] = s_busy[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -593,6 +612,14 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             if (j + 1 < n && !wait(kv_full(sk), (uk / kSlots) & 1)) break;
             if (!wait(p_full(g), mma_tiles & 1)) break;
             ++mma_tiles;
+            // One group's block of products (this P V, the next Q K) at a time: mixed, both
+            // blocks end late, the groups' softmaxes fall together and stay so, 1.8 us a tile
+            // of keys against 1.3.  (A matter of speed alone: the flags are plain, and
+            // nobody waits for long.)
+            if (both) {
+              for (int x = 0; x < kBusyPolls && s_busy[1 - g] != 0; ++x) {}
+              if (lane == 0) s_busy[g] = 1;
+            }
             tc_fence_after();
             if (elected()) {
               const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
@@ -612,6 +639,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               }
             }
             __syncwarp();
+            if (both && lane == 0) s_busy[g] = 0;
           }
         }
         if (failed && lane == 0) give_up();
@@ -689,6 +717,31 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               for (int x = 0; x < 128; ++x)
                 if (x >= left) s[x] = 0xFF800000u;   // -inf
             }
+            // P against the running maximum as it stands, and the tile's maximum beside
+            // it: the two do not wait for one another (1.36 us a tile of keys against 1.5 one
+            // after the other).  Where the maximum has to move P is computed again.
+            const uint64_t sc2 = pair(__float_as_uint(sc), __float_as_uint(sc));
+            uint64_t sum[4];
+            auto exps = [&](float ref) {
+              const uint64_t ref2 = pair(__float_as_uint(ref), __float_as_uint(ref));
+#pragma unroll
+              for (int x = 0; x < 4; ++x) sum[x] = 0ull;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  float p0, p1;
+                  unpair(fma2(pair(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), sc2, ref2), p0, p1);
+                  p0 = ex2(p0);
+                  p1 = ex2(p1);
+                  sum[e & 3] = add2(sum[e & 3], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                  p[e] = bf16x2(p0, p1);
+                }
+                tmem_st16(t_s + 16 * x, p);
+              }
+            };
+            exps(m == -CUDART_INF_F ? 0.0f : -m);
             float mx[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) mx[x] = fmaxf(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
@@ -699,42 +752,20 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
               const float m_new = fmaxf(m, top);
               const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - m_new);
-              if (j > 0) {   // rescale O, once the product before has been added to it
-                if (!mbar_wait(o_done(g), (n_tile_g - 1) & 1, wait_ns)) failed = true;
-                failed = __any_sync(0xffffffffu, failed);
-                if (failed) break;
-                tc_fence_after();
+              if (j > 0) {   // rescale O, to which the product before has been added (its commit came first)
                 const float fo = m == -CUDART_INF_F ? 1.0f : f;   // O is 0 there
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  uint32_t o[32];
-                  tmem_ld32(t_o + 32 * x, o);
-                  tmem_wait_ld32(o);
+                for (int x = 0; x < 8; ++x) {
+                  uint32_t o[16];
+                  tmem_ld16(t_o + 16 * x, o);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
-                  tmem_st32(t_o + 32 * x, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+                  tmem_st16(t_o + 16 * x, o);
                 }
               }
               l *= f;
               m = m_new;
-            }
-            const float ref = m == -CUDART_INF_F ? 0.0f : -m;
-            const uint64_t sc2 = pair(__float_as_uint(sc), __float_as_uint(sc));
-            const uint64_t ref2 = pair(__float_as_uint(ref), __float_as_uint(ref));
-            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t p[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float p0, p1;
-                unpair(fma2(pair(s[64 * x + 2 * e], s[64 * x + 2 * e + 1]), sc2, ref2), p0, p1);
-                p0 = ex2(p0);
-                p1 = ex2(p1);
-                sum[e & 3] = add2(sum[e & 3], pair(__float_as_uint(p0), __float_as_uint(p1)));
-                p[e] = bf16x2(p0, p1);
-              }
-              tmem_st32(t_s + 32 * x, p);
+              exps(m == -CUDART_INF_F ? 0.0f : -m);
             }
             float l0, l1;
             unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
