@@ -861,73 +861,77 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 constexpr int kJoinThreads = 256;
 
 // CTA (c, y) joins rows 32 y .. of the tile that CTA c of the kernel above began
-// and did not end; a row a lane, 16 channels a warp.  With m* the largest of the
-// parts' m: O = sum 2^(m_i - m*) O_i / sum 2^(m_i - m*) l_i.
+// and did not end; a row a lane, 16 channels a warp, two parts at a time:
+// with m the running maximum, O = sum 2^(m_i - m) O_i, l = sum 2^(m_i - m) l_i.
 __global__ void __launch_bounds__(kJoinThreads)
 chunk_combine_kernel(const ChunkArgs a) {
-  __shared__ int s_slot[2 * kMaxCtas];
-  __shared__ int s_n;
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_prerequisite_grids();
   const Header* hdr = reinterpret_cast<const Header*>(a.ws_hdr);
   const Header hd = hdr[c];
+  // the CTAs behind, up to the one where the tile ends, 32 at a time
+  int state = 0, ends = 0;
+  auto read_window = [&](int d0) {
+    const int d = d0 + lane;
+    state = d < a.n_cta ? hdr[d].a_state : 0;
+    ends = d < a.n_cta ? hdr[d].a_ends : 1;
+  };
+  read_window(c + 1);
   if (!hd.b_open || hd.b_state == 2 || (int)blockIdx.y * 32 >= hd.rows) return;
-  if (warp == 0) {
-    int n = 0;
-    if (hd.b_state == 1) {
-      if (lane == 0) s_slot[0] = 2 * c + 1;
-      n = 1;
-    }
-    // the CTAs behind, up to the one where the tile ends
-    for (int d0 = c + 1; d0 < a.n_cta; d0 += 32) {
-      const int d = d0 + lane;
-      int state = 0, ends = 0;
-      if (d < a.n_cta) {
-        state = hdr[d].a_state;
-        ends = hdr[d].a_ends;
-      }
-      const unsigned e = __ballot_sync(0xffffffffu, ends != 0);
-      const unsigned within = e ? (e & -e) | ((e & -e) - 1) : 0xffffffffu;
-      const unsigned valid = __ballot_sync(0xffffffffu, state == 1) & within;
-      if (__ballot_sync(0xffffffffu, state == 2) & within) {   // one CTA had it all and wrote it out
-        n = 0;
-        break;
-      }
-      if (valid >> lane & 1) s_slot[n + __popc(valid & ((1u << lane) - 1))] = 2 * d;
-      n += __popc(valid);
-      if (e) break;
-    }
-    if (lane == 0) s_n = n;
-  }
-  __syncthreads();
-  const int n = s_n, r = blockIdx.y * 32 + lane;
-  if (n == 0 || r >= hd.rows) return;
+  const int r = blockIdx.y * 32 + lane;
+  const bool on = r < hd.rows;
   const int64_t stride = (int64_t)a.slot_rows * (kH + 2);
-  const float* ml = a.ws_o + (int64_t)a.slot_rows * kH + 2 * r;
-  const float* po = a.ws_o + (int64_t)(4 * warp * a.slot_rows + r) * 4;
-  float m = -CUDART_INF_F;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) m = fmaxf(m, ml[s_slot[i] * stride]);
-  float acc[16], l = 0.0f;
+  const float* ml = a.ws_o + (int64_t)a.slot_rows * kH + 2 * (on ? r : 0);
+  const float* po = a.ws_o + (int64_t)(4 * warp * a.slot_rows + (on ? r : 0)) * 4;
+  float acc[16], l = 0.0f, m = -CUDART_INF_F;
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-#pragma unroll 2
-  for (int i = 0; i < n; ++i) {
-    const int64_t at = s_slot[i] * stride;
-    const float2 st = *reinterpret_cast<const float2*>(ml + at);
-    float4 o[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] = *reinterpret_cast<const float4*>(po + at + (int64_t)x * a.slot_rows * 4);
-    const float f = st.x == -CUDART_INF_F ? (st.y == st.y ? 0.0f : 1.0f) : ex2(st.x - m);   // a NaN sum stays
-    l = fmaf(f, st.y, l);
+  bool any = false;
+  auto join = [&](int s0, int s1) {   // s1 < 0: one part
+    const int64_t at0 = s0 * stride, at1 = (s1 < 0 ? s0 : s1) * stride;
+    const float2 t0 = *reinterpret_cast<const float2*>(ml + at0), t1 = *reinterpret_cast<const float2*>(ml + at1);
+    float4 o0[4], o1[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      acc[4 * x] = fmaf(f, o[x].x, acc[4 * x]);
-      acc[4 * x + 1] = fmaf(f, o[x].y, acc[4 * x + 1]);
-      acc[4 * x + 2] = fmaf(f, o[x].z, acc[4 * x + 2]);
-      acc[4 * x + 3] = fmaf(f, o[x].w, acc[4 * x + 3]);
+      o0[x] = *reinterpret_cast<const float4*>(po + at0 + (int64_t)x * a.slot_rows * 4);
+      o1[x] = *reinterpret_cast<const float4*>(po + at1 + (int64_t)x * a.slot_rows * 4);
     }
+    const float m_new = max3(m, t0.x, t1.x);
+    // a part without keys weighs nothing, one whose sum is NaN stays NaN
+    auto factor = [&](float mi, float li) { return mi == -CUDART_INF_F ? (li == li ? 0.0f : 1.0f) : ex2(mi - m_new); };
+    const float f = any ? factor(m, l) : 0.0f, f0 = factor(t0.x, t0.y), f1 = s1 < 0 ? 0.0f : factor(t1.x, t1.y);
+    l = fmaf(l, f, fmaf(t0.y, f0, s1 < 0 ? 0.0f : t1.y * f1));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float u0[4] = {o0[x].x, o0[x].y, o0[x].z, o0[x].w}, u1[4] = {o1[x].x, o1[x].y, o1[x].z, o1[x].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        acc[4 * x + e] = fmaf(acc[4 * x + e], f, fmaf(u0[e], f0, s1 < 0 ? 0.0f : u1[e] * f1));
+    }
+    m = m_new;
+    any = true;
+  };
+  int waiting = hd.b_state == 1 ? 2 * c + 1 : -1;   // a part without a second one yet
+  for (int d0 = c + 1; d0 < a.n_cta; d0 += 32) {
+    if (d0 > c + 1) read_window(d0);
+    const unsigned e = __ballot_sync(0xffffffffu, ends != 0);
+    const unsigned within = e ? (e & -e) | ((e & -e) - 1) : 0xffffffffu;
+    if (__ballot_sync(0xffffffffu, state == 2) & within) return;   // one CTA had it all and wrote it out
+    unsigned valid = __ballot_sync(0xffffffffu, state == 1) & within;
+    while (valid) {
+      const int s = 2 * (d0 + __ffs(valid) - 1);
+      valid &= valid - 1;
+      if (waiting < 0) {
+        waiting = s;
+      } else {
+        join(waiting, s);
+        waiting = -1;
+      }
+    }
+    if (e) break;
   }
+  if (waiting >= 0) join(waiting, -1);
+  if (!any || !on) return;
   const float scale = l > 0.0f ? 1.0f / l : l;
   const int row = hd.row0 + r;
   const int token = row / a.G;
