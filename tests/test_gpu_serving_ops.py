@@ -373,3 +373,66 @@ def test_operators_in_a_captured_graph(cuda_device):
             assert torch.equal(a.permute(0, 2, 1).reshape(-1, 128)[rows], b.permute(0, 2, 1).reshape(-1, 128)[rows])
         assert torch.equal(replayed[-1], table)
     status_ok()
+
+
+# --------------------------------------------------------------- the binding
+
+def test_binding_refuses_what_does_not_fit(cuda_device):
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    table = i32(2, 1, 3)
+    for args, text in (
+            ((i32(3), i32(2), table, i32(4), 5), "ctx_len"), ((i32(2), i32(2).long(), table, i32(4), 5), "new_len"),
+            ((i32(2), i32(2), i32(2, 3), i32(4), 5), "page_table"), ((i32(2), i32(2), table, i32(4), -1), "n_rows"),
+            ((i32(2), i32(2), table, i32(2, 2), 5), "free_pages"), ((i32(2).cpu(), i32(2), table, i32(4), 5), "ctx_len"),
+            ((i32(2), i32(2), i32(2, 1, 6)[:, :, ::2], i32(4), 5), "page_table")):
+        with pytest.raises(L.LynxError, match=text):
+            L.lynx_assign_pages(*args)
+    with pytest.raises(L.LynxError, match="slots"):
+        L.lynx_assign_pages(i32(2), i32(2), table, i32(4), 5, slots=i32(5, 1))
+    with pytest.raises(TypeError):
+        L.lynx_assign_pages(i32(2), i32(2), table, i32(4), "5")
+    slots = torch.zeros(2, 1, dtype=torch.int64, device="cuda")
+    good = dict(qkv=bf(2, 384), n_q_heads=1, n_kv_heads=1, cos_sin=None, positions=i32(2), slots=slots, k_pages=bf(1, 128, 256),
+                v_pages=bf(1, 128, 256))
+    for kw, text in ((dict(qkv=bf(2, 383)), "qkv"), (dict(qkv=bf(2, 768)[:, ::2]), "qkv"), (dict(n_kv_heads=0), "qkv"),
+                     (dict(positions=i32(3)), "positions"), (dict(k_pages=bf(1, 128, 128)), "k_pages"),
+                     (dict(v_pages=bf(2, 128, 256)), "v_pages"), (dict(cos_sin=torch.zeros(4, 24, device="cuda")), "rot_dim"),
+                     (dict(q_weight=torch.zeros(64, device="cuda")), "q_weight"), (dict(q_out=bf(2, 2, 128)), "q_out")):
+        with pytest.raises(L.LynxError, match=text):
+            L.lynx_qkv_append(**{**good, **kw})
+    good = dict(q=bf(2, 2, 128), cu_q=i32(2), k_pages=bf(1, 128, 256), v_pages=bf(1, 128, 256), page_table=i32(1, 1, 1),
+                ctx_len=i32(1), n_kv_heads=1)
+    for kw, text in ((dict(q=bf(2, 2, 64)), "q must"), (dict(cu_q=i32(3)), "cu_q"), (dict(n_kv_heads=2), "page_table"),
+                     (dict(out=bf(2, 2, 128).half()), "out"), (dict(out_dtype=torch.float16), "out_dtype"),
+                     (dict(lse=bf(2, 2)), "lse"), (dict(workspace=torch.zeros(4, device="cuda")), "workspace"),
+                     (dict(sm_scale=-1.0), "sm_scale"), (dict(ctx_len=i32(1).cpu()), "ctx_len")):
+        with pytest.raises(L.LynxError, match=text):
+            L.lynx_chunk_attn_bf16(**{**good, **kw})
+    p = torch.zeros(1, 3, 8, device="cuda")
+    good = dict(p=p, q=p[:, :2], draft=i32(1, 2), u=torch.zeros(1, 3, device="cuda"))
+    for kw, text in ((dict(p=p.double()), "p must"), (dict(p=p[:, :1]), "p must"), (dict(q=p), "q must"),
+                     (dict(q=p[:, :2].bfloat16()), "q must"), (dict(draft=i32(1, 3)), "draft"),
+                     (dict(u=torch.zeros(1, 2, device="cuda")), "u must"), (dict(n_draft=i32(2)), "n_draft"),
+                     (dict(p=p.transpose(1, 2)), "p must")):
+        with pytest.raises(L.LynxError, match=text):
+            L.lynx_verify_drafts(**{**good, **kw})
+    status_ok()
+
+
+def test_outputs_that_are_passed_come_back_and_streams_are_used(cuda_device):
+    s = torch.cuda.Stream()
+    tok, n = torch.empty(1, 2, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    p = torch.zeros(1, 2, 50, device="cuda")
+    p[0, :, 3] = 1.0
+    torch.cuda.synchronize()
+    a, b = L.lynx_verify_drafts(p, None, torch.full((1, 1), 3, dtype=torch.int32, device="cuda"),
+                                torch.zeros(1, 2, device="cuda"), tokens=tok, n_accept=n, stream=s)
+    assert a is tok and b is n
+    s.synchronize()
+    assert tok.tolist() == [[3, 3]] and n.tolist() == [1]
+    with torch.cuda.stream(s):               # torch's current stream
+        t2, _ = L.lynx_verify_drafts(p, None, torch.full((1, 1), 4, dtype=torch.int32, device="cuda"),
+                                     torch.full((1, 2), 0.5, device="cuda"))
+    s.synchronize()
+    assert t2.tolist() == [[3, -1]]
