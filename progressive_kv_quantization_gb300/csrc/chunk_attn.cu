@@ -240,7 +240,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v, int wide) {
 
 // A request's tiles on the cost line of one head, in 1/256 keys: tile m costs
 // its keys (those before the chunk plus 256 / G more with every tile under a
-// causal mask) and 256 keys for its start and end.
+// causal mask) and, for its start and end, 512 keys, or 256 if one group does
+// (measured: 5.1 and 2.1 us a tile, 1.2 and 1.0 us for 128 keys).
 struct Request {
   int q_base, T, ctx, tiles;
   long long base, step;
@@ -270,7 +271,7 @@ __device__ __forceinline__ Request load_request(const ChunkArgs& a, int b) {
   r.T = hi - lo;
   r.ctx = min(max(ctx, 0), max_keys);
   r.tiles = (r.T * a.G + kTileRows - 1) / kTileRows;
-  r.base = (long long)((a.causal ? max(r.ctx - r.T, 0) : r.ctx) + 256) << 8;
+  r.base = (long long)((a.causal ? max(r.ctx - r.T, 0) : r.ctx) + (r.T * a.G > kGroupRows ? 512 : 256)) << 8;
   r.step = a.causal ? 65536 / a.G : 0;
   return r;
 }
