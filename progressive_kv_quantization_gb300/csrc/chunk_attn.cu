@@ -302,9 +302,10 @@ __device__ __forceinline__ V warp_scan(V v) {   // inclusive
 __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, volatile int* s_n_items, Header* s_hdr,
                                            const volatile int* s_abort) {
   const int lane = threadIdx.x & 31;
+  const Request first = load_request(a, lane);
   long long Wh = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const Request r = load_request(a, b0 + lane);
+    const Request r = b0 == 0 ? first : load_request(a, b0 + lane);
     Wh += __shfl_sync(0xffffffffu, warp_scan(r.at(r.tiles)), 31);
   }
   const long long W = Wh * a.Hkv;
@@ -332,7 +333,7 @@ __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, vola
     long long before = 0, next = h * Wh + seg1;
     int n_items = 0;
     for (int b0 = 0; b0 < a.B && before < seg1; b0 += 32) {
-      const Request r = load_request(a, b0 + lane);
+      const Request r = b0 == 0 ? first : load_request(a, b0 + lane);
       const long long len = r.at(r.tiles);
       const long long end = before + warp_scan(len), p = end - len;
       before = __shfl_sync(0xffffffffu, end, 31);
@@ -453,6 +454,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
   }
   __syncthreads();
   tc_fence_after();
