@@ -14,17 +14,29 @@
 //
 // Warps.  0-3 and 4-7: softmax of the two groups, one row a thread; 8 and 11:
 // issue the groups' tcgen05.mma; 9: TMA of K and V tiles through a ring; 10: the
-// lists of tiles.  S and O of both
-// groups live in tensor memory (4 x 128 columns).  P overwrites S as BF16 and is
-// the A operand of O += P V from there.  While one group does its softmax the
-// tensor core works for the other.
+// lists of tiles.  S and O of both groups live in tensor memory (4 x 128 columns).
+// P overwrites S as BF16 and is the A operand of O += P V from there.  While one
+// group does its softmax the tensor core works for the other, one block of products
+// (P V, the next Q K^T) at a time.
 //
 // Softmax in one pass over the keys.  The running maximum moves only where a
 // score leads it by more than 8 in log2 units, so that O is rescaled (a round
-// trip through registers) on few tiles; P is at most 2^8.  Row sums are taken
-// of the float32 probabilities.  P is rounded to BF16 for the matrix product
-// (kind::f16 wants V's type): a relative 2^-9 a term, unbiased, about the size of
-// the BF16 output's own rounding once summed.
+// trip through registers) on few tiles; P is at most 2^8.  P is taken against the
+// maximum as it stands, beside the search for the tile's, and again if that moves
+// it.  Row sums are taken of the float32 probabilities.  P is rounded to BF16 for
+// the matrix product (kind::f16 wants V's type): half a step, 2^-8 of a term at
+// most, either way, so that over many keys it falls below the BF16 output's own
+// rounding.
+//
+// What bounds it (GB300, 16 or 32 query heads over 4 or 8 KV heads).  Many rows: the
+// tensor core, 4 x 128 x 128 x 128 products in 2,048 clocks for two groups; a tile of
+// keys takes 1.36 us against 1.08 at the clock seen.  8,192 tokens before 8,192 to
+// 131,072 keys run at 1,640-1,730 TFLOP/s call after call (power-capped; the library's
+// BF16 matrix product does 1,849 in a burst, 1,663 sustained).  The rest is the
+// hand-over between softmax and products, ~430 clocks of a group's 2,800.  One token a
+// request over long contexts: memory, 6.25 TB/s of keys and values (92% of a copy).
+// A short prompt: 13 us, of which the two launches, the lists and one tile's chain of
+// waits are all but one.
 //
 // Work split.  The tiles of all requests and heads stand on one line, each as
 // long as its estimated cost; the line is cut into equal parts, one a CTA, one
@@ -43,6 +55,7 @@
 // their V rows are zeroed in shared memory (0 x NaN would be NaN).
 
 #include "lynx_internal.cuh"
+#include "f32x2.cuh"
 #include "tma_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -74,7 +87,7 @@ constexpr int kNumBars = 2 * kSlots + 9;
 constexpr int kOffItems = kOffBar + 8 * kNumBars;
 constexpr int kItemInts = 10;
 constexpr int kOffMisc = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
-constexpr int kSmem = kOffMisc + 80;   // number of items, header (32, at 16), tensor memory, abort flag (at 64), busy flags
+constexpr int kSmem = kOffMisc + 80;   // items, header (at 16), tensor memory (at 64), abort and busy flags
 constexpr int kSmemAlloc = kSmem + 1024;
 static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
 
@@ -151,13 +164,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* v) {
       : LYNX_R8(v, 0), LYNX_R8(v, 8), LYNX_R8(v, 16), LYNX_R8(v, 24)
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::LYNX_I8(v, 0),
-      LYNX_I8(v, 8), LYNX_I8(v, 16), LYNX_I8(v, 24), "r"(addr)
-      : "memory");
-}
 // 16 columns, waited for
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v) {
   asm volatile(
@@ -195,29 +201,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -726,10 +709,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             // P against the running maximum as it stands, and the tile's maximum beside
             // it: the two do not wait for one another (1.36 us a tile of keys against 1.5 one
             // after the other).  Where the maximum has to move P is computed again.
-            const uint64_t sc2 = pair(__float_as_uint(sc), __float_as_uint(sc));
+            const uint64_t sc2 = pair(sc, sc);
             uint64_t sum[4];
             auto exps = [&](float ref) {
-              const uint64_t ref2 = pair(__float_as_uint(ref), __float_as_uint(ref));
+              const uint64_t ref2 = pair(ref, ref);
 #pragma unroll
               for (int x = 0; x < 4; ++x) sum[x] = 0ull;
 #pragma unroll
@@ -741,7 +724,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
                   unpair(fma2(pair(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), sc2, ref2), p0, p1);
                   p0 = ex2(p0);
                   p1 = ex2(p1);
-                  sum[e & 3] = add2(sum[e & 3], pair(__float_as_uint(p0), __float_as_uint(p1)));
+                  sum[e & 3] = add2(sum[e & 3], pair(p0, p1));
                   p[e] = bf16x2(p0, p1);
                 }
                 tmem_st16(t_s + 16 * x, p);

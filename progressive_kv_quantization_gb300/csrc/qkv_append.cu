@@ -10,14 +10,21 @@
 // row and all its heads; float32, rounded once to BF16.
 //
 // A half-warp holds one head of one row, 8 channels (16 bytes) a lane; a pair's
-// other half is rot / 16 lanes away (a shuffle) or in the same lane.  A CTA
-// takes 32 rows and either a group of query heads or one KV head (or a part of its
-// channels).  Cosines and
-// sines stay in registers over the heads of a row.  Keys and values pass
-// through shared memory, token-major in, and leave with one token per lane:
-// where slots follow one another (a chunk of one request) a warp's store is 64
-// contiguous bytes of a channel row.
+// other half is rot / 16 lanes away (a shuffle) or in the same lane.  A CTA takes
+// 32 rows and either a group of query heads or one KV head (or a part of its
+// channels).  Cosines and sines stay in registers over the heads of a row.  Keys
+// and values pass through shared memory, token-major in, and leave with one token
+// per lane: where slots follow one another (a chunk of one request) a warp's store
+// is 64 contiguous bytes of a channel row.
+//
+// What bounds it on a GB300.  Many rows: memory; 27,000 rows of 32 + 8 heads take
+// 119 us, 5.7 TB/s read and written (84% of a copy; the slots' 2-byte stores meet in
+// L2, DRAM moves the algorithmic bytes).  Some thousand rows (12.5 us for 4,096 of 16 +
+// 4 heads, half-split pairs and norms, all in L2): latency at 32 warps an SM (64
+// registers), the exchange of pairs the longest part.  A decode step of 64 rows (3.3 us):
+// the launch, the position and then the cosines at it.
 
+#include "f32x2.cuh"
 #include "lynx_internal.cuh"
 
 #include <cuda_bf16.h>
@@ -30,15 +37,6 @@ constexpr int kHalfWarps = kThreads / 16;
 constexpr int kTile = 32;                  // rows per CTA
 constexpr int kBatch = 4;                  // query heads of a row read at once
 constexpr int kPitch = kH / 2 + 1;         // words per staged token: the reading lanes (one token each) hit all banks
-
-__device__ __forceinline__ void unpack(const uint4& x, float (&v)[8]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -97,18 +95,28 @@ __device__ __forceinline__ Turn load_turn(const float* row, int rot, const float
   return t;
 }
 
-// One head; all lanes of a warp together.  The other halves come from lane
+// One head; all lanes of a warp together.  Two channels an instruction where pairs are
+// neighbours (40,000 rows of 32 + 8: 168.6 us against 171.6); half-split, the second copy
+// of the operands costs registers that spill (189.4 us against 181.0).  The other halves come from lane
 // `partner` (packed), or are the lane's own.
 template <bool INTERLEAVED>
 __device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, int partner, bool norm, float eps) {
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
   float a[8], o[8];
-  unpack(x, a);
-  if (INTERLEAVED) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = a[i ^ 1];
-  } else {
-    unpack(make_uint4(__shfl_sync(0xffffffffu, x.x, partner), __shfl_sync(0xffffffffu, x.y, partner),
-                      __shfl_sync(0xffffffffu, x.z, partner), __shfl_sync(0xffffffffu, x.w, partner)), o);
+  for (int i = 0; i < 4; ++i) {
+    a[2 * i] = __uint_as_float(xw[i] << 16);
+    a[2 * i + 1] = __uint_as_float(xw[i] & 0xFFFF0000u);
+  }
+  if (!INTERLEAVED) {
+    uint32_t ow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ow[i] = __shfl_sync(0xffffffffu, xw[i], partner);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(ow[i] << 16);
+      o[2 * i + 1] = __uint_as_float(ow[i] & 0xFFFF0000u);
+    }
   }
   float r = 1.0f;
   if (norm) {
@@ -122,8 +130,15 @@ __device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, int 
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float y0 = fmaf(a[2 * i], t.c[2 * i], o[2 * i] * t.s[2 * i]) * r;
-    const float y1 = fmaf(a[2 * i + 1], t.c[2 * i + 1], o[2 * i + 1] * t.s[2 * i + 1]) * r;
+    float y0, y1;
+    if (INTERLEAVED) {
+      const uint64_t as = pair(a[2 * i], a[2 * i + 1]), os = pair(a[2 * i + 1], a[2 * i]);
+      const uint64_t cs = pair(t.c[2 * i], t.c[2 * i + 1]), ss = pair(t.s[2 * i], t.s[2 * i + 1]);
+      unpair(mul2(fma2(as, cs, mul2(os, ss)), pair(r, r)), y0, y1);
+    } else {
+      y0 = fmaf(a[2 * i], t.c[2 * i], o[2 * i] * t.s[2 * i]) * r;
+      y1 = fmaf(a[2 * i + 1], t.c[2 * i + 1], o[2 * i + 1] * t.s[2 * i + 1]) * r;
+    }
     const __nv_bfloat162 p = __floats2bfloat162_rn(y0, y1);
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }

@@ -17,9 +17,13 @@
 // and re-reads the one run in question.  One launch, no workspace, no atomics;
 // every value of the two rows is read once.
 //
-// Bound by the reads of the two rows for a batch, by the chain draft -> gather
-// -> row -> exchange for one request.
+// Bound by the chain draft -> gather -> row -> exchange -> search for few requests
+// (4.8 us for one of 32,000 values) and by the reads of the two rows for many: 256 of
+// 151,936 float32 values take 54.6 us (5.7 TB/s, 84% of a copy); 32 take 11.2 us (51%),
+// of which some 5 are the chain.  A request's values are in flight three runs a warp
+// deep, in shared memory: loads to registers held fewer.
 
+#include "f32x2.cuh"
 #include "lynx_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -53,18 +57,12 @@ struct Units {
     asm("sub.rn.sat.f32 %0, %1, %2;" : "=f"(w) : "f"(p), "f"(q));
     return w;
   }
-  static __device__ __forceinline__ uint64_t both(float v) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(v));
-    return d;
-  }
   __device__ __forceinline__ void add2(float w0, float w1) {
-    uint64_t w, h, t, rest, l;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(w0), "f"(w1));
-    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(h) : "l"(w), "l"(both(8.0f)));
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(h), "l"(both(-8.0f)));
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rest) : "l"(t), "l"(both(-1.0f)), "l"(w));   // exact, below 2^-20
-    asm("add.rm.f32x2 %0, %1, %2;" : "=l"(l) : "l"(rest), "l"(both(0x1p-17f)));
+    const uint64_t w = pair(w0, w1);
+    const uint64_t h = add2_down(w, pair(8.0f, 8.0f));
+    const uint64_t top = lynx::add2(h, pair(-8.0f, -8.0f));
+    const uint64_t rest = fma2(top, pair(-1.0f, -1.0f), w);   // exact, below 2^-20
+    const uint64_t l = add2_down(rest, pair(0x1p-17f, 0x1p-17f));
     hi += (uint32_t)h + (uint32_t)(h >> 32) - 2u * 0x41000000u;   // bits of 8
     lo += (uint32_t)l + (uint32_t)(l >> 32) - 2u * 0x37000000u;   // bits of 2^-17
   }
@@ -303,7 +301,9 @@ verify_drafts_kernel(const VerifyArgs a) {
 
 template <typename T>
 cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
-  // CTAs per request: as many as the machine has room for, at most 8
+  // CTAs per request: as many as run at once, at most 8 (the portable cluster).  us for
+  // rows of 151,936: 32 requests 10.0 (8 CTAs) against 13.6 (4); 64: 14.7 (4) against
+  // 18.6 (8); 256: 54.6 (1) against 69.5 (8).
   int C = 8;
   while (C > 1 && (int64_t)a.B * C > 2 * device_sm_count()) C >>= 1;
   cudaLaunchConfig_t cfg = {};
