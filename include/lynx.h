@@ -399,8 +399,9 @@ int lynx_attn_merge(const float* o_a, const float* lse_a, const float* o_b, cons
  * The operators around attention in one step of a serving loop: pages and slots
  * for the step's new tokens (lynx_assign_pages), their queries, keys and values
  * (lynx_qkv_append), their attention to the paged cache (lynx_chunk_attn_bf16),
- * and the verification of drafted tokens (lynx_verify_drafts).  Integer arrays and probabilities need only the
- * alignment of their elements here; other buffers 16 bytes as everywhere.
+ * and the verification of drafted tokens (lynx_verify_drafts).  Integer arrays
+ * and probabilities need only the alignment of their elements here; other
+ * buffers 16 bytes as everywhere.  An output must not share memory with an input.
  */
 
 /* Pages, positions and slots of the new tokens of a ragged batch, from the
@@ -424,7 +425,9 @@ int lynx_attn_merge(const float* o_a, const float* lse_a, const float* o_b, cons
  * the missing ones take Hkv ids each (page by page, head 0 first) in request
  * order.  A request whose new tokens do not fit (a length below 0 or past
  * max_pages * 256: device error word 3; rows past n_rows) is refused and
- * takes no pages.  A request that the free list is too short for is refused
+ * takes no pages.  Pages beyond ceil(ctx / 256) that a request still has because its
+ * length was set back (rejected drafts) are not known here: their ids go back to the
+ * free list, or another page is taken in their place.  A request that the free list is too short for is refused
  * too, and so is every later one that needs a page: ids are dealt by running
  * sum, so that the outcome does not depend on what later requests ask for.
  * Rows of refused requests and rows behind the last request get position -1

@@ -13,7 +13,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -52,6 +52,7 @@ class Call {
     if (!THPVariable_Check(first) || !THPVariable_Unpack(first).is_cuda())
       raise("%s must live on a CUDA device", name);
     device_ = THPVariable_Unpack(first).device();
+    on_device_.set_device(device_);
   }
 
   // any tensor of the call's device
@@ -93,20 +94,21 @@ class Call {
     return THPVariable_Wrap(std::move(t));
   }
 
-  void* stream(PyObject* o) const {
-    if (o != Py_None) return PyLong_AsVoidPtr(o);
-    return c10::cuda::getCurrentCUDAStream(device_.index()).stream();
+  // The call's stream, torch's current one while the call lasts: what is allocated
+  // here (outputs, a workspace) comes from that stream's memory and goes back to it.
+  void* stream(PyObject* o) {
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device_.index()).stream();
+    void* const s = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw Raised{};
+    on_stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s), device_.index()));
+    return s;
   }
 
-  // f() with the tensors' device current
   template <typename F>
   void launch(F f) {
-    const c10::DeviceIndex before = c10::cuda::current_device();
-    if (before != device_.index()) c10::cuda::set_device(device_.index());
     PyThreadState* const held = PyEval_SaveThread();   // a full launch queue blocks here
     const int status = f();
     PyEval_RestoreThread(held);
-    if (before != device_.index()) c10::cuda::set_device(before);
     if (status != LYNX_OK) {
       PyErr_Format(g_error, "%s: %s (%s)", fn_, lynx_status_string(status), lynx_last_error());
       throw Raised{};
@@ -118,6 +120,8 @@ class Call {
  private:
   const char* fn_;
   c10::Device device_{c10::kCPU};
+  c10::cuda::OptionalCUDAGuard on_device_;   // the tensors' device is current while the call lasts
+  c10::cuda::OptionalCUDAStreamGuard on_stream_;
 };
 
 // a new reference that is given up when an error is raised
@@ -187,13 +191,13 @@ PyObject* assign_pages(PyObject* const* a) {
   void* fresh = c.at(a[1], at::kInt, {B}, "new_len");
   const int64_t n_free = THPVariable_Check(a[3]) ? THPVariable_Unpack(a[3]).numel() : 0;
   void* free_pages = c.at(a[3], at::kInt, {n_free}, "free_pages");
+  void* stream = c.stream(a[10]);
   Out cu, pos, slots, out, taken;
   cu.o = c.make(a[5], at::kInt, {B + 1}, "cu_new", &cu.p);
   pos.o = c.make(a[6], at::kInt, {n_rows}, "positions", &pos.p);
   slots.o = c.make(a[7], at::kLong, {n_rows, Hkv}, "slots", &slots.p);
   out.o = c.make(a[8], at::kInt, {B}, "ctx_out", &out.p);
   taken.o = c.make(a[9], at::kInt, {1}, "n_taken", &taken.p);
-  void* stream = c.stream(a[10]);
   const int b = dim32(B, "B"), h = dim32(Hkv, "Hkv"), mp = dim32(pages, "max_pages"), nf = dim32(n_free, "free_pages");
   c.launch([&] {
     return lynx_assign_pages((int32_t*)ctx, (int32_t*)fresh, b, h, (int32_t*)t, mp, (int32_t*)free_pages, nf, n_rows,
@@ -234,9 +238,9 @@ PyObject* qkv_append(PyObject* const* a) {
   void* v = c.at(a[7], at::kBFloat16, {n_pool, 128, 256}, "v_pages");
   const float eps = to_float(a[10]);
   const int interleaved = PyObject_IsTrue(a[11]);
+  void* stream = c.stream(a[13]);
   Out q;
   q.o = c.make(a[12], at::kBFloat16, {n_rows, Hq, 128}, "q_out", &q.p);
-  void* stream = c.stream(a[13]);
   c.launch([&] {
     return lynx_qkv_append(qkv.data_ptr(), n_rows, stride, Hq, Hkv, 128, (float*)wq, (float*)wk, eps, (float*)table,
                            max_pos, rot, interleaved, (int32_t*)pos, (int64_t*)slots, q.p, k, v, n_pool, stream);
@@ -272,6 +276,7 @@ PyObject* chunk_attn_bf16(PyObject* const* a) {
     if (type != at::kBFloat16 && type != at::kFloat) raise("out must be bfloat16 or float32");
     f32 = type == at::kFloat;
   }
+  void* stream = c.stream(a[13]);
   Out out, lse, ws;
   out.o = c.make(a[9], f32 ? at::kFloat : at::kBFloat16, {n_rows, Hq, 128}, "out", &out.p);
   lse.o = c.make(a[10], at::kFloat, {n_rows, Hq}, "lse", &lse.p);
@@ -287,7 +292,6 @@ PyObject* chunk_attn_bf16(PyObject* const* a) {
     ws.p = w.data_ptr();
     ws_bytes = w.nbytes();
   }
-  void* stream = c.stream(a[13]);
   c.launch([&] {
     return lynx_chunk_attn_bf16(q.data_ptr(), n_rows, stride, (int32_t*)cu, B, Hq, n_kv, 128, k, v, n_pool, (int32_t*)t,
                                 pages, (int32_t*)ctx, scale, causal, out.p, f32 ? LYNX_OUT_F32 : LYNX_OUT_BF16,
@@ -318,10 +322,10 @@ PyObject* verify_drafts(PyObject* const* a) {
   void* draft = c.at(a[2], at::kInt, {B, T}, "draft");
   void* u = c.at(a[3], at::kFloat, {B, (int64_t)T + 1}, "u");
   void* n_draft = a[4] == Py_None ? nullptr : c.at(a[4], at::kInt, {B}, "n_draft");
+  void* stream = c.stream(a[7]);
   Out tokens, n;
   tokens.o = c.make(a[5], at::kInt, {B, (int64_t)T + 1}, "tokens", &tokens.p);
   n.o = c.make(a[6], at::kInt, {B}, "n_accept", &n.p);
-  void* stream = c.stream(a[7]);
   c.launch([&] {
     return lynx_verify_drafts(p.data_ptr(), B > 1 ? p.stride(0) : 0, p.stride(1), q_at, qb, qt,
                               type == at::kFloat ? LYNX_OUT_F32 : LYNX_OUT_BF16, B, T, V, (int32_t*)draft,

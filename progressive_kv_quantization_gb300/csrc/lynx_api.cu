@@ -6,6 +6,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "lynx_internal.cuh"
@@ -35,6 +36,22 @@ int cuda_fail(cudaError_t e, const char* where) {
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 // not on a multiple of its element's size (NULL is)
 bool off_type(const void* p, int size) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(size - 1)) != 0; }
+// two spans of bytes with one in common
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+// a written buffer that shares bytes with a read one
+bool overlap(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span& w : written)
+    for (const Span& r : read)
+      if (overlap(w, r)) return true;
+  return false;
+}
 
 int check_params(const lynx_params_t* p) {
   if (p == nullptr) return fail(LYNX_ERR_INVALID_ARG, "params is NULL");
@@ -730,8 +747,10 @@ int lynx_assign_pages(const int32_t* ctx_len, const int32_t* new_len, int B, int
       off_type(cu_new, 4) || off_type(positions, 4) || off_type(slots, 8) || off_type(ctx_out, 4) ||
       off_type(n_taken, 4))
     return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
-  if (ctx_out == ctx_len || ctx_out == new_len)
-    return fail(LYNX_ERR_INVALID_ARG, "ctx_out must not be ctx_len or new_len");
+  const int64_t n4 = (int64_t)B * 4, rows = n_rows;
+  if (overlap({{cu_new, n4 + 4}, {positions, rows * 4}, {slots, rows * Hkv * 8}, {ctx_out, n4}, {n_taken, 4}},
+              {{ctx_len, n4}, {new_len, n4}, {free_pages, (int64_t)n_free * 4}}))
+    return fail(LYNX_ERR_INVALID_ARG, "an output overlaps ctx_len, new_len or free_pages");
   int* status = device_status_ptr();
   if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
   const AssignArgs a{ctx_len, new_len, page_table, free_pages, cu_new, positions, slots, ctx_out,
@@ -771,6 +790,9 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
       (n_rows / 32 + 1) * ((int64_t)Hq + 8 * (int64_t)Hkv) > 0x7fffffff)
     return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%lld, Hq=%d, Hkv=%d too large", (long long)n_rows, Hq, Hkv);
   if (n_pool_pages > ((int64_t)1 << 40)) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages too large");
+  const int64_t width = ((int64_t)Hq + 2 * (int64_t)Hkv) * kH;
+  if (overlap({q_out, n_rows * Hq * kH * 2}, {qkv_bf16, ((n_rows - 1) * row_stride + width) * 2}))
+    return fail(LYNX_ERR_INVALID_ARG, "q_out overlaps the rows of qkv");
   int* status = device_status_ptr();
   if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
   AppendArgs a{};
@@ -849,6 +871,10 @@ int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride,
   if (workspace == nullptr || workspace_bytes < need)
     return fail(LYNX_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                 workspace ? workspace_bytes : (size_t)0);
+  const int64_t n_out = n_rows * Hq * kH * (out_dtype == LYNX_OUT_F32 ? 4 : 2);
+  if (overlap({{out, n_out}, {lse, n_rows * Hq * 4}, {workspace, (int64_t)need}},
+              {{q_bf16, ((n_rows - 1) * row_stride + (int64_t)Hq * kH) * 2}}))
+    return fail(LYNX_ERR_INVALID_ARG, "out, lse or the workspace overlaps the rows of q");
   int* status = device_status_ptr();
   if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
   ChunkArgs a{};
@@ -901,6 +927,9 @@ int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, co
   if (off_type(p, size) || off_type(q, size) || off_type(draft, 4) || off_type(n_draft, 4) || off_type(u, 4) ||
       off_type(tokens, 4) || off_type(n_accept, 4))
     return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
+  const int64_t n4 = (int64_t)B * 4;
+  if (overlap({{tokens, n4 * (T + 1)}, {n_accept, n4}}, {{draft, n4 * T}, {n_draft, n4}, {u, n4 * (T + 1)}}))
+    return fail(LYNX_ERR_INVALID_ARG, "an output overlaps draft, n_draft or u");
   const VerifyArgs a{p, q, p_stride_b, p_stride_t, q_stride_b, q_stride_t, draft, n_draft, u, tokens, n_accept, B, T, V};
   cudaError_t e = launch_verify_drafts(a, prob_dtype == LYNX_OUT_BF16, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "lynx_verify_drafts launch");

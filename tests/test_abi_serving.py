@@ -83,6 +83,46 @@ def test_verify_drafts_argument_checks(lynx_lib, a):
     assert call(dt=0, p=ctypes.c_void_p(a.value + 1)) == -3
 
 
+def test_outputs_that_share_memory_with_inputs_are_refused(lynx_lib, a):
+    """Spans that meet in one element only; every call is refused before a launch."""
+    def at(offset):
+        return ctypes.c_void_p((1 << 40) + offset)
+    far = [at((i + 1) << 32) for i in range(16)]
+
+    def assign(**kw):
+        x = dict(ctx=far[0], new=far[1], free=far[2], cu=far[3], pos=far[4], slots=far[5], out=far[6], taken=far[7])
+        x.update(kw)
+        return lynx_lib.lynx_assign_pages(x["ctx"], x["new"], 8, 2, far[8], 4, x["free"], 9, 5, x["cu"], x["pos"],
+                                          x["slots"], x["out"], x["taken"], None)
+    for name, size in (("cu", 36), ("pos", 20), ("slots", 80), ("out", 32), ("taken", 4)):
+        for read, length in (("ctx", 32), ("new", 32), ("free", 36)):
+            base = 1 << 20
+            assert assign(**{name: at(base), read: at(base + size // 8 * 8 - 8 if size > 8 else base)}) == -1
+            assert assign(**{read: at(base), name: at(base + (length - 4) // 8 * 8)}) == -1
+
+    def append(qkv, q, n, stride):
+        return lynx_lib.lynx_qkv_append(qkv, n, stride, 4, 2, 128, None, None, 0.0, None, 0, 0, 0, far[0], far[1], q,
+                                        far[2], far[3], 4, None)
+    last = (2 * 1032 + 1024) * 2          # bytes from the first row's start to the third one's end
+    assert append(at(0), at(last - 16), 3, 1032) == -1
+    assert append(at(3 * 1024 - 16), at(0), 3, 1032) == -1
+    size = lynx_lib.lynx_chunk_attn_workspace_size(3, 1, 4, 2, 128)
+
+    def chunk(q=far[0], out=far[1], lse=far[2], ws=far[3], dt=0):
+        return lynx_lib.lynx_chunk_attn_bf16(q, 3, 1032, far[4], 1, 4, 2, 128, far[5], far[6], 4, far[7], 1, far[8], 0.1,
+                                             1, out, dt, lse, ws, size, None)
+    span = (2 * 1032 + 512) * 2
+    assert chunk(q=at(0), out=at(0)) == -1 and chunk(q=at(0), out=at(span - 16)) == -1
+    assert chunk(q=at(0), lse=at(span - 4)) == -1 and chunk(q=at(0), ws=at(span - 16)) == -1
+    assert chunk(out=at(0), q=at(3 * 1024 - 16)) == -1 and chunk(out=at(0), dt=1, q=at(3 * 2048 - 16)) == -1
+    assert chunk(ws=at(0), q=at(size // 16 * 16 - 16)) == -1
+
+    def verify(d=far[0], nd=far[1], u=far[2], tok=far[3], n=far[4]):
+        return lynx_lib.lynx_verify_drafts(far[5], 400, 100, far[6], 300, 100, 1, 2, 3, 100, d, nd, u, tok, n, None)
+    assert verify(tok=at(0), d=at(28)) == -1 and verify(tok=at(0), u=at(0)) == -1 and verify(tok=at(4), nd=at(0)) == -1
+    assert verify(n=at(0), d=at(4)) == -1 and verify(n=at(28), u=at(0)) == -1 and verify(n=far[1]) == -1
+
+
 def test_bindings_refuse_host_tensors():
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(L.LynxError, match="CUDA"):

@@ -111,7 +111,7 @@ def test_a_serving_loop_equals_attention_over_the_whole_sequences(cuda_device, g
         assert ctx.tolist() == [len(s) for s in seqs]
     ref = reference(seqs, Hq, Hkv, lp.wq.cpu().numpy(), lp.wk.cpu().numpy(), lp.cos_sin.cpu().numpy())
     for b in range(B):
-        # P's rounding to BF16 (2^-9 of the largest |v|) and scores that differ where float32 and
+        # P's rounding to BF16 (half a step: 2^-8 of the largest |v|) and scores that differ where float32 and
         # float64 round a query or key to different BF16 neighbours: a step of 2^-8 of one factor of
         # 128, |q k| / sqrt(128) of a few units: together below 2^-6 of the largest |v|
         vm = np.abs(seqs[b][:, Hq + Hkv:]).max()
@@ -144,7 +144,8 @@ def test_finished_pages_serve_the_packed_cache(cuda_device):
     torch.cuda.synchronize()
     L.lynx_device_status()
     vm = float(lp.v[ids].float().abs().max())
-    # the same dequantised cache, rounded to BF16 for the chunk kernel (2^-9 of a value and of a key) and P to BF16
+    # the same dequantised cache, rounded to BF16 for the chunk kernel (half a step, 2^-8, of a value and of a
+    # key) and P to BF16 (2^-8)
     assert float((again - full[:, 0]).abs().max()) <= 2.0 ** -6 * vm
     # a full code is within half a step of the 8-bit compander: a few per cent of a chunk's range
     assert float((exact - full[:, 0]).norm() / exact.norm()) < 0.1
