@@ -29,6 +29,11 @@
  *   lynx_decode_attn_uniform, lynx_split_nibbles
  *                         the single-precision comparators of §6.1 (uniform
  *                         INT8 / INT4, Lynx-INT8, Lynx-INT4).
+ *   lynx_assign_pages, lynx_qkv_append, lynx_chunk_attn_bf16, lynx_verify_drafts
+ *                         the operators around attention in a serving step over
+ *                         BF16 pages: pages and slots of new tokens, their norm,
+ *                         rotation and write, attention of ragged chunks
+ *                         (prefill), verification of drafted tokens (§4.3).
  *
  * ---------------------------------------------------------------------------
  * Data layout (all sizes for H = 128 channels, P = 256 tokens, C = 32):
