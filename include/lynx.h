@@ -448,7 +448,7 @@ int lynx_assign_pages(const int32_t* ctx_len, const int32_t* new_len, int B, int
  *   qkv_bf16    rows of Hq query heads, Hkv key heads and Hkv value heads of 128
  *               BF16 each; row r begins at r * row_stride elements (>= (Hq + 2
  *               Hkv) * 128, a multiple of 8)
- *   q_weight, k_weight   [128] float32 norm weights (NULL: no norm):
+ *   q_weight, k_weight   [128] float32 norm weights, 16-byte aligned (NULL: no norm):
  *               y = x / sqrt(mean(x^2) + norm_eps) * weight
  *   cos_sin     [max_pos][rot_dim] float32: the rot_dim / 2 cosines of a
  *               position, then its rot_dim / 2 sines (16-byte aligned)

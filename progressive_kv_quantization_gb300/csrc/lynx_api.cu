@@ -782,9 +782,9 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
   if (!qkv_bf16 || !positions || !slots || !q_out || !k_pages || !v_pages)
     return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
   if (misaligned(qkv_bf16) || misaligned(q_out) || misaligned(k_pages) || misaligned(v_pages) ||
-      (cos_sin && misaligned(cos_sin)) || row_stride % 8 != 0)
-    return fail(LYNX_ERR_ALIGNMENT, "rows of qkv, q_out, the pools and cos_sin must be 16-byte aligned");
-  if (off_type(q_weight, 4) || off_type(k_weight, 4) || off_type(positions, 4) || off_type(slots, 8))
+      misaligned(cos_sin) || misaligned(q_weight) || misaligned(k_weight) || row_stride % 8 != 0)
+    return fail(LYNX_ERR_ALIGNMENT, "rows of qkv, q_out, the pools, the weights and cos_sin must be 16-byte aligned");
+  if (off_type(positions, 4) || off_type(slots, 8))
     return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
   if (n_rows > 1 << 30 || (int64_t)Hq + 8 * (int64_t)Hkv > 65535 ||
       (n_rows / 32 + 1) * ((int64_t)Hq + 8 * (int64_t)Hkv) > 0x7fffffff)

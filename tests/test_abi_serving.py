@@ -48,6 +48,15 @@ def test_qkv_append_argument_checks(lynx_lib, a):
     assert call(n=0, qkv=None, pos=None, slots=None, q=None, k=None, v=None, cs=None) == 0
 
 
+def test_qkv_append_refuses_norm_weights_off_16_bytes(lynx_lib, a):
+    """A slice of a longer weight vector: the kernel reads four weights at once."""
+    def call(wq, wk):
+        return lynx_lib.lynx_qkv_append(a, 1, 384, 1, 1, 128, wq, wk, 1e-6, a, 4, 128, 0, a, a, a, a, a, 1, None)
+    for off in (4, 8, 12):
+        w = ctypes.c_void_p(a.value + off)
+        assert call(w, None) == -3 and call(None, w) == -3
+
+
 def test_chunk_attn_argument_checks(lynx_lib, a):
     size = lynx_lib.lynx_chunk_attn_workspace_size(1, 1, 4, 2, 128)
 
