@@ -38,10 +38,9 @@ constexpr int kTile = 32;                  // rows per CTA
 constexpr int kBatch = 4;                  // query heads of a row read at once
 constexpr int kPitch = kH / 2 + 1;         // words per staged token: the reading lanes (one token each) hit all banks
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 // A row's rotation with the norm weight in it, for the lane's 8 channels: with x'
@@ -50,73 +49,50 @@ struct Turn {
   float c[8], s[8];
 };
 
-// `row`: the position's cosines and sines; c0: the lane's first channel; o0: where
-// the other halves of its pairs begin
+// `row`: the position's cosines and sines; ca, cb: the lane's channels, four from
+// each (INTERLEAVED or behind the rotated ones: cb = ca + 4)
 template <bool INTERLEAVED>
-__device__ __forceinline__ Turn load_turn(const float* row, int rot, const float* weight, int c0, int o0) {
+__device__ __forceinline__ Turn load_turn(const float* row, int rot, const float* weight, int ca, int cb) {
   Turn t;
-  const int half = rot >> 1;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     t.c[i] = 1.0f;
     t.s[i] = 0.0f;
   }
-  if (c0 < rot) {
-    if (INTERLEAVED) {
-      const float4 c = *reinterpret_cast<const float4*>(row + c0 / 2);
-      const float4 s = *reinterpret_cast<const float4*>(row + half + c0 / 2);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, sc[4] = {s.x, s.y, s.z, s.w};
+  if (ca < rot) {
+    float c[4], s[4];
+    load4(row + (INTERLEAVED ? ca / 2 : ca), c);
+    load4(row + rot / 2 + (INTERLEAVED ? ca / 2 : ca), s);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        t.c[2 * i] = t.c[2 * i + 1] = cc[i];
-        t.s[2 * i] = -sc[i];
-        t.s[2 * i + 1] = sc[i];
-      }
-    } else {
-      const bool low = c0 < half;
-      const int i0 = low ? c0 : o0;
-      load8(row + i0, t.c);
-      load8(row + half + i0, t.s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (low) t.s[i] = -t.s[i];
+    for (int i = 0; i < 4; ++i) {
+      const int lo = INTERLEAVED ? 2 * i : i, hi = INTERLEAVED ? 2 * i + 1 : i + 4;
+      t.c[lo] = t.c[hi] = c[i];
+      t.s[lo] = -s[i];
+      t.s[hi] = s[i];
     }
   }
   if (weight) {
-    float w[8], o[8];
-    load8(weight + c0, w);
-    load8(weight + o0, o);
+    float w[8];
+    load4(weight + ca, w);
+    load4(weight + cb, w + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       t.c[i] *= w[i];
-      t.s[i] *= INTERLEAVED ? o[i ^ 1] : o[i];
+      t.s[i] *= w[INTERLEAVED ? i ^ 1 : i ^ 4];
     }
   }
   return t;
 }
 
-// One head; all lanes of a warp together.  Two channels an instruction where pairs are
-// neighbours (40,000 rows of 32 + 8: 168.6 us against 171.6); half-split, the second copy
-// of the operands costs registers that spill (189.4 us against 181.0).  The other halves come from lane
-// `partner` (packed), or are the lane's own.
+// One head; all lanes of a warp together.  Two channels an instruction.
 template <bool INTERLEAVED>
-__device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, int partner, bool norm, float eps) {
+__device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool norm, float eps) {
   const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-  float a[8], o[8];
+  float a[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     a[2 * i] = __uint_as_float(xw[i] << 16);
     a[2 * i + 1] = __uint_as_float(xw[i] & 0xFFFF0000u);
-  }
-  if (!INTERLEAVED) {
-    uint32_t ow[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ow[i] = __shfl_sync(0xffffffffu, xw[i], partner);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __uint_as_float(ow[i] << 16);
-      o[2 * i + 1] = __uint_as_float(ow[i] & 0xFFFF0000u);
-    }
   }
   float r = 1.0f;
   if (norm) {
@@ -129,18 +105,13 @@ __device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, int 
   }
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; i += 2) {
+    const int o0 = INTERLEAVED ? i + 1 : i ^ 4, o1 = INTERLEAVED ? i : o0 + 1;
     float y0, y1;
-    if (INTERLEAVED) {
-      const uint64_t as = pair(a[2 * i], a[2 * i + 1]), os = pair(a[2 * i + 1], a[2 * i]);
-      const uint64_t cs = pair(t.c[2 * i], t.c[2 * i + 1]), ss = pair(t.s[2 * i], t.s[2 * i + 1]);
-      unpair(mul2(fma2(as, cs, mul2(os, ss)), pair(r, r)), y0, y1);
-    } else {
-      y0 = fmaf(a[2 * i], t.c[2 * i], o[2 * i] * t.s[2 * i]) * r;
-      y1 = fmaf(a[2 * i + 1], t.c[2 * i + 1], o[2 * i + 1] * t.s[2 * i + 1]) * r;
-    }
+    unpair(mul2(fma2(pair(a[i], a[i + 1]), pair(t.c[i], t.c[i + 1]), mul2(pair(a[o0], a[o1]), pair(t.s[i], t.s[i + 1]))),
+                pair(r, r)), y0, y1);
     const __nv_bfloat162 p = __floats2bfloat162_rn(y0, y1);
-    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    w[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -155,17 +126,15 @@ qkv_append_kernel(const AppendArgs a) {
   const int64_t row0 = (int64_t)(a.whole_rows ? blockIdx.x / n_jobs : blockIdx.x % n_tiles) * kTile;
   const bool is_kv = job >= a.q_jobs;
   const int kv_head = is_kv ? (job - a.q_jobs) / a.kv_parts : 0;
-  const int half = a.rot >> 1;
-  // the lane that holds the other halves of this lane's pairs, and their channels
-  const int c0 = 8 * lane16;
-  int away = 0;
-  if (!INTERLEAVED && c0 < a.rot) away = c0 < half ? half : -half;
-  const int partner = lane + away / 8, o0 = c0 + away;
+  // the lane's channels: four at ca and four at cb, so that a pair's halves are in
+  // one lane
+  const bool apart = !INTERLEAVED && 8 * lane16 < a.rot;
+  const int ca = (apart ? 4 : 8) * lane16, cb = apart ? ca + a.rot / 2 : ca + 4;
   allow_dependent_launch();
   wait_prerequisite_grids();
   const float* weight = is_kv ? a.k_weight : a.q_weight;
   auto finish = [&](const uint4& x, const Turn& turn) {
-    return norm_rotate<INTERLEAVED>(x, turn, partner, weight != nullptr, a.norm_eps);
+    return norm_rotate<INTERLEAVED>(x, turn, weight != nullptr, a.norm_eps);
   };
   // position of a row that takes part, or -1
   auto checked = [&](int pos) {
@@ -176,12 +145,20 @@ qkv_append_kernel(const AppendArgs a) {
     return pos;
   };
   auto turn_at = [&](int pos) {
-    return load_turn<INTERLEAVED>(a.cos_sin + (int64_t)(pos < 0 ? 0 : pos) * a.rot, a.rot, weight, c0, o0);
+    return load_turn<INTERLEAVED>(a.cos_sin + (int64_t)(pos < 0 ? 0 : pos) * a.rot, a.rot, weight, ca, cb);
   };
   // heads are read before their row's position is known (what is skipped is not written)
   auto head_at = [&](int64_t row, int h) {
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (row < a.n_rows) x = *(reinterpret_cast<const uint4*>(a.qkv + row * a.row_stride + (int64_t)h * kH) + lane16);
+    if (row < a.n_rows) {
+      const uint16_t* src = a.qkv + row * a.row_stride + (int64_t)h * kH;
+      if (INTERLEAVED) {
+        x = *reinterpret_cast<const uint4*>(src + ca);
+      } else {
+        const uint2 lo = *reinterpret_cast<const uint2*>(src + ca), hi = *reinterpret_cast<const uint2*>(src + cb);
+        x = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
     return x;
   };
   constexpr int kSteps = kTile / kHalfWarps;   // rows of a half-warp
@@ -217,7 +194,14 @@ qkv_append_kernel(const AppendArgs a) {
         for (int i = 0; i < kBatch; ++i) {
           if (h + i >= h1) break;
           const uint4 r = finish(x[i], turn);
-          if (p >= 0) *(reinterpret_cast<uint4*>(a.q_out + (row * a.Hq + h + i) * kH) + lane16) = r;
+          if (p < 0) continue;
+          uint16_t* dst = a.q_out + (row * a.Hq + h + i) * kH;
+          if (INTERLEAVED) {
+            *reinterpret_cast<uint4*>(dst + ca) = r;
+          } else {
+            *reinterpret_cast<uint2*>(dst + ca) = make_uint2(r.x, r.y);
+            *reinterpret_cast<uint2*>(dst + cb) = make_uint2(r.z, r.w);
+          }
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) x[i] = next[i];
@@ -241,10 +225,10 @@ qkv_append_kernel(const AppendArgs a) {
     const int t = k * kHalfWarps + hw;
     const uint4 r = finish(xk[k], turn_at(checked(pos[k])));
     const uint4 v = xv[k];
-    uint32_t* dk = s_kv[0] + t * kPitch + 4 * lane16;
-    uint32_t* dv = s_kv[1] + t * kPitch + 4 * lane16;
-    dk[0] = r.x; dk[1] = r.y; dk[2] = r.z; dk[3] = r.w;
-    dv[0] = v.x; dv[1] = v.y; dv[2] = v.z; dv[3] = v.w;
+    uint32_t* dk = s_kv[0] + t * kPitch;
+    uint32_t* dv = s_kv[1] + t * kPitch;
+    dk[ca / 2] = r.x; dk[ca / 2 + 1] = r.y; dk[cb / 2] = r.z; dk[cb / 2 + 1] = r.w;
+    dv[ca / 2] = v.x; dv[ca / 2 + 1] = v.y; dv[cb / 2] = v.z; dv[cb / 2 + 1] = v.w;
   }
   __syncthreads();
   // one token per lane, a pair of channels at a time
