@@ -37,6 +37,16 @@ static_assert(kThreads == 256, "eight steps of bisection; a row of a CTA's tile 
 
 __device__ __forceinline__ int add(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kMost); }
 
+// A row of the tile: where its page's id stands for head 0 and how far on for the
+// next head (the page table, or the free list for a fresh page), and its place in
+// the page; kBegins: the first row of a fresh page; -1: a row without a slot
+struct Row {
+  const int32_t* ids;
+  int stride;
+  int at;
+};
+constexpr int kBegins = kP;
+
 template <int kTile>   // rows per CTA
 __global__ void __launch_bounds__(kThreads)
 assign_pages_kernel(const AssignArgs a) {
@@ -46,9 +56,8 @@ assign_pages_kernel(const AssignArgs a) {
   __shared__ int s_held[kThreads];   // pages held; -1: refused
   __shared__ int2 s_warp[kThreads / 32];
   __shared__ int s_taken;
-  __shared__ int r_pos[kTile];                 // position of the tile's row; -1: none
-  __shared__ int r_req[kTile];
-  __shared__ int r_free[kTile];                // free-list index of the row's page, head 0; -1: in the table
+  __shared__ Row s_row[kTile];
+  __shared__ int64_t s_entry[kTile];   // of rows at kBegins: the table entry of their page, head 0
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row0 = blockIdx.x * kTile;
@@ -56,7 +65,8 @@ assign_pages_kernel(const AssignArgs a) {
   const bool first = blockIdx.x == 0;
   const int max_keys = a.max_pages * kP;
 
-  if (tid < kTile) r_pos[tid] = -1;
+  int pos = -1;   // of row row0 + tid
+  if (tid < kTile) s_row[tid].at = -1;
   if (tid == 0) s_taken = 0;
   allow_dependent_launch();
   wait_prerequisite_grids();
@@ -124,38 +134,45 @@ assign_pages_kernel(const AssignArgs a) {
         if (s_rows[mid] <= r) i = mid; else j = mid;
       }
       if (s_held[i] >= 0) {
-        const int pos = s_ctx[i] + r - s_rows[i];
+        pos = s_ctx[i] + r - s_rows[i];
         const int page = pos / kP;
-        r_pos[tid] = pos;
-        r_req[tid] = b0 + i;
-        r_free[tid] = page < s_held[i] ? -1 : s_free[i] + (page - s_held[i]) * a.Hkv;
+        const int64_t entry = (int64_t)(b0 + i) * a.Hkv * a.max_pages + page;
+        Row row;
+        row.at = pos % kP;
+        if (page < s_held[i]) {
+          row.ids = a.page_table + entry;
+          row.stride = a.max_pages;
+        } else {
+          row.ids = a.free_pages + s_free[i] + (page - s_held[i]) * a.Hkv;
+          row.stride = 1;
+          if (row.at == 0) {
+            row.at = kBegins;
+            s_entry[tid] = entry;
+          }
+        }
+        s_row[tid] = row;
       }
     }
     __syncthreads();
   }
   if (first && tid == 0) a.n_taken[0] = s_taken;
 
-  if (tid < row1 - row0) a.positions[row0 + tid] = r_pos[tid];
-  // slots, kBatch a thread at a time, so that their table entries are read together
+  if (tid < row1 - row0) a.positions[row0 + tid] = pos;
+  // slots, kBatch a thread at a time, so that their ids are read together
   const int n_out = (row1 - row0) * a.Hkv;
   const int dr = kThreads / a.Hkv, dh = kThreads - dr * a.Hkv;
   int r = tid / a.Hkv, h = tid - r * a.Hkv;
+  int64_t* slots = a.slots + (int64_t)row0 * a.Hkv;
   for (int i0 = tid; i0 < n_out; i0 += kBatch * kThreads) {
-    int id[kBatch], pos[kBatch];
-    int32_t* fresh[kBatch];   // the entry of a page that begins here
+    int id[kBatch], at[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      pos[k] = -1;
+      at[k] = -1;
       id[k] = 0;
-      fresh[k] = nullptr;
       if (i0 + k * kThreads < n_out) {
-        pos[k] = r_pos[r];
-        if (pos[k] >= 0) {
-          int32_t* entry = a.page_table + ((int64_t)r_req[r] * a.Hkv + h) * a.max_pages + pos[k] / kP;
-          const int f = r_free[r];
-          id[k] = f < 0 ? *entry : a.free_pages[f + h];
-          if (f >= 0 && pos[k] % kP == 0) fresh[k] = entry;
-        }
+        const Row row = s_row[r];
+        at[k] = row.at;
+        if (row.at >= 0) id[k] = row.ids[(int64_t)h * row.stride];
       }
       r += dr;
       h += dh;
@@ -166,9 +183,13 @@ assign_pages_kernel(const AssignArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (i0 + k * kThreads >= n_out) break;
-      if (fresh[k]) *fresh[k] = id[k];
-      a.slots[(int64_t)row0 * a.Hkv + i0 + k * kThreads] = pos[k] >= 0 ? (int64_t)id[k] * kP + pos[k] % kP : -1;
+      const int i = i0 + k * kThreads;
+      if (i >= n_out) break;
+      if (at[k] == kBegins) {
+        const int row = i / a.Hkv;
+        a.page_table[s_entry[row] + (int64_t)(i - row * a.Hkv) * a.max_pages] = id[k];
+      }
+      slots[i] = at[k] >= 0 ? (int64_t)id[k] * kP + at[k] % kP : -1;
     }
   }
 }
