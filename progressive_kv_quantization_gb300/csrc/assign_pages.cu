@@ -17,10 +17,10 @@
 // fresh pages' first positions are all new rows, and no other row reads those
 // entries (it takes the id from the free list itself), so nothing races.
 //
-// Bound by the launch and the chain lengths -> sums -> table -> slots: 3.0 us for a
-// decode step of 64 requests, 6.4 us for 100,000 rows of 8 heads, whose slots (8 bytes
-// a row and head) would take 1 us at the memory's rate.  (There each SM gets two or
-// three CTAs of 256 rows and issues 55% of the time: sums, bisection, slots.)
+// Bound by the launch and the chain lengths -> sums -> row -> table -> slot: 3.1 us for a
+// decode step of 64 requests (the host's call; 2.8 us on the GPU), 5.7 us for 100,000
+// rows of 8 heads, whose slots (8 bytes a row and head) would take 1 us at the memory's
+// rate.
 
 #include "lynx_internal.cuh"
 
@@ -28,7 +28,6 @@ namespace lynx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;
 // Sums stop here: past every number of rows and of free ids (2^30 at most), and
 // two such numbers still add up within 32 bits.  Addition cut off at a bound is
 // associative, so the sums are the same in any order.
@@ -159,6 +158,7 @@ assign_pages_kernel(const AssignArgs a) {
 
   if (tid < row1 - row0) a.positions[row0 + tid] = pos;
   // slots, kBatch a thread at a time, so that their ids are read together
+  constexpr int kBatch = 1024 / kTile;
   const int n_out = (row1 - row0) * a.Hkv;
   const int dr = kThreads / a.Hkv, dh = kThreads - dr * a.Hkv;
   int r = tid / a.Hkv, h = tid - r * a.Hkv;
@@ -197,9 +197,12 @@ assign_pages_kernel(const AssignArgs a) {
 }  // namespace
 
 cudaError_t launch_assign_pages(const AssignArgs& a, cudaStream_t s) {
-  // 128 rows a CTA, or 256 where the sums over the requests would be formed too
-  // often: 351K slots 6.3 against 6.8 us, 802K slots 7.4 against 6.4.
-  const bool wide = (int64_t)a.n_rows * a.Hkv > 1 << 19;
+  // 128 rows a CTA; 256 where the CTAs, each of which goes through the requests in
+  // groups of kThreads, would not all be there at once (eight fit an SM).  us with 128
+  // against 256: 90,000 rows 5.2 / 6.1, 100,000 rows of 8 heads 5.7 / 5.5, 160,000 rows 6.5 /
+  // 6.5, 250,000 rows 7.9 / 6.5, 60,000 rows of 1,000 requests 8.7 / 6.7.
+  const int64_t groups = (a.B + kThreads - 1) / kThreads;
+  const bool wide = a.n_rows * groups > (int64_t)128 * 8 * device_sm_count();
   const int tile = wide ? 256 : 128;
   const int grid = a.n_rows > tile ? (a.n_rows + tile - 1) / tile : 1;
   return launch_programmatic(wide ? assign_pages_kernel<256> : assign_pages_kernel<128>, dim3(grid), dim3(kThreads), 0, s,
