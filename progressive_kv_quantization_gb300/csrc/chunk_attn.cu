@@ -111,6 +111,11 @@ struct Header {
 // ------------------------------------------------------------------ PTX
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// 16 bytes, or zeros where `bytes` is 0
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -638,6 +643,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int two_tokens = 2 / a.G, two_rows = 2 - two_tokens * a.G;
     while (const int n_items = next_list()) {
       // ================= softmax: group g, one row a thread
       const int g = warp >> 2;
@@ -648,36 +654,43 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         while (i >= 0 && (items[i].kind == kNothing || items[i].rows <= g * kGroupRows)) --i;
         return i;
       };
-      // this thread's row of an item's queries, as 16-byte pieces
-      auto query_row = [&](const Item& it) -> const uint4* {
-        const int row = it.row0 + g * kGroupRows + r, token = row / a.G;
-        if (g * kGroupRows + r >= it.rows || it.k0 == it.k1) return nullptr;
-        return reinterpret_cast<const uint4*>(a.q + (int64_t)(it.q_base + token) * a.q_stride +
-                                              (it.h * a.G + row - token * a.G) * kH);
-      };
-      // an item's queries to shared memory, swizzled; the products that read the
-      // item's before have all been seen to be done
+      // An item's queries on their way to shared memory, swizzled, 16 lanes a row; the
+      // products that read the item's before have all been seen to be done.
       auto load_queries = [&](const Item& it) {
         if (it.k0 == it.k1) return;
-        const uint4* src = query_row(it);
-        uint8_t* q = smem + kOffQ + g * kQBytes + r * 128;
-        uint4 v[16];
+        const int rows = it.rows - g * kGroupRows;
+        const int r0 = (warp & 3) * 32 + (lane >> 4), row = it.row0 + g * kGroupRows + r0;
+        int token = row / a.G, head = row - token * a.G;
+        const uint16_t* src = a.q + (int64_t)it.q_base * a.q_stride + it.h * a.G * kH + 8 * (lane & 15);
+        const uint32_t q = base + kOffQ + g * kQBytes + ((lane & 15) >> 3) * kBox;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = src ? src[x] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int x = 0; x < 16; ++x) *reinterpret_cast<uint4*>(q + (x >> 3) * kBox + (((x & 7) ^ (r & 7)) << 4)) = v[x];
+        for (int x = 0; x < 16; ++x) {
+          const int rx = r0 + 2 * x;
+          const bool real = rx < rows;   // rows past the item's last are zeros
+          copy_async16(q + rx * 128 + (((lane & 7) ^ (rx & 7)) << 4),
+                       real ? src + (int64_t)token * a.q_stride + head * kH : a.q, real ? 16 : 0);
+          head += two_rows;
+          token += two_tokens;
+          if (head >= a.G) {
+            head -= a.G;
+            ++token;
+          }
+        }
+      };
+      auto queries_there = [&](const Item& it) {
+        if (it.k0 == it.k1) return;
+        copies_done();
         fence_proxy_async();
         mbar_arrive(q_full(g));
       };
       int i = next_active(n_items - 1);
-      if (i >= 0) load_queries(items[i]);
+      if (i >= 0) {
+        load_queries(items[i]);
+        queries_there(items[i]);
+      }
       while (i >= 0 && !failed) {
         const Item& it = items[i];
         i = next_active(i - 1);
-        if (i >= 0) {   // on their way to L2 meanwhile
-          const uint4* src = query_row(items[i]);
-          if (src) asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(src));
-        }
         const int row = it.row0 + g * kGroupRows + r;
         const bool real = g * kGroupRows + r < it.rows;
         const int token = row / a.G, hq = it.h * a.G + row - token * a.G;
@@ -693,6 +706,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             failed = __any_sync(0xffffffffu, failed);
             if (failed) break;
             tc_fence_after();
+            if (j == n - 1 && i >= 0) load_queries(items[i]);   // the last product with this item's is done
             uint32_t s[128];
 #pragma unroll
             for (int x = 0; x < 4; ++x) tmem_ld32(t_s + 32 * x, s + 32 * x);
@@ -766,13 +780,14 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           }
           if (failed) break;
           // the next item's first product runs while this one's output is written
-          if (i >= 0) load_queries(items[i]);
+          if (i >= 0) queries_there(items[i]);
           if (!mbar_wait(o_done(g), (n_tile_g - 1) & 1, wait_ns)) failed = true;
           failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
           tc_fence_after();
         } else if (i >= 0) {
           load_queries(items[i]);
+          queries_there(items[i]);
         }
         // ---- the row's output, or its part
         const bool part = it.kind != kDirect;
@@ -824,6 +839,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 
   allow_dependent_launch();
   if (*s_abort) {
+    copies_done();
     // the copies and products in flight end before the memory they use is given up
     if (warp == kTmaWarp && lane == 0) {
       for (uint32_t u = n_kv_ring > kSlots ? n_kv_ring - kSlots : 0; u < n_kv_ring; ++u)
