@@ -607,12 +607,19 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             if (!wait(p_full(g), mma_tiles & 1)) break;
             ++mma_tiles;
             // One group's block of products (this P V, the next Q K) at a time: mixed, both
-            // blocks end late, the groups' softmaxes fall together and stay so, 1.8 us a tile
-            // of keys against 1.3.  (A matter of speed alone: the flags are plain, and
-            // nobody waits for long.)
+            // blocks end late, the groups' softmaxes fall together and stay so, 2.0 us a tile
+            // of keys against 1.4.  A group says that it wants to before it looks at the
+            // other, and the second one steps back, so that no two begin at once.  (A matter
+            // of speed alone: nobody waits for long.)
             if (both) {
-              for (int x = 0; x < kBusyPolls && s_busy[1 - g] != 0; ++x) {}
-              if (lane == 0) s_busy[g] = 1;
+              s_busy[g] = 1;
+              for (int x = 0; x < kBusyPolls && s_busy[1 - g] != 0; ++x) {
+                if (g == 1) {
+                  s_busy[1] = 0;
+                  for (; x < kBusyPolls && s_busy[0] != 0; ++x) {}
+                  s_busy[1] = 1;
+                }
+              }
             }
             tc_fence_after();
             if (elected()) {
