@@ -224,6 +224,11 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v, int wide) {
   }
 }
 
+// x / d for 32-bit x, with magic = ceil(2^64 / d) (0 for d = 1): exact
+__device__ __forceinline__ int div_by(int x, unsigned long long magic) {
+  return magic ? (int)__umul64hi((unsigned long long)(unsigned)x, magic) : x;
+}
+
 // ------------------------------------------------------------------ work split
 
 // A request's tiles on the cost line of one head, in 1/256 keys: tile m costs
@@ -260,7 +265,7 @@ __device__ __forceinline__ Request load_request(const ChunkArgs& a, int b) {
   r.ctx = min(max(ctx, 0), max_keys);
   r.tiles = (r.T * a.G + kTileRows - 1) / kTileRows;
   r.base = (long long)((a.causal ? max(r.ctx - r.T, 0) : r.ctx) + (r.T * a.G > kGroupRows ? 512 : 256)) << 8;
-  r.step = a.causal ? 65536 / a.G : 0;
+  r.step = a.causal ? div_by(65536, a.by_G) : 0;
   return r;
 }
 
@@ -297,24 +302,27 @@ __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, vola
     Wh += __shfl_sync(0xffffffffu, warp_scan(r.at(r.tiles)), 31);
   }
   const long long W = Wh * a.Hkv;
-  // CTAs that get a part (64-bit divisions would take as long as the rest of this)
-  unsigned n_cta = (unsigned)max(1ll, min((long long)gridDim.x, W >> (kMinKeysLog2 + 8)));
+  // CTAs that get a part (divisions would take as long as the rest of this)
+  int n_cta = (int)max(1ll, min((long long)gridDim.x, W >> (kMinKeysLog2 + 8)));
   // A multiple of the heads, where that leaves no more than 1/32 of the CTAs idle
   // or they are not all used anyway: then each head has its own CTAs.
-  const unsigned heads = (unsigned)a.Hkv, over = n_cta % heads;
-  const bool by_head = n_cta >= heads && (n_cta < gridDim.x || over * 32 <= gridDim.x);
+  const int grid = (int)gridDim.x, each = div_by(n_cta, a.by_heads), over = n_cta - each * a.Hkv;
+  const bool by_head = n_cta >= a.Hkv && (n_cta < grid || over * 32 <= grid);
   if (by_head) n_cta -= over;
-  const unsigned per = by_head ? n_cta / heads : n_cta, share = 0xFFFFFFFFu / per;
-  auto cut = [&](unsigned i) {   // where CTA i begins
+  const int per = by_head ? each : n_cta;
+  // about 2^32 / per: the same for all CTAs, and (per - 1) shares stay below 2^32
+  const unsigned share = __float2uint_rz(__fdividef(4294967040.0f, (float)per));
+  auto cut = [&](int i) {   // where CTA i begins
     if (i >= n_cta) return W;
-    const unsigned whole = i / per;
+    // i / per: i + 1/2 is 1 / (2 per) away from its multiples, and both are 256 at most
+    const unsigned whole = by_head ? (unsigned)__fdividef((float)i + 0.5f, (float)per) : 0u;
     const unsigned long long len = by_head ? Wh : W;
     return (long long)(whole * len + __umul64hi(len, (unsigned long long)((i - whole * per) * share) << 32));
   };
-  long long x0 = cut(blockIdx.x);
-  const long long x1 = cut(blockIdx.x + 1);
+  long long x0 = cut((int)blockIdx.x);
+  const long long x1 = cut((int)blockIdx.x + 1);
   while (x0 < x1) {
-    long long h = (long long)(__ll2float_rn(x0) / __ll2float_rn(Wh));   // off by one at most
+    long long h = (long long)__fdividef(__ll2float_rn(x0), __ll2float_rn(Wh));   // off by one at most
     h -= h * Wh > x0;
     h += (h + 1) * Wh <= x0;
     const long long seg0 = x0 - h * Wh, seg1 = min(x1 - h * Wh, Wh);
@@ -341,7 +349,7 @@ __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, vola
           if (at == kMaxItems) stop = h * Wh + p + r.at(m);
           break;
         }
-        const int last = min(r.T - 1, (int)(((long long)kTileRows * (m + 1) - 1) / a.G));
+        const int last = min(r.T - 1, div_by(kTileRows * (m + 1) - 1, a.by_G));
         const int n_kv = (visible(a, r.ctx, r.T, last) + kTileKeys - 1) / kTileKeys;
         const long long from = r.at(m), cost = r.at(m + 1) - from;
         const bool starts = lo <= from, ends = hi >= from + cost;
@@ -995,6 +1003,8 @@ cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {
   if (!bf16_page_map(&tk, a.k_pages, a.n_pool) || !bf16_page_map(&tv, a.v_pages, a.n_pool))
     return cudaErrorInvalidValue;
   a.n_cta = chunk_ctas();
+  a.by_G = a.G > 1 ? ~0ull / a.G + 1 : 0;
+  a.by_heads = a.Hkv > 1 ? ~0ull / a.Hkv + 1 : 0;
   a.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   a.slot_rows = chunk_slot_rows(a.n_rows, a.G);
   a.ws_hdr = workspace;

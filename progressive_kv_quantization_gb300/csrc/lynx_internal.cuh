@@ -279,6 +279,7 @@ struct ChunkArgs {
   // set by the launcher
   int n_cta, slot_rows;
   int out_wide;                 // out is 32-byte aligned
+  unsigned long long by_G, by_heads;   // ceil(2^64 / G), ceil(2^64 / Hkv); 0 for 1
   void* ws_hdr;
   float* ws_o;
 };
