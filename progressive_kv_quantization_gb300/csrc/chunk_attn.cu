@@ -75,6 +75,12 @@ constexpr int kMmaWarp = 8, kTmaWarp = 9, kListWarp = 10, kMmaWarp1 = 11;
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 208, kRegsOther = 80;   // of 168 each at launch: 256 x 208 + 128 x 80 <= 384 x 168
 constexpr int kMaxItems = 24;
+// Tiles of keys of a part, at least: a smaller one goes to the CTA with the rest, whose
+// tile then needs no join.  us with 1 / 2 / 3 / 4 / 6: one prompt of 2,048 tokens (32 / 8
+// heads) 50.6 / 45.5 / 50.0 / 49.4 / 51.8, eight of 1,024 59.2 / 57.1 / 57.1 / 57.3 / 59.8, 12
+// chunks of 300 before 5,000 keys 52.7 / 53.6 / 52.0 / 52.1 / 57.4.  Not where a CTA gets
+// fewer than 1,024 keys: 17 tokens over 1,000 keys 13.1 / 13.6.
+constexpr int kLeastPart = 2, kLeastPartKeysLog2 = 10;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kBusyPolls = 4096;               // some 100 us
@@ -309,6 +315,7 @@ __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, vola
   const int grid = (int)gridDim.x, each = div_by(n_cta, a.by_heads), over = n_cta - each * a.Hkv;
   const bool by_head = n_cta >= a.Hkv && (n_cta < grid || over * 32 <= grid);
   if (by_head) n_cta -= over;
+  const int least_part = W >> (kLeastPartKeysLog2 + 8) >= n_cta ? kLeastPart : 1;
   const int per = by_head ? each : n_cta;
   // about 2^32 / per: the same for all CTAs, and (per - 1) shares stay below 2^32
   const unsigned share = __float2uint_rz(__fdividef(4294967040.0f, (float)per));
@@ -363,7 +370,8 @@ __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, vola
         it.ctx = r.ctx;
         // where a cut falls among the tile's keys: the same function on both of its sides, not decreasing
         auto key_tile = [&](long long x) {
-          return min(n_kv, (int)(__ll2float_rn(x - from) * (float)n_kv / __ll2float_rn(cost)));
+          const int k = (int)(__ll2float_rn(x - from) * (float)n_kv / __ll2float_rn(cost));
+          return k < least_part ? 0 : k > n_kv - least_part ? n_kv : k;
         };
         it.k0 = starts ? 0 : key_tile(lo);
         it.k1 = ends ? n_kv : key_tile(hi);
