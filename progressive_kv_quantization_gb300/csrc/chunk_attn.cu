@@ -30,13 +30,14 @@
 //
 // What bounds it (GB300, 16 or 32 query heads over 4 or 8 KV heads).  Many rows: the
 // tensor core, 4 x 128 x 128 x 128 products in 2,048 clocks for two groups; a tile of
-// keys takes 1.36 us against 1.08 at the clock seen.  8,192 tokens before 8,192 to
-// 131,072 keys run at 1,640-1,730 TFLOP/s call after call (power-capped; the library's
-// BF16 matrix product does 1,849 in a burst, 1,663 sustained).  The rest is the
-// hand-over between softmax and products, ~430 clocks of a group's 2,800.  One token a
-// request over long contexts: memory, 6.25 TB/s of keys and values (92% of a copy).
-// A short prompt: 13 us, of which the two launches, the lists and one tile's chain of
-// waits are all but one.
+// keys takes 1.4 us against 1.08 at the clock seen.  2,048 tokens at the end of 131,072
+// keys run at 1,640-1,770 TFLOP/s call after call (power-capped; the library's BF16
+// matrix product does 1,849 in a burst, 1,663 sustained).  The rest is a group's chain:
+// softmax ~1,350 clocks, its products 1,024, hand-overs ~400.  A tile's start and end cost
+// ~4.5 us (first scores, last products, output), so that 3,000 tokens of six requests
+// over 8,000 keys run at 1,330.  One token a request over long contexts: memory, 6.27 TB/s
+// of keys and values (93% of a copy).  A short prompt: 12.8 us, of which the two launches,
+// the lists (~2.5 us) and one tile's chain of waits are all but one.
 //
 // Work split.  The tiles of all requests and heads stand on one line, each as
 // long as its estimated cost; the line is cut into equal parts, one a CTA, one
@@ -84,7 +85,8 @@ constexpr int kLeastPart = 2, kLeastPartKeysLog2 = 10;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kBusyPolls = 4096;               // some 100 us
-constexpr int kMinKeysLog2 = 8;                // least cost of a CTA's part of the work, in keys
+constexpr int kMinKeysLog2 = 7;                // least cost of a CTA's part of the work, in keys; us for 17 tokens
+                                               // over 1,000 keys: 12.8 (7), 13.2 (8), 16.1 (9)
 
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + 2 * kQBytes;
@@ -240,7 +242,7 @@ __device__ __forceinline__ int div_by(int x, unsigned long long magic) {
 // A request's tiles on the cost line of one head, in 1/256 keys: tile m costs
 // its keys (those before the chunk plus 256 / G more with every tile under a
 // causal mask) and, for its start and end, 512 keys, or 256 if one group does
-// (measured: 5.1 and 2.1 us a tile, 1.2 and 1.0 us for 128 keys).
+// (512 and 256 are the best of 384, 448, 512, 640 and 192, 256, 384).
 struct Request {
   int q_base, T, ctx, tiles;
   long long base, step;

@@ -9,19 +9,20 @@
 // computed as rsqrt(..) (x_a (w_a cos) - x_b (w_b sin)), the brackets once for a
 // row and all its heads; float32, rounded once to BF16.
 //
-// A half-warp holds one head of one row, 8 channels (16 bytes) a lane; a pair's
-// other half is rot / 16 lanes away (a shuffle) or in the same lane.  A CTA takes
-// 32 rows and either a group of query heads or one KV head (or a part of its
-// channels).  Cosines and sines stay in registers over the heads of a row.  Keys
-// and values pass through shared memory, token-major in, and leave with one token
-// per lane: where slots follow one another (a chunk of one request) a warp's store
-// is 64 contiguous bytes of a channel row.
+// A half-warp holds one head of one row, 8 channels (16 bytes) a lane: 8 neighbours, or
+// for half-split pairs four of the first half and the four that belong to them, so
+// that a pair is in one lane (16 + 4 heads, 4,096 rows: 10.1 us; with 8 neighbours and an
+// exchange between lanes 12.5).  A CTA takes 32 rows and either a group of query heads or
+// one KV head (or a part of its channels).  Cosines and sines stay in registers over
+// the heads of a row.  Keys and values pass through shared memory, token-major in, and
+// leave with one token per lane: where slots follow one another (a chunk of one request)
+// a warp's store is 64 contiguous bytes of a channel row.
 //
-// What bounds it on a GB300.  Many rows: memory; 27,000 rows of 32 + 8 heads take
-// 119 us, 5.7 TB/s read and written (84% of a copy; the slots' 2-byte stores meet in
-// L2, DRAM moves the algorithmic bytes).  Some thousand rows (12.5 us for 4,096 of 16 +
-// 4 heads, half-split pairs and norms, all in L2): latency at 32 warps an SM (64
-// registers), the exchange of pairs the longest part.  A decode step of 64 rows (3.3 us):
+// What bounds it on a GB300.  Many rows: memory; 40,000 rows of 32 + 8 heads take 166 us,
+// 6.1 TB/s read and written (90% of a copy; the slots' 2-byte stores meet in L2, DRAM
+// moves the algorithmic bytes), 27,292 rows with norms and a half of each head rotated
+// interleaved 120 us (83%).  Some thousand rows, all in L2: latency at 32 warps an SM (64
+// registers; 5.2 TB/s for 4,096 rows of 16 + 4 heads).  A decode step of 64 rows (2.8 us):
 // the launch, the position and then the cosines at it.
 
 #include "f32x2.cuh"
@@ -271,8 +272,8 @@ cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s) {
   // Order of the CTAs: one job's tiles side by side (neighbours write
   // neighbouring slots while the lines are in L2), or, where rows and pages exceed
   // L2, one tile's jobs (what runs at a time reads whole rows of DRAM).  us for
-  // 4,096 rows of 16 + 4 heads: 11.1 against 13.4; 40,000 rows of 32 + 8: 206
-  // against 190.
+  // 4,096 rows of 16 + 4 heads: 10.1 against 13.1; 40,000 rows of 32 + 8: 180
+  // against 166.
   a.whole_rows = a.n_rows * (a.Hq + 2 * a.Hkv) * (4 * kH) > ((int64_t)100 << 20);
   const unsigned grid = (unsigned)(tiles * (a.q_jobs + a.Hkv * a.kv_parts));
   return launch_programmatic(a.interleaved ? qkv_append_kernel<true> : qkv_append_kernel<false>, dim3(grid),
