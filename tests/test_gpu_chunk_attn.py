@@ -136,6 +136,29 @@ def test_requests_of_one_group_between_requests_of_two(cuda_device):
         check(x, True, *call(x, True))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv", [
+    ([3, 1, 40], [300, 2000, 600], 128, 1), ([2, 5], [700, 5], 300, 1), ([1, 7], [900, 260], 257, 1),
+    ([1, 70, 3], [400, 300, 5], 160, 160), ([2, 129], [200, 129], 304, 152), ([1] * 9, [513] * 9, 200, 40)])
+def test_many_heads_of_either_kind(cuda_device, new, ctx, Hq, Hkv, causal):
+    """More query heads a group than half a tile or a whole one has rows, and more KV
+    heads than there are CTAs."""
+    x = batch(new, ctx, Hq, Hkv, Hq + Hkv)
+    check(x, causal, *call(x, causal))
+
+
+def test_a_prompt_cut_everywhere(cuda_device):
+    """Prompts of every length around the tile's, so that cuts fall near both ends of
+    tiles of few keys."""
+    rng = np.random.default_rng(3)
+    new = [int(n) for n in rng.integers(1, 420, 60)]
+    x = batch(new, [n + int(rng.integers(0, 300)) for n in new], 8, 2, 17)
+    check(x, True, *call(x, True))
+    for n in (1500, 1537, 1999, 2048):
+        x = batch([n], [n + n % 5], 16, 8, n)
+        check(x, True, *call(x, True))
+
+
 def test_rows_that_see_no_key(cuda_device):
     # more new tokens than keys: the first rows see none
     x = batch([300, 5], [100, 0], 4, 2, 8)

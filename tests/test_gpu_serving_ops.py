@@ -323,6 +323,19 @@ def test_verify_large_vocabulary_limit(cuda_device):
                              torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, 2, device="cuda"))
 
 
+def test_verify_many_requests_of_the_largest_vocabulary(cuda_device):
+    """One CTA a request with all 4,096 of its runs: uniform rows, whose tokens follow
+    from u alone (each weight is 2^20 units of a sum of 2^40)."""
+    B, V = 200, 1 << 20
+    p = torch.full((1, 2, V), 2.0 ** -20, dtype=torch.bfloat16, device="cuda").expand(B, 2, V)
+    u = torch.rand(B, 2, generator=torch.Generator("cuda").manual_seed(4), device="cuda")
+    u[0, 1], u[1, 1] = 0.0, 1.0 - 2.0 ** -24
+    draft = torch.full((B, 1), -1, dtype=torch.int32, device="cuda")
+    tok, n = L.lynx_verify_drafts(p, None, draft, u)
+    want = (u[:, 1].double() * 2.0 ** 24).floor().long() >> 4
+    assert torch.equal(tok[:, 0].long(), want) and (tok[:, 1] == -1).all() and (n == 0).all()
+
+
 # --------------------------------------------------------------- graphs and streams
 
 def test_operators_in_a_captured_graph(cuda_device):
