@@ -18,7 +18,7 @@
 // entries (it takes the id from the free list itself), so nothing races.
 //
 // Bound by the launch and the chain lengths -> sums -> row -> table -> slot: 3.1 us for a
-// decode step of 64 requests (the host's call; 2.8 us on the GPU), 5.7 us for 100,000
+// decode step of 64 requests (the host's call; 2.6 us on the GPU), 5.5 us for 100,000
 // rows of 8 heads, whose slots (8 bytes a row and head) would take 1 us at the memory's
 // rate.
 
@@ -47,7 +47,7 @@ struct Row {
 constexpr int kBegins = kP;
 
 template <int kTile>   // rows per CTA
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)   // 48 registers: all ids of a thread in flight (34: 11% slower)
 assign_pages_kernel(const AssignArgs a) {
   __shared__ int s_rows[kThreads];   // rows before request i of the group
   __shared__ int s_free[kThreads];   // first free-list index of request i
@@ -70,11 +70,14 @@ assign_pages_kernel(const AssignArgs a) {
   allow_dependent_launch();
   wait_prerequisite_grids();
 
+  auto lengths = [&](int b) { return b < a.B ? make_int2(a.ctx_len[b], a.new_len[b]) : make_int2(0, 0); };
+  int2 next = lengths(tid);   // of the next group, on their way
   int rows_before = 0, free_before = 0;   // over the groups behind us
   for (int b0 = 0; b0 < a.B && (first || rows_before < row1); b0 += kThreads) {
     const int b = b0 + tid;
     const bool in = b < a.B;
-    const int ctx = in ? a.ctx_len[b] : 0, asked = in ? a.new_len[b] : 0;
+    const int ctx = next.x, asked = next.y;
+    next = lengths(b + kThreads);
     bool valid = in && ctx >= 0 && asked >= 0 && (long long)ctx + asked <= max_keys;
     if (in && !valid && first) atomicExch(a.status, 3);
     const int rows = min(max(asked, 0), kMost);
@@ -85,27 +88,33 @@ assign_pages_kernel(const AssignArgs a) {
     // rows do not fit count too: behind it no request with rows fits, so no sum
     // that matters has them.
     int row_end = rows, free_end = ids;
+    auto scan = [&](int steps) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, row_end, o), v = __shfl_up_sync(0xffffffffu, free_end, o);
-      if (lane >= o) {
-        row_end = add(row_end, u);
-        free_end = add(free_end, v);
+      for (int o = 1; o < steps; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, row_end, o), v = __shfl_up_sync(0xffffffffu, free_end, o);
+        if (lane >= o) {
+          row_end = add(row_end, u);
+          free_end = add(free_end, v);
+        }
       }
-    }
+    };
+    scan(32);
     if (lane == 31) s_warp[warp] = make_int2(row_end, free_end);
     __syncthreads();
-    int rows_warp = rows_before, free_warp = free_before;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int2 u = s_warp[w];
-      rows_before = add(rows_before, u.x);
-      free_before = add(free_before, u.y);
-      if (w < warp) {
-        rows_warp = add(rows_warp, u.x);
-        free_warp = add(free_warp, u.y);
-      }
-    }
+    // the sums of the warps in front of this one, and of all
+    const int row_mine = row_end, free_mine = free_end;
+    const int2 u = lane < kThreads / 32 ? s_warp[lane] : make_int2(0, 0);
+    row_end = u.x;
+    free_end = u.y;
+    scan(kThreads / 32);
+    const int before = max(warp - 1, 0);
+    int rows_warp = __shfl_sync(0xffffffffu, row_end, before), free_warp = __shfl_sync(0xffffffffu, free_end, before);
+    rows_warp = add(rows_before, warp > 0 ? rows_warp : 0);
+    free_warp = add(free_before, warp > 0 ? free_warp : 0);
+    rows_before = add(rows_before, __shfl_sync(0xffffffffu, row_end, kThreads / 32 - 1));
+    free_before = add(free_before, __shfl_sync(0xffffffffu, free_end, kThreads / 32 - 1));
+    row_end = row_mine;
+    free_end = free_mine;
     row_end = add(row_end, rows_warp);
     free_end = add(free_end, free_warp);
     valid = valid && row_end <= a.n_rows;
@@ -197,12 +206,13 @@ assign_pages_kernel(const AssignArgs a) {
 }  // namespace
 
 cudaError_t launch_assign_pages(const AssignArgs& a, cudaStream_t s) {
-  // 128 rows a CTA; 256 where the CTAs, each of which goes through the requests in
-  // groups of kThreads, would not all be there at once (eight fit an SM).  us with 128
-  // against 256: 90,000 rows 5.2 / 6.1, 100,000 rows of 8 heads 5.7 / 5.5, 160,000 rows 6.5 /
-  // 6.5, 250,000 rows 7.9 / 6.5, 60,000 rows of 1,000 requests 8.7 / 6.7.
+  // 128 rows a CTA, or 256 where the sums would be formed by too many CTAs: by more than
+  // eight an SM, or four where a CTA has few slots to write.  us with 128 against 256, by
+  // rows and heads: 70,000 x 4 4.4 / 4.7, 90,000 x 4 4.4 / 4.0, 120,000 x 1 4.8 / 4.4, 250,000 x 1
+  // 7.7 / 5.3, 60,000 x 8 4.7 / 6.0, 100,000 x 8 5.5 / 6.0, 120,000 x 8 6.0 / 6.1, of 1,000 requests
+  // 60,000 x 8 6.8 / 6.0.
   const int64_t groups = (a.B + kThreads - 1) / kThreads;
-  const bool wide = a.n_rows * groups > (int64_t)128 * 8 * device_sm_count();
+  const bool wide = a.n_rows * groups > (int64_t)128 * (a.Hkv > 4 ? 8 : 4) * device_sm_count();
   const int tile = wide ? 256 : 128;
   const int grid = a.n_rows > tile ? (a.n_rows + tile - 1) / tile : 1;
   return launch_programmatic(wide ? assign_pages_kernel<256> : assign_pages_kernel<128>, dim3(grid), dim3(kThreads), 0, s,
