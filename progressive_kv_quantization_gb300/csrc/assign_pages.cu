@@ -119,9 +119,11 @@ assign_pages_kernel(const AssignArgs a) {
     free_end = add(free_end, free_warp);
     valid = valid && row_end <= a.n_rows;
     const bool granted = valid && (need == 0 || free_end <= a.n_free);
-    const int row_begin = row_end - rows;   // of no use where the sum has been cut off, and not used
-    s_rows[tid] = row_begin;
-    s_free[tid] = free_end - ids;
+    // The first row is the sum of the requests in front, not row_end - rows: that is too
+    // small where the sum has been cut off, and the bisection needs s_rows in order.
+    const int rows_lanes = __shfl_up_sync(0xffffffffu, row_mine, 1);
+    s_rows[tid] = add(rows_warp, lane > 0 ? rows_lanes : 0);
+    s_free[tid] = free_end - ids;   // read of granted requests, whose sums are whole
     s_ctx[tid] = ctx;
     s_held[tid] = granted ? held : -1;
     if (first && in) {

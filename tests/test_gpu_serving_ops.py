@@ -98,6 +98,37 @@ def test_assign_pages_takes_the_rest_of_a_list(cuda_device):
     status_ok()
 
 
+@pytest.mark.parametrize("huge", [2 ** 30 - 3, 2 ** 30, 2 ** 30 + 1, 2 ** 31 - 1])
+@pytest.mark.parametrize("at", [1, 2, 31, 32, 33, 64, 255, 256, 257, 300])
+def test_assign_pages_a_huge_request_is_refused_alone(cuda_device, at, huge):
+    """Its length passes what the running sums hold; the requests in front of it keep
+    their rows and pages, those behind it that ask for nothing their lengths."""
+    rng = np.random.default_rng(at)
+    Hkv, max_pages, B = 2, 3, at + 6
+    ctx = rng.integers(0, 600, B)
+    new = rng.integers(0, 4, B)
+    new[rng.random(B) < 0.3] = 150                     # some take fresh pages
+    new = np.minimum(new, max_pages * 256 - ctx)
+    new[0] = 5
+    new[at:] = [huge, 0, 3, 0, huge, 0]
+    ids = rng.permutation(2 * B * Hkv * max_pages)
+    table = ids[:B * Hkv * max_pages].reshape(B, Hkv, max_pages)
+    for behind in (0, 3, 200):
+        got = check_assign(ctx, new, table, ids[B * Hkv * max_pages:], int(new[:at].sum()) + behind)
+        assert int(got[3][0]) == ctx[0] + 5 and int(got[1][0]) == ctx[0]
+    torch.cuda.synchronize()
+    with pytest.raises(L.LynxError, match="ctx_len"):
+        L.lynx_device_status()
+
+
+def test_assign_pages_a_huge_request_that_its_table_would_hold(cuda_device):
+    """The same with a length that is in order: its rows do not fit, the others' do."""
+    max_pages = (1 << 22) + 1
+    ctx, new = np.array([0, 10, 255, 7]), np.array([4, 3, 2 ** 30, 0])
+    check_assign(ctx, new, np.zeros((4, 1, max_pages), dtype=np.int64), np.arange(100, 103), 10)
+    status_ok()
+
+
 # --------------------------------------------------------------- QKV append
 
 def check_append(n_rows, Hq, Hkv, rot, interleaved, norm, seed, pad_cols=0, skip=0.0, run=True):
