@@ -492,7 +492,9 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
  *               one each.
  * Scores and sums in float32; the probabilities are rounded to BF16 for the
  * product with the values (their sum is not), an error of about 2^-9 / sqrt(keys
- * that matter) of the output, at most 2^-8.  Keys and values of positions below
+ * that matter) of the output, at most 2^-8; the matrix unit's additions are cut
+ * off, an error of at most 2^-13 of the probabilities' sum over the values'
+ * magnitudes, however long the context.  Keys and values of positions below
  * ctx_len must be finite; positions past it in the last page may hold anything.
  * Limits: Hq % Hkv == 0, B <= 65535, n_rows * Hq / Hkv <= 2^30, n_pool_pages <
  * 2^24. */

@@ -28,10 +28,16 @@
 // most, either way, so that over many keys it falls below the BF16 output's own
 // rounding.
 //
+// Sums of long contexts.  What the tensor core's float32 accumulator does not hold is
+// cut off and not rounded, so that the errors of O's additions add up: -5e-5 of the value
+// over 16,384 keys, -4.8e-4 over 131,072, -4e-3 over a million (values of one sign).  So O
+// is taken out every 16,384 keys and added up, rounded, in the workspace: some 6,000
+// clocks for both groups, most of them L2's for 128 KB a CTA, 3% of 131,072 keys' time.
+//
 // What bounds it (GB300, 16 or 32 query heads over 4 or 8 KV heads).  Many rows: the
 // tensor core, 4 x 128 x 128 x 128 products in 2,048 clocks for two groups; a tile of
 // keys takes 1.4 us against 1.08 at the clock seen.  2,048 tokens at the end of 131,072
-// keys run at 1,640-1,770 TFLOP/s call after call (power-capped; the library's BF16
+// keys run at some 1,620 TFLOP/s call after call (power-capped; the library's BF16
 // matrix product does 1,849 in a burst, 1,663 sustained).  The rest is a group's chain:
 // softmax ~1,350 clocks, its products 1,024, hand-overs ~400.  A tile's start and end cost
 // ~4.5 us (first scores, last products, output), so that 3,000 tokens of six requests
@@ -84,6 +90,11 @@ constexpr int kMaxItems = 24;
 constexpr int kLeastPart = 2, kLeastPartKeysLog2 = 10;
 constexpr int kMaxCtas = 256;                  // of the grid; the GB300's 152 SMs get one each
 constexpr float kLazyLog2 = 8.0f;
+// Tiles of keys that are summed up in tensor memory.  Error (131,072 keys, values with an
+// offset) and us with 64 / 128 / 256: 3.1e-5, 1,371 / 6.7e-5, 1,345 / 1.3e-4, 1,332; never
+// taken out: 4.9e-4, 1,307.
+constexpr int kSumTiles = 128;
+static_assert((kSumTiles & (kSumTiles - 1)) == 0, "kSumTiles");
 constexpr int kBusyPolls = 4096;               // some 100 us
 constexpr int kMinKeysLog2 = 7;                // least cost of a CTA's part of the work, in keys; us for 17 tokens
                                                // over 1,000 keys: 12.8 (7), 13.2 (8), 16.1 (9)
@@ -91,7 +102,7 @@ constexpr int kMinKeysLog2 = 7;                // least cost of a CTA's part of 
 constexpr int kOffQ = 0;
 constexpr int kOffRing = kOffQ + 2 * kQBytes;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
-constexpr int kNumBars = 2 * kSlots + 9;
+constexpr int kNumBars = 2 * kSlots + 10;
 constexpr int kOffItems = kOffBar + 8 * kNumBars;
 constexpr int kItemInts = 10;
 constexpr int kOffMisc = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
@@ -438,6 +449,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   auto p_full = [&](int g) { return bars + 8 * (4 + g); };
   auto o_done = [&](int g) { return bars + 8 * (6 + g); };
   const uint32_t drained = bars + 8 * 8;   // used once, by a CTA that gives up
+  const uint32_t met = bars + 8 * 9;       // both groups, behind a sum that was taken out
 
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
@@ -451,6 +463,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       mbar_init(o_done(g), 1);
     }
     mbar_init(drained, 2);
+    mbar_init(met, 2 * kGroupRows);
     *s_hdr = Header{0, 0, 0, 0, 0, 0, 0, 0};
     *s_abort = 0;
     s_busy[0] = s_busy[1] = 0;
@@ -479,6 +492,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   // counters of each role, running over all items
   uint32_t n_kv_ring = 0;     // K and V tiles through the ring (producer; MMA warp)
   uint32_t n_tile_g = 0;      // S tiles of this thread's group (softmax)
+  uint32_t n_met = 0;         // phases of `met`
   uint32_t mma_items = 0, mma_tiles = 0;   // of the tensor-core warp's group
   bool failed = false;
 
@@ -640,15 +654,16 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               }
             }
             tc_fence_after();
+            const bool more = (j & (kSumTiles - 1)) != 0;   // to the sum in O, or O begins again
             if (elected()) {
               const uint64_t v = v_desc + (uint64_t)(sv * (kSlot >> 4));
               if (steps == 8) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, j > 0 || ks > 0);
+                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, more || ks > 0);
               } else {
                 for (int ks = 0; ks < steps; ++ks)
-                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, j > 0 || ks > 0);
+                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, more || ks > 0);
               }
               tc_commit(o_done(g));
               tc_commit(kv_empty(sv));
@@ -726,82 +741,143 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           // rows past the tile's last hold zero queries: whatever they sum up is not written
           const int seen = real ? visible(a, it.ctx, it.T, token) : 0x7fffffff;
           const float sc = a.scale_log2;
-          for (int j = 0; j < n; ++j) {
-            if (!mbar_wait(s_full(g), n_tile_g & 1, wait_ns)) failed = true;
+          for (int j = 0;;) {
+            const int j0 = j, j1 = min(n, j0 + kSumTiles);
+            for (; j < j1; ++j) {
+              if (!mbar_wait(s_full(g), n_tile_g & 1, wait_ns)) failed = true;
+              failed = __any_sync(0xffffffffu, failed);
+              if (failed) break;
+              tc_fence_after();
+              if (j == n - 1 && i >= 0) load_queries(items[i]);   // the last product with this item's is done
+              uint32_t s[128];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) tmem_ld32(t_s + 32 * x, s + 32 * x);
+              tmem_wait_ld32(s);
+              tmem_hold32(s + 32);
+              tmem_hold32(s + 64);
+              tmem_hold32(s + 96);
+              const int left = seen - (it.k0 + j) * kTileKeys;
+              if (__any_sync(0xffffffffu, left < kTileKeys)) {
+#pragma unroll
+                for (int x = 0; x < 128; ++x)
+                  if (x >= left) s[x] = 0xFF800000u;   // -inf
+              }
+              // P against the running maximum as it stands, and the tile's maximum beside
+              // it: the two do not wait for one another (1.36 us a tile of keys against 1.5 one
+              // after the other).  Where the maximum has to move P is computed again.
+              const uint64_t sc2 = pair(sc, sc);
+              uint64_t sum[4];
+              auto exps = [&](float ref) {
+                const uint64_t ref2 = pair(ref, ref);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sum[x] = 0ull;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  uint32_t p[16];
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    float p0, p1;
+                    unpair(fma2(pair(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), sc2, ref2), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
+                    sum[e & 3] = add2(sum[e & 3], pair(p0, p1));
+                    p[e] = bf16x2(p0, p1);
+                  }
+                  tmem_st16(t_s + 16 * x, p);
+                }
+              };
+              exps(m == -CUDART_INF_F ? 0.0f : -m);
+              float mx[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) mx[x] = fmaxf(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+#pragma unroll
+              for (int x = 8; x < 64; ++x)
+                mx[x & 7] = max3(mx[x & 7], __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+              const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
+              if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
+                const float m_new = fmaxf(m, top);
+                const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - m_new);
+                if (j > j0) {   // rescale O, to which the product before has been added (its commit came first)
+                  const float fo = m == -CUDART_INF_F ? 1.0f : f;   // O is 0 there
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) {
+                    uint32_t o[16];
+                    tmem_ld16(t_o + 16 * x, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+                    tmem_st16(t_o + 16 * x, o);
+                  }
+                }
+                l *= f;
+                m = m_new;
+                exps(m == -CUDART_INF_F ? 0.0f : -m);
+              }
+              float l0, l1;
+              unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+              l += l0 + l1;
+              tmem_wait_st_();
+              tc_fence_before();
+              mbar_arrive(p_full(g));
+              ++n_tile_g;
+            }
+            if (failed || n <= kSumTiles) break;
+            // O, once the last product of a segment of keys from j0 on is done, goes to the
+            // row's sum in the CTA's third slot, which is laid out as a part with the maximum
+            // that it is against; behind the last segment the sum goes to O.
+            const bool last = j == n;
+            if (!mbar_wait(last ? o_done(g) : s_full(g), (last ? n_tile_g - 1 : n_tile_g) & 1, wait_ns)) failed = true;
             failed = __any_sync(0xffffffffu, failed);
             if (failed) break;
             tc_fence_after();
-            if (j == n - 1 && i >= 0) load_queries(items[i]);   // the last product with this item's is done
-            uint32_t s[128];
+            float* sum = a.ws_o + (int64_t)(2 * a.n_cta + c) * a.slot_rows * (kH + 2);
+            float* sum_max = sum + a.slot_rows * kH + g * kGroupRows + r;
+            float4* sum_o = reinterpret_cast<float4*>(sum) + g * kGroupRows + r;
+            const bool add = j0 > 0 && real;
+            const float m_sum = add ? *sum_max : -CUDART_INF_F;
+            const float f = m_sum == -CUDART_INF_F ? 1.0f : ex2(m_sum - m);   // no keys yet: the sum is 0, or NaN and stays so
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              uint32_t o[64];
+              float4 u[16];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) tmem_ld32(t_s + 32 * x, s + 32 * x);
-            tmem_wait_ld32(s);
-            tmem_hold32(s + 32);
-            tmem_hold32(s + 64);
-            tmem_hold32(s + 96);
-            const int left = seen - (it.k0 + j) * kTileKeys;
-            if (__any_sync(0xffffffffu, left < kTileKeys)) {
+              for (int e = 0; e < 16; ++e)
+                u[e] = add ? sum_o[(16 * x + e) * a.slot_rows] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-              for (int x = 0; x < 128; ++x)
-                if (x >= left) s[x] = 0xFF800000u;   // -inf
-            }
-            // P against the running maximum as it stands, and the tile's maximum beside
-            // it: the two do not wait for one another (1.36 us a tile of keys against 1.5 one
-            // after the other).  Where the maximum has to move P is computed again.
-            const uint64_t sc2 = pair(sc, sc);
-            uint64_t sum[4];
-            auto exps = [&](float ref) {
-              const uint64_t ref2 = pair(ref, ref);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) sum[x] = 0ull;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  float p0, p1;
-                  unpair(fma2(pair(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), sc2, ref2), p0, p1);
-                  p0 = ex2(p0);
-                  p1 = ex2(p1);
-                  sum[e & 3] = add2(sum[e & 3], pair(p0, p1));
-                  p[e] = bf16x2(p0, p1);
-                }
-                tmem_st16(t_s + 16 * x, p);
+              for (int y = 0; y < 2; ++y) {
+                tmem_ld32(t_o + 64 * x + 32 * y, o + 32 * y);
+                tmem_wait_ld32(o + 32 * y);
               }
-            };
-            exps(m == -CUDART_INF_F ? 0.0f : -m);
-            float mx[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) mx[x] = fmaxf(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
-#pragma unroll
-            for (int x = 8; x < 64; ++x)
-              mx[x & 7] = max3(mx[x & 7], __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
-            const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
-            if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
-              const float m_new = fmaxf(m, top);
-              const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - m_new);
-              if (j > 0) {   // rescale O, to which the product before has been added (its commit came first)
-                const float fo = m == -CUDART_INF_F ? 1.0f : f;   // O is 0 there
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                  uint32_t o[16];
-                  tmem_ld16(t_o + 16 * x, o);
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
-                  tmem_st16(t_o + 16 * x, o);
-                }
+              for (int e = 0; e < 16; ++e) {
+                o[4 * e] = __float_as_uint(fmaf(u[e].x, f, __uint_as_float(o[4 * e])));
+                o[4 * e + 1] = __float_as_uint(fmaf(u[e].y, f, __uint_as_float(o[4 * e + 1])));
+                o[4 * e + 2] = __float_as_uint(fmaf(u[e].z, f, __uint_as_float(o[4 * e + 2])));
+                o[4 * e + 3] = __float_as_uint(fmaf(u[e].w, f, __uint_as_float(o[4 * e + 3])));
+                if (real && !last)
+                  reinterpret_cast<uint4*>(sum_o)[(16 * x + e) * a.slot_rows] =
+                      make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
               }
-              l *= f;
-              m = m_new;
-              exps(m == -CUDART_INF_F ? 0.0f : -m);
+              __syncwarp();
+              if (last) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) tmem_st16(t_o + 64 * x + 16 * y, o + 16 * y);
+              }
             }
-            float l0, l1;
-            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
-            l += l0 + l1;
-            tmem_wait_st_();
-            tc_fence_before();
-            mbar_arrive(p_full(g));
-            ++n_tile_g;
+            if (last) {
+              tmem_wait_st_();
+              break;
+            }
+            if (real) *sum_max = m;
+            // Begun one behind the other by more than a tile of keys, the groups stay so
+            // and leave the ring no room to load ahead: 3,300 clocks a tile of keys against
+            // 2,740.
+            if (it.rows > kGroupRows) {
+              mbar_arrive(met);
+              if (!mbar_wait(met, n_met & 1, wait_ns)) failed = true;
+              ++n_met;
+              failed = __any_sync(0xffffffffu, failed);
+              if (failed) break;
+            }
           }
           if (failed) break;
           // the next item's first product runs while this one's output is written
@@ -995,7 +1071,7 @@ int chunk_slot_rows(int64_t n_rows, int G) {
 }
 
 size_t chunk_ws_bytes(int64_t n_rows, int G) {
-  return (size_t)kMaxCtas * sizeof(Header) + (size_t)2 * chunk_ctas() * chunk_slot_rows(n_rows, G) * (kH + 2) * 4;
+  return (size_t)kMaxCtas * sizeof(Header) + (size_t)3 * chunk_ctas() * chunk_slot_rows(n_rows, G) * (kH + 2) * 4;
 }
 
 cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {

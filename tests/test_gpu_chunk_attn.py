@@ -404,3 +404,79 @@ def test_context_offsets_pass_32_bits(cuda_device):
     torch.cuda.synchronize()
     L.lynx_device_status()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("n", [131072, 400001])
+def test_sums_over_long_contexts_do_not_drift(cuda_device, n):
+    """2,048 tokens at the end of a long context, float32 output, sampled rows.  With p the
+    row's probabilities:
+      P's rounding: independent errors of at most 2^-8 p_j, 2^-8 / sqrt(3) p_j in the mean
+        square; 7 standard deviations are below 4 * 2^-8 sqrt(sum p_j^2 v_j^2);
+      the matrix unit's float32 sums, which are cut off and not rounded, so that their
+        errors add up: a unit of 2^-23 for each of 1,024 additions of 16 keys, after which
+        the sum is taken out and added up rounded: 2^-13 sum p_j |v_j|;
+      scores and all else in float32: 2^-15 sum p_j |v_j|."""
+    T, Hq, Hkv = 2048, 16, 4
+    x = batch([T], [n], Hq, Hkv, n)
+    v = x["v"]
+    v.copy_(torch.where(torch.isfinite(v), v.abs() + 0.1, v))     # one sign: what is cut off adds up
+    out, lse = call(x, True, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    rng = np.random.default_rng(n)
+    ids = x["table"][0].long()
+    err = []
+    for t in [0, 1, T - 1, *rng.integers(0, T, 20)]:
+        h = int(rng.integers(0, Hq))
+        seen = n - T + int(t) + 1
+        k = x["k"][ids[h // 4]].permute(0, 2, 1).reshape(-1, D)[:seen].double()
+        v = x["v"][ids[h // 4]].permute(0, 2, 1).reshape(-1, D)[:seen].double()
+        s = k @ x["q"][int(t), h].double() / math.sqrt(D)
+        p = torch.softmax(s, 0)
+        o, d = p @ v, out[int(t), h].double() - p @ v
+        lim = 2.0 ** -6 * torch.sqrt(p.square() @ v.square()) + (2.0 ** -13 + 2.0 ** -15) * (p @ v.abs())
+        assert bool((d.abs() <= lim).all()), float((d.abs() / lim).max())
+        assert abs(float(torch.logsumexp(s, 0)) - float(lse[int(t), h])) < LSE_TOL
+        err.append(float((d / o).mean()))
+    # and together: P's rounding falls out of the mean over rows and channels
+    assert abs(np.mean(err)) < 2.0 ** -13 + 2.0 ** -15
+
+
+@pytest.mark.parametrize("shape", ["up", "down", "late", "flat"])
+@pytest.mark.parametrize("new,n", [([1] * 200, 40000), ([100] * 80, 33000)])
+def test_sums_that_are_taken_out_follow_the_running_maximum(cuda_device, new, n, shape):
+    """So many requests over one long context that a CTA goes through tens of thousands of
+    keys: its sums are taken out against one maximum and go on against another.  One
+    group of rows a tile, and both.  The bound is that of the test above."""
+    Hq, Hkv, B = 2, 1, len(new)
+    x = batch([sum(new)], [n], Hq, Hkv, n)
+    ids = x["table"][0, 0].long()
+    pos = torch.arange(ids.numel() * 256, device="cuda").float()
+    ramp = {"up": pos / 1000, "down": -pos / 1000, "late": 40.0 * (pos == n - 7000), "flat": 0 * pos}[shape]
+    k = x["k"][ids]
+    k[:, 0, :] = torch.where(torch.isfinite(k[:, 0, :].float()), ramp.view(-1, 256).bfloat16(), k[:, 0, :])
+    x["k"][ids] = k
+    x["q"][:, :, 0] = 8.0
+    x["cu"] = torch.tensor([sum(new[:b]) for b in range(B + 1)], dtype=torch.int32, device="cuda")
+    x["ctx"] = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    x["table"] = x["table"].expand(B, -1, -1).contiguous()
+    size = L.lynx_chunk_attn_workspace_size(sum(new), B, Hq, Hkv, D)
+    ws = torch.full((size + 512,), 0xFF, dtype=torch.uint8, device="cuda")     # NaN in every place
+    a = call(x, True, out_dtype=torch.float32, workspace=ws[256:256 + size])
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    assert (ws[:256] == 0xFF).all() and (ws[256 + size:] == 0xFF).all()
+    b = call(x, True, out_dtype=torch.float32)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    keys = x["k"][ids].permute(0, 2, 1).reshape(-1, D).double()
+    vals = x["v"][ids].permute(0, 2, 1).reshape(-1, D).double()
+    for i, r in enumerate(np.random.default_rng(n).integers(0, sum(new), 30)):
+        t = int(r) % new[0]
+        seen = n - new[0] + t + 1
+        s = keys[:seen] @ x["q"][int(r), i % 2].double() / math.sqrt(D)
+        p, v = torch.softmax(s, 0), vals[:seen]
+        d = (a[0][int(r), i % 2].double() - p @ v).abs()
+        # scores here go up to 8 * 40 / sqrt(128) = 28 more: 128 additions of 2^-24 of that
+        lim = 2.0 ** -6 * torch.sqrt(p.square() @ v.square()) + (2.0 ** -13 + 2.0 ** -15 + 2.0 ** -12) * (p @ v.abs())
+        assert bool((d <= lim).all()), float((d / lim).max())
+        assert abs(float(torch.logsumexp(s, 0)) - float(a[1][int(r), i % 2])) < 2 * LSE_TOL
