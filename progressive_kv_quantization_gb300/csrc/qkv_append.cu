@@ -21,7 +21,7 @@
 // What bounds it on a GB300.  Many rows: memory; 40,000 rows of 32 + 8 heads take 166 us,
 // 6.1 TB/s read and written (90% of a copy; the slots' 2-byte stores meet in L2, DRAM
 // moves the algorithmic bytes), 27,292 rows with norms and a half of each head rotated
-// interleaved 120 us (83%).  Some thousand rows, all in L2: latency at 32 warps an SM (64
+// interleaved 124 us (81%).  Some thousand rows, all in L2: latency at 32 warps an SM (64
 // registers; 5.2 TB/s for 4,096 rows of 16 + 4 heads).  A decode step of 64 rows (2.8 us):
 // the launch, the position and then the cosines at it.
 
@@ -85,9 +85,13 @@ __device__ __forceinline__ Turn load_turn(const float* row, int rot, const float
   return t;
 }
 
-// One head; all lanes of a warp together.  Two channels an instruction.
-template <bool INTERLEAVED>
-__device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool norm, float eps) {
+// One head; all lanes of a warp together.  Two channels an instruction.  turned: the
+// lane's channels are rotated (WHOLE: every lane's).  Others take nothing from their
+// partners, not even 0 times them, which is NaN where the partner is not finite; without
+// a norm they are copied.  (That costs 27,292 rows with half of each head rotated 3 us;
+// heads rotated as a whole have a kernel of their own, without it.)
+template <bool INTERLEAVED, bool WHOLE>
+__device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool turned, bool norm, float eps) {
   const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
   float a[8];
 #pragma unroll
@@ -109,15 +113,27 @@ __device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool
   for (int i = 0; i < 8; i += 2) {
     const int o0 = INTERLEAVED ? i + 1 : i ^ 4, o1 = INTERLEAVED ? i : o0 + 1;
     float y0, y1;
-    unpair(mul2(fma2(pair(a[i], a[i + 1]), pair(t.c[i], t.c[i + 1]), mul2(pair(a[o0], a[o1]), pair(t.s[i], t.s[i + 1]))),
-                pair(r, r)), y0, y1);
+    const uint64_t own = pair(a[i], a[i + 1]), other = pair(a[o0], a[o1]);
+    const uint64_t c = pair(t.c[i], t.c[i + 1]), s = pair(t.s[i], t.s[i + 1]);
+    uint64_t y;
+    if (WHOLE) {
+      y = fma2(own, c, mul2(other, s));
+    } else {
+      y = mul2(own, c);
+      if (turned) y = fma2(other, s, y);
+    }
+    unpair(mul2(y, pair(r, r)), y0, y1);
     const __nv_bfloat162 p = __floats2bfloat162_rn(y0, y1);
     w[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  if (!WHOLE && !norm) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = turned ? w[i] : xw[i];
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool INTERLEAVED>
+template <bool INTERLEAVED, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 4)
 qkv_append_kernel(const AppendArgs a) {
   __shared__ uint32_t s_kv[2][kTile * kPitch];
@@ -135,7 +151,7 @@ qkv_append_kernel(const AppendArgs a) {
   wait_prerequisite_grids();
   const float* weight = is_kv ? a.k_weight : a.q_weight;
   auto finish = [&](const uint4& x, const Turn& turn) {
-    return norm_rotate<INTERLEAVED>(x, turn, weight != nullptr, a.norm_eps);
+    return norm_rotate<INTERLEAVED, WHOLE>(x, turn, 8 * lane16 < a.rot, weight != nullptr, a.norm_eps);
   };
   // position of a row that takes part, or -1
   auto checked = [&](int pos) {
@@ -276,8 +292,10 @@ cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s) {
   // against 166.
   a.whole_rows = a.n_rows * (a.Hq + 2 * a.Hkv) * (4 * kH) > ((int64_t)100 << 20);
   const unsigned grid = (unsigned)(tiles * (a.q_jobs + a.Hkv * a.kv_parts));
-  return launch_programmatic(a.interleaved ? qkv_append_kernel<true> : qkv_append_kernel<false>, dim3(grid),
-                             dim3(kThreads), 0, s, a);
+  const bool whole = a.rot == kH;
+  auto* const kernel = a.interleaved ? whole ? qkv_append_kernel<true, true> : qkv_append_kernel<true, false>
+                                     : whole ? qkv_append_kernel<false, true> : qkv_append_kernel<false, false>;
+  return launch_programmatic(kernel, dim3(grid), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace lynx

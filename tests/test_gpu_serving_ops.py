@@ -252,6 +252,52 @@ def test_append_position_offsets_pass_32_bits(cuda_device):
     assert int((k != 0).any(2).any(1).sum()) == 1
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("rot,interleaved", [(0, False), (0, True), (64, False), (64, True), (112, False), (16, True)])
+def test_append_keeps_infinities_and_nan_to_their_channels(cuda_device, rot, interleaved, norm):
+    """A channel that is not finite reaches the other one of its rotated pair, and under a
+    norm what the formula says; channels that are neither rotated nor normalised are
+    copied, every bit."""
+    Hq, Hkv, n_rows = 2, 1, 128 * 3
+    rng = np.random.default_rng(rot)
+    x = torch.from_numpy(rng.standard_normal((n_rows, Hq + 2 * Hkv, 128)).astype(np.float32)).bfloat16()
+    x[1::7, :, 5::9] = -0.0
+    odd = torch.tensor([float("inf"), float("-inf"), float("nan")]).bfloat16()
+    for r in range(n_rows):                                  # one channel a row
+        x[r, :, r // 3] = odd[r % 3]
+    x = x.cuda()
+    max_pos = 50
+    ang = rng.uniform(0.1, 1.4, (max_pos, rot // 2))
+    table = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+    pos = rng.integers(0, max_pos, n_rows)
+    w = rng.uniform(0.5, 2, 128).astype(np.float32) if norm else None
+    k = torch.zeros(2, 128, 256, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    slots = torch.arange(n_rows, device="cuda").view(-1, 1)
+    q = L.lynx_qkv_append(x.view(n_rows, -1), Hq, Hkv, cu(table) if rot else None, cu(pos, torch.int32), slots, k, v,
+                          q_weight=None if w is None else cu(w), k_weight=None if w is None else cu(w), norm_eps=0.0,
+                          interleaved=interleaved)
+    status_ok()
+    with np.errstate(invalid="ignore"):
+        ref = sv.norm_rotate(x[:, :Hq + Hkv].double().cpu().numpy(), w, 0.0, table[pos, :rot // 2].astype(np.float64),
+                             table[pos, rot // 2:].astype(np.float64), interleaved)
+    kg = k.permute(0, 2, 1).reshape(-1, 1, 128)[:n_rows]
+    vg = v.permute(0, 2, 1).reshape(-1, 1, 128)[:n_rows]
+    bits = lambda t: t.contiguous().view(torch.int16)
+    got = torch.cat([q, kg], 1)
+    g = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(g), np.isnan(ref))
+    inf = np.isinf(ref)
+    assert np.array_equal(np.isinf(g), inf) and np.array_equal(g[inf], ref[inf])
+    fin = np.isfinite(ref)
+    # half a BF16 step of the value, and the float32 part as in near(): |x| is below 6, times 2
+    # for a weight, twice for a pair; a mean over values that are not finite leaves zeros
+    assert np.all(np.abs(g[fin] - ref[fin]) <= 2.0 ** -8 * np.abs(ref[fin]) + 64 * 2.0 ** -24 * 24)
+    if not norm:
+        assert torch.equal(bits(got[..., rot:]), bits(x[:, :Hq + Hkv, rot:]))
+    assert torch.equal(bits(vg), bits(x[:, Hq + Hkv:]))
+
+
 # --------------------------------------------------------------- draft verification
 
 def probs(rng, shape, sharp):
