@@ -94,7 +94,7 @@ constexpr float kLazyLog2 = 8.0f;
 // offset) and us with 64 / 128 / 256: 3.1e-5, 1,371 / 6.7e-5, 1,345 / 1.3e-4, 1,332; never
 // taken out: 4.9e-4, 1,307.
 constexpr int kSumTiles = 128;
-static_assert((kSumTiles & (kSumTiles - 1)) == 0, "kSumTiles");
+static_assert(kSumTiles > 0 && (kSumTiles & (kSumTiles - 1)) == 0, "kSumTiles");
 constexpr int kBusyPolls = 4096;               // some 100 us
 constexpr int kMinKeysLog2 = 7;                // least cost of a CTA's part of the work, in keys; us for 17 tokens
                                                // over 1,000 keys: 12.8 (7), 13.2 (8), 16.1 (9)
@@ -293,8 +293,13 @@ __device__ __forceinline__ int visible(const ChunkArgs& a, int ctx, int T, int t
   return a.causal ? max(ctx - T + token + 1, 0) : ctx;
 }
 
-// all warps meet here from their own loops
-__device__ __forceinline__ void sync_all() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+// All warps meet here from their own loops, some of which one lane alone goes through.
+// (bar.sync and the .aligned instructions below, tcgen05.ld and .st among them, want the
+// warp's lanes together; behind code that may part them a __syncwarp brings them so.)
+__device__ __forceinline__ void sync_all() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 
 template <typename V>
 __device__ __forceinline__ V warp_scan(V v) {   // inclusive
@@ -716,6 +721,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             ++token;
           }
         }
+        __syncwarp();
       };
       auto queries_there = [&](const Item& it) {
         if (it.k0 == it.k1) return;
@@ -761,6 +767,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 #pragma unroll
                 for (int x = 0; x < 128; ++x)
                   if (x >= left) s[x] = 0xFF800000u;   // -inf
+                __syncwarp();
               }
               // P against the running maximum as it stands, and the tile's maximum beside
               // it: the two do not wait for one another (1.36 us a tile of keys against 1.5 one
@@ -797,6 +804,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
                 const float m_new = fmaxf(m, top);
                 const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - m_new);
+                __syncwarp();
                 if (j > j0) {   // rescale O, to which the product before has been added (its commit came first)
                   const float fo = m == -CUDART_INF_F ? 1.0f : f;   // O is 0 there
 #pragma unroll
@@ -842,6 +850,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 u[e] = add ? sum_o[(16 * x + e) * a.slot_rows] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              __syncwarp();
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 tmem_ld32(t_o + 64 * x + 32 * y, o + 32 * y);
@@ -903,6 +912,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t o[32];
+          __syncwarp();
           if (n > 0) {
             tmem_ld32(t_o + 32 * x, o);
             tmem_wait_ld32(o);
