@@ -4,8 +4,10 @@ and ``_build/lynx_binding.so``, the native part of the Python binding.
 Each .cu file compiles to an object in parallel; the objects link into one
 shared library with the CUDA runtime linked statically, so the library needs
 only the NVIDIA driver at run time.  The binding (one C++ file against torch's
-headers) links to that library.  Rebuilds only when a source or header is newer
-than the libraries.
+headers) links to that library; where it cannot be built (no torch, no g++) the
+library is there all the same and a warning says what is missing.  Each is built
+again when one of its sources or headers is newer, the binding also for another
+torch or Python.
 """
 from __future__ import annotations
 
@@ -13,7 +15,9 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
+from importlib import metadata
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -42,21 +46,39 @@ def nvcc() -> str:
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files.append(os.path.join(CSRC, "binding.cpp"))
     files.append(os.path.join(INCLUDE, "lynx.h"))
     return files
 
 
+def _newer(target: str, files) -> bool:
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(f) <= t for f in files)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    return os.path.exists(LIB) and _newer(LIB, _inputs())
+
+
+def _binding_of() -> str:
+    """The torch and Python that the binding is built for."""
+    try:
+        return f"torch {metadata.version('torch')} {sysconfig.get_config_var('SOABI')}"
+    except metadata.PackageNotFoundError:
+        return "no torch"
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING + ".of"):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    with open(BINDING + ".of") as f:
+        of = f.read()
+    return of == _binding_of() and _newer(BINDING, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "lynx.h")])
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile (if needed) and return the path of liblynx.so."""
-    if not force and up_to_date():
+    library, binding = force or not up_to_date(), force or not binding_up_to_date()
+    if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -85,24 +107,33 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
         return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
 
+    def link(what, tmp, target, cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"linking {what} failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, target)
+
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, SOURCES))
-        binding_obj, torch_lib = binding.result()
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    # torch's libraries are in the process when the binding is imported
-    tmp = BINDING + ".tmp"
-    cmd = ["g++", "-shared", "-o", tmp, binding_obj, "-L", BUILD, "-l:liblynx.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
-           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"linking the binding failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+        made = ex.submit(compile_binding) if binding else None
+        objs = list(ex.map(compile_one, SOURCES)) if library else []
+    if library:
+        tmp = LIB + ".tmp"
+        link("liblynx.so", tmp, LIB, [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
+    if binding:
+        try:
+            obj, torch_lib = made.result()
+            tmp = BINDING + ".tmp"
+            # torch's libraries are in the process when the binding is imported
+            link("the binding", tmp, BINDING,
+                 ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-l:liblynx.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
+                  "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+            with open(BINDING + ".of", "w") as f:
+                f.write(_binding_of())
+        except (RuntimeError, ImportError, OSError) as e:
+            if os.path.exists(BINDING):
+                os.remove(BINDING)   # built from other sources, or for another torch
+            warnings.warn(f"{os.path.basename(BINDING)} was not built, the serving-step calls of the Python package "
+                          f"need it: {e}")
     return LIB
 
 
