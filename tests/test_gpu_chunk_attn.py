@@ -480,3 +480,51 @@ def test_sums_that_are_taken_out_follow_the_running_maximum(cuda_device, new, n,
         lim = 2.0 ** -6 * torch.sqrt(p.square() @ v.square()) + (2.0 ** -13 + 2.0 ** -15 + 2.0 ** -12) * (p @ v.abs())
         assert bool((d <= lim).all()), float((d / lim).max())
         assert abs(float(torch.logsumexp(s, 0)) - float(a[1][int(r), i % 2])) < 2 * LSE_TOL
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv", [
+    ([1], [50001], 8, 2), ([3, 40], [50001, 20000], 8, 2), ([300, 1], [5000, 9000], 6, 3), ([700], [3000], 4, 1),
+    ([64] * 5, [1999, 128, 4097, 640, 777], 16, 4), ([1] * 70, [1 + 53 * i for i in range(70)], 4, 2)])
+def test_every_tile_and_every_key_has_its_weight(cuda_device, new, ctx, Hq, Hkv, causal):
+    """Values that tell the keys apart.  1 in channel c for the keys of tile c (of 128
+    tiles at a time): the output is the tiles' probabilities, so that a tile left out, taken
+    twice or from another page is off by all of it.  Then 1 in channel c for key c of
+    every tile.  Sums of probabilities, each rounded to BF16 (half a step: 2^-8 of it), 2^-12
+    for everything in float32 and what the matrix unit cuts off."""
+    x = batch(new, ctx, Hq, Hkv, sum(ctx) + Hq)
+    n_tiles = max(-(-c // 128) for c in ctx)
+    masks = range(-(-n_tiles // 128) + 1)
+    eye = torch.eye(128, dtype=torch.bfloat16, device="cuda")
+    outs = []
+    for w in masks:
+        v = torch.zeros_like(x["v"])
+        for b, n in enumerate(ctx):
+            pages = -(-n // 256)
+            if w == masks[-1]:
+                one = torch.cat([eye, eye], 1).expand(pages, -1, -1)
+            else:
+                tile = torch.arange(2 * pages, device="cuda") - 128 * w            # of each half page
+                one = (tile.view(-1, 2, 1) == torch.arange(128, device="cuda")).bfloat16()
+                one = one.permute(0, 2, 1).repeat_interleave(128, 2)
+            for h in range(Hkv):
+                v[x["table"][b, h, :pages].long()] = one
+        outs.append(call(dict(x, v=v), causal, out_dtype=torch.float32)[0].double())
+    torch.cuda.synchronize()
+    L.lynx_device_status()
+    lo = 0
+    for b, (T, n) in enumerate(zip(new, ctx)):
+        seen = (n - T + 1 + torch.arange(T, device="cuda")).clamp(min=0) if causal else torch.full((T,), n, device="cuda")
+        for hq in range(Hq):
+            ids = x["table"][b, hq // (Hq // Hkv), :-(-n // 256)].long()
+            k = x["k"][ids].permute(0, 2, 1).reshape(-1, D)[:n].double()
+            s = x["q"][lo:lo + T, hq].double() @ k.T / math.sqrt(D)
+            s = s.masked_fill(torch.arange(n, device="cuda") >= seen[:, None], -math.inf)
+            p = torch.nan_to_num(torch.softmax(s, 1))                              # a row without keys: 0
+            p = torch.nn.functional.pad(p, (0, n_tiles * 128 - n)).view(T, n_tiles, 128)
+            ref = [torch.nn.functional.pad(p.sum(2), (0, 128 * (len(masks) - 1) - n_tiles)).view(T, -1, 128)[:, w]
+                   for w in masks[:-1]] + [p.sum(1)]
+            for o, r in zip(outs, ref):
+                err = (o[lo:lo + T, hq] - r).abs()
+                assert bool((err <= (2.0 ** -8 + 2.0 ** -12) * r + 1e-9).all()), (b, hq, float((err - r / 256).max()))
+        lo += T
