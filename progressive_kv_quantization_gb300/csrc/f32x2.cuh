@@ -16,13 +16,6 @@ __device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__flo
 __device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-// the two values of a packed BF16 pair
-__device__ __forceinline__ uint64_t pair_of_bf16x2(uint32_t w) { return pair(w << 16, w & 0xFFFF0000u); }
-__device__ __forceinline__ uint64_t swapped(uint64_t v) {
-  float lo, hi;
-  unpair(v, lo, hi);
-  return pair(hi, lo);
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
