@@ -313,9 +313,9 @@ __device__ __forceinline__ V warp_scan(V v) {   // inclusive
 
 // The list warp: measures the line, finds this CTA's part of it and hands out
 // the part's items, the tiles of one head at a time and at most kMaxItems.
-// Requests are taken 32 at a time, one a lane, the next ones on their way.  (One
-// warp and one place in the code: the list's instructions are fetched once, which
-// is most of the time that a short list takes.)
+// Requests are taken 32 at a time, one a lane; each list starts again from the
+// first.  (One warp and one place in the code: the list's instructions are fetched
+// once, which is most of the time that a short list takes.)
 __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, volatile int* s_n_items, Header* s_hdr,
                                            const volatile int* s_abort) {
   const int lane = threadIdx.x & 31;
