@@ -34,6 +34,9 @@
  *                         BF16 pages: pages and slots of new tokens, their norm,
  *                         rotation and write, attention of ragged chunks
  *                         (prefill), verification of drafted tokens (§4.3).
+ *   lynx_decode_attn_e4m3
+ *                         serving over pages in 8 bits: E4M3 codes with a scale
+ *                         for each block of 32 tokens of a head.
  *
  * ---------------------------------------------------------------------------
  * Data layout (all sizes for H = 128 channels, P = 256 tokens, C = 32):
@@ -533,16 +536,47 @@ int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, co
                        int64_t q_stride_t, int prob_dtype, int B, int T, int V, const int32_t* draft,
                        const int32_t* n_draft, const float* u, int32_t* tokens, int32_t* n_accept, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Pages in 8 bits.  A serving loop that keeps its own keys and values in half the
+ * memory of BF16 pages can append to them token by token, which the encoders'
+ * whole-page statistics do not allow.
+ *   k_pages, v_pages   pools [n_pool_pages][256][128] of E4M3 codes (4 exponent and 3
+ *               mantissa bits, largest value 448), token-major: token t of a page is 128
+ *               consecutive bytes
+ *   scales      [n_pool_pages][2][8] bytes: of the 8 blocks of 32 tokens of the page's
+ *               keys, then of its values.  Byte s stands for the factor 2^(s - 127); 74 <= s
+ *               <= 198 (another byte counts as the nearer bound).
+ * A value is code * 2^(s - 127), exactly a BF16 number.  Page ids, page_table and
+ * ctx_len are those of the BF16 pages, and lynx_assign_pages serves both.  Codes
+ * of positions below ctx_len must not be NaN (0x7F, 0xFF); codes and scales of what lies
+ * behind may be anything.  Limit: n_pool_pages < 2^23.
+ */
+
+/* Decode / verification attention over pages in 8 bits: arguments as
+ * lynx_decode_attn_bf16, but only q, the pools, scales, out and the workspace need 16-byte
+ * alignment.  Scores and sums in float32, the probabilities held in 22 bits.
+ *   workspace   device scratch of lynx_decode_attn_e4m3_workspace_size() bytes,
+ *               clobbered.  Calls that may overlap need one each.
+ * out and lse must not share memory with q.  Limits as lynx_decode_attn. */
+int lynx_decode_attn_e4m3(const void* q_bf16, int B, int T, int Hq, int Hkv, int head_dim, const void* k_pages,
+                          const void* v_pages, const uint8_t* scales, int64_t n_pool_pages, const int32_t* page_table,
+                          int max_pages, const int32_t* ctx_len, float sm_scale, int causal, float* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lynx_decode_attn_e4m3 for the given shape on the current
+ * device (0 for invalid shapes); it does not depend on the contexts' lengths. */
+size_t lynx_decode_attn_e4m3_workspace_size(int B, int T, int Hq, int Hkv, int head_dim);
+
 /* Workspace bytes needed by lynx_decode_attn / lynx_decode_attn_bf16 for the
  * given shape on the current device (0 for invalid shapes). */
 size_t lynx_decode_attn_workspace_size(int B, int T, int Hq, int Hkv, int head_dim, int max_pages);
 
 /* Test hook (not for production use; off by default): the next n_calls calls
  * of lynx_decode_attn, lynx_decode_attn_bf16, lynx_decode_attn_int4,
- * lynx_decode_attn_uniform, lynx_chunk_attn_bf16, lynx_reconstruct or
- * lynx_encode_tokens made from this host thread run with a fault planted on the host side of the launch:
+ * lynx_decode_attn_uniform, lynx_decode_attn_e4m3, lynx_chunk_attn_bf16,
+ * lynx_reconstruct or lynx_encode_tokens made from this host thread run with a fault planted on the host side of the launch:
  * every CTA never issues the copy of its first V page (decode; its first V tile
- * in lynx_chunk_attn_bf16), of its first
+ * in lynx_chunk_attn_bf16 and over pages in 8 bits), of its first
  * page (reconstruct) or of its first item (the token encoder's TMA-staged
  * kernel; an input that admits no tensor map takes the other kernel, which
  * has no waits, and the call runs normally), and every bounded wait of those

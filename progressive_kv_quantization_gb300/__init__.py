@@ -29,6 +29,8 @@ from .lynx import (  # noqa: F401
     lynx_verify_drafts,
     lynx_chunk_attn_bf16,
     lynx_chunk_attn_workspace_size,
+    lynx_decode_attn_e4m3,
+    lynx_decode_attn_e4m3_workspace_size,
     lynx_reconstruct,
     load,
 )

@@ -29,6 +29,8 @@ PyObject* g_error = nullptr;   // lynx.LynxError
 const char* type_name(at::ScalarType t) {
   switch (t) {
     case at::kBFloat16: return "torch.bfloat16";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
+    case at::kByte: return "torch.uint8";
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
     case at::kLong: return "torch.int64";
@@ -133,6 +135,26 @@ struct Out {
     PyObject* r = o;
     o = nullptr;
     return r;
+  }
+};
+
+// the caller's workspace, or one of `size()` bytes that lives as long as the call
+struct Scratch {
+  void* p;
+  size_t bytes;
+  at::Tensor own;
+  template <typename F>
+  Scratch(Call& c, PyObject* o, F size) {
+    if (o == Py_None) {
+      bytes = size();
+      own = at::empty({(int64_t)(bytes < 16 ? 16 : bytes)}, at::TensorOptions().dtype(at::kByte).device(c.device()));
+      p = own.data_ptr();
+    } else {
+      const at::Tensor& w = c.tensor(o, "workspace");
+      if (!w.is_contiguous()) raise("workspace must be a contiguous tensor");
+      p = w.data_ptr();
+      bytes = w.nbytes();
+    }
   }
 };
 
@@ -277,25 +299,14 @@ PyObject* chunk_attn_bf16(PyObject* const* a) {
     f32 = type == at::kFloat;
   }
   void* stream = c.stream(a[13]);
-  Out out, lse, ws;
+  Out out, lse;
   out.o = c.make(a[9], f32 ? at::kFloat : at::kBFloat16, {n_rows, Hq, 128}, "out", &out.p);
   lse.o = c.make(a[10], at::kFloat, {n_rows, Hq}, "lse", &lse.p);
-  size_t ws_bytes = 0;
-  at::Tensor own;
-  if (a[12] == Py_None) {
-    ws_bytes = lynx_chunk_attn_workspace_size(n_rows, B, Hq, n_kv, 128);
-    own = at::empty({(int64_t)(ws_bytes < 16 ? 16 : ws_bytes)}, at::TensorOptions().dtype(at::kByte).device(c.device()));
-    ws.p = own.data_ptr();
-  } else {
-    const at::Tensor& w = c.tensor(a[12], "workspace");
-    if (!w.is_contiguous()) raise("workspace must be a contiguous tensor");
-    ws.p = w.data_ptr();
-    ws_bytes = w.nbytes();
-  }
+  const Scratch ws(c, a[12], [&] { return lynx_chunk_attn_workspace_size(n_rows, B, Hq, n_kv, 128); });
   c.launch([&] {
     return lynx_chunk_attn_bf16(q.data_ptr(), n_rows, stride, (int32_t*)cu, B, Hq, n_kv, 128, k, v, n_pool, (int32_t*)t,
                                 pages, (int32_t*)ctx, scale, causal, out.p, f32 ? LYNX_OUT_F32 : LYNX_OUT_BF16,
-                                (float*)lse.p, ws.p, ws_bytes, stream);
+                                (float*)lse.p, ws.p, ws.bytes, stream);
   });
   return tuple({&out, &lse});
 }
@@ -334,6 +345,48 @@ PyObject* verify_drafts(PyObject* const* a) {
   return tuple({&tokens, &n});
 }
 
+// pools of pages in 8 bits and their scales
+struct Pools8 {
+  void *k, *v, *scales;
+  int64_t n;
+  Pools8(Call& c, PyObject* k_pages, PyObject* v_pages, PyObject* scale_bytes) {
+    const at::Tensor& kp = c.tensor(k_pages, "k_pages");
+    n = kp.dim() == 3 ? kp.size(0) : 0;
+    k = c.at(k_pages, at::kFloat8_e4m3fn, {n, 256, 128}, "k_pages");
+    v = c.at(v_pages, at::kFloat8_e4m3fn, {n, 256, 128}, "v_pages");
+    scales = c.at(scale_bytes, at::kByte, {n, 2, 8}, "scales");
+  }
+};
+
+// q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads, sm_scale, causal, out, lse, workspace, stream
+PyObject* decode_attn_e4m3(PyObject* const* a) {
+  Call c("lynx_decode_attn_e4m3", a[0], "q");
+  const at::Tensor& qt = c.tensor(a[0], "q");
+  if (qt.dim() != 4) raise("q must be [B, T, Hq, 128]");
+  const int64_t b = qt.size(0), t = qt.size(1), hq = qt.size(2);
+  void* q = c.at(a[0], at::kBFloat16, {b, t, hq, 128}, "q");
+  const int B = dim32(b, "B"), T = dim32(t, "T"), Hq = dim32(hq, "Hq"), n_kv = to_int(a[6], "n_kv_heads");
+  const Pools8 pools(c, a[1], a[2], a[3]);
+  const at::Tensor& tt = c.tensor(a[4], "page_table");
+  if (tt.dim() != 3) raise("page_table must be [B, Hkv, max_pages]");
+  const int pages = dim32(tt.size(2), "max_pages");
+  void* table = c.at(a[4], at::kInt, {b, n_kv, pages}, "page_table");
+  void* ctx = c.at(a[5], at::kInt, {b}, "ctx_len");
+  const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt(128.0)) : to_float(a[7]);
+  const int causal = PyObject_IsTrue(a[8]);
+  void* stream = c.stream(a[12]);
+  Out out, lse;
+  out.o = c.make(a[9], at::kFloat, {b, t, hq, 128}, "out", &out.p);
+  lse.o = c.make(a[10], at::kFloat, {b, t, hq}, "lse", &lse.p);
+  const Scratch ws(c, a[11], [&] { return lynx_decode_attn_e4m3_workspace_size(B, T, Hq, n_kv, 128); });
+  c.launch([&] {
+    return lynx_decode_attn_e4m3(q, B, T, Hq, n_kv, 128, pools.k, pools.v, (uint8_t*)pools.scales, pools.n,
+                                 (int32_t*)table, pages, (int32_t*)ctx, scale, causal, (float*)out.p, (float*)lse.p,
+                                 ws.p, ws.bytes, stream);
+  });
+  return tuple({&out, &lse});
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XDECREF(g_error);
@@ -348,6 +401,7 @@ PyMethodDef kMethods[] = {
     {"qkv_append", FAST((entry<14, qkv_append>))},
     {"chunk_attn_bf16", FAST((entry<14, chunk_attn_bf16>))},
     {"verify_drafts", FAST((entry<8, verify_drafts>))},
+    {"decode_attn_e4m3", FAST((entry<13, decode_attn_e4m3>))},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "lynx_binding", nullptr, -1, kMethods};
 

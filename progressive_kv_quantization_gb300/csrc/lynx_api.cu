@@ -936,6 +936,82 @@ int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, co
   return LYNX_OK;
 }
 
+namespace {
+
+// what the calls over pages in 8 bits have in common
+int check_e4m3_pools(const void* k_pages, const void* v_pages, const uint8_t* scales, int64_t n_pool) {
+  if (!k_pages || !v_pages || !scales) return fail(LYNX_ERR_INVALID_ARG, "NULL page pool or scales");
+  if (n_pool < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool);
+  if (n_pool >= (int64_t)1 << 23) return fail(LYNX_ERR_UNSUPPORTED, "n_pool_pages=%lld too large", (long long)n_pool);
+  if (misaligned(k_pages) || misaligned(v_pages) || misaligned(scales))
+    return fail(LYNX_ERR_ALIGNMENT, "the pools and scales must be 16-byte aligned");
+  return LYNX_OK;
+}
+
+}  // namespace
+
+size_t lynx_decode_attn_e4m3_workspace_size(int B, int T, int Hq, int Hkv, int head_dim) {
+  if (check_decode_shape(B, T, Hq, Hkv, head_dim, 1) != LYNX_OK) return 0;
+  return decode_e4m3_ws_bytes(T * (Hq / Hkv));
+}
+
+int lynx_decode_attn_e4m3(const void* q_bf16, int B, int T, int Hq, int Hkv, int head_dim, const void* k_pages,
+                          const void* v_pages, const uint8_t* scales, int64_t n_pool_pages, const int32_t* page_table,
+                          int max_pages, const int32_t* ctx_len, float sm_scale, int causal, float* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error[0] = '\0';
+  int st = check_decode_shape(B, T, Hq, Hkv, head_dim, max_pages);
+  if (st != LYNX_OK) return st;
+  if ((int64_t)max_pages * kP > 0x7fffff00) return fail(LYNX_ERR_UNSUPPORTED, "max_pages too large");
+  st = check_e4m3_pools(k_pages, v_pages, scales, n_pool_pages);
+  if (st != LYNX_OK) return st;
+  if (!q_bf16 || !page_table || !ctx_len || !out) return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
+  if (misaligned(q_bf16) || misaligned(out) || misaligned(workspace))
+    return fail(LYNX_ERR_ALIGNMENT, "q, out and the workspace must be 16-byte aligned");
+  if (off_type(page_table, 4) || off_type(ctx_len, 4) || off_type(lse, 4))
+    return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
+  if (causal != 0 && causal != 1) return fail(LYNX_ERR_INVALID_ARG, "causal=%d", causal);
+  if (!(sm_scale > 0.0f) || !isfinite(sm_scale))
+    return fail(LYNX_ERR_INVALID_ARG, "sm_scale=%g must be finite and > 0", (double)sm_scale);
+  const size_t need = decode_e4m3_ws_bytes(T * (Hq / Hkv));
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(LYNX_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                workspace ? workspace_bytes : (size_t)0);
+  const int64_t n_q = (int64_t)B * T * Hq;
+  if (overlap({{out, n_q * kH * 4}, {lse, n_q * 4}, {workspace, (int64_t)need}}, {{q_bf16, n_q * kH * 2}}))
+    return fail(LYNX_ERR_INVALID_ARG, "out, lse or the workspace overlaps q");
+  int* status = device_status_ptr();
+  if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
+  DecodeE4m3Args a{};
+  a.q = static_cast<const uint16_t*>(q_bf16);
+  a.k_pages = static_cast<const uint8_t*>(k_pages);
+  a.v_pages = static_cast<const uint8_t*>(v_pages);
+  a.scales = scales;
+  a.page_table = page_table;
+  a.ctx_len = ctx_len;
+  a.out = out;
+  a.lse = lse;
+  a.status = status;
+  a.n_pool = n_pool_pages;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.max_pages = max_pages;
+  a.causal = causal;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.wait_ns = kDefaultWaitNs;
+  if (g_inject_calls > 0) {   // test hook, off unless armed
+    --g_inject_calls;
+    a.inject = 1;
+    a.wait_ns = 1000000ull;
+  }
+  cudaError_t e = launch_decode_e4m3(a, workspace, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lynx_decode_attn_e4m3 launch");
+  return LYNX_OK;
+}
+
 int lynx_test_inject_wait_timeout(int n_calls) {
   g_last_error[0] = '\0';
   if (n_calls < 0) return fail(LYNX_ERR_INVALID_ARG, "n_calls=%d < 0", n_calls);

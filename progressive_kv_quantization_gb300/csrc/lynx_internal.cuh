@@ -283,6 +283,33 @@ struct ChunkArgs {
   void* ws_hdr;
   float* ws_o;
 };
+// ---- pages in 8 bits (E4M3 codes, a scale for 32 tokens of a head)
+
+struct DecodeE4m3Args {
+  const uint16_t* q;
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const uint8_t* scales;
+  const int32_t* page_table;
+  const int32_t* ctx_len;
+  float* out;
+  float* lse;               // NULL to skip
+  int* status;
+  int64_t n_pool;
+  int B, T, Hq, Hkv, G, max_pages, causal;
+  float scale_log2;
+  unsigned long long wait_ns;   // as DecodeArgs
+  int inject;                   // test hook: every CTA's first V tile is never copied
+  // set by the launcher
+  int tile_rows, n_tiles, n_cta;
+  void* ws_hdr;
+  float* ws_o;
+  template <typename Hdr>
+  __host__ __device__ Hdr* ws_hdr_as() const { return static_cast<Hdr*>(ws_hdr); }
+};
+size_t decode_e4m3_ws_bytes(int rows);
+cudaError_t launch_decode_e4m3(DecodeE4m3Args a, void* workspace, cudaStream_t s);
+
 size_t chunk_ws_bytes(int64_t n_rows, int G);
 cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s);
 

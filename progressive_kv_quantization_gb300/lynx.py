@@ -90,6 +90,9 @@ SIGNATURES = {
                                     _F32, _I32, _VP, _I32, _VP, _VP, _SZ, _VP]),
     "lynx_verify_drafts": (_I32, [_VP, _I64, _I64, _VP, _I64, _I64, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP,
                                   _VP, _VP]),
+    "lynx_decode_attn_e4m3": (_I32, [_VP, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _I64, _VP, _I32, _VP, _F32, _I32,
+                                     _VP, _VP, _VP, _SZ, _VP]),
+    "lynx_decode_attn_e4m3_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
     "lynx_decode_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "lynx_device_status": (_I32, []),
     "lynx_test_inject_wait_timeout": (_I32, [_I32]),
@@ -585,6 +588,21 @@ def lynx_verify_drafts(p, q, draft, u, n_draft=None, tokens=None, n_accept=None,
     [B])."""
     return (_binding or _native()).verify_drafts(p, q, draft, u, n_draft, tokens, n_accept,
                                                  stream and stream.cuda_stream)
+
+
+def lynx_decode_attn_e4m3_workspace_size(B, T, Hq, Hkv, head_dim) -> int:
+    return int(load().lynx_decode_attn_e4m3_workspace_size(B, T, Hq, Hkv, head_dim))
+
+
+def lynx_decode_attn_e4m3(q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads: int, sm_scale=None,
+                          causal=False, out=None, lse=None, workspace=None, stream=None):
+    """Attention of q bf16 [B, T, Hq, 128] over pages in 8 bits: k_pages / v_pages
+    float8_e4m3fn [n, 256, 128], token-major, scales uint8 [n, 2, 8] (keys, values; byte
+    s of a block of 32 tokens stands for the factor 2^(s - 127)).  Returns (out f32 [B, T,
+    Hq, 128], lse f32 [B, T, Hq])."""
+    return (_binding or _native()).decode_attn_e4m3(q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads,
+                                                    sm_scale, causal, out, lse, workspace,
+                                                    stream and stream.cuda_stream)
 
 
 def lynx_device_status():

@@ -1,0 +1,74 @@
+"""Caches of pages in 8 bits for the tests, and how far attention over them may be
+off (no GPU code here)."""
+from __future__ import annotations
+
+import numpy as np
+
+from oracle import e4m3
+
+NAN_CODE = 0x7F
+
+
+def to_bf16(x):
+    """The nearest BF16 numbers, as float64."""
+    b = np.asarray(x, dtype=np.float32).view(np.uint32).astype(np.uint64)
+    b = (b + 0x7FFF + ((b >> 16) & 1)) & 0xFFFF0000
+    return b.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+class Cache:
+    """Pages of requests of the given lengths in a shuffled pool.  Positions behind a
+    request's last token hold NaN codes, blocks behind it bytes outside the scales' range."""
+
+    def __init__(self, lens, Hkv, seed, max_pages=None, spare=3, spread=0.0, poison=True):
+        rng = np.random.default_rng(seed)
+        pages = [-(-max(n, 0) // e4m3.PAGE) for n in lens]
+        self.max_pages = max_pages or max(1, max(pages))
+        n = sum(pages) * Hkv + spare
+        order = rng.permutation(n)
+        self.table = np.full((len(lens), Hkv, self.max_pages), -7, dtype=np.int32)
+        self.codes, self.scales = [], []
+        for _ in range(2):
+            x = rng.standard_normal((n, e4m3.PAGE, e4m3.H)) + rng.standard_normal(e4m3.H)
+            if spread:   # blocks of other sizes
+                size = np.exp2(rng.integers(-spread, spread + 1, (n, e4m3.PAGE // e4m3.BLOCK)))
+                x *= np.repeat(size, e4m3.BLOCK, axis=1)[:, :, None]
+            c, s = e4m3.quantise_pages(x)
+            self.codes.append(c)
+            self.scales.append(s)
+        at = 0
+        for b, length in enumerate(lens):
+            for h in range(Hkv):
+                for j in range(pages[b]):
+                    page = order[at]
+                    at += 1
+                    self.table[b, h, j] = page
+                    left = length - j * e4m3.PAGE
+                    if poison and left < e4m3.PAGE:
+                        for c, s in zip(self.codes, self.scales):
+                            c[page, left:] = NAN_CODE
+                            s[page, -(-left // e4m3.BLOCK):] = rng.choice([0, 255, 73, 199])
+        self.lens, self.Hkv = lens, Hkv
+
+    def values(self, b, h):
+        """Keys and values of a request and head, float64 [len, 128]."""
+        n = self.lens[b]
+        ids = self.table[b, h, :-(-n // e4m3.PAGE)]
+        return [e4m3.dequantise_pages(c[ids], s[ids]).reshape(-1, e4m3.H)[:n] for c, s in zip(self.codes, self.scales)]
+
+    def pools(self):
+        """(k codes, v codes, scales [n, 2, 8])"""
+        return self.codes[0], self.codes[1], np.stack(self.scales, 1)
+
+
+def score_error(q, k, scale):
+    """How far a score may be off: products of the codes and BF16 numbers are exact, and of
+    the float32 sum of 128 of them eight partial sums (one a product of 16) are cut off at
+    2^-23 of what they hold at most, with a few roundings of factors behind them."""
+    return 16 * 2.0 ** -23 * scale * float((np.abs(q) @ np.abs(k).T).max(initial=0.0))
+
+
+def decode_bound(q, k, v, scale):
+    """How far an output may be off, for probabilities of 22 bits: twice the scores' error
+    (in p and in the sum), the exponential's 2^-21 and the sums' roundings."""
+    return (2 * score_error(q, k, scale) + 2.0 ** -18) * float(np.abs(v).max(initial=0.0))
