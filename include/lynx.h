@@ -34,7 +34,7 @@
  *                         BF16 pages: pages and slots of new tokens, their norm,
  *                         rotation and write, attention of ragged chunks
  *                         (prefill), verification of drafted tokens (§4.3).
- *   lynx_decode_attn_e4m3
+ *   lynx_decode_attn_e4m3, lynx_chunk_attn_e4m3
  *                         serving over pages in 8 bits: E4M3 codes with a scale
  *                         for each block of 32 tokens of a head.
  *
@@ -563,6 +563,15 @@ int lynx_decode_attn_e4m3(const void* q_bf16, int B, int T, int Hq, int Hkv, int
                           int max_pages, const int32_t* ctx_len, float sm_scale, int causal, float* out, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention of a ragged batch of chunks of new tokens over pages in 8 bits:
+ * arguments, workspace (lynx_chunk_attn_workspace_size), rounding and errors as
+ * lynx_chunk_attn_bf16 over the BF16 pages that the codes stand for.  sm_scale <= 2^20. */
+int lynx_chunk_attn_e4m3(const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq,
+                         int Hkv, int head_dim, const void* k_pages, const void* v_pages, const uint8_t* scales,
+                         int64_t n_pool_pages, const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                         float sm_scale, int causal, void* out, int out_dtype, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* Workspace bytes of lynx_decode_attn_e4m3 for the given shape on the current
  * device (0 for invalid shapes); it does not depend on the contexts' lengths. */
 size_t lynx_decode_attn_e4m3_workspace_size(int B, int T, int Hq, int Hkv, int head_dim);
@@ -574,7 +583,7 @@ size_t lynx_decode_attn_workspace_size(int B, int T, int Hq, int Hkv, int head_d
 /* Test hook (not for production use; off by default): the next n_calls calls
  * of lynx_decode_attn, lynx_decode_attn_bf16, lynx_decode_attn_int4,
  * lynx_decode_attn_uniform, lynx_decode_attn_e4m3, lynx_chunk_attn_bf16,
- * lynx_reconstruct or lynx_encode_tokens made from this host thread run with a fault planted on the host side of the launch:
+ * lynx_chunk_attn_e4m3, lynx_reconstruct or lynx_encode_tokens made from this host thread run with a fault planted on the host side of the launch:
  * every CTA never issues the copy of its first V page (decode; its first V tile
  * in lynx_chunk_attn_bf16 and over pages in 8 bits), of its first
  * page (reconstruct) or of its first item (the token encoder's TMA-staged

@@ -270,45 +270,54 @@ PyObject* qkv_append(PyObject* const* a) {
   return q.take();
 }
 
-// q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_heads, sm_scale, causal, out, lse, out is float32, workspace,
-// stream
-PyObject* chunk_attn_bf16(PyObject* const* a) {
-  Call c("lynx_chunk_attn_bf16", a[0], "q");
-  const at::Tensor& q = c.tensor(a[0], "q");
+// The chunks' rows, tables and outputs, whatever the pages hold; arguments from `a` on: page_table, ctx_len,
+// n_kv_heads, sm_scale, causal, out, lse, out is float32, workspace, stream
+template <typename F>
+PyObject* chunk_attn(Call& c, PyObject* rows, PyObject* bounds, PyObject* const* a, F call) {
+  const at::Tensor& q = c.tensor(rows, "q");
   if (q.scalar_type() != at::kBFloat16 || q.dim() != 3 || q.size(2) != 128 || q.stride(2) != 1 ||
       (q.size(1) > 1 && q.stride(1) != 128))
     raise("q must be a bfloat16 tensor [n_rows, Hq, 128] with contiguous rows");
   const int64_t n_rows = q.size(0), stride = n_rows > 1 ? q.stride(0) : q.size(1) * 128;
-  const int Hq = dim32(q.size(1), "Hq"), n_kv = to_int(a[6], "n_kv_heads");
-  const at::Tensor& table = c.tensor(a[4], "page_table");
+  const int Hq = dim32(q.size(1), "Hq"), n_kv = to_int(a[2], "n_kv_heads");
+  const at::Tensor& table = c.tensor(a[0], "page_table");
   if (table.dim() != 3 || table.size(1) != n_kv) raise("page_table must be [B, Hkv, max_pages]");
   const int B = dim32(table.size(0), "B"), pages = dim32(table.size(2), "max_pages");
-  void* t = c.at(a[4], at::kInt, {B, n_kv, pages}, "page_table");
-  void* cu = c.at(a[1], at::kInt, {(int64_t)B + 1}, "cu_q");
-  void* ctx = c.at(a[5], at::kInt, {B}, "ctx_len");
+  void* t = c.at(a[0], at::kInt, {B, n_kv, pages}, "page_table");
+  void* cu = c.at(bounds, at::kInt, {(int64_t)B + 1}, "cu_q");
+  void* ctx = c.at(a[1], at::kInt, {B}, "ctx_len");
+  const float scale = a[3] == Py_None ? (float)(1.0 / std::sqrt(128.0)) : to_float(a[3]);
+  const int causal = PyObject_IsTrue(a[4]);
+  bool f32 = PyObject_IsTrue(a[7]) == 1;
+  if (a[5] != Py_None) {
+    const at::ScalarType type = c.tensor(a[5], "out").scalar_type();
+    if (type != at::kBFloat16 && type != at::kFloat) raise("out must be bfloat16 or float32");
+    f32 = type == at::kFloat;
+  }
+  void* stream = c.stream(a[9]);
+  Out out, lse;
+  out.o = c.make(a[5], f32 ? at::kFloat : at::kBFloat16, {n_rows, Hq, 128}, "out", &out.p);
+  lse.o = c.make(a[6], at::kFloat, {n_rows, Hq}, "lse", &lse.p);
+  const Scratch ws(c, a[8], [&] { return lynx_chunk_attn_workspace_size(n_rows, B, Hq, n_kv, 128); });
+  c.launch([&] {
+    return call(q.data_ptr(), n_rows, stride, (int32_t*)cu, B, Hq, n_kv, (int32_t*)t, pages, (int32_t*)ctx, scale, causal,
+                out.p, f32 ? LYNX_OUT_F32 : LYNX_OUT_BF16, (float*)lse.p, ws.p, ws.bytes, stream);
+  });
+  return tuple({&out, &lse});
+}
+
+// q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_heads, sm_scale, causal, out, lse, out is float32, workspace,
+// stream
+PyObject* chunk_attn_bf16(PyObject* const* a) {
+  Call c("lynx_chunk_attn_bf16", a[0], "q");
   const at::Tensor& kp = c.tensor(a[2], "k_pages");
   const int64_t n_pool = kp.dim() == 3 ? kp.size(0) : 0;
   void* k = c.at(a[2], at::kBFloat16, {n_pool, 128, 256}, "k_pages");
   void* v = c.at(a[3], at::kBFloat16, {n_pool, 128, 256}, "v_pages");
-  const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt(128.0)) : to_float(a[7]);
-  const int causal = PyObject_IsTrue(a[8]);
-  bool f32 = PyObject_IsTrue(a[11]) == 1;
-  if (a[9] != Py_None) {
-    const at::ScalarType type = c.tensor(a[9], "out").scalar_type();
-    if (type != at::kBFloat16 && type != at::kFloat) raise("out must be bfloat16 or float32");
-    f32 = type == at::kFloat;
-  }
-  void* stream = c.stream(a[13]);
-  Out out, lse;
-  out.o = c.make(a[9], f32 ? at::kFloat : at::kBFloat16, {n_rows, Hq, 128}, "out", &out.p);
-  lse.o = c.make(a[10], at::kFloat, {n_rows, Hq}, "lse", &lse.p);
-  const Scratch ws(c, a[12], [&] { return lynx_chunk_attn_workspace_size(n_rows, B, Hq, n_kv, 128); });
-  c.launch([&] {
-    return lynx_chunk_attn_bf16(q.data_ptr(), n_rows, stride, (int32_t*)cu, B, Hq, n_kv, 128, k, v, n_pool, (int32_t*)t,
-                                pages, (int32_t*)ctx, scale, causal, out.p, f32 ? LYNX_OUT_F32 : LYNX_OUT_BF16,
-                                (float*)lse.p, ws.p, ws.bytes, stream);
+  return chunk_attn(c, a[0], a[1], a + 4, [&](auto q, int64_t n_rows, int64_t stride, auto cu, int B, int Hq, int n_kv,
+                                              auto... rest) {
+    return lynx_chunk_attn_bf16(q, n_rows, stride, cu, B, Hq, n_kv, 128, k, v, n_pool, rest...);
   });
-  return tuple({&out, &lse});
 }
 
 // p, q, draft, u, n_draft, tokens, n_accept, stream
@@ -387,6 +396,18 @@ PyObject* decode_attn_e4m3(PyObject* const* a) {
   return tuple({&out, &lse});
 }
 
+// q, cu_q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads, sm_scale, causal, out, lse, out is float32,
+// workspace, stream
+PyObject* chunk_attn_e4m3(PyObject* const* a) {
+  Call c("lynx_chunk_attn_e4m3", a[0], "q");
+  const Pools8 pools(c, a[2], a[3], a[4]);
+  return chunk_attn(c, a[0], a[1], a + 5, [&](auto q, int64_t n_rows, int64_t stride, auto cu, int B, int Hq, int n_kv,
+                                              auto... rest) {
+    return lynx_chunk_attn_e4m3(q, n_rows, stride, cu, B, Hq, n_kv, 128, pools.k, pools.v, (uint8_t*)pools.scales,
+                                pools.n, rest...);
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XDECREF(g_error);
@@ -402,6 +423,7 @@ PyMethodDef kMethods[] = {
     {"chunk_attn_bf16", FAST((entry<14, chunk_attn_bf16>))},
     {"verify_drafts", FAST((entry<8, verify_drafts>))},
     {"decode_attn_e4m3", FAST((entry<13, decode_attn_e4m3>))},
+    {"chunk_attn_e4m3", FAST((entry<15, chunk_attn_e4m3>))},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "lynx_binding", nullptr, -1, kMethods};
 

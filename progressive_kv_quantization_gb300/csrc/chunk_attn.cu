@@ -61,6 +61,7 @@
 // Keys past ctx_len in the last page take no part: their scores are replaced, and
 // their V rows are zeroed in shared memory (0 x NaN would be NaN).
 
+#include "e4m3.cuh"
 #include "lynx_internal.cuh"
 #include "f32x2.cuh"
 #include "tma_ptx.cuh"
@@ -76,11 +77,9 @@ constexpr int kTileRows = 2 * kGroupRows;
 constexpr int kTileKeys = 128;
 constexpr int kBox = 16384;                    // TMA box: 64 tokens x 128 channels
 constexpr int kSlot = 2 * kBox;                // one K or V tile
-constexpr int kSlots = 5;
 constexpr int kQBytes = 2 * kBox;              // a group's queries: two halves [128 rows][64 channels]
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kListWarp = 10, kMmaWarp1 = 11;
-constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 208, kRegsOther = 80;   // of 168 each at launch: 256 x 208 + 128 x 80 <= 384 x 168
+constexpr int kConvertWarp = 12;               // and the three behind it; pages in 8 bits only
 constexpr int kMaxItems = 24;
 // Tiles of keys of a part, at least: a smaller one goes to the CTA with the rest, whose
 // tile then needs no join.  us with 1 / 2 / 3 / 4 / 6: one prompt of 2,048 tokens (32 / 8
@@ -99,16 +98,32 @@ constexpr int kBusyPolls = 4096;               // some 100 us
 constexpr int kMinKeysLog2 = 7;                // least cost of a CTA's part of the work, in keys; us for 17 tokens
                                                // over 1,000 keys: 12.8 (7), 13.2 (8), 16.1 (9)
 
-constexpr int kOffQ = 0;
-constexpr int kOffRing = kOffQ + 2 * kQBytes;
-constexpr int kOffBar = kOffRing + kSlots * kSlot;
-constexpr int kNumBars = 2 * kSlots + 10;
-constexpr int kOffItems = kOffBar + 8 * kNumBars;
 constexpr int kItemInts = 10;
-constexpr int kOffMisc = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
-constexpr int kSmem = kOffMisc + 80;   // items, header (at 16), tensor memory (at 64), abort and busy flags
-constexpr int kSmemAlloc = kSmem + 1024;
-static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
+constexpr int kRawTile = kTileKeys * kH;       // a K or V tile in 8 bits
+// sizes and places in shared memory; E: pages in 8 bits
+template <bool E>
+struct Layout {
+  static constexpr int kThreads = E ? 512 : 384;
+  // registers a thread, of 168 or 128 each at launch: 256 x 208 + 128 x 80 <= 384 x 168,
+  // 256 x 200 + 128 x 64 + 128 x 48 = 512 x 128
+  static constexpr int kRegsSoftmax = E ? 200 : 208, kRegsOther = E ? 64 : 80, kRegsConvert = 48;
+  static constexpr int kSlots = E ? 4 : 5;     // K and V tiles in BF16
+  static constexpr int kRawSlots = E ? 2 : 0;  // in 8 bits, on their way to those
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffRing = kOffQ + 2 * kQBytes;
+  static constexpr int kOffRaw = kOffRing + kSlots * kSlot;
+  static constexpr int kOffScale = kOffRaw + kRawSlots * kRawTile;
+  static constexpr int kOffBar = kOffScale + kRawSlots * kScaleBytes;
+  static constexpr int kNumBars = 2 * kSlots + 10 + 2 * kRawSlots;
+  static constexpr int kOffItems = kOffBar + ((8 * kNumBars + 15) / 16) * 16;
+  static constexpr int kOffMisc = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
+  static constexpr int kSmem = kOffMisc + 80;   // items, header (at 16), tensor memory (at 64), abort and busy flags
+  static constexpr int kSmemAlloc = kSmem + 1024;
+  static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
+};
+// Values in 8 bits become BF16 numbers times 2^-64, which holds every scale: the
+// scores' factor and the outputs make up for it.
+constexpr float kE4m3Up = 18446744073709551616.0f;
 
 // one tile, or the part of one, of a CTA
 struct Item {
@@ -232,6 +247,25 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// Two E4M3 codes, each in the upper byte of 16 bits, as BF16 numbers times `f2`: exponent
+// and mantissa go to the places that BF16 has for them, where they stand for
+// code * 2^-120, subnormal codes among them; exact.  (A NaN code counts as 480.)
+__device__ __forceinline__ uint32_t bf16x2_of_e4m3(uint32_t codes, uint32_t f2) {
+  const uint32_t x = ((codes >> 4) & 0x07F007F0u) | (codes & 0x80008000u);
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(f2));
+  return d;
+}
+
 // 32 bytes: a whole sector at once, if the address is a multiple of 32
 __device__ __forceinline__ void store32(void* p, const uint32_t* v, int wide) {
   if (wide) {
@@ -296,9 +330,10 @@ __device__ __forceinline__ int visible(const ChunkArgs& a, int ctx, int T, int t
 // All warps meet here from their own loops, some of which one lane alone goes through.
 // (bar.sync and the .aligned instructions below, tcgen05.ld and .st among them, want the
 // warp's lanes together; behind code that may part them a __syncwarp brings them so.)
+template <int Threads>
 __device__ __forceinline__ void sync_all() {
   __syncwarp();
-  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+  asm volatile("bar.sync 1, %0;" ::"n"(Threads) : "memory");
 }
 
 template <typename V>
@@ -316,6 +351,7 @@ __device__ __forceinline__ V warp_scan(V v) {   // inclusive
 // Requests are taken 32 at a time, one a lane; each list starts again from the
 // first.  (One warp and one place in the code: the list's instructions are fetched
 // once, which is most of the time that a short list takes.)
+template <int Threads>
 __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, volatile int* s_n_items, Header* s_hdr,
                                            const volatile int* s_abort) {
   const int lane = threadIdx.x & 31;
@@ -418,19 +454,22 @@ __device__ __forceinline__ void make_lists(const ChunkArgs& a, Item* items, vola
     x0 = next;
     if (lane == 0) *s_n_items = min(n_items, kMaxItems);
     __syncwarp();
-    sync_all();   // the list is there
-    sync_all();   // and done with
+    sync_all<Threads>();   // the list is there
+    sync_all<Threads>();   // and done with
     if (*s_abort) return;
   }
   if (lane == 0) *s_n_items = 0;
   __syncwarp();
-  sync_all();
+  sync_all<Threads>();
 }
 
 // ------------------------------------------------------------------ kernel
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool E>
+__global__ void __launch_bounds__(Layout<E>::kThreads, 1)
 chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  using S = Layout<E>;
+  constexpr int kSlots = S::kSlots, kOffQ = S::kOffQ, kOffRing = S::kOffRing, kOffItems = S::kOffItems, kOffMisc = S::kOffMisc;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -445,7 +484,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   volatile int* s_busy = reinterpret_cast<volatile int*>(smem + kOffMisc + 72);   // a group's products are being issued
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 68);
 
-  const uint32_t bar0 = base + kOffBar;
+  const uint32_t bar0 = base + S::kOffBar;
   auto kv_full = [&](int s) { return bar0 + 8 * s; };
   auto kv_empty = [&](int s) { return bar0 + 8 * (kSlots + s); };
   const uint32_t bars = bar0 + 8 * 2 * kSlots;
@@ -455,10 +494,12 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   auto o_done = [&](int g) { return bars + 8 * (6 + g); };
   const uint32_t drained = bars + 8 * 8;   // used once, by a CTA that gives up
   const uint32_t met = bars + 8 * 9;       // both groups, behind a sum that was taken out
+  auto raw_full = [&](int s) { return bars + 8 * (10 + s); };
+  auto raw_empty = [&](int s) { return bars + 8 * (10 + S::kRawSlots + s); };
 
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(kv_full(s), 1);
+      mbar_init(kv_full(s), E ? 4 : 1);   // E: the converting warps
       mbar_init(kv_empty(s), 2);   // both groups
     }
     for (int g = 0; g < 2; ++g) {
@@ -466,6 +507,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       mbar_init(s_full(g), 1);
       mbar_init(p_full(g), kGroupRows);
       mbar_init(o_done(g), 1);
+    }
+    for (int s = 0; s < S::kRawSlots; ++s) {
+      mbar_init(raw_full(s), 1);
+      mbar_init(raw_empty(s), 4);
     }
     mbar_init(drained, 2);
     mbar_init(met, 2 * kGroupRows);
@@ -495,7 +540,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     *s_abort = 1;
   };
   // counters of each role, running over all items
-  uint32_t n_kv_ring = 0;     // K and V tiles through the ring (producer; MMA warp)
+  uint32_t n_kv_ring = 0;     // K and V tiles through the ring (producer; converting and MMA warps)
   uint32_t n_tile_g = 0;      // S tiles of this thread's group (softmax)
   uint32_t n_met = 0;         // phases of `met`
   uint32_t mma_items = 0, mma_tiles = 0;   // of the tensor-core warp's group
@@ -504,18 +549,69 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   // Every role goes through the lists of items that the list warp makes, and
   // meets the others in front of and behind each.
   auto next_list = [&]() {
-    sync_all();
+    sync_all<S::kThreads>();
     return *s_n_items;
   };
   auto list_done = [&]() {   // false: a wait has run out somewhere
-    sync_all();
+    sync_all<S::kThreads>();
     return *s_abort == 0;
   };
 
-  if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  if (E && warp >= kConvertWarp) {
+    // ================= E: tiles in 8 bits to BF16, swizzled as the products want them.  A
+    // warp takes 32 tokens, a block of one scale; 8 lanes that read or write together
+    // have two tokens that differ in bits 0 and 2, so that their pieces of 16 bytes lie in
+    // different banks on both sides.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsConvert));
+    const int part = lane & 3, tok = (lane >> 3) ^ (lane & 4 ? 5 : 0), block = warp - kConvertWarp;
+    const uint32_t row = (uint32_t)(32 * block + tok) * kH;   // bytes in either layout
+    constexpr int kRing = E ? S::kRawSlots : 1;
+    while (const int n_items = next_list()) {
+      for (int i = n_items - 1; i >= 0 && !failed; --i) {
+        const int k0 = items[i].k0, k1 = items[i].k1;
+        if (items[i].kind == kNothing || k0 == k1) continue;
+        for (int k = 2 * k0; k < 2 * k1; ++k, ++n_kv_ring) {
+          const int rs = n_kv_ring % kRing, s = n_kv_ring % kSlots;
+          if (!mbar_wait(raw_full(rs), (n_kv_ring / kRing) & 1, wait_ns)) failed = true;
+          if (n_kv_ring >= kSlots && !mbar_wait(kv_empty(s), (n_kv_ring / kSlots - 1) & 1, wait_ns)) failed = true;
+          failed = __any_sync(0xffffffffu, failed);
+          if (failed) break;
+          const int byte = smem[S::kOffScale + rs * kScaleBytes + 8 * (k & 1) + 4 * (k >> 1 & 1) + block];
+          // 2^(s - 127 - 64) and the 2^120 between an E4M3 code and the same bits as BF16
+          const uint32_t f = (uint32_t)(min(max(byte, kScaleLo), kScaleHi) + 56) << 7, f2 = f | f << 16;
+          const uint32_t src = base + S::kOffRaw + rs * kRawTile + row, dst = base + kOffRing + s * kSlot + row;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {      // 8 tokens
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {    // 64 channels
+              const uint4 c = lds16(src + x * 8 * kH + (((4 * h + part) ^ tok) << 4));
+              const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[2 * e] = bf16x2_of_e4m3(__byte_perm(w[e], 0u, 0x1404u), f2);
+                o[2 * e + 1] = bf16x2_of_e4m3(__byte_perm(w[e], 0u, 0x3424u), f2);
+              }
+              const uint32_t to = dst + h * kBox + x * 8 * kH;
+              sts16(to + (((2 * part) ^ tok) << 4), o);
+              sts16(to + (((2 * part + 1) ^ tok) << 4), o + 4);
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(kv_full(s));
+            mbar_arrive(raw_empty(rs));
+          }
+        }
+      }
+      if (failed && lane == 0) give_up();
+      if (!list_done()) break;
+    }
+  } else if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsOther));
     if (warp == kListWarp) {
-      make_lists(a, items, s_n_items, s_hdr, s_abort);
+      make_lists<S::kThreads>(a, items, s_n_items, s_hdr, s_abort);
     } else {
     while (const int n_items = next_list()) {
       if (warp == kTmaWarp) {
@@ -538,8 +634,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               }
 #pragma unroll
               for (int kv = 0; kv < 2; ++kv) {
-                const int s = n_kv_ring % kSlots;
-                if (n_kv_ring >= kSlots && !mbar_wait(kv_empty(s), (n_kv_ring / kSlots - 1) & 1, wait_ns)) {
+                constexpr int kRing = E ? S::kRawSlots : kSlots;
+                const int s = n_kv_ring % kRing;
+                if (n_kv_ring >= kRing &&
+                    !mbar_wait(E ? raw_empty(s) : kv_empty(s), (n_kv_ring / kRing - 1) & 1, wait_ns)) {
                   give_up();
                   failed = true;
                   break;
@@ -548,10 +646,17 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
                   ++n_kv_ring;
                   continue;
                 }
-                const uint32_t dst = base + kOffRing + s * kSlot;
-                mbar_expect_tx(kv_full(s), kSlot);
-                tma_tile_g2s(dst, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys, (int)(id * kH), kv_full(s));
-                tma_tile_g2s(dst + kBox, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys + 64, (int)(id * kH), kv_full(s));
+                if constexpr (E) {
+                  mbar_expect_tx(raw_full(s), kRawTile + kScaleBytes);
+                  tma_tile_g2s(base + S::kOffRaw + s * kRawTile, kv ? &tm_v : &tm_k, 0, (int)(id * kP) + (k & 1) * kTileKeys,
+                               raw_full(s));
+                  bulk_g2s(base + S::kOffScale + s * kScaleBytes, a.scales + id * kScaleBytes, kScaleBytes, raw_full(s));
+                } else {
+                  const uint32_t dst = base + kOffRing + s * kSlot;
+                  mbar_expect_tx(kv_full(s), kSlot);
+                  tma_tile_g2s(dst, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys, (int)(id * kH), kv_full(s));
+                  tma_tile_g2s(dst + kBox, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys + 64, (int)(id * kH), kv_full(s));
+                }
                 ++n_kv_ring;
               }
             }
@@ -567,7 +672,11 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         const int g = warp == kMmaWarp ? 0 : 1;
         const uint32_t t_s = uni(tmem) + g * 128, t_o = uni(tmem) + 256 + g * 128;
         const uint64_t q_desc = desc_k(uni(base) + kOffQ + g * kQBytes);
-        const uint64_t k_desc = desc_mn(uni(base) + kOffRing), v_desc = desc_k(uni(base) + kOffRing);
+        // a BF16 page is channel-major, one in 8 bits token-major: K and V change places
+        const uint64_t k_desc = E ? desc_k(uni(base) + kOffRing) : desc_mn(uni(base) + kOffRing);
+        const uint64_t v_desc = E ? desc_mn(uni(base) + kOffRing) : desc_k(uni(base) + kOffRing);
+        auto step_k = [](int ks) { return (uint64_t)((ks >> 2) * (kBox >> 4) + (ks & 3) * 2); };   // 16 along K, K-major
+        auto step_mn = [](int ks) { return (uint64_t)(ks * 128); };                                // MN-major
         for (int i = n_items - 1; i >= 0 && !failed; --i) {
           const int n = uni(items[i].k1 - items[i].k0);
           const bool both = uni(items[i].rows) > kGroupRows;
@@ -595,7 +704,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             const uint64_t k = k_desc + (uint64_t)(s * (kSlot >> 4));
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              mma_ss(t_s, q_desc + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, k + ks * 128, kIdescMn, ks > 0);
+              mma_ss(t_s, q_desc + step_k(ks), k + (E ? step_k(ks) : step_mn(ks)), E ? kIdesc : kIdescMn, ks > 0);
             tc_commit(s_full(g));
           };
           if (!wait(kv_full(u0 % kSlots), (u0 / kSlots) & 1) || !wait(q_full(g), mma_items & 1)) break;
@@ -613,7 +722,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             if (!wait(kv_full(sv), (uv / kSlots) & 1)) break;
             const int tail = keys - j * kTileKeys;   // valid keys of the tile
             const int steps = uni(min(8, (tail + 15) >> 4));   // products of 16 keys that hold valid ones
-            if (tail < steps * 16) {
+            if (!E && tail < steps * 16) {   // (codes in 8 bits become numbers, whatever they are)
               // Zero the V rows of the last product's tokens past the context: 16-byte
               // pieces of 8 tokens, the one that the context ends in value by value.
               // (Both groups' warps do so; they write the same.)
@@ -665,10 +774,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               if (steps == 8) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, more || ks > 0);
+                  mma_ts(t_o, t_s + ks * 8, v + (E ? step_mn(ks) : step_k(ks)), E ? kIdescMn : kIdesc, more || ks > 0);
               } else {
                 for (int ks = 0; ks < steps; ++ks)
-                  mma_ts(t_o, t_s + ks * 8, v + (ks >> 2) * (kBox >> 4) + (ks & 3) * 2, kIdesc, more || ks > 0);
+                  mma_ts(t_o, t_s + ks * 8, v + (E ? step_mn(ks) : step_k(ks)), E ? kIdescMn : kIdesc, more || ks > 0);
               }
               tc_commit(o_done(g));
               tc_commit(kv_empty(sv));
@@ -687,7 +796,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoftmax));
     const int two_tokens = 2 / a.G, two_rows = 2 - two_tokens * a.G;
     while (const int n_items = next_list()) {
       // ================= softmax: group g, one row a thread
@@ -901,7 +1010,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         }
         // ---- the row's output, or its part
         const bool part = it.kind != kDirect;
-        const float scale = part ? 1.0f : l > 0.0f ? 1.0f / l : l;   // 0 for a row without keys, NaN stays
+        const float scale = (E ? kE4m3Up : 1.0f) * (part ? 1.0f : l > 0.0f ? 1.0f / l : l);   // 0 for a row without keys, NaN stays
         const int rr = g * kGroupRows + r;
         float* slot = a.ws_o + (int64_t)(2 * c + (it.kind == kPartB)) * a.slot_rows * (kH + 2);
         if (part) {
@@ -953,8 +1062,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     copies_done();
     // the copies and products in flight end before the memory they use is given up
     if (warp == kTmaWarp && lane == 0) {
-      for (uint32_t u = n_kv_ring > kSlots ? n_kv_ring - kSlots : 0; u < n_kv_ring; ++u)
-        if (!(a.inject && u == 1)) mbar_wait(kv_full(u % kSlots), (u / kSlots) & 1, wait_ns);
+      constexpr int kRing = E ? S::kRawSlots : kSlots;
+      for (uint32_t u = n_kv_ring > kRing ? n_kv_ring - kRing : 0; u < n_kv_ring; ++u)
+        if (!(a.inject && u == 1)) mbar_wait(E ? raw_full(u % kRing) : kv_full(u % kRing), (u / kRing) & 1, wait_ns);
     }
     if (warp == kMmaWarp || warp == kMmaWarp1) {
       if (elected()) tc_commit(drained);
@@ -1084,20 +1194,17 @@ size_t chunk_ws_bytes(int64_t n_rows, int G) {
   return (size_t)kMaxCtas * sizeof(Header) + (size_t)3 * chunk_ctas() * chunk_slot_rows(n_rows, G) * (kH + 2) * 4;
 }
 
-cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {
+template <bool E>
+cudaError_t launch_chunk(ChunkArgs a, const CUtensorMap& tk, const CUtensorMap& tv, void* workspace, cudaStream_t s) {
   static bool configured[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+        cudaFuncSetAttribute(chunk_attn_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<E>::kSmemAlloc);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  if (n_pool_too_large(a.n_pool)) return cudaErrorInvalidValue;
-  CUtensorMap tk, tv;
-  if (!bf16_page_map(&tk, a.k_pages, a.n_pool) || !bf16_page_map(&tv, a.v_pages, a.n_pool))
-    return cudaErrorInvalidValue;
   a.n_cta = chunk_ctas();
   a.by_G = a.G > 1 ? ~0ull / a.G + 1 : 0;
   a.by_heads = a.Hkv > 1 ? ~0ull / a.Hkv + 1 : 0;
@@ -1105,9 +1212,26 @@ cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s) {
   a.slot_rows = chunk_slot_rows(a.n_rows, a.G);
   a.ws_hdr = workspace;
   a.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * sizeof(Header));
-  cudaError_t e = launch_programmatic(chunk_attn_kernel, dim3(a.n_cta), dim3(kThreads), kSmemAlloc, s, a, tk, tv);
+  cudaError_t e = launch_programmatic(chunk_attn_kernel<E>, dim3(a.n_cta), dim3(Layout<E>::kThreads),
+                                      Layout<E>::kSmemAlloc, s, a, tk, tv);
   if (e != cudaSuccess) return e;
   return launch_programmatic(chunk_combine_kernel, dim3(a.n_cta, (a.slot_rows + 31) / 32), dim3(kJoinThreads), 0, s, a);
+}
+
+cudaError_t launch_chunk_attn(const ChunkArgs& a, void* workspace, cudaStream_t s) {
+  if (n_pool_too_large(a.n_pool)) return cudaErrorInvalidValue;
+  CUtensorMap tk, tv;
+  if (!bf16_page_map(&tk, a.k_pages, a.n_pool) || !bf16_page_map(&tv, a.v_pages, a.n_pool))
+    return cudaErrorInvalidValue;
+  return launch_chunk<false>(a, tk, tv, workspace, s);
+}
+
+cudaError_t launch_chunk_attn_e4m3(ChunkArgs a, void* workspace, cudaStream_t s) {
+  CUtensorMap tk, tv;
+  // a page is two tiles of 128 rows of 128 bytes
+  if (!plane_map(&tk, a.k_codes, 2 * a.n_pool) || !plane_map(&tv, a.v_codes, 2 * a.n_pool)) return cudaErrorInvalidValue;
+  a.scale_log2 *= kE4m3Up;
+  return launch_chunk<true>(a, tk, tv, workspace, s);
 }
 
 }  // namespace lynx

@@ -840,10 +840,27 @@ size_t lynx_chunk_attn_workspace_size(int64_t n_rows, int B, int Hq, int Hkv, in
   return chunk_ws_bytes(n_rows, Hq / Hkv);
 }
 
-int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq,
-                         int Hkv, int head_dim, const void* k_pages, const void* v_pages, int64_t n_pool_pages,
-                         const int32_t* page_table, int max_pages, const int32_t* ctx_len, float sm_scale, int causal,
-                         void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+
+// what the calls over pages in 8 bits have in common
+int check_e4m3_pools(const void* k_pages, const void* v_pages, const uint8_t* scales, int64_t n_pool) {
+  if (!k_pages || !v_pages || !scales) return fail(LYNX_ERR_INVALID_ARG, "NULL page pool or scales");
+  if (n_pool < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool);
+  if (n_pool >= (int64_t)1 << 23) return fail(LYNX_ERR_UNSUPPORTED, "n_pool_pages=%lld too large", (long long)n_pool);
+  if (misaligned(k_pages) || misaligned(v_pages) || misaligned(scales))
+    return fail(LYNX_ERR_ALIGNMENT, "the pools and scales must be 16-byte aligned");
+  return LYNX_OK;
+}
+
+}  // namespace
+
+namespace {
+
+// e4m3: the pools are pages in 8 bits with their scales
+int chunk_common(bool e4m3, const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq, int Hkv,
+                 int head_dim, const void* k_pages, const void* v_pages, const uint8_t* scales, int64_t n_pool_pages,
+                 const int32_t* page_table, int max_pages, const int32_t* ctx_len, float sm_scale, int causal, void* out,
+                 int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream, const char* launch) {
   g_last_error[0] = '\0';
   int st = check_chunk_shape(n_rows, B, Hq, Hkv, head_dim);
   if (st != LYNX_OK) return st;
@@ -856,10 +873,15 @@ int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride,
   if (causal != 0 && causal != 1) return fail(LYNX_ERR_INVALID_ARG, "causal=%d", causal);
   if (!(sm_scale > 0.0f) || !isfinite(sm_scale))
     return fail(LYNX_ERR_INVALID_ARG, "sm_scale=%g must be finite and > 0", (double)sm_scale);
+  if (e4m3 && sm_scale > 1048576.0f) return fail(LYNX_ERR_UNSUPPORTED, "sm_scale=%g > 2^20", (double)sm_scale);
   if (n_rows == 0) return LYNX_OK;
   if (!q_bf16 || !cu_q || !k_pages || !v_pages || !page_table || !ctx_len || !out)
     return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
   if (n_pool_pages < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool_pages);
+  if (e4m3) {
+    st = check_e4m3_pools(k_pages, v_pages, scales, n_pool_pages);
+    if (st != LYNX_OK) return st;
+  }
   if (n_pool_too_large(n_pool_pages))
     return fail(LYNX_ERR_UNSUPPORTED, "n_pool_pages=%lld too large", (long long)n_pool_pages);
   if (misaligned(q_bf16) || misaligned(k_pages) || misaligned(v_pages) || misaligned(out) || misaligned(workspace) ||
@@ -884,8 +906,14 @@ int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride,
   a.cu_q = cu_q;
   a.ctx_len = ctx_len;
   a.page_table = page_table;
-  a.k_pages = static_cast<const uint16_t*>(k_pages);
-  a.v_pages = static_cast<const uint16_t*>(v_pages);
+  if (e4m3) {
+    a.k_codes = static_cast<const uint8_t*>(k_pages);
+    a.v_codes = static_cast<const uint8_t*>(v_pages);
+    a.scales = scales;
+  } else {
+    a.k_pages = static_cast<const uint16_t*>(k_pages);
+    a.v_pages = static_cast<const uint16_t*>(v_pages);
+  }
   a.n_pool = n_pool_pages;
   a.out = out;
   a.lse = lse;
@@ -904,9 +932,31 @@ int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride,
     a.inject = 1;
     a.wait_ns = 1000000ull;
   }
-  cudaError_t e = launch_chunk_attn(a, workspace, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "lynx_chunk_attn_bf16 launch");
+  cudaError_t e = e4m3 ? launch_chunk_attn_e4m3(a, workspace, static_cast<cudaStream_t>(stream))
+                       : launch_chunk_attn(a, workspace, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, launch);
   return LYNX_OK;
+}
+
+}  // namespace
+
+int lynx_chunk_attn_bf16(const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq,
+                         int Hkv, int head_dim, const void* k_pages, const void* v_pages, int64_t n_pool_pages,
+                         const int32_t* page_table, int max_pages, const int32_t* ctx_len, float sm_scale, int causal,
+                         void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return chunk_common(false, q_bf16, n_rows, row_stride, cu_q, B, Hq, Hkv, head_dim, k_pages, v_pages, nullptr,
+                             n_pool_pages, page_table, max_pages, ctx_len, sm_scale, causal, out, out_dtype, lse,
+                             workspace, workspace_bytes, stream, "lynx_chunk_attn_bf16 launch");
+}
+
+int lynx_chunk_attn_e4m3(const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq,
+                         int Hkv, int head_dim, const void* k_pages, const void* v_pages, const uint8_t* scales,
+                         int64_t n_pool_pages, const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                         float sm_scale, int causal, void* out, int out_dtype, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return chunk_common(true, q_bf16, n_rows, row_stride, cu_q, B, Hq, Hkv, head_dim, k_pages, v_pages, scales,
+                            n_pool_pages, page_table, max_pages, ctx_len, sm_scale, causal, out, out_dtype, lse,
+                            workspace, workspace_bytes, stream, "lynx_chunk_attn_e4m3 launch");
 }
 
 int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, const void* q, int64_t q_stride_b,
@@ -935,20 +985,6 @@ int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, co
   if (e != cudaSuccess) return cuda_fail(e, "lynx_verify_drafts launch");
   return LYNX_OK;
 }
-
-namespace {
-
-// what the calls over pages in 8 bits have in common
-int check_e4m3_pools(const void* k_pages, const void* v_pages, const uint8_t* scales, int64_t n_pool) {
-  if (!k_pages || !v_pages || !scales) return fail(LYNX_ERR_INVALID_ARG, "NULL page pool or scales");
-  if (n_pool < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool);
-  if (n_pool >= (int64_t)1 << 23) return fail(LYNX_ERR_UNSUPPORTED, "n_pool_pages=%lld too large", (long long)n_pool);
-  if (misaligned(k_pages) || misaligned(v_pages) || misaligned(scales))
-    return fail(LYNX_ERR_ALIGNMENT, "the pools and scales must be 16-byte aligned");
-  return LYNX_OK;
-}
-
-}  // namespace
 
 size_t lynx_decode_attn_e4m3_workspace_size(int B, int T, int Hq, int Hkv, int head_dim) {
   if (check_decode_shape(B, T, Hq, Hkv, head_dim, 1) != LYNX_OK) return 0;

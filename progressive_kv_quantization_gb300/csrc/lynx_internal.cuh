@@ -267,6 +267,9 @@ struct ChunkArgs {
   const int32_t* page_table;
   const uint16_t* k_pages;
   const uint16_t* v_pages;
+  const uint8_t* k_codes;   // pages in 8 bits, instead of the two above
+  const uint8_t* v_codes;
+  const uint8_t* scales;
   int64_t n_pool;
   void* out;
   float* lse;            // NULL to skip
@@ -311,6 +314,7 @@ size_t decode_e4m3_ws_bytes(int rows);
 cudaError_t launch_decode_e4m3(DecodeE4m3Args a, void* workspace, cudaStream_t s);
 
 size_t chunk_ws_bytes(int64_t n_rows, int G);
-cudaError_t launch_chunk_attn(ChunkArgs a, void* workspace, cudaStream_t s);
+cudaError_t launch_chunk_attn(const ChunkArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_chunk_attn_e4m3(ChunkArgs a, void* workspace, cudaStream_t s);
 
 }  // namespace lynx

@@ -93,6 +93,8 @@ SIGNATURES = {
     "lynx_decode_attn_e4m3": (_I32, [_VP, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _I64, _VP, _I32, _VP, _F32, _I32,
                                      _VP, _VP, _VP, _SZ, _VP]),
     "lynx_decode_attn_e4m3_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "lynx_chunk_attn_e4m3": (_I32, [_VP, _I64, _I64, _VP, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _I64, _VP, _I32, _VP,
+                                    _F32, _I32, _VP, _I32, _VP, _VP, _SZ, _VP]),
     "lynx_decode_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "lynx_device_status": (_I32, []),
     "lynx_test_inject_wait_timeout": (_I32, [_I32]),
@@ -603,6 +605,17 @@ def lynx_decode_attn_e4m3(q, k_pages, v_pages, scales, page_table, ctx_len, n_kv
     return (_binding or _native()).decode_attn_e4m3(q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads,
                                                     sm_scale, causal, out, lse, workspace,
                                                     stream and stream.cuda_stream)
+
+
+def lynx_chunk_attn_e4m3(q, cu_q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads: int, sm_scale=None,
+                         causal=True, out=None, lse=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """lynx_chunk_attn_bf16 over pages in 8 bits (k_pages, v_pages, scales as
+    lynx_decode_attn_e4m3); the workspace is lynx_chunk_attn_workspace_size's."""
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise LynxError("out_dtype must be torch.bfloat16 or torch.float32")
+    return (_binding or _native()).chunk_attn_e4m3(q, cu_q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads,
+                                                   sm_scale, causal, out, lse, out_dtype is torch.float32, workspace,
+                                                   stream and stream.cuda_stream)
 
 
 def lynx_device_status():
