@@ -34,7 +34,7 @@
  *                         BF16 pages: pages and slots of new tokens, their norm,
  *                         rotation and write, attention of ragged chunks
  *                         (prefill), verification of drafted tokens (§4.3).
- *   lynx_decode_attn_e4m3, lynx_chunk_attn_e4m3
+ *   lynx_qkv_append_e4m3, lynx_decode_attn_e4m3, lynx_chunk_attn_e4m3
  *                         serving over pages in 8 bits: E4M3 codes with a scale
  *                         for each block of 32 tokens of a head.
  *
@@ -551,6 +551,23 @@ int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, co
  * of positions below ctx_len must not be NaN (0x7F, 0xFF); codes and scales of what lies
  * behind may be anything.  Limit: n_pool_pages < 2^23.
  */
+
+/* lynx_qkv_append into pages in 8 bits; arguments and errors as there, with the
+ * scales of the pools.  The new rows of one block of 32 tokens must follow one another, in
+ * the order of their tokens and without a gap (as lynx_assign_pages gives them).  Of a block
+ * that rows are written to, with x the float32 keys (behind norm and rotation) or
+ * values of those rows:
+ *   s' = the smallest byte in 74..198 with max |x| <= 448 * 2^(s' - 127) (198 if none), but no
+ *        smaller than the block's byte s unless the rows begin at the block's first token
+ *   code = x * 2^(127 - s'), rounded once to E4M3 (to nearest even, at most 448);
+ *   codes in front of the rows become code * 2^(s - s'), rounded again (which changes a value
+ *   only where it becomes a subnormal code)
+ * so that a block's first token forgets what the page held before, and drafts that are
+ * taken back leave at most a larger scale behind.  Codes behind the rows stay as they are. */
+int lynx_qkv_append_e4m3(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
+                         const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
+                         int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
+                         void* k_pages, void* v_pages, uint8_t* scales, int64_t n_pool_pages, void* stream);
 
 /* Decode / verification attention over pages in 8 bits: arguments as
  * lynx_decode_attn_bf16, but only q, the pools, scales, out and the workspace need 16-byte

@@ -229,10 +229,10 @@ PyObject* assign_pages(PyObject* const* a) {
   return tuple({&cu, &pos, &slots, &out, &taken});
 }
 
-// qkv, n_q_heads, n_kv_heads, cos_sin, positions, slots, k_pages, v_pages, q_weight, k_weight, norm_eps, interleaved,
-// q_out, stream
-PyObject* qkv_append(PyObject* const* a) {
-  Call c("lynx_qkv_append", a[0], "qkv");
+// The rows and what becomes of them, whatever the pages hold; arguments of `a`: qkv, n_q_heads, n_kv_heads, cos_sin,
+// positions, slots; of `b`: q_weight, k_weight, norm_eps, interleaved, q_out, stream
+template <typename F>
+PyObject* append(Call& c, PyObject* const* a, PyObject* const* b, F call) {
   const at::Tensor& qkv = c.tensor(a[0], "qkv");
   const int Hq = to_int(a[1], "n_q_heads"), Hkv = to_int(a[2], "n_kv_heads");
   if (qkv.scalar_type() != at::kBFloat16 || qkv.dim() != 2 || (qkv.size(1) > 1 && qkv.stride(1) != 1))
@@ -250,24 +250,35 @@ PyObject* qkv_append(PyObject* const* a) {
     rot = dim32(cs.size(1), "cos_sin");
     table = c.at(a[3], at::kFloat, {max_pos, rot}, "cos_sin");
   }
-  if (a[8] != Py_None) wq = c.at(a[8], at::kFloat, {128}, "q_weight");
-  if (a[9] != Py_None) wk = c.at(a[9], at::kFloat, {128}, "k_weight");
+  if (b[0] != Py_None) wq = c.at(b[0], at::kFloat, {128}, "q_weight");
+  if (b[1] != Py_None) wk = c.at(b[1], at::kFloat, {128}, "k_weight");
   void* pos = c.at(a[4], at::kInt, {n_rows}, "positions");
   void* slots = c.at(a[5], at::kLong, {n_rows, Hkv}, "slots");
+  const float eps = to_float(b[2]);
+  const int interleaved = PyObject_IsTrue(b[3]);
+  void* stream = c.stream(b[5]);
+  Out q;
+  q.o = c.make(b[4], at::kBFloat16, {n_rows, Hq, 128}, "q_out", &q.p);
+  c.launch([&] {
+    return call(qkv.data_ptr(), n_rows, stride, Hq, Hkv, 128, (float*)wq, (float*)wk, eps, (float*)table, max_pos, rot,
+                interleaved, (int32_t*)pos, (int64_t*)slots, q.p, stream);
+  });
+  return q.take();
+}
+
+// qkv, n_q_heads, n_kv_heads, cos_sin, positions, slots, k_pages, v_pages, q_weight, k_weight, norm_eps, interleaved,
+// q_out, stream
+PyObject* qkv_append(PyObject* const* a) {
+  Call c("lynx_qkv_append", a[0], "qkv");
   const at::Tensor& kp = c.tensor(a[6], "k_pages");
   const int64_t n_pool = kp.dim() == 3 ? kp.size(0) : 0;
   void* k = c.at(a[6], at::kBFloat16, {n_pool, 128, 256}, "k_pages");
   void* v = c.at(a[7], at::kBFloat16, {n_pool, 128, 256}, "v_pages");
-  const float eps = to_float(a[10]);
-  const int interleaved = PyObject_IsTrue(a[11]);
-  void* stream = c.stream(a[13]);
-  Out q;
-  q.o = c.make(a[12], at::kBFloat16, {n_rows, Hq, 128}, "q_out", &q.p);
-  c.launch([&] {
-    return lynx_qkv_append(qkv.data_ptr(), n_rows, stride, Hq, Hkv, 128, (float*)wq, (float*)wk, eps, (float*)table,
-                           max_pos, rot, interleaved, (int32_t*)pos, (int64_t*)slots, q.p, k, v, n_pool, stream);
+  return append(c, a, a + 8, [&](auto qkv, int64_t n_rows, int64_t stride, int Hq, int Hkv, int D, auto wq, auto wk, float eps,
+                                 auto table, int max_pos, int rot, int interleaved, auto pos, auto slots, auto q, auto stream) {
+    return lynx_qkv_append(qkv, n_rows, stride, Hq, Hkv, D, wq, wk, eps, table, max_pos, rot, interleaved, pos, slots, q, k,
+                           v, n_pool, stream);
   });
-  return q.take();
 }
 
 // The chunks' rows, tables and outputs, whatever the pages hold; arguments from `a` on: page_table, ctx_len,
@@ -396,6 +407,18 @@ PyObject* decode_attn_e4m3(PyObject* const* a) {
   return tuple({&out, &lse});
 }
 
+// qkv, n_q_heads, n_kv_heads, cos_sin, positions, slots, k_pages, v_pages, scales, q_weight, k_weight, norm_eps,
+// interleaved, q_out, stream
+PyObject* qkv_append_e4m3(PyObject* const* a) {
+  Call c("lynx_qkv_append_e4m3", a[0], "qkv");
+  const Pools8 pools(c, a[6], a[7], a[8]);
+  return append(c, a, a + 9, [&](auto qkv, int64_t n_rows, int64_t stride, int Hq, int Hkv, int D, auto wq, auto wk, float eps,
+                                 auto table, int max_pos, int rot, int interleaved, auto pos, auto slots, auto q, auto stream) {
+    return lynx_qkv_append_e4m3(qkv, n_rows, stride, Hq, Hkv, D, wq, wk, eps, table, max_pos, rot, interleaved, pos, slots, q,
+                                pools.k, pools.v, (uint8_t*)pools.scales, pools.n, stream);
+  });
+}
+
 // q, cu_q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads, sm_scale, causal, out, lse, out is float32,
 // workspace, stream
 PyObject* chunk_attn_e4m3(PyObject* const* a) {
@@ -424,6 +447,7 @@ PyMethodDef kMethods[] = {
     {"verify_drafts", FAST((entry<8, verify_drafts>))},
     {"decode_attn_e4m3", FAST((entry<13, decode_attn_e4m3>))},
     {"chunk_attn_e4m3", FAST((entry<15, chunk_attn_e4m3>))},
+    {"qkv_append_e4m3", FAST((entry<15, qkv_append_e4m3>))},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "lynx_binding", nullptr, -1, kMethods};
 

@@ -760,10 +760,23 @@ int lynx_assign_pages(const int32_t* ctx_len, const int32_t* new_len, int B, int
   return LYNX_OK;
 }
 
-int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
-                    const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
-                    int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
-                    void* k_pages, void* v_pages, int64_t n_pool_pages, void* stream) {
+namespace {
+
+// what the calls over pages in 8 bits have in common
+int check_e4m3_pools(const void* k_pages, const void* v_pages, const uint8_t* scales, int64_t n_pool) {
+  if (!k_pages || !v_pages || !scales) return fail(LYNX_ERR_INVALID_ARG, "NULL page pool or scales");
+  if (n_pool < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool);
+  if (n_pool >= (int64_t)1 << 23) return fail(LYNX_ERR_UNSUPPORTED, "n_pool_pages=%lld too large", (long long)n_pool);
+  if (misaligned(k_pages) || misaligned(v_pages) || misaligned(scales))
+    return fail(LYNX_ERR_ALIGNMENT, "the pools and scales must be 16-byte aligned");
+  return LYNX_OK;
+}
+
+// e4m3: the pools are pages in 8 bits with their scales
+int append_common(bool e4m3, const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
+                  const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
+                  int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
+                  void* k_pages, void* v_pages, uint8_t* scales, int64_t n_pool_pages, void* stream, const char* launch) {
   g_last_error[0] = '\0';
   if (n_rows < 0 || Hq < 1 || Hkv < 1)
     return fail(LYNX_ERR_INVALID_ARG, "n_rows=%lld Hq=%d Hkv=%d", (long long)n_rows, Hq, Hkv);
@@ -793,6 +806,10 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
   const int64_t width = ((int64_t)Hq + 2 * (int64_t)Hkv) * kH;
   if (overlap({q_out, n_rows * Hq * kH * 2}, {qkv_bf16, ((n_rows - 1) * row_stride + width) * 2}))
     return fail(LYNX_ERR_INVALID_ARG, "q_out overlaps the rows of qkv");
+  if (e4m3) {
+    const int st = check_e4m3_pools(k_pages, v_pages, scales, n_pool_pages);
+    if (st != LYNX_OK) return st;
+  }
   int* status = device_status_ptr();
   if (!status) return fail(LYNX_ERR_CUDA, "cannot resolve the device status word");
   AppendArgs a{};
@@ -811,13 +828,39 @@ int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, in
   a.positions = positions;
   a.slots = slots;
   a.q_out = static_cast<uint16_t*>(q_out);
-  a.k_pages = static_cast<uint16_t*>(k_pages);
-  a.v_pages = static_cast<uint16_t*>(v_pages);
+  if (e4m3) {
+    a.k_codes = static_cast<uint8_t*>(k_pages);
+    a.v_codes = static_cast<uint8_t*>(v_pages);
+    a.scales = scales;
+  } else {
+    a.k_pages = static_cast<uint16_t*>(k_pages);
+    a.v_pages = static_cast<uint16_t*>(v_pages);
+  }
   a.n_pool = n_pool_pages;
   a.status = status;
   cudaError_t e = launch_qkv_append(a, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "lynx_qkv_append launch");
+  if (e != cudaSuccess) return cuda_fail(e, launch);
   return LYNX_OK;
+}
+
+}  // namespace
+
+int lynx_qkv_append(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
+                    const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
+                    int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
+                    void* k_pages, void* v_pages, int64_t n_pool_pages, void* stream) {
+  return append_common(false, qkv_bf16, n_rows, row_stride, Hq, Hkv, head_dim, q_weight, k_weight, norm_eps, cos_sin,
+                       max_pos, rot_dim, interleaved, positions, slots, q_out, k_pages, v_pages, nullptr, n_pool_pages,
+                       stream, "lynx_qkv_append launch");
+}
+
+int lynx_qkv_append_e4m3(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
+                         const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
+                         int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,
+                         void* k_pages, void* v_pages, uint8_t* scales, int64_t n_pool_pages, void* stream) {
+  return append_common(true, qkv_bf16, n_rows, row_stride, Hq, Hkv, head_dim, q_weight, k_weight, norm_eps, cos_sin,
+                       max_pos, rot_dim, interleaved, positions, slots, q_out, k_pages, v_pages, scales, n_pool_pages,
+                       stream, "lynx_qkv_append_e4m3 launch");
 }
 
 namespace {
@@ -839,20 +882,6 @@ size_t lynx_chunk_attn_workspace_size(int64_t n_rows, int B, int Hq, int Hkv, in
   if (check_chunk_shape(n_rows, B, Hq, Hkv, head_dim) != LYNX_OK) return 0;
   return chunk_ws_bytes(n_rows, Hq / Hkv);
 }
-
-namespace {
-
-// what the calls over pages in 8 bits have in common
-int check_e4m3_pools(const void* k_pages, const void* v_pages, const uint8_t* scales, int64_t n_pool) {
-  if (!k_pages || !v_pages || !scales) return fail(LYNX_ERR_INVALID_ARG, "NULL page pool or scales");
-  if (n_pool < 1) return fail(LYNX_ERR_INVALID_ARG, "n_pool_pages=%lld < 1", (long long)n_pool);
-  if (n_pool >= (int64_t)1 << 23) return fail(LYNX_ERR_UNSUPPORTED, "n_pool_pages=%lld too large", (long long)n_pool);
-  if (misaligned(k_pages) || misaligned(v_pages) || misaligned(scales))
-    return fail(LYNX_ERR_ALIGNMENT, "the pools and scales must be 16-byte aligned");
-  return LYNX_OK;
-}
-
-}  // namespace
 
 namespace {
 

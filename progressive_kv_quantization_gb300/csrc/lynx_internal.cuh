@@ -238,6 +238,9 @@ struct AppendArgs {
   uint16_t* q_out;
   uint16_t* k_pages;
   uint16_t* v_pages;
+  uint8_t* k_codes;        // pages in 8 bits, instead of the two above
+  uint8_t* v_codes;
+  uint8_t* scales;
   int64_t n_pool;
   int* status;
   int heads_per_job, q_jobs, kv_parts, whole_rows;   // set by the launcher

@@ -25,10 +25,21 @@
 // registers; 5.2 TB/s for 4,096 rows of 16 + 4 heads).  A decode step of 64 rows (2.8 us):
 // the launch, the position and then the cosines at it.
 
+//
+// Pages in 8 bits (lynx_qkv_append_e4m3).  A block of 32 tokens has one scale, so that its
+// new rows (a run: rows that follow one another in one block) are quantised together, and what
+// stands in front of them is rounded again where the scale grows.  A CTA takes the
+// runs that begin in its 32 rows, with up to 31 rows behind them: float32 keys and the values
+// wait in shared memory for the run's maximum, a page's token is then one 128-byte store.
+// Powers of two as scales make the rounding that of E4M3 alone, and rounding a code
+// again under a larger one changes it only where it becomes subnormal.
+
+#include "e4m3.cuh"
 #include "f32x2.cuh"
 #include "lynx_internal.cuh"
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 namespace lynx {
 namespace {
@@ -38,6 +49,8 @@ constexpr int kHalfWarps = kThreads / 16;
 constexpr int kTile = 32;                  // rows per CTA
 constexpr int kBatch = 4;                  // query heads of a row read at once
 constexpr int kPitch = kH / 2 + 1;         // words per staged token: the reading lanes (one token each) hit all banks
+constexpr int kRows8 = 2 * kTile - 1;      // pages in 8 bits: rows that the runs of a tile reach
+constexpr int kSmem8 = kRows8 * kH * 6;    // their keys (float32) and values (BF16)
 
 __device__ __forceinline__ void load4(const float* p, float* v) {
   const float4 a = *reinterpret_cast<const float4*>(p);
@@ -91,7 +104,7 @@ __device__ __forceinline__ Turn load_turn(const float* row, int rot, const float
 // a norm they are copied.  (That costs 27,292 rows with half of each head rotated 3 us;
 // heads rotated as a whole have a kernel of their own, without it.)
 template <bool INTERLEAVED, bool WHOLE>
-__device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool turned, bool norm, float eps) {
+__device__ __forceinline__ void norm_rotate(const uint4& x, const Turn& t, bool turned, bool norm, float eps, float* out) {
   const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
   float a[8];
 #pragma unroll
@@ -108,11 +121,9 @@ __device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool
     for (int k = 8; k > 0; k >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
     r = rsqrtf(ss * (1.0f / kH) + eps);
   }
-  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {
     const int o0 = INTERLEAVED ? i + 1 : i ^ 4, o1 = INTERLEAVED ? i : o0 + 1;
-    float y0, y1;
     const uint64_t own = pair(a[i], a[i + 1]), other = pair(a[o0], a[o1]);
     const uint64_t c = pair(t.c[i], t.c[i + 1]), s = pair(t.s[i], t.s[i + 1]);
     uint64_t y;
@@ -122,8 +133,19 @@ __device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool
       y = mul2(own, c);
       if (turned) y = fma2(other, s, y);
     }
-    unpair(mul2(y, pair(r, r)), y0, y1);
-    const __nv_bfloat162 p = __floats2bfloat162_rn(y0, y1);
+    unpair(mul2(y, pair(r, r)), out[i], out[i + 1]);
+  }
+}
+// the same, rounded
+template <bool INTERLEAVED, bool WHOLE>
+__device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool turned, bool norm, float eps) {
+  float y[8];
+  norm_rotate<INTERLEAVED, WHOLE>(x, t, turned, norm, eps, y);
+  const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(y[i], y[i + 1]);
     w[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
   }
   if (!WHOLE && !norm) {
@@ -133,10 +155,25 @@ __device__ __forceinline__ uint4 norm_rotate(const uint4& x, const Turn& t, bool
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool INTERLEAVED, bool WHOLE>
+// four float32 values as codes
+__device__ __forceinline__ uint32_t e4m3x4(float x0, float x1, float x2, float x3) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x1), "f"(x0));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x3), "f"(x2));
+  return (uint32_t)lo | (uint32_t)hi << 16;
+}
+// four codes times f, rounded once
+__device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
+  const uint32_t lo = f16x2_of(codes), hi = f16x2_of_high(codes);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo)), y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return e4m3x4(x.x * f, x.y * f, y.x * f, y.y * f);
+}
+
+// E: pages in 8 bits
+template <bool INTERLEAVED, bool WHOLE, bool E>
 __global__ void __launch_bounds__(kThreads, 4)
 qkv_append_kernel(const AppendArgs a) {
-  __shared__ uint32_t s_kv[2][kTile * kPitch];
+  __shared__ uint32_t s_kv[2][E ? 1 : kTile * kPitch];
   const int tid = threadIdx.x, lane = tid & 31, lane16 = tid & 15, hw = tid >> 4;
   const unsigned n_jobs = a.q_jobs + a.Hkv * a.kv_parts, n_tiles = (unsigned)((a.n_rows + kTile - 1) / kTile);
   const int job = (int)(a.whole_rows ? blockIdx.x % n_jobs : blockIdx.x / n_tiles);
@@ -227,12 +264,134 @@ qkv_append_kernel(const AppendArgs a) {
     return;
   }
 
-  // ---- a KV head: keys and values to shared memory, then out by channel
+  // ---- a KV head: keys and values to shared memory, then out by channel (E: by token)
   uint4 xk[kSteps], xv[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
     xk[k] = head_at(row_hw + k * kHalfWarps, a.Hq + kv_head);
     xv[k] = head_at(row_hw + k * kHalfWarps, a.Hq + a.Hkv + kv_head);
+  }
+  if constexpr (E) {
+    extern __shared__ __align__(16) float s_dyn[];
+    float4* s_k = reinterpret_cast<float4*>(s_dyn);                        // [row][the lane's two fours][lane]
+    uint4* s_v = reinterpret_cast<uint4*>(s_dyn + kRows8 * kH);            // [row][lane]
+    __shared__ int64_t s_slot[2 * kTile];    // of the rows from row0 - 1 on; -1: not written
+    __shared__ uint32_t s_starts[2];         // rows that begin a run
+    __shared__ uint32_t s_top[2][2 * kTile]; // at a run's first row: largest magnitude of keys and values, as bits
+    __shared__ int s_old[2][2 * kTile];      // and the scales that its block had, 0 if it begins the block
+    if (tid < 2 * kTile) {
+      const int64_t row = row0 - 1 + tid;
+      int64_t slot = -1;
+      if (row >= 0 && row < a.n_rows) {
+        const int p = a.positions[row];
+        slot = a.slots[row * a.Hkv + kv_head];
+        if (p < 0 || (a.rot > 0 && p >= a.max_pos)) slot = -1;
+        if (slot >= a.n_pool * kP) {
+          atomicExch(a.status, 5);
+          slot = -1;
+        }
+      }
+      s_slot[tid] = slot < 0 ? -1 : slot;
+      s_top[0][tid] = s_top[1][tid] = 0u;
+    }
+    __syncthreads();
+    if (tid < 2 * kTile) {
+      const int64_t slot = s_slot[tid];
+      const bool starts = tid > 0 && slot >= 0 && (slot % kC == 0 || s_slot[tid - 1] != slot - 1);
+      const unsigned m = __ballot_sync(0xffffffffu, starts);
+      if (lane == 0) s_starts[tid >> 5] = m;
+      const uint8_t* old = a.scales + slot / kP * kScaleBytes + slot % kP / kC;
+      const bool behind = starts && tid <= kTile && slot % kC != 0;
+      s_old[0][tid] = behind ? min(max((int)old[0], kScaleLo), kScaleHi) : 0;
+      s_old[1][tid] = behind ? min(max((int)old[kChunks], kScaleLo), kScaleHi) : 0;
+    }
+    __syncthreads();
+    const unsigned long long starts = (unsigned long long)s_starts[1] << 32 | s_starts[0];
+    // first row of row i's run, or 0 if that is none of the tile's
+    auto run_of = [&](int i) {
+      const int st = i < 2 * kTile && s_slot[i] >= 0 ? 63 - __clzll((long long)(starts & ((2ull << i) - 1))) : 0;
+      return st > 0 && st <= kTile ? st : 0;
+    };
+#pragma unroll
+    for (int k = 0; k < 2 * kSteps; ++k) {
+      const int i = 1 + k * kHalfWarps + hw, run = run_of(i);
+      if (!__any_sync(0xffffffffu, run > 0)) continue;
+      const int64_t row = row0 + i - 1;
+      uint4 xk_i, xv_i;
+      int p;
+      if (k < kSteps) {
+        xk_i = xk[k];
+        xv_i = xv[k];
+        p = pos[k];
+      } else {
+        xk_i = head_at(row, a.Hq + kv_head);
+        xv_i = head_at(row, a.Hq + a.Hkv + kv_head);
+        p = row < a.n_rows ? a.positions[row] : -1;
+      }
+      p = checked(p);
+      float y[8];
+      norm_rotate<INTERLEAVED, WHOLE>(xk_i, turn_at(p), 8 * lane16 < a.rot, weight != nullptr, a.norm_eps, y);
+      uint32_t top_k = 0, top_v = 0;
+      const uint32_t vw[4] = {xv_i.x, xv_i.y, xv_i.z, xv_i.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top_k = max(top_k, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top_v = max(top_v, max(vw[e] & 0x7FFF0000u, vw[e] << 16 & 0x7FFF0000u));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, o));
+        top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+      }
+      if (run > 0) {
+        s_k[(i - 1) * 32 + lane16] = make_float4(y[0], y[1], y[2], y[3]);
+        s_k[(i - 1) * 32 + 16 + lane16] = make_float4(y[4], y[5], y[6], y[7]);
+        s_v[(i - 1) * 16 + lane16] = xv_i;
+        if (lane16 == 0) {
+          atomicMax(&s_top[0][run], top_k);   // a maximum does not depend on the order
+          atomicMax(&s_top[1][run], top_v);
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2 * kSteps; ++k) {
+      const int i = 1 + k * kHalfWarps + hw, run = run_of(i);
+      if (run == 0) continue;
+      const int64_t slot = s_slot[i];
+      const int old_k = s_old[0][run], old_v = s_old[1][run];
+      const int sk = max(scale_byte(__uint_as_float(s_top[0][run])), old_k);
+      const int sv = max(scale_byte(__uint_as_float(s_top[1][run])), old_v);
+      const float fk = __uint_as_float((uint32_t)(254 - sk) << 23), fv = __uint_as_float((uint32_t)(254 - sv) << 23);
+      const float4 k0 = s_k[(i - 1) * 32 + lane16], k1 = s_k[(i - 1) * 32 + 16 + lane16];
+      const uint4 v = s_v[(i - 1) * 16 + lane16];
+      auto half = [](uint32_t w, bool high) { return __uint_as_float(high ? w & 0xFFFF0000u : w << 16); };
+      uint8_t* kd = a.k_codes + slot * kH;
+      uint8_t* vd = a.v_codes + slot * kH;
+      *reinterpret_cast<uint32_t*>(kd + ca) = e4m3x4(k0.x * fk, k0.y * fk, k0.z * fk, k0.w * fk);
+      *reinterpret_cast<uint32_t*>(kd + cb) = e4m3x4(k1.x * fk, k1.y * fk, k1.z * fk, k1.w * fk);
+      *reinterpret_cast<uint32_t*>(vd + ca) = e4m3x4(half(v.x, false) * fv, half(v.x, true) * fv, half(v.y, false) * fv, half(v.y, true) * fv);
+      *reinterpret_cast<uint32_t*>(vd + cb) = e4m3x4(half(v.z, false) * fv, half(v.z, true) * fv, half(v.w, false) * fv, half(v.w, true) * fv);
+      if (i != run) continue;
+      // the block's scales, and what stands in front of the run under grown ones
+      if (lane16 == 0) {
+        uint8_t* s = a.scales + slot / kP * kScaleBytes + slot % kP / kC;
+        s[0] = (uint8_t)sk;
+        s[kChunks] = (uint8_t)sv;
+      }
+      const int64_t first = slot / kC * kC;
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {
+        const int was = which ? old_v : old_k, now = which ? sv : sk;
+        if (was == 0 || now <= was) continue;
+        const float f = now - was > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - (now - was)) << 23);
+        for (int64_t t = first; t < slot; ++t) {
+          uint2* d = reinterpret_cast<uint2*>((which ? a.v_codes : a.k_codes) + t * kH) + lane16;
+          const uint2 x = *d;
+          *d = make_uint2(rescaled(x.x, f), rescaled(x.y, f));
+        }
+      }
+    }
+    return;
   }
   const int64_t slot_row = row0 + lane;
   const int slot_pos = slot_row < a.n_rows ? a.positions[slot_row] : -1;
@@ -271,6 +430,25 @@ qkv_append_kernel(const AppendArgs a) {
   }
 }
 
+template <bool E>
+cudaError_t launch_kernel(const AppendArgs& a, unsigned grid, cudaStream_t s) {
+  const bool whole = a.rot == kH;
+  auto* const kernel = a.interleaved ? whole ? qkv_append_kernel<true, true, E> : qkv_append_kernel<true, false, E>
+                                     : whole ? qkv_append_kernel<false, true, E> : qkv_append_kernel<false, false, E>;
+  if (E) {
+    static bool configured[64][4] = {{false}};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    bool* done = dev >= 0 && dev < 64 ? &configured[dev][2 * (a.interleaved != 0) + whole] : nullptr;
+    if (!done || !*done) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem8);
+      if (e != cudaSuccess) return e;
+      if (done) *done = true;
+    }
+  }
+  return launch_programmatic(kernel, dim3(grid), dim3(kThreads), E ? kSmem8 : 0, s, a);
+}
+
 }  // namespace
 
 cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s) {
@@ -284,7 +462,7 @@ cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s) {
   // eight CTAs (each norms and rotates the whole head), since every token of a
   // decode step writes 2 bytes of a sector of its own in each channel
   a.kv_parts = 1;
-  while (a.kv_parts < 8 && tiles * (a.q_jobs + a.Hkv * a.kv_parts) < 2 * device_sm_count()) a.kv_parts <<= 1;
+  while (!a.k_codes && a.kv_parts < 8 && tiles * (a.q_jobs + a.Hkv * a.kv_parts) < 2 * device_sm_count()) a.kv_parts <<= 1;
   // Order of the CTAs: one job's tiles side by side (neighbours write
   // neighbouring slots while the lines are in L2), or, where rows and pages exceed
   // L2, one tile's jobs (what runs at a time reads whole rows of DRAM).  us for
@@ -292,10 +470,7 @@ cudaError_t launch_qkv_append(AppendArgs a, cudaStream_t s) {
   // against 166.
   a.whole_rows = a.n_rows * (a.Hq + 2 * a.Hkv) * (4 * kH) > ((int64_t)100 << 20);
   const unsigned grid = (unsigned)(tiles * (a.q_jobs + a.Hkv * a.kv_parts));
-  const bool whole = a.rot == kH;
-  auto* const kernel = a.interleaved ? whole ? qkv_append_kernel<true, true> : qkv_append_kernel<true, false>
-                                     : whole ? qkv_append_kernel<false, true> : qkv_append_kernel<false, false>;
-  return launch_programmatic(kernel, dim3(grid), dim3(kThreads), 0, s, a);
+  return a.k_codes ? launch_kernel<true>(a, grid, s) : launch_kernel<false>(a, grid, s);
 }
 
 }  // namespace lynx

@@ -95,6 +95,8 @@ SIGNATURES = {
     "lynx_decode_attn_e4m3_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
     "lynx_chunk_attn_e4m3": (_I32, [_VP, _I64, _I64, _VP, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _I64, _VP, _I32, _VP,
                                     _F32, _I32, _VP, _I32, _VP, _VP, _SZ, _VP]),
+    "lynx_qkv_append_e4m3": (_I32, [_VP, _I64, _I64, _I32, _I32, _I32, _VP, _VP, _F32, _VP, _I32, _I32, _I32, _VP, _VP,
+                                    _VP, _VP, _VP, _VP, _I64, _VP]),
     "lynx_decode_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "lynx_device_status": (_I32, []),
     "lynx_test_inject_wait_timeout": (_I32, [_I32]),
@@ -615,6 +617,16 @@ def lynx_chunk_attn_e4m3(q, cu_q, k_pages, v_pages, scales, page_table, ctx_len,
         raise LynxError("out_dtype must be torch.bfloat16 or torch.float32")
     return (_binding or _native()).chunk_attn_e4m3(q, cu_q, k_pages, v_pages, scales, page_table, ctx_len, n_kv_heads,
                                                    sm_scale, causal, out, lse, out_dtype is torch.float32, workspace,
+                                                   stream and stream.cuda_stream)
+
+
+def lynx_qkv_append_e4m3(qkv, n_q_heads: int, n_kv_heads: int, cos_sin, positions, slots, k_pages, v_pages, scales,
+                         q_weight=None, k_weight=None, norm_eps: float = 1e-6, interleaved=False, q_out=None, stream=None):
+    """lynx_qkv_append into pages in 8 bits (k_pages, v_pages, scales as
+    lynx_decode_attn_e4m3).  The rows of one block of 32 tokens must follow one another;
+    a block's scale grows with its new tokens, and what it held is rounded again."""
+    return (_binding or _native()).qkv_append_e4m3(qkv, n_q_heads, n_kv_heads, cos_sin, positions, slots, k_pages, v_pages,
+                                                   scales, q_weight, k_weight, norm_eps, interleaved, q_out,
                                                    stream and stream.cuda_stream)
 
 
