@@ -34,6 +34,8 @@
  *                         BF16 pages: pages and slots of new tokens, their norm,
  *                         rotation and write, attention of ragged chunks
  *                         (prefill), verification of drafted tokens (§4.3).
+ *   lynx_token_logprobs   log probabilities of a step's tokens, entropies and
+ *                         the most likely alternatives.
  *   lynx_qkv_append_e4m3, lynx_decode_attn_e4m3, lynx_chunk_attn_e4m3
  *                         serving over pages in 8 bits: E4M3 codes with a scale
  *                         for each block of 32 tokens of a head.
@@ -535,6 +537,26 @@ size_t lynx_chunk_attn_workspace_size(int64_t n_rows, int B, int Hq, int Hkv, in
 int lynx_verify_drafts(const void* p, int64_t p_stride_b, int64_t p_stride_t, const void* q, int64_t q_stride_b,
                        int64_t q_stride_t, int prob_dtype, int B, int T, int V, const int32_t* draft,
                        const int32_t* n_draft, const float* u, int32_t* tokens, int32_t* n_accept, void* stream);
+
+/* Log probabilities of given tokens under the model's logits, the entropies of the
+ * distributions, and their most likely tokens.
+ *   logits      row r of V values at r * row_stride elements; logit_dtype
+ *               LYNX_OUT_F32 or LYNX_OUT_BF16
+ *   tokens      [n_rows] int32
+ *   logprob     [n_rows] float32: x_token - ln sum_k e^(x_k); -inf for an id outside
+ *               0..V-1 (such as the -1 behind lynx_verify_drafts' last token)
+ *   entropy     [n_rows] float32: -sum_k p_k ln p_k (in nats)
+ *   top_ids, top_logprobs   [n_rows][n_top] int32, float32: the n_top most likely
+ *               tokens, the most likely one first and the lower id first where logits are
+ *               equal, and their log probabilities (n_top = 0: NULL allowed)
+ * Sums in float32.  A logit of -inf has no weight (log probability -inf; a row of nothing
+ * else: entropy 0); with NaN or +inf in a row its log probabilities (but those of -inf)
+ * and entropy are NaN and its ids any.
+ * Limits: 0 <= n_top <= min(V, 32), V <= 2^24, n_rows <= 2^24.  n_rows == 0 is a no-op.
+ * The arrays need only the alignment of their elements. */
+int lynx_token_logprobs(const void* logits, int64_t row_stride, int logit_dtype, int64_t n_rows, int V,
+                        const int32_t* tokens, int n_top, float* logprob, float* entropy, int32_t* top_ids,
+                        float* top_logprobs, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Pages in 8 bits.  A serving loop that keeps its own keys and values in half the

@@ -143,3 +143,26 @@ def chunk_attention(q, cu_q, k_pages, v_pages, page_table, ctx_len, n_kv_heads, 
                 with np.errstate(divide="ignore"):
                     lse[lo:hi, h * G + g] = m0 + np.log(l)
     return out, lse
+
+
+def token_logprobs(logits, tokens, n_top):
+    """logits [N, V] float64 -> (log probability of each token, entropy, ids and log
+    probabilities of the n_top largest, the lower id first where they are equal)."""
+    N, V = logits.shape
+    logprob, entropy = np.full(N, -np.inf), np.zeros(N)
+    ids, top = np.zeros((N, n_top), dtype=np.int64), np.zeros((N, n_top))
+    for r in range(N):
+        x = logits[r]
+        ids[r] = np.argsort(-x, kind="stable")[:n_top]
+        m = x.max()
+        if m == -np.inf:
+            top[r] = -np.inf
+            continue
+        d = x - m
+        e = np.exp(d)
+        log_s = math.log(e.sum())
+        top[r] = d[ids[r]] - log_s
+        if 0 <= tokens[r] < V:
+            logprob[r] = d[tokens[r]] - log_s
+        entropy[r] = log_s - np.sum(e[e > 0] * d[e > 0]) / e.sum()
+    return logprob, entropy, ids, top

@@ -33,6 +33,7 @@ from .lynx import (  # noqa: F401
     lynx_decode_attn_e4m3_workspace_size,
     lynx_chunk_attn_e4m3,
     lynx_qkv_append_e4m3,
+    lynx_token_logprobs,
     lynx_reconstruct,
     load,
 )

@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/DimVector.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -46,7 +47,12 @@ struct Raised {};
   throw Raised{};
 }
 
-using Shape = std::initializer_list<int64_t>;
+// sizes as a braced list or a vector
+struct Shape {
+  at::IntArrayRef sizes;
+  Shape(const std::initializer_list<int64_t>& s) : sizes(s.begin(), s.size()) {}
+  Shape(const at::DimVector& s) : sizes(s.data(), s.size()) {}
+};
 
 class Call {
  public:
@@ -70,10 +76,10 @@ class Call {
     const at::Tensor& t = THPVariable_Unpack(o);
     if (t.scalar_type() != type || !t.is_contiguous())
       raise("%s must be a contiguous %s tensor", name, type_name(type));
-    if (!t.sizes().equals(at::IntArrayRef(shape))) {
+    if (!t.sizes().equals(shape.sizes)) {
       char want[128];
       int at = 0;
-      for (int64_t s : shape) at += snprintf(want + at, sizeof(want) - at, at ? ", %lld" : "%lld", (long long)s);
+      for (int64_t s : shape.sizes) at += snprintf(want + at, sizeof(want) - at, at ? ", %lld" : "%lld", (long long)s);
       raise("%s must have the shape (%s)", name, want);
     }
     if (t.device() != device_) raise("%s must live on the device of the other tensors", name);
@@ -91,7 +97,7 @@ class Call {
       Py_INCREF(o);
       return o;
     }
-    at::Tensor t = at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(device_));
+    at::Tensor t = at::empty(shape.sizes, at::TensorOptions().dtype(type).device(device_));
     *ptr = t.data_ptr();
     return THPVariable_Wrap(std::move(t));
   }
@@ -431,6 +437,41 @@ PyObject* chunk_attn_e4m3(PyObject* const* a) {
   });
 }
 
+// logits, tokens, n_top, logprob, entropy, top_ids, top_logprobs, stream
+PyObject* token_logprobs(PyObject* const* a) {
+  Call c("lynx_token_logprobs", a[0], "logits");
+  const at::Tensor& x = c.tensor(a[0], "logits");
+  const at::ScalarType type = x.scalar_type();
+  const int64_t dims = x.dim();
+  if ((type != at::kFloat && type != at::kBFloat16) || (dims != 2 && dims != 3) ||
+      (x.size(dims - 1) > 1 && x.stride(dims - 1) != 1))
+    raise("logits must be a float32 or bfloat16 tensor [n_rows, V] or [B, T, V] with contiguous rows");
+  const int64_t B = x.size(0), T = dims == 3 ? x.size(1) : 1;
+  // rows one stride apart, over both dimensions
+  const int64_t stride = dims == 3 && T > 1 ? x.stride(1) : B > 1 ? x.stride(0) : x.size(dims - 1);
+  if (dims == 3 && B > 1 && T > 1 && x.stride(0) != T * stride) raise("the rows of logits must lie one stride apart");
+  const int V = dim32(x.size(dims - 1), "V"), n_top = to_int(a[2], "n_top");
+  if (n_top < 0) raise("n_top must not be negative");
+  auto shape = [&](int64_t more) {
+    at::DimVector s(x.sizes().begin(), x.sizes().end() - 1);
+    if (more >= 0) s.push_back(more);
+    return s;
+  };
+  const at::DimVector rows = shape(-1), tops = shape(n_top);
+  void* tokens = c.at(a[1], at::kInt, rows, "tokens");
+  void* stream = c.stream(a[7]);
+  Out lp, h, ids, top;
+  lp.o = c.make(a[3], at::kFloat, rows, "logprob", &lp.p);
+  h.o = c.make(a[4], at::kFloat, rows, "entropy", &h.p);
+  ids.o = c.make(a[5], at::kInt, tops, "top_ids", &ids.p);
+  top.o = c.make(a[6], at::kFloat, tops, "top_logprobs", &top.p);
+  c.launch([&] {
+    return lynx_token_logprobs(x.data_ptr(), stride, type == at::kFloat ? LYNX_OUT_F32 : LYNX_OUT_BF16, B * T, V,
+                               (int32_t*)tokens, n_top, (float*)lp.p, (float*)h.p, (int32_t*)ids.p, (float*)top.p, stream);
+  });
+  return tuple({&lp, &h, &ids, &top});
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XDECREF(g_error);
@@ -448,6 +489,7 @@ PyMethodDef kMethods[] = {
     {"decode_attn_e4m3", FAST((entry<13, decode_attn_e4m3>))},
     {"chunk_attn_e4m3", FAST((entry<15, chunk_attn_e4m3>))},
     {"qkv_append_e4m3", FAST((entry<15, qkv_append_e4m3>))},
+    {"token_logprobs", FAST((entry<8, token_logprobs>))},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "lynx_binding", nullptr, -1, kMethods};
 

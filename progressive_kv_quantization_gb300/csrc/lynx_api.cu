@@ -1077,6 +1077,35 @@ int lynx_decode_attn_e4m3(const void* q_bf16, int B, int T, int Hq, int Hkv, int
   return LYNX_OK;
 }
 
+int lynx_token_logprobs(const void* logits, int64_t row_stride, int logit_dtype, int64_t n_rows, int V,
+                        const int32_t* tokens, int n_top, float* logprob, float* entropy, int32_t* top_ids,
+                        float* top_logprobs, void* stream) {
+  g_last_error[0] = '\0';
+  if (n_rows < 0 || V < 1) return fail(LYNX_ERR_INVALID_ARG, "n_rows=%lld < 0 or V=%d < 1", (long long)n_rows, V);
+  if (V > kLogprobsMaxVocab) return fail(LYNX_ERR_UNSUPPORTED, "V=%d > %d", V, kLogprobsMaxVocab);
+  if (n_rows > 1 << 24) return fail(LYNX_ERR_UNSUPPORTED, "n_rows=%lld too large", (long long)n_rows);
+  if (n_top < 0 || n_top > V) return fail(LYNX_ERR_INVALID_ARG, "n_top=%d outside 0..V", n_top);
+  if (n_top > kLogprobsMaxTop) return fail(LYNX_ERR_UNSUPPORTED, "n_top=%d > %d", n_top, kLogprobsMaxTop);
+  if (logit_dtype != LYNX_OUT_BF16 && logit_dtype != LYNX_OUT_F32)
+    return fail(LYNX_ERR_INVALID_ARG, "logit_dtype=%d (need 0 = BF16 or 1 = F32)", logit_dtype);
+  if (n_rows == 0) return LYNX_OK;
+  if (row_stride < V && n_rows > 1) return fail(LYNX_ERR_INVALID_ARG, "row_stride=%lld < V", (long long)row_stride);
+  if (!logits || !tokens || !logprob || !entropy || (n_top > 0 && (!top_ids || !top_logprobs)))
+    return fail(LYNX_ERR_INVALID_ARG, "NULL buffer pointer");
+  const int size = logit_dtype == LYNX_OUT_F32 ? 4 : 2;
+  if (off_type(logits, size) || off_type(tokens, 4) || off_type(logprob, 4) || off_type(entropy, 4) ||
+      off_type(top_ids, 4) || off_type(top_logprobs, 4))
+    return fail(LYNX_ERR_ALIGNMENT, "an array is not aligned to its element size");
+  const int64_t n4 = n_rows * 4;
+  if (overlap({{logprob, n4}, {entropy, n4}, {top_ids, n4 * n_top}, {top_logprobs, n4 * n_top}},
+              {{logits, ((n_rows - 1) * row_stride + V) * size}, {tokens, n4}}))
+    return fail(LYNX_ERR_INVALID_ARG, "an output overlaps logits or tokens");
+  const LogprobsArgs a{logits, row_stride, n_rows, V, tokens, n_top, logprob, entropy, top_ids, top_logprobs};
+  cudaError_t e = launch_token_logprobs(a, logit_dtype == LYNX_OUT_BF16, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "lynx_token_logprobs launch");
+  return LYNX_OK;
+}
+
 int lynx_test_inject_wait_timeout(int n_calls) {
   g_last_error[0] = '\0';
   if (n_calls < 0) return fail(LYNX_ERR_INVALID_ARG, "n_calls=%d < 0", n_calls);

@@ -261,6 +261,22 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify_drafts(const VerifyArgs& a, bool bf16, cudaStream_t s);
 
+constexpr int kLogprobsMaxTop = 32;
+constexpr int kLogprobsMaxVocab = 1 << 24;
+struct LogprobsArgs {
+  const void* logits;
+  int64_t row_stride;      // elements
+  int64_t n_rows;
+  int V;
+  const int32_t* tokens;
+  int n_top;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+};
+cudaError_t launch_token_logprobs(const LogprobsArgs& a, bool bf16, cudaStream_t s);
+
 struct ChunkArgs {
   const uint16_t* q;
   int64_t q_stride;      // elements between rows

@@ -1,0 +1,409 @@
+// Log probabilities of given tokens under their logits, the entropies of the
+// distributions, and their most likely tokens (lynx_token_logprobs), in one pass
+// over the logits.
+//
+//   d_k = x_k - max x,  s = sum_k e^(d_k),  t = sum_k e^(d_k) d_k
+//   log p_k = d_k - ln s,  entropy = ln s - t / s
+// (in powers of two: d log2(e), and ln 2 times the result)
+//
+// A thread-block cluster takes a row, each CTA a contiguous part of it, a thread
+// every 256th piece of 16 bytes.  s and t are kept against a reference that follows
+// the thread's maximum at a distance of at most 6 (so that both are scaled again on few pieces),
+// and are brought to the row's maximum at the end.
+//
+// The n most likely tokens (equal ones: the lowest first) as 64-bit keys: the float's bits in
+// an order of whole numbers, and under them the token's from behind.  While the logits go by,
+// a thread only notes its largest value and the piece that it is in.  The n-th largest of the
+// notes of 64 groups of 4 threads is a bound that at least n tokens of the CTA's part reach;
+// only threads whose own note reaches it (some n of 256) are gone through again, by
+// their whole warp, and the tokens that reach the bound, a few more than n, are ranked by counting.
+//
+// Bound by the reads of the logits for many rows, by the chain (launch, one round trip
+// of loads, the reductions, the second look) for few.
+
+#include "f32x2.cuh"
+#include "lynx_internal.cuh"
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+namespace cg = cooperative_groups;
+
+namespace lynx {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;               // pieces of a thread read at once
+constexpr int kGroups = kThreads / 4;
+constexpr int kMaxTop = kLogprobsMaxTop;
+constexpr int kFound = 2048;            // tokens that reach the bound, at most
+constexpr int kMaxCluster = 8;
+constexpr float kLag = 6.0f;            // of the reference behind the maximum
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLeast = -1024.0f;      // 2^kLeast is 0, and so is the product of the two
+static_assert(kGroups >= kMaxTop && kFound >= kGroups * 4 * 8, "bounds on what reaches the bound");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// the larger one, NaN if one is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// floats in the order of whole numbers, -0 as 0; never 0
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+using Key = unsigned long long;   // 0: none
+__device__ __forceinline__ Key key_of(float x, int token) {
+  return (Key)ordered(x) << 32 | (0xFFFFFFFFu - (uint32_t)token);
+}
+
+template <typename T>
+struct Piece {   // 16 bytes of a row
+  static constexpr int kN = 16 / sizeof(T);
+  uint4 raw;
+  __device__ __forceinline__ float at(int e) const {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if (sizeof(T) == 4) return __uint_as_float(w[e]);
+    return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+  }
+  __device__ __forceinline__ float largest() const {
+    float m = fmaxf(at(0), at(1));
+#pragma unroll
+    for (int e = 2; e < kN; e += 2) m = max3(m, at(e), at(e + 1));
+    return m;
+  }
+};
+
+// sums against the reference `ref` (natural units)
+struct Sums {
+  float ref = -3.402823466e38f;
+  uint64_t s = 0, t = 0;   // pairs
+
+  // to a reference `to` >= ref, of one value each
+  static __device__ __forceinline__ void move(float from, float to, float& s, float& t) {
+    const float d = fmaxf((from - to) * kLog2e, kLeast), f = ex2(d);
+    t = f * fmaf(d, s, t);
+    s *= f;
+  }
+  __device__ __forceinline__ void follow(float largest) {
+    if (largest > ref + kLag) {
+      float s0, s1, t0, t1;
+      unpair(s, s0, s1);
+      unpair(t, t0, t1);
+      move(ref, largest, s0, t0);
+      move(ref, largest, s1, t1);
+      s = pair(s0, s1);
+      t = pair(t0, t1);
+      ref = largest;
+    }
+  }
+  __device__ __forceinline__ void add(float x0, float x1) {
+    float d0, d1;
+    unpair(mul2(add2(pair(x0, x1), pair(-ref, -ref)), pair(kLog2e, kLog2e)), d0, d1);
+    d0 = max_nan(d0, kLeast);   // of a logit of -inf; NaN stays
+    d1 = max_nan(d1, kLeast);
+    const uint64_t e = pair(ex2(d0), ex2(d1));
+    s = add2(s, e);
+    t = fma2(e, pair(d0, d1), t);
+  }
+};
+
+// what a CTA has found, read by the cluster's first
+struct Found {
+  float top, s, t;   // largest logit, sums against it
+  Key best[kMaxTop];
+};
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads, 4)
+token_logprobs_kernel(const LogprobsArgs a) {
+  using P = Piece<T>;
+  __shared__ Found s_found;
+  __shared__ float s_part[kWarps][2];
+  __shared__ Key s_group[TOP ? kGroups : 1];
+  __shared__ Key s_keys[TOP ? kFound : 1];
+  __shared__ Key s_bound;
+  __shared__ int s_count;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int64_t row = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
+  // the row as whole pieces, and up to 2 (kN - 1) tokens in front of and behind them, which are rank 0's
+  const int front = min((int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T), a.V);
+  const int pieces = (a.V - front) / P::kN, behind = front + pieces * P::kN;
+  const int k0 = (int)((int64_t)pieces * rank / C), k1 = (int)((int64_t)pieces * (rank + 1) / C);
+  const uint4* body = reinterpret_cast<const uint4*>(x + front);
+  const int loose = front + a.V - behind;
+  const int loose_at = rank == 0 && tid < loose ? (tid < front ? tid : behind + tid - front) : -1;
+  auto value = [&](int i) { return static_cast<float>(x[i]); };
+
+  wait_prerequisite_grids();
+  float token_x = 0.0f;
+  int token = -1;
+  if (rank == 0 && tid == 0) {
+    token = a.tokens[row];
+    if (token >= 0 && token < a.V) token_x = value(token);
+  }
+
+  Sums sums;
+  float top = -CUDART_INF_F;
+  int top_k = -1;   // the piece that it is in
+  auto take = [&](const P& p, int k, float m) {
+    if (TOP ? m > top || top_k < 0 : m > top) {
+      top = m;
+      top_k = k;
+    }
+#pragma unroll
+    for (int e = 0; e < P::kN; e += 2) sums.add(p.at(e), p.at(e + 1));
+  };
+  float loose_x = -CUDART_INF_F;
+  if (loose_at >= 0) {
+    loose_x = value(loose_at);
+    sums.follow(loose_x);
+    sums.add(loose_x, -CUDART_INF_F);
+  }
+  {
+    constexpr int kStep = kBatch * kThreads;
+    int k = k0 + tid;
+    P next[kBatch];
+    // whole batches, the next one on its way
+    const int whole = (k1 - k0) / kStep;
+    if (whole > 0) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) next[u].raw = __ldg(body + k + u * kThreads);
+    }
+    for (int b = 0; b < whole; ++b, k += kStep) {
+      P cur[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) cur[u] = next[u];
+      if (b + 1 < whole) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) next[u].raw = __ldg(body + k + kStep + u * kThreads);
+      }
+      float m[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) m[u] = cur[u].largest();
+      sums.follow(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) take(cur[u], k + u * kThreads, m[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (k + u * kThreads < k1) next[u].raw = __ldg(body + k + u * kThreads);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (k + u * kThreads < k1) {
+        const float m = next[u].largest();
+        sums.follow(m);
+        take(next[u], k + u * kThreads, m);
+      }
+  }
+
+  // ---- the CTA's maximum and sums
+  float cta_top = fmaxf(top, loose_x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) cta_top = fmaxf(cta_top, __shfl_xor_sync(0xffffffffu, cta_top, o));
+  if (lane == 0) s_part[warp][0] = cta_top;
+  if (TOP) {
+    // a thread's note: its largest value, and the last token of its piece
+    Key note = top_k < 0 ? 0 : key_of(top, front + top_k * P::kN + P::kN - 1);
+    note = max(note, __shfl_xor_sync(0xffffffffu, note, 1));
+    note = max(note, __shfl_xor_sync(0xffffffffu, note, 2));
+    if ((lane & 3) == 0) s_group[tid >> 2] = note;
+    if (tid == 0) s_count = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) cta_top = fmaxf(cta_top, s_part[w][0]);
+  float s, t;
+  {
+    float s1, t1;
+    unpair(sums.s, s, s1);
+    unpair(sums.t, t, t1);
+    s += s1;
+    t += t1;
+    // cta_top is below the reference only where nothing was added
+    Sums::move(sums.ref, fmaxf(cta_top, sums.ref), s, t);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  __shared__ float s_sums[kWarps][2];
+  if (lane == 0) {
+    s_sums[warp][0] = s;
+    s_sums[warp][1] = t;
+  }
+  if (TOP && warp == 0) {
+    // the n-th largest note; they differ from one another, but for those that are 0
+    const Key n0 = s_group[lane], n1 = s_group[lane + 32];
+    int r0 = 0, r1 = 0;
+#pragma unroll 8
+    for (int i = 0; i < kGroups; ++i) {
+      const Key o = s_group[i];
+      r0 += o > n0 || (o == n0 && i < lane);
+      r1 += o > n1 || (o == n1 && i < lane + 32);
+    }
+    if (r0 == a.n_top - 1) s_bound = n0;
+    if (r1 == a.n_top - 1) s_bound = n1;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    s = t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      s += s_sums[w][0];
+      t += s_sums[w][1];
+    }
+    s_found.top = cta_top;
+    s_found.s = s;
+    s_found.t = t;
+  }
+
+  if (TOP) {
+    // ---- the tokens that reach the bound
+    int n;
+    while (true) {
+      const Key bound = s_bound;
+      auto look = [&](float v, int i) {
+        const Key key = key_of(v, i);
+        if (key >= bound) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kFound) s_keys[at] = key;
+        }
+      };
+      if (loose_at >= 0) look(loose_x, loose_at);
+      // a thread's best possible key: its value and the first token of the piece
+      unsigned who = __ballot_sync(0xffffffffu, top_k >= 0 && key_of(top, front + top_k * P::kN) >= bound);
+      while (who) {
+        const int l = __ffs(who) - 1;
+        who &= who - 1;
+        for (int k = k0 + 32 * warp + l + lane * kThreads; k < k1; k += 32 * kThreads) {
+          P p;
+          p.raw = __ldg(body + k);
+#pragma unroll
+          for (int e = 0; e < P::kN; ++e) look(p.at(e), front + k * P::kN + e);
+        }
+      }
+      __syncthreads();
+      n = s_count;
+      if (n <= kFound) break;
+      // Too many (values that rise within one thread's pieces): the n_top-th largest of those
+      // that found room is a higher bound.
+      Key higher = 0;
+      for (int i = tid; i < kFound; i += kThreads) {
+        int r = 0;
+        for (int j = 0; j < kFound; ++j) r += s_keys[j] > s_keys[i];
+        if (r == a.n_top - 1) higher = s_keys[i];
+      }
+      __syncthreads();
+      if (tid == 0) s_count = 0;
+      if (higher) s_bound = higher;
+      __syncthreads();
+    }
+    // ranks; a CTA's part may hold fewer than n_top tokens
+    if (tid < kMaxTop) s_found.best[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+      const Key own = s_keys[i];
+      int r = 0;
+      for (int j = 0; j < n; ++j) r += s_keys[j] > own;
+      if (r < a.n_top) s_found.best[r] = own;
+    }
+  }
+
+  // ---- the row
+  if (C > 1) cluster.sync(); else __syncthreads();
+  if (rank == 0) {
+    float row_top = -CUDART_INF_F;
+    for (int c = 0; c < C; ++c) row_top = fmaxf(row_top, cluster.map_shared_rank(&s_found, c)->top);
+    s = t = 0.0f;
+    for (int c = 0; c < C; ++c) {
+      const Found* f = cluster.map_shared_rank(&s_found, c);
+      float cs = f->s, ct = f->t;
+      const float from = f->top;
+      if (from != row_top) Sums::move(from, row_top, cs, ct);
+      s += cs;
+      t += ct;
+    }
+    const float log_s = log2f(s);
+    auto logprob = [&](float v) { return v == -CUDART_INF_F ? v : fmaf(-kLn2, log_s, v - row_top); };
+    if (tid == 0) {
+      const bool real = token >= 0 && token < a.V;
+      a.logprob[row] = real ? logprob(token_x) : -CUDART_INF_F;
+      const float h = s == 0.0f ? 0.0f : kLn2 * (log_s - t / s);   // nothing but -inf: 0
+      a.entropy[row] = h < 0.0f ? 0.0f : h;                         // roundings, where one token has it all
+    }
+    if (TOP) {
+      if (C > 1) {
+        // the CTAs' best, ranked again
+        for (int i = tid; i < C * a.n_top; i += kThreads)
+          s_keys[i] = cluster.map_shared_rank(&s_found, i / a.n_top)->best[i % a.n_top];
+        __syncthreads();
+      }
+      const int n = C > 1 ? C * a.n_top : a.n_top;
+      const Key* keys = C > 1 ? s_keys : s_found.best;
+      for (int i = tid; i < n; i += kThreads) {
+        const Key own = keys[i];
+        if (own == 0) continue;
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += keys[j] > own;
+        if (r < a.n_top) {
+          a.top_ids[row * a.n_top + r] = (int32_t)(0xFFFFFFFFu - (uint32_t)own);
+          a.top_logprobs[row * a.n_top + r] = logprob(unordered((uint32_t)(own >> 32)));
+        }
+      }
+    }
+  }
+  allow_dependent_launch();
+  if (C > 1) cluster.sync();   // the first CTA has read the others' memory
+}
+
+template <typename T, bool TOP>
+cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t s) {
+  // CTAs a row: as many as run at once, at most a portable cluster, with at least 1,024 pieces each
+  int C = kMaxCluster;
+  while (C > 1 && (a.n_rows * C > 4 * device_sm_count() || (int64_t)a.V * (int)sizeof(T) < (int64_t)C * 16384)) C >>= 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.n_rows * C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOP>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const LogprobsArgs& a, bool bf16, cudaStream_t s) {
+  if (bf16) return a.n_top > 0 ? launch_t<__nv_bfloat16, true>(a, s) : launch_t<__nv_bfloat16, false>(a, s);
+  return a.n_top > 0 ? launch_t<float, true>(a, s) : launch_t<float, false>(a, s);
+}
+
+}  // namespace lynx

@@ -97,6 +97,7 @@ SIGNATURES = {
                                     _F32, _I32, _VP, _I32, _VP, _VP, _SZ, _VP]),
     "lynx_qkv_append_e4m3": (_I32, [_VP, _I64, _I64, _I32, _I32, _I32, _VP, _VP, _F32, _VP, _I32, _I32, _I32, _VP, _VP,
                                     _VP, _VP, _VP, _VP, _I64, _VP]),
+    "lynx_token_logprobs": (_I32, [_VP, _I64, _I32, _I64, _I32, _VP, _I32, _VP, _VP, _VP, _VP, _VP]),
     "lynx_decode_attn_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "lynx_device_status": (_I32, []),
     "lynx_test_inject_wait_timeout": (_I32, [_I32]),
@@ -628,6 +629,17 @@ def lynx_qkv_append_e4m3(qkv, n_q_heads: int, n_kv_heads: int, cos_sin, position
     return (_binding or _native()).qkv_append_e4m3(qkv, n_q_heads, n_kv_heads, cos_sin, positions, slots, k_pages, v_pages,
                                                    scales, q_weight, k_weight, norm_eps, interleaved, q_out,
                                                    stream and stream.cuda_stream)
+
+
+def lynx_token_logprobs(logits, tokens, n_top: int = 0, logprob=None, entropy=None, top_ids=None, top_logprobs=None,
+                        stream=None):
+    """Log probabilities of tokens int32 [n_rows] (or [B, T]) under logits [n_rows, V]
+    (or [B, T, V]), float32 or bfloat16, rows one stride apart.  Returns (logprob f32 [n_rows], -inf
+    for ids outside 0..V-1; entropy f32 [n_rows]; top_ids i32 [n_rows, n_top] and
+    top_logprobs f32 [n_rows, n_top], the most likely tokens, the lower id first where
+    they are equal)."""
+    return (_binding or _native()).token_logprobs(logits, tokens, n_top, logprob, entropy, top_ids, top_logprobs,
+                                                  stream and stream.cuda_stream)
 
 
 def lynx_device_status():
