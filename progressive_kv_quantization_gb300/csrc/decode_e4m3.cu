@@ -50,10 +50,6 @@
 namespace lynx {
 namespace {
 
-constexpr int kWarps = 4;                     // consumers; the producer is one more
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kUnit = 128;                    // keys
-constexpr int kTile = kUnit * kH;             // bytes of a K or V tile
 constexpr int kSlots = 5;
 constexpr int kItemCost = 1;                  // units
 constexpr int kMinCost = 2;                   // units of a CTA's part, at least
@@ -62,16 +58,33 @@ constexpr int kQPitch = 2 * kH + 16;          // bytes of a query row
 constexpr int kOPitch = kH + 4;               // floats of a row at the join of the warps
 constexpr float kLazyLog2 = 5.0f;             // lead of a score over the running maximum that moves it
 constexpr float kUpLog2 = 10.0f;              // p is held times 2^10
+constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kOffRing = 0;
-constexpr int kOffScale = kOffRing + kSlots * kTile;
-constexpr int kOffQ = kOffScale + kSlots * kScaleBytes;
-constexpr int kOffO = kOffQ + 2 * 16 * kQPitch;             // [warp][8 rows][kOPitch]
-constexpr int kOffM = kOffO + kWarps * 8 * kOPitch * 4;     // m [warp][16], l [warp][16]
-constexpr int kOffBar = kOffM + 2 * kWarps * 16 * 4;
-constexpr int kSmem = kOffBar + 8 * (2 * kSlots + 4) + 16;
-constexpr int kSmemAlloc = kSmem + 1024;
-static_assert(2 * (kSmemAlloc + 1024) <= 233472, "two CTAs an SM");
+// NT: tiles of 8 query rows, W: consuming warps
+template <int NT, int W>
+struct Layout {
+  // The producer is one warp.  Tiles of more rows than 8 do not fit the 168 registers that are left to
+  // a thread then: three idle warps complete its warpgroup, which gives registers up; of 128 or 168
+  // each at launch, 128 x 216 + 128 x 40 = 256 x 128, 256 x 232 + 128 x 40 = 384 x 168.
+  static constexpr bool kSplit = NT > 1;
+  static constexpr int kThreads = 32 * (W + (kSplit ? 4 : 1));
+  static constexpr int kRegs = W == 4 ? 216 : 232, kRegsProducer = 40;
+  static constexpr int kCtas = 8 / W;                       // an SM
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kUnit = 32 * W;                      // keys
+  static constexpr int kTile = kUnit * kH;                  // bytes of a K or V tile
+  static constexpr int kOffRing = 0;
+  static constexpr int kOffScale = kOffRing + kSlots * kTile;
+  static constexpr int kOffRaw = kOffScale + kSlots * kScaleBytes;     // two items' query rows as they are
+  static constexpr int kOffQ = kOffRaw + 2 * kRows * kQPitch;          // as operands [NT][k-step pair][lane] 16 bytes
+  static constexpr int kOffRow = kOffQ + NT * 4 * 32 * 16;             // a row's factor and visible keys
+  static constexpr int kOffO = kOffRow + 2 * kRows * 4;                // [warp][8 rows][kOPitch]
+  static constexpr int kOffM = kOffO + W * 8 * kOPitch * 4;            // m [warp][row], l [warp][row]
+  static constexpr int kOffBar = kOffM + 2 * W * kRows * 4;
+  static constexpr int kSmem = kOffBar + 8 * (2 * kSlots + 4) + 16;
+  static constexpr int kSmemAlloc = kSmem + 1024;
+  static_assert(kCtas * (kSmemAlloc + 1024) <= 233472, "shared memory");
+};
 
 // what a CTA tells the join: its part of an item that an earlier CTA began (a_*), and
 // the item that it began and did not end (b_*)
@@ -117,10 +130,16 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_
 __device__ __forceinline__ uint32_t scaled_half2(uint32_t w, float f) {
   return half2_bits(__floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f));
 }
-__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+// an 8 x 8 matrix of 16-bit values, a row's pair a lane, transposed
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
 
 // This CTA's part of the line, item by item; every warp goes through it by itself
 // and all of them see the same.
+template <int Unit>
 struct Walk {
   const DecodeE4m3Args& a;
   long long x, x1;
@@ -129,7 +148,7 @@ struct Walk {
   __device__ void load(int i) {
     const int c = i < a.B ? a.ctx_len[i] : 0;
     ctx = min(max(c, 0), a.max_pages * kP);
-    units = (ctx + kUnit - 1) / kUnit;
+    units = (ctx + Unit - 1) / Unit;
   }
   __device__ explicit Walk(const DecodeE4m3Args& args) : a(args) {
     const int lane = threadIdx.x & 31;
@@ -204,11 +223,12 @@ struct Walk {
   }
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int NT, int W>
+__global__ void __launch_bounds__(Layout<NT, W>::kThreads, Layout<NT, W>::kCtas)
 decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
-  constexpr int R = 8 * NT;
+  using S = Layout<NT, W>;
+  constexpr int R = S::kRows, kUnit = S::kUnit, kTile = S::kTile, kPerPage = kP / kUnit;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -217,40 +237,44 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
   const int g = lane >> 2, t = lane & 3;
   const int c = blockIdx.x;
 
-  const uint32_t bars = base + kOffBar;
+  const uint32_t bars = base + S::kOffBar;
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (kSlots + s); };
   auto q_full = [&](int s) { return bars + 8 * (2 * kSlots + s); };
   auto q_empty = [&](int s) { return bars + 8 * (2 * kSlots + 2 + s); };
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffBar + 8 * (2 * kSlots + 4));
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + S::kOffBar + 8 * (2 * kSlots + 4));
+  auto sync_consumers = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
 
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), kWarps);
+      mbar_init(empty(s), W);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), kWarps);
+      mbar_init(q_empty(s), W);
     }
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid == 32 * kWarps) {
+  if (tid == 32 * W) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
   }
   __syncthreads();
   // every access to global memory follows this wait
   wait_prerequisite_grids();
+  allow_dependent_launch();   // the join's CTAs come as these leave
 
-  Walk walk(a);
   Part p;
   uint32_t n_tiles = 0, n_q = 0;   // tiles through the ring, and query tiles
   bool failed = false;
 
-  if (warp == kWarps) {
+  if (warp >= W) {
+    if (S::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsProducer));
+    if (warp > W) return;
     // ================= producer
+    Walk<kUnit> walk(a);
     uint32_t issued_q = 0;
     while (!failed && walk.next(p)) {
       if (p.starts && lane == 0) {
@@ -266,7 +290,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
       __syncwarp();
       if (lane < p.rows) {
         const int row = p.row0 + lane, token = row / a.G;
-        bulk_g2s(base + kOffQ + qs * 16 * kQPitch + lane * kQPitch,
+        bulk_g2s(base + S::kOffRaw + qs * R * kQPitch + lane * kQPitch,
                  a.q + (((int64_t)p.b * a.T + token) * a.Hq + p.h * a.G + row - token * a.G) * kH, 2 * kH, q_full(qs));
       }
       __syncwarp();
@@ -274,12 +298,12 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
       ++issued_q;
       if (lane == 0) {
         const int32_t* ids = a.page_table + ((int64_t)p.b * a.Hkv + p.h) * a.max_pages;
-        int next_id = ids[p.k0 >> 1];
+        int next_id = ids[p.k0 / kPerPage];
         int64_t id = 0;
         for (int k = p.k0; k < p.k1 && !failed; ++k) {
-          if (k == p.k0 || !(k & 1)) {
+          if (k == p.k0 || k % kPerPage == 0) {
             id = next_id;
-            if (((k >> 1) + 1) * 2 < p.k1) next_id = ids[(k >> 1) + 1];
+            if ((k / kPerPage + 1) * kPerPage < p.k1) next_id = ids[k / kPerPage + 1];
             if (id < 0 || id >= a.n_pool) {
               atomicExch(a.status, 2);
               id = 0;
@@ -295,33 +319,39 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
             ++n_tiles;
             if (a.inject && n_tiles == 2) continue;   // test hook: the first V tile never arrives
             mbar_expect_tx(full(s), kTile + kScaleBytes);
-            tma_tile_g2s(base + kOffRing + s * kTile, kv ? &tm_v : &tm_k, 0, (int)(id * kP) + (k & 1) * kUnit, full(s));
-            bulk_g2s(base + kOffScale + s * kScaleBytes, a.scales + id * kScaleBytes, kScaleBytes, full(s));
+#pragma unroll
+            for (int x = 0; x < kUnit; x += 128)      // boxes of 128 tokens
+              tma_tile_g2s(base + S::kOffRing + s * kTile + x * kH, kv ? &tm_v : &tm_k, 0,
+                           (int)(id * kP) + k % kPerPage * kUnit + x, full(s));
+            bulk_g2s(base + S::kOffScale + s * kScaleBytes, a.scales + id * kScaleBytes, kScaleBytes, full(s));
           }
         }
       }
       failed = __any_sync(0xffffffffu, failed);
     }
-    if (lane == 0) {
-      if (failed) {
-        atomicExch(a.status, 1);
-        *s_abort = 1;
-        // the copies in flight end before the memory they go to is given up
-        for (uint32_t u = n_tiles > kSlots ? n_tiles - kSlots : 0; u < n_tiles; ++u)
-          if (!(a.inject && u == 1)) mbar_wait(full(u % kSlots), (u / kSlots) & 1, a.wait_ns);
-        for (uint32_t u = issued_q > 2 ? issued_q - 2 : 0; u < issued_q; ++u) mbar_wait(q_full(u & 1), (u >> 1) & 1, a.wait_ns);
-      }
+    if (lane == 0 && failed) {
+      atomicExch(a.status, 1);
+      *s_abort = 1;
+      // the copies in flight end before the memory they go to is given up
+      for (uint32_t u = n_tiles > kSlots ? n_tiles - kSlots : 0; u < n_tiles; ++u)
+        if (!(a.inject && u == 1)) mbar_wait(full(u % kSlots), (u / kSlots) & 1, a.wait_ns);
+      for (uint32_t u = issued_q > 2 ? issued_q - 2 : 0; u < issued_q; ++u) mbar_wait(q_full(u & 1), (u >> 1) & 1, a.wait_ns);
     }
     __syncwarp();
   } else {
     // ================= consumers: warp w has tokens 32 w .. 32 w + 31 of each unit
+    if (S::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
+    Walk<kUnit> walk(a);
     Header hdr{0, 0, 0, 0, 0, 0, 0, 0};
-    float* s_o = reinterpret_cast<float*>(smem + kOffO);
-    float* s_m = reinterpret_cast<float*>(smem + kOffM);
-    float* s_l = s_m + kWarps * 16;
-    const uint8_t* s_scale = smem + kOffScale;
-    const int n_of = (g >> 1) | ((g & 1) << 2);   // the token of column g, and the lane's 16 channels
-    // byte offsets in a tile: K row of column g and piece t; V rows t and t + 4, piece n_of, whose
+    float* s_o = reinterpret_cast<float*>(smem + S::kOffO);
+    float* s_m = reinterpret_cast<float*>(smem + S::kOffM);
+    float* s_l = s_m + W * R;
+    uint4* s_q = reinterpret_cast<uint4*>(smem + S::kOffQ);
+    float* s_factor = reinterpret_cast<float*>(smem + S::kOffRow);
+    int* s_seen = reinterpret_cast<int*>(s_factor + R);
+    const uint8_t* s_scale = smem + S::kOffScale;
+    const int n_of = (g >> 1) | ((g & 1) << 2);   // the token of row g of a K fragment, and the lane's 16 channels of V
+    // byte offsets in a tile: K row n_of and pieces t, 4 + t; V rows t and t + 4, piece n_of, whose
     // second half comes first in every other pair of lane groups
     const uint32_t v_half = 4 * (g & 2);
     const uint32_t k_at = (uint32_t)(32 * warp + n_of) * kH, k_piece0 = (uint32_t)(t ^ n_of) << 4,
@@ -345,16 +375,18 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
         }
       }
       if (p.kind == kNothing) continue;
-      float m_run[NT], l_run[NT], sc[NT];
-      int nv[NT];
+      // the lane's query rows are 8 nr + 2 t + e
+      float m_run[NT][2], l_run[NT][2], sc[NT][2];
       float O[8][NT][4];
-      uint32_t qa[8][2 * NT];   // k-step 4 j + w: rows g (and g + 8) of channels 64 j + 16 t + 4 w + 0, 1 then + 2, 3
+      uint4 own_q[4];   // NT = 1: the operands that s_q holds otherwise
+      const int own_seen = !a.causal ? p.ctx : p.ctx - a.T + 1;
 #pragma unroll
       for (int nr = 0; nr < NT; ++nr) {
-        m_run[nr] = -CUDART_INF_F;
-        l_run[nr] = 0.0f;
-        const int row = p.row0 + 8 * nr + g;
-        nv[nr] = 8 * nr + g >= p.rows ? 0 : a.causal ? p.ctx - a.T + row / a.G + 1 : p.ctx;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m_run[nr][e] = -CUDART_INF_F;
+          l_run[nr][e] = sc[nr][e] = 0.0f;
+        }
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -362,15 +394,16 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
       }
       if (p.k0 < p.k1) {
         if (!failed) failed = __any_sync(0xffffffffu, !mbar_wait(q_full(n_q & 1), (n_q >> 1) & 1, a.wait_ns));
-        const uint32_t q_rows = base + kOffQ + (n_q & 1) * 16 * kQPitch;
-#pragma unroll
-        for (int nr = 0; nr < NT; ++nr) {
-          // rows past the item's last are zeros
-          const bool real = 8 * nr + g < p.rows && !failed;
+        const uint32_t q_rows = base + S::kOffRaw + (n_q & 1) * R * kQPitch;
+        // the operands of a tile of 8 rows, a warp a tile (a single one: every warp its own): row g, of k-step 4 j + w the channels
+        // 64 j + 16 t + 4 w + 0, 1 then + 2, 3
+        for (int nr = NT == 1 ? 0 : warp; nr < NT; nr += W) {
+          const int r = 8 * nr + g;
+          const bool real = r < p.rows && !failed;   // rows past the item's last are zeros
           uint4 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            x[i] = real ? lds16(q_rows + (8 * nr + g) * kQPitch + 128 * (i >> 1) + 32 * t + 16 * (i & 1)) : make_uint4(0u, 0u, 0u, 0u);
+            x[i] = real ? lds16(q_rows + r * kQPitch + 128 * (i >> 1) + 32 * t + 16 * (i & 1)) : make_uint4(0u, 0u, 0u, 0u);
           uint32_t top = 0;   // largest magnitude, as BF16 bits
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -383,19 +416,30 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
           // 2^(14 - exponent of the largest); the scale and its inverse stay normal numbers
           const int up = top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 7), -100), 100);
           const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-          sc[nr] = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {   // 8 channels: two k-steps
-            const int ks = 4 * (i >> 1) + 2 * (i & 1);
-            qa[ks][nr] = scaled_half2(x[i].x, f);
-            qa[ks][NT + nr] = scaled_half2(x[i].y, f);
-            qa[ks + 1][nr] = scaled_half2(x[i].z, f);
-            qa[ks + 1][NT + nr] = scaled_half2(x[i].w, f);
+            const uint4 h = make_uint4(scaled_half2(x[i].x, f), scaled_half2(x[i].y, f), scaled_half2(x[i].z, f), scaled_half2(x[i].w, f));
+            if (NT == 1) own_q[i] = h; else s_q[(nr * 4 + i) * 32 + lane] = h;
+          }
+          const float factor = a.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+          if (NT == 1) {
+            sc[0][0] = __shfl_sync(0xffffffffu, factor, 8 * t);
+            sc[0][1] = __shfl_sync(0xffffffffu, factor, 8 * t + 4);
+          } else if (t == 0) {
+            s_factor[r] = factor;
+            s_seen[r] = r >= p.rows ? 0 : a.causal ? p.ctx - a.T + (p.row0 + r) / a.G + 1 : p.ctx;
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(q_empty(n_q & 1));
         ++n_q;
+        if (NT > 1) {
+          sync_consumers();
+#pragma unroll
+          for (int nr = 0; nr < NT; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sc[nr][e] = s_factor[8 * nr + 2 * t + e];
+        }
       }
 
       // the key that the last row sees last, and those that all rows see
@@ -406,74 +450,91 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
         const int s_k = n_tiles % kSlots, s_v = (n_tiles + 1) % kSlots;
         const int pos = k * kUnit + 32 * warp;   // of the block's first token
         const bool any = pos < last;             // the warp's block holds a key that is seen
+        const int block = k % kPerPage * (kUnit / kC) + warp;
         if (!mbar_wait(full(s_k), (n_tiles / kSlots) & 1, a.wait_ns)) failed = true;
         failed = __any_sync(0xffffffffu, failed);
         if (failed) continue;
-        float s[4][4];
-        float corr[NT];
+        float s[2][NT][4];   // [16 tokens]: rows 2 t, 2 t + 1 of token n_of, then of n_of + 8
+        float corr[NT][2];
         bool grow = false;
         if (any) {
-          const uint32_t tile = base + kOffRing + s_k * kTile + k_at;
+          const uint32_t tile = base + S::kOffRing + s_k * kTile + k_at;
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
+          for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+            for (int nr = 0; nr < NT; ++nr)
 #pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              const uint4 x = lds16(tile + nt * 8 * kH + (jj ? k_piece1 : k_piece0));
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              for (int e = 0; e < 4; ++e) s[mt][nr][e] = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t* q = qa[4 * jj + e];
-                mma_f16(s[nt], q[0], NT > 1 ? q[1] : 0u, q[NT], NT > 1 ? q[2 * NT - 1] : 0u, f16x2_of(w[e]), f16x2_of_high(w[e]));
-              }
+          for (int jj = 0; jj < 2; ++jj) {
+            uint4 x[2][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i >> 1][i & 1] = lds16(tile + i * 8 * kH + (jj ? k_piece1 : k_piece0));
+            if (jj == 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(empty(s_k));
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // two k-steps
+              uint4 q[NT];
+#pragma unroll
+              for (int nr = 0; nr < NT; ++nr) q[nr] = NT == 1 ? own_q[2 * jj + h] : s_q[(nr * 4 + 2 * jj + h) * 32 + lane];
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                  auto word = [&](const uint4& v) { return h == 0 ? e == 0 ? v.x : v.y : e == 0 ? v.z : v.w; };
+                  const uint32_t w0 = word(x[mt][0]), w1 = word(x[mt][1]);
+                  const uint32_t a0 = f16x2_of(w0), a1 = f16x2_of(w1), a2 = f16x2_of_high(w0), a3 = f16x2_of_high(w1);
+#pragma unroll
+                  for (int nr = 0; nr < NT; ++nr)
+                    mma_f16(s[mt][nr], a0, a1, a2, a3, e == 0 ? q[nr].x : q[nr].z, e == 0 ? q[nr].y : q[nr].w);
+                }
             }
           }
-          const float ks = scale_of(s_scale[s_k * kScaleBytes + 4 * (k & 1) + warp]);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty(s_k));
-
-          // the lane's scores: rows 8 nr + g, tokens 8 nt + t + 4 e
-          float f[NT], top[NT];
+          const float ks = scale_of(s_scale[s_k * kScaleBytes + block]);
           const bool whole = pos + 32 <= common;
+          float f[NT][2], top[NT][2];
 #pragma unroll
-          for (int nr = 0; nr < NT; ++nr) {
-            f[nr] = fmaxf(sc[nr] * ks, 1.17549435e-38f);   // not 0: a masked score times it is -inf
-            top[nr] = -CUDART_INF_F;
+          for (int nr = 0; nr < NT; ++nr)
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int e = 0; e < 2; ++e) {
+              f[nr][e] = fmaxf(sc[nr][e] * ks, 1.17549435e-38f);   // not 0: a masked score times it is -inf
+              if (!whole) {
+                const int r = 8 * nr + 2 * t + e;
+                const int n = NT > 1 ? s_seen[r] : r >= p.rows ? 0 : a.causal ? own_seen + (p.row0 + r) / a.G : p.ctx;
+                const int seen = n - pos - n_of;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& v = s[nt][2 * nr + e];
-                if (!whole && pos + 8 * nt + t + 4 * e >= nv[nr]) v = -CUDART_INF_F;
-                top[nr] = fmaxf(top[nr], v);
+                for (int i = 0; i < 4; ++i)
+                  if (8 * i >= seen) s[i >> 1][nr][2 * (i & 1) + e] = -CUDART_INF_F;
               }
-            top[nr] *= f[nr];
-            grow |= top[nr] > m_run[nr] + kLazyLog2;
-          }
+              top[nr][e] = fmaxf(fmaxf(s[0][nr][e], s[0][nr][2 + e]), fmaxf(s[1][nr][e], s[1][nr][2 + e])) * f[nr][e];
+              grow |= top[nr][e] > m_run[nr][e] + kLazyLog2;
+            }
           grow = __any_sync(0xffffffffu, grow);
 #pragma unroll
-          for (int nr = 0; nr < NT; ++nr) {
-            float m = m_run[nr];
-            if (grow) {
-              float x = fmaxf(top[nr], __shfl_xor_sync(0xffffffffu, top[nr], 1));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-              m = fmaxf(m, x);
-            }
-            corr[nr] = !grow || m == -CUDART_INF_F ? 1.0f : ex2(m_run[nr] - m);
-            m_run[nr] = m;
-            const float ref = m == -CUDART_INF_F ? 0.0f : kUpLog2 - m;   // a masked score gives 0 in any case
-            float sum = 0.0f;
+          for (int nr = 0; nr < NT; ++nr)
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& v = s[nt][2 * nr + e];
-                v = ex2(fmaf(v, f[nr], ref));
-                sum += v;
+            for (int e = 0; e < 2; ++e) {
+              float m = m_run[nr][e];
+              if (grow) {
+                float x = top[nr][e];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                m = fmaxf(m, x);
+                corr[nr][e] = m == -CUDART_INF_F ? 1.0f : ex2(m_run[nr][e] - m);
+                l_run[nr][e] *= corr[nr][e];
+                m_run[nr][e] = m;
               }
-            l_run[nr] = fmaf(l_run[nr], corr[nr], sum);
-          }
+              const float ref = m == -CUDART_INF_F ? 0.0f : kUpLog2 - m;   // a masked score gives 0 in any case
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float& v = s[i >> 1][nr][2 * (i & 1) + e];
+                v = ex2(fmaf(v, f[nr][e], ref));
+                l_run[nr][e] += v;
+              }
+            }
         } else {
           __syncwarp();
           if (lane == 0) mbar_arrive(empty(s_k));
@@ -483,32 +544,30 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
         failed = __any_sync(0xffffffffu, failed);
         if (failed) continue;
         if (any) {
-          // p as two FP16 numbers: (b0, b1) of k-step kv are n-tiles 2 kv and 2 kv + 1
-          uint32_t hi[4][NT], lo[4][NT];
+          // p as two FP16 numbers, transposed to pairs of tokens: (b0, b1) of k-step kv
+          uint32_t hi[2][NT][2], lo[2][NT][2];
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+          for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-            for (int nr = 0; nr < NT; ++nr) {
-              const __half2 h = __floats2half2_rn(s[nt][2 * nr], s[nt][2 * nr + 1]);
-              const float2 r = __half22float2(h);
-              hi[nt][nr] = half2_bits(h);
-              lo[nt][nr] = half2_bits(__floats2half2_rn(s[nt][2 * nr] - r.x, s[nt][2 * nr + 1] - r.y));
-            }
-          if (grow) {   // the lane's outputs are of rows 8 nr + 2 t + e: their factors are in lanes 8 t + 4 e
+            for (int nr = 0; nr < NT; ++nr)
 #pragma unroll
-            for (int nr = 0; nr < NT; ++nr) {
-              const float c0 = __shfl_sync(0xffffffffu, corr[nr], 8 * t), c1 = __shfl_sync(0xffffffffu, corr[nr], 8 * t + 4);
-#pragma unroll
-              for (int mt = 0; mt < 8; ++mt) {
-                O[mt][nr][0] *= c0;
-                O[mt][nr][1] *= c1;
-                O[mt][nr][2] *= c0;
-                O[mt][nr][3] *= c1;
+              for (int i = 0; i < 2; ++i) {
+                const float p0 = s[kv][nr][2 * i], p1 = s[kv][nr][2 * i + 1];
+                const __half2 h = __floats2half2_rn(p0, p1);
+                const float2 r = __half22float2(h);
+                hi[kv][nr][i] = transposed(half2_bits(h));
+                lo[kv][nr][i] = transposed(half2_bits(__floats2half2_rn(p0 - r.x, p1 - r.y)));
               }
-            }
+          if (grow) {
+#pragma unroll
+            for (int nr = 0; nr < NT; ++nr)
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) O[mt][nr][e] *= corr[nr][e & 1];
           }
-          const uint32_t tile = base + kOffRing + s_v * kTile;
-          const float vs = scale_of(s_scale[s_v * kScaleBytes + 8 + 4 * (k & 1) + warp]);
+          const uint32_t tile = base + S::kOffRing + s_v * kTile;
+          const float vs = scale_of(s_scale[s_v * kScaleBytes + kChunks + block]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {   // 8 of the lane's 16 channels
             uint2 x[2][4];   // [kv][tokens t, t + 4, t + 8, t + 12]
@@ -540,16 +599,25 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
 #pragma unroll
               for (int kv = 0; kv < 2; ++kv) {
                 auto word = [&](int i) { return w == 0 ? x[kv][i].x : x[kv][i].y; };
+                uint32_t v[2][4];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {   // channels 4 w + 2 i, + 1 of the 8
                   const uint32_t ab = prmt(word(0), word(1), i ? 0x7362u : 0x5140u), cd = prmt(word(2), word(3), i ? 0x7362u : 0x5140u);
-                  const uint32_t a0 = f16x2_of(ab), a1 = f16x2_of_high(ab), a2 = f16x2_of(cd), a3 = f16x2_of_high(cd);
-#pragma unroll
-                  for (int nr = 0; nr < NT; ++nr) {
-                    mma_f16(U[i][nr], a0, a1, a2, a3, hi[2 * kv][nr], hi[2 * kv + 1][nr]);
-                    mma_f16(U[i][nr], a0, a1, a2, a3, lo[2 * kv][nr], lo[2 * kv + 1][nr]);
-                  }
+                  v[i][0] = f16x2_of(ab);
+                  v[i][1] = f16x2_of_high(ab);
+                  v[i][2] = f16x2_of(cd);
+                  v[i][3] = f16x2_of_high(cd);
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int nr = 0; nr < NT; ++nr)
+                    mma_f16(U[i][nr], v[i][0], v[i][1], v[i][2], v[i][3], hi[kv][nr][0], hi[kv][nr][1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int nr = 0; nr < NT; ++nr)
+                    mma_f16(U[i][nr], v[i][0], v[i][1], v[i][2], v[i][3], lo[kv][nr][0], lo[kv][nr][1]);
               }
 #pragma unroll
               for (int i = 0; i < 2; ++i)
@@ -568,18 +636,21 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
         }
       }
 
-      // ---- the four warps' sums, joined and written (8 rows at a time)
+      // ---- the warps' sums, joined and written (8 rows at a time)
 #pragma unroll
-      for (int nr = 0; nr < NT; ++nr) {
-        float l = l_run[nr];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (t == 0) {
-          s_m[warp * 16 + 8 * nr + g] = m_run[nr];
-          s_l[warp * 16 + 8 * nr + g] = l;
+      for (int nr = 0; nr < NT; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float l = l_run[nr][e];
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          if (g == 0) {
+            s_m[warp * R + 8 * nr + 2 * t + e] = m_run[nr][e];
+            s_l[warp * R + 8 * nr + 2 * t + e] = l;
+          }
         }
-      }
-      float* slot = a.ws_o + (int64_t)(2 * c + (p.kind == kPartB)) * R * (kH + 2);
+      float* slot = a.ws_o + (int64_t)(2 * c + (p.kind == kPartB)) * a.tile_rows * (kH + 2);
 #pragma unroll
       for (int nr = 0; nr < NT; ++nr) {
         if (8 * nr >= p.rows) break;
@@ -593,38 +664,44 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
           *reinterpret_cast<float4*>(o + kOPitch + ((4 * i) ^ v_half)) = make_float4(u[1], u[3], v[1], v[3]);
         }
         sync_consumers();
-        // row tid / 16, channels 4 (tid % 16) and 64 + that
-        const int r = 8 * nr + (tid >> 4), ch = 4 * (tid & 15);
-        float mw[kWarps], m = -CUDART_INF_F, l = 0.0f;
+        // a row of 8 by 4 W lanes, four channels each at a time
+        constexpr int kLanes = 4 * W;
+        const int rr = tid / kLanes, r = 8 * nr + rr, ch = 4 * (tid % kLanes);
+        float mw[W], m = -CUDART_INF_F, l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          mw[w] = s_m[w * 16 + r];
+        for (int w = 0; w < W; ++w) {
+          mw[w] = s_m[w * R + r];
           m = fmaxf(m, mw[w]);
         }
-        float4 u0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u1 = u0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = mw[w] == -CUDART_INF_F ? 0.0f : ex2(mw[w] - m);
-          l = fmaf(s_l[w * 16 + r], f, l);
-          const float* o4 = s_o + (w * 8 + (tid >> 4)) * kOPitch + ch;
-          const float4 v0 = *reinterpret_cast<const float4*>(o4), v1 = *reinterpret_cast<const float4*>(o4 + 64);
-          u0.x = fmaf(v0.x, f, u0.x); u0.y = fmaf(v0.y, f, u0.y); u0.z = fmaf(v0.z, f, u0.z); u0.w = fmaf(v0.w, f, u0.w);
-          u1.x = fmaf(v1.x, f, u1.x); u1.y = fmaf(v1.y, f, u1.y); u1.z = fmaf(v1.z, f, u1.z); u1.w = fmaf(v1.w, f, u1.w);
+        for (int w = 0; w < W; ++w) {
+          mw[w] = mw[w] == -CUDART_INF_F ? 0.0f : ex2(mw[w] - m);   // the warp's factor
+          l = fmaf(s_l[w * R + r], mw[w], l);
         }
-        if (r < p.rows && !failed) {
-          if (p.kind == kDirect) {
-            const int row = p.row0 + r, token = row / a.G;
-            const int64_t at = ((int64_t)p.b * a.T + token) * a.Hq + p.h * a.G + row - token * a.G;
-            const float f = l > 0.0f ? 1.0f / l : l;   // 0 for a row without keys, NaN stays
-            float* out = a.out + at * kH + ch;
-            *reinterpret_cast<float4*>(out) = make_float4(u0.x * f, u0.y * f, u0.z * f, u0.w * f);
-            *reinterpret_cast<float4*>(out + 64) = make_float4(u1.x * f, u1.y * f, u1.z * f, u1.w * f);
-            if (ch == 0 && a.lse) a.lse[at] = l == 0.0f ? -CUDART_INF_F : (m - kUpLog2 + log2f(l)) * 0.6931471805599453f;
-          } else {
-            float* out = slot + r * kH + ch;
-            *reinterpret_cast<float4*>(out) = u0;
-            *reinterpret_cast<float4*>(out + 64) = u1;
-            if (ch == 0) *reinterpret_cast<float2*>(slot + R * kH + 2 * r) = make_float2(m, l);
+        const int row = p.row0 + r, token = row / a.G;
+        const int64_t at = ((int64_t)p.b * a.T + token) * a.Hq + p.h * a.G + row - token * a.G;
+        const bool direct = p.kind == kDirect;
+        const float f = !direct ? 1.0f : l > 0.0f ? 1.0f / l : l;   // 0 for a row without keys, NaN stays
+        float* dst = direct ? a.out + at * kH : slot + r * kH;
+#pragma unroll
+        for (int x = 0; x < kH; x += 4 * kLanes) {
+          float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + rr) * kOPitch + x + ch);
+            u.x = fmaf(v.x, mw[w], u.x);
+            u.y = fmaf(v.y, mw[w], u.y);
+            u.z = fmaf(v.z, mw[w], u.z);
+            u.w = fmaf(v.w, mw[w], u.w);
+          }
+          if (r < p.rows && !failed)
+            *reinterpret_cast<float4*>(dst + x + ch) = make_float4(u.x * f, u.y * f, u.z * f, u.w * f);
+        }
+        if (r < p.rows && !failed && ch == 0) {
+          if (!direct) {
+            *reinterpret_cast<float2*>(slot + a.tile_rows * kH + 2 * r) = make_float2(m, l);
+          } else if (a.lse) {
+            a.lse[at] = l == 0.0f ? -CUDART_INF_F : (m - kUpLog2 + log2f(l)) * kLn2;
           }
         }
         sync_consumers();   // the area is free again
@@ -637,8 +714,6 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
     sync_consumers();
     if (tid == 0) a.ws_hdr_as<Header>()[c] = *s_abort ? Header{0, 0, 0, 0, 0, 0, 0, 0} : hdr;
   }
-  __syncwarp();
-  allow_dependent_launch();
 }
 
 // ------------------------------------------------------------------ join of the parts
@@ -657,7 +732,7 @@ decode_e4m3_join(const DecodeE4m3Args a) {
   const Header* hdr = a.ws_hdr_as<Header>();
   const Header hd = hdr[c];
   if (!hd.b_open || hd.b_state == 2 || r >= hd.rows) return;
-  const int R = a.tile_rows <= 8 ? 8 : 16;
+  const int R = a.tile_rows;
   float m = -CUDART_INF_F, l = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   auto add = [&](int slot) {
@@ -714,49 +789,54 @@ decode_e4m3_join(const DecodeE4m3Args a) {
   const int row = hd.row0 + r, token = row / a.G;
   const int64_t at = ((int64_t)hd.b * a.T + token) * a.Hq + hd.h * a.G + row - token * a.G;
   *reinterpret_cast<float4*>(a.out + at * kH + 4 * lane) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -CUDART_INF_F : (top - kUpLog2 + log2f(sum)) * 0.6931471805599453f;
+  if (lane == 0 && a.lse) a.lse[at] = sum == 0.0f ? -CUDART_INF_F : (top - kUpLog2 + log2f(sum)) * kLn2;
 }
 
-template <int NT>
-cudaError_t launch(const DecodeE4m3Args& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+template <int NT, int W>
+cudaError_t launch(DecodeE4m3Args a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  using S = Layout<NT, W>;
   static bool configured[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !configured[dev]) {
     const cudaError_t e =
-        cudaFuncSetAttribute(decode_e4m3_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+        cudaFuncSetAttribute(decode_e4m3_kernel<NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemAlloc);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
-  return launch_programmatic(decode_e4m3_kernel<NT>, dim3(a.n_cta), dim3(kThreads), kSmemAlloc, s, a, tk, tv);
+  const int n_cta = device_sm_count() * S::kCtas;
+  cudaError_t e = launch_programmatic(decode_e4m3_kernel<NT, W>, dim3(n_cta < kMaxCtas ? n_cta : kMaxCtas),
+                                      dim3(S::kThreads), S::kSmemAlloc, s, a, tk, tv);
+  if (e != cudaSuccess) return e;
+  const int rows = a.T * a.G;
+  return launch_programmatic(decode_e4m3_join, dim3(n_cta < kMaxCtas ? n_cta : kMaxCtas, rows < a.tile_rows ? rows : a.tile_rows),
+                             dim3(32 * kJoinWarps), 0, s, a);
 }
 
-int tile_rows(int rows) { return rows <= 8 ? 8 : 16; }
-int n_ctas() {
-  const int n = 2 * device_sm_count();
-  return n < kMaxCtas ? n : kMaxCtas;
-}
+int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32; }
 
 }  // namespace
 
 size_t decode_e4m3_ws_bytes(int rows) {
-  return (size_t)kMaxCtas * sizeof(Header) + (size_t)2 * n_ctas() * tile_rows(rows) * (kH + 2) * 4;
+  const int n = 2 * device_sm_count();
+  return (size_t)kMaxCtas * sizeof(Header) + (size_t)2 * (n < kMaxCtas ? n : kMaxCtas) * tile_rows(rows) * (kH + 2) * 4;
 }
 
 cudaError_t launch_decode_e4m3(DecodeE4m3Args a, void* workspace, cudaStream_t s) {
   const int rows = a.T * a.G;
   a.tile_rows = tile_rows(rows);
   a.n_tiles = (rows + a.tile_rows - 1) / a.tile_rows;
-  a.n_cta = n_ctas();
   a.ws_hdr = workspace;
   a.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * sizeof(Header));
   CUtensorMap tk, tv;
   // a page is two tiles of 128 rows of 128 bytes
   if (!plane_map(&tk, a.k_pages, 2 * a.n_pool) || !plane_map(&tv, a.v_pages, 2 * a.n_pool)) return cudaErrorInvalidValue;
-  cudaError_t e = a.tile_rows == 8 ? launch<1>(a, tk, tv, s) : launch<2>(a, tk, tv, s);
-  if (e != cudaSuccess) return e;
-  return launch_programmatic(decode_e4m3_join, dim3(a.n_cta, rows < a.tile_rows ? rows : a.tile_rows),
-                             dim3(32 * kJoinWarps), 0, s, a);
+  switch (a.tile_rows) {
+    case 8: return launch<1, 4>(a, tk, tv, s);
+    case 16: return launch<2, 4>(a, tk, tv, s);
+    case 24: return launch<3, 8>(a, tk, tv, s);
+    default: return launch<4, 8>(a, tk, tv, s);
+  }
 }
 
 }  // namespace lynx

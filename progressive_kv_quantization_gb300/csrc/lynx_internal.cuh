@@ -323,7 +323,7 @@ struct DecodeE4m3Args {
   unsigned long long wait_ns;   // as DecodeArgs
   int inject;                   // test hook: every CTA's first V tile is never copied
   // set by the launcher
-  int tile_rows, n_tiles, n_cta;
+  int tile_rows, n_tiles;
   void* ws_hdr;
   float* ws_o;
   template <typename Hdr>
