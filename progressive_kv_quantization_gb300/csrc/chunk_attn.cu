@@ -67,6 +67,7 @@
 #include "tma_ptx.cuh"
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <math_constants.h>
 
 namespace lynx {
@@ -107,22 +108,26 @@ struct Layout {
   // registers a thread, of 168 or 128 each at launch: 256 x 208 + 128 x 80 <= 384 x 168,
   // 256 x 200 + 128 x 64 + 128 x 48 = 512 x 128
   static constexpr int kRegsSoftmax = E ? 200 : 208, kRegsOther = E ? 64 : 80, kRegsConvert = 48;
-  static constexpr int kSlots = E ? 4 : 5;     // K and V tiles in BF16
-  static constexpr int kRawSlots = E ? 2 : 0;  // in 8 bits, on their way to those
+  // Tiles through a ring, K and V in turn (BF16); E: keys as codes, values as codes and as BF16,
+  // through a ring each, and the keys' scales, which the softmax reads behind the products
+  static constexpr int kSlots = 5, kKeySlots = 3, kRawSlots = 3, kValueSlots = 2, kKeyScales = 4;
   static constexpr int kOffQ = 0;
   static constexpr int kOffRing = kOffQ + 2 * kQBytes;
-  static constexpr int kOffRaw = kOffRing + kSlots * kSlot;
-  static constexpr int kOffScale = kOffRaw + kRawSlots * kRawTile;
-  static constexpr int kOffBar = kOffScale + kRawSlots * kScaleBytes;
-  static constexpr int kNumBars = 2 * kSlots + 10 + 2 * kRawSlots;
+  static constexpr int kOffKeys = kOffRing + (E ? kValueSlots : kSlots) * kSlot;
+  static constexpr int kOffRaw = kOffKeys + (E ? kKeySlots * kRawTile : 0);
+  static constexpr int kOffScale = kOffRaw + (E ? kRawSlots * kRawTile : 0);
+  static constexpr int kOffKeyScale = kOffScale + (E ? kRawSlots * kScaleBytes : 0);
+  static constexpr int kOffRowUp = kOffKeyScale + (E ? kKeyScales * kScaleBytes : 0);
+  static constexpr int kOffBar = kOffRowUp + (E ? kTileRows : 0);
+  static constexpr int kNumBars = 10 + 2 * (E ? kKeySlots + kRawSlots + kValueSlots : kSlots);
   static constexpr int kOffItems = kOffBar + ((8 * kNumBars + 15) / 16) * 16;
   static constexpr int kOffMisc = kOffItems + ((kMaxItems * kItemInts * 4 + 15) / 16) * 16;
   static constexpr int kSmem = kOffMisc + 80;   // items, header (at 16), tensor memory (at 64), abort and busy flags
   static constexpr int kSmemAlloc = kSmem + 1024;
   static_assert(kSmemAlloc <= 232448, "shared memory (chunk attention)");
 };
-// Values in 8 bits become BF16 numbers times 2^-64, which holds every scale: the
-// scores' factor and the outputs make up for it.
+// Values in 8 bits become BF16 numbers times 2^-64, which holds every scale: the outputs
+// make up for it.
 constexpr float kE4m3Up = 18446744073709551616.0f;
 
 // one tile, or the part of one, of a CTA
@@ -167,6 +172,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// E4M3 operands
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
 // one lane of a whole warp, the same one every time
 __device__ __forceinline__ bool elected() {
   uint32_t p;
@@ -192,6 +204,8 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
 // float32 accumulators, BF16 operands, 128 x 128; the B operand K-major or MN-major
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (16u << 17) | (8u << 24);
 constexpr uint32_t kIdescMn = kIdesc | (1u << 16);
+// E4M3 operands, both K-major
+constexpr uint32_t kIdesc8 = (1u << 4) | (16u << 17) | (8u << 24);
 
 #define LYNX_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
 #define LYNX_I8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
@@ -251,6 +265,22 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
+}
+// four BF16 values (two words) times f as the sums of two codes each
+__device__ __forceinline__ void split_e4m3x4(uint32_t w0, uint32_t w1, float f, uint32_t& hi, uint32_t& lo) {
+  const uint32_t w[2] = {w0, w1};
+  hi = lo = 0;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float x0 = __uint_as_float(w[e] << 16) * f, x1 = __uint_as_float(w[e] & 0xFFFF0000u) * f;
+    uint16_t h, l;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(x1), "f"(x0));
+    const uint32_t back = f16x2_of(h);
+    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&back));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(x1 - r.y), "f"(x0 - r.x));
+    hi |= (uint32_t)h << (16 * e);
+    lo |= (uint32_t)l << (16 * e);
+  }
 }
 __device__ __forceinline__ void sts16(uint32_t addr, const uint32_t* v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -469,7 +499,7 @@ template <bool E>
 __global__ void __launch_bounds__(Layout<E>::kThreads, 1)
 chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   using S = Layout<E>;
-  constexpr int kSlots = S::kSlots, kOffQ = S::kOffQ, kOffRing = S::kOffRing, kOffItems = S::kOffItems, kOffMisc = S::kOffMisc;
+  constexpr int kOffQ = S::kOffQ, kOffRing = S::kOffRing, kOffItems = S::kOffItems, kOffMisc = S::kOffMisc;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -485,9 +515,18 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 68);
 
   const uint32_t bar0 = base + S::kOffBar;
-  auto kv_full = [&](int s) { return bar0 + 8 * s; };
-  auto kv_empty = [&](int s) { return bar0 + 8 * (kSlots + s); };
-  const uint32_t bars = bar0 + 8 * 2 * kSlots;
+  // Tile u of the CTA: even K, odd V of tile u / 2 of keys.  Its slot, how often that was in use before,
+  // and the barriers of the tile that the products read.
+  auto slot_of = [](uint32_t u) {
+    return E ? u & 1 ? (u >> 1) % S::kValueSlots : (u >> 1) % S::kKeySlots : u % S::kSlots;
+  };
+  auto turn_of = [](uint32_t u) {
+    return E ? u & 1 ? (u >> 1) / S::kValueSlots : (u >> 1) / S::kKeySlots : u / S::kSlots;
+  };
+  auto kv_full = [&](uint32_t u) { return bar0 + 8 * (slot_of(u) + (E && (u & 1) ? S::kKeySlots : 0)); };
+  const uint32_t bar1 = bar0 + 8 * (E ? S::kKeySlots + S::kValueSlots : S::kSlots);
+  auto kv_empty = [&](uint32_t u) { return bar1 + 8 * (slot_of(u) + (E && (u & 1) ? S::kKeySlots : 0)); };
+  const uint32_t bars = bar1 + (bar1 - bar0);
   auto q_full = [&](int g) { return bars + 8 * g; };
   auto s_full = [&](int g) { return bars + 8 * (2 + g); };
   auto p_full = [&](int g) { return bars + 8 * (4 + g); };
@@ -498,9 +537,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   auto raw_empty = [&](int s) { return bars + 8 * (10 + S::kRawSlots + s); };
 
   if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) {
-      mbar_init(kv_full(s), E ? 4 : 1);   // E: the converting warps
-      mbar_init(kv_empty(s), 2);   // both groups
+    for (uint32_t u = 0; u < (E ? 2 * S::kKeySlots : S::kSlots); ++u) {
+      if (E && (u & 1) && u / 2 >= S::kValueSlots) continue;
+      mbar_init(kv_full(u), E && (u & 1) ? 4 : 1);   // E: the converting warps
+      mbar_init(kv_empty(u), 2);   // both groups
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_full(g), kGroupRows);
@@ -508,7 +548,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       mbar_init(p_full(g), kGroupRows);
       mbar_init(o_done(g), 1);
     }
-    for (int s = 0; s < S::kRawSlots; ++s) {
+    for (int s = 0; s < (E ? S::kRawSlots : 0); ++s) {
       mbar_init(raw_full(s), 1);
       mbar_init(raw_empty(s), 4);
     }
@@ -540,8 +580,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     *s_abort = 1;
   };
   // counters of each role, running over all items
-  uint32_t n_kv_ring = 0;     // K and V tiles through the ring (producer; converting and MMA warps)
+  uint32_t n_kv_ring = 0;     // K and V tiles (producer; converting and MMA warps)
   uint32_t n_tile_g = 0;      // S tiles of this thread's group (softmax)
+  uint32_t n_keys = 0;        // E: tiles of keys in front of the item (softmax)
   uint32_t n_met = 0;         // phases of `met`
   uint32_t mma_items = 0, mma_tiles = 0;   // of the tensor-core warp's group
   bool failed = false;
@@ -558,25 +599,25 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   };
 
   if (E && warp >= kConvertWarp) {
-    // ================= E: tiles in 8 bits to BF16, swizzled as the products want them.  A
-    // warp takes 32 tokens, a block of one scale; 8 lanes that read or write together
+    // ================= E: tiles of values in 8 bits to BF16, swizzled as the products want
+    // them.  A warp takes 32 tokens, a block of one scale; 8 lanes that read or write together
     // have two tokens that differ in bits 0 and 2, so that their pieces of 16 bytes lie in
     // different banks on both sides.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsConvert));
     const int part = lane & 3, tok = (lane >> 3) ^ (lane & 4 ? 5 : 0), block = warp - kConvertWarp;
     const uint32_t row = (uint32_t)(32 * block + tok) * kH;   // bytes in either layout
-    constexpr int kRing = E ? S::kRawSlots : 1;
     while (const int n_items = next_list()) {
       for (int i = n_items - 1; i >= 0 && !failed; --i) {
         const int k0 = items[i].k0, k1 = items[i].k1;
         if (items[i].kind == kNothing || k0 == k1) continue;
-        for (int k = 2 * k0; k < 2 * k1; ++k, ++n_kv_ring) {
-          const int rs = n_kv_ring % kRing, s = n_kv_ring % kSlots;
-          if (!mbar_wait(raw_full(rs), (n_kv_ring / kRing) & 1, wait_ns)) failed = true;
-          if (n_kv_ring >= kSlots && !mbar_wait(kv_empty(s), (n_kv_ring / kSlots - 1) & 1, wait_ns)) failed = true;
+        for (int k = k0; k < k1; ++k, n_kv_ring += 2) {
+          const uint32_t u = n_kv_ring + 1, n = n_kv_ring >> 1;
+          const int rs = n % S::kRawSlots, s = slot_of(u);
+          if (!mbar_wait(raw_full(rs), (n / S::kRawSlots) & 1, wait_ns)) failed = true;
+          if (n >= S::kValueSlots && !mbar_wait(kv_empty(u), (turn_of(u) - 1) & 1, wait_ns)) failed = true;
           failed = __any_sync(0xffffffffu, failed);
           if (failed) break;
-          const int byte = smem[S::kOffScale + rs * kScaleBytes + 8 * (k & 1) + 4 * (k >> 1 & 1) + block];
+          const int byte = smem[S::kOffScale + rs * kScaleBytes + kChunks + 4 * (k & 1) + block];
           // 2^(s - 127 - 64) and the 2^120 between an E4M3 code and the same bits as BF16
           const uint32_t f = (uint32_t)(min(max(byte, kScaleLo), kScaleHi) + 56) << 7, f2 = f | f << 16;
           const uint32_t src = base + S::kOffRaw + rs * kRawTile + row, dst = base + kOffRing + s * kSlot + row;
@@ -600,7 +641,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(kv_full(s));
+            mbar_arrive(kv_full(u));
             mbar_arrive(raw_empty(rs));
           }
         }
@@ -634,10 +675,11 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               }
 #pragma unroll
               for (int kv = 0; kv < 2; ++kv) {
-                constexpr int kRing = E ? S::kRawSlots : kSlots;
-                const int s = n_kv_ring % kRing;
-                if (n_kv_ring >= kRing &&
-                    !mbar_wait(E ? raw_empty(s) : kv_empty(s), (n_kv_ring / kRing - 1) & 1, wait_ns)) {
+                const uint32_t u = n_kv_ring, n = u >> 1;
+                const int rs = n % S::kRawSlots;   // E: of a V tile
+                const bool raw_v = E && kv;
+                const uint32_t turn = raw_v ? n / S::kRawSlots : turn_of(u);
+                if (turn > 0 && !mbar_wait(raw_v ? raw_empty(rs) : kv_empty(u), (turn - 1) & 1, wait_ns)) {
                   give_up();
                   failed = true;
                   break;
@@ -647,15 +689,18 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
                   continue;
                 }
                 if constexpr (E) {
-                  mbar_expect_tx(raw_full(s), kRawTile + kScaleBytes);
-                  tma_tile_g2s(base + S::kOffRaw + s * kRawTile, kv ? &tm_v : &tm_k, 0, (int)(id * kP) + (k & 1) * kTileKeys,
-                               raw_full(s));
-                  bulk_g2s(base + S::kOffScale + s * kScaleBytes, a.scales + id * kScaleBytes, kScaleBytes, raw_full(s));
+                  const uint32_t bar = kv ? raw_full(rs) : kv_full(u);
+                  mbar_expect_tx(bar, kRawTile + kScaleBytes);
+                  tma_tile_g2s(base + (kv ? S::kOffRaw + rs * kRawTile : S::kOffKeys + slot_of(u) * kRawTile),
+                               kv ? &tm_v : &tm_k, 0, (int)(id * kP) + (k & 1) * kTileKeys, bar);
+                  // the keys' scales are read until the next tile's product is issued: they outlive their slot
+                  bulk_g2s(base + (kv ? S::kOffScale + rs * kScaleBytes : S::kOffKeyScale + n % S::kKeyScales * kScaleBytes),
+                           a.scales + id * kScaleBytes, kScaleBytes, bar);
                 } else {
-                  const uint32_t dst = base + kOffRing + s * kSlot;
-                  mbar_expect_tx(kv_full(s), kSlot);
-                  tma_tile_g2s(dst, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys, (int)(id * kH), kv_full(s));
-                  tma_tile_g2s(dst + kBox, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys + 64, (int)(id * kH), kv_full(s));
+                  const uint32_t dst = base + kOffRing + slot_of(u) * kSlot;
+                  mbar_expect_tx(kv_full(u), kSlot);
+                  tma_tile_g2s(dst, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys, (int)(id * kH), kv_full(u));
+                  tma_tile_g2s(dst + kBox, kv ? &tm_v : &tm_k, (k & 1) * kTileKeys + 64, (int)(id * kH), kv_full(u));
                 }
                 ++n_kv_ring;
               }
@@ -672,8 +717,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         const int g = warp == kMmaWarp ? 0 : 1;
         const uint32_t t_s = uni(tmem) + g * 128, t_o = uni(tmem) + 256 + g * 128;
         const uint64_t q_desc = desc_k(uni(base) + kOffQ + g * kQBytes);
-        // a BF16 page is channel-major, one in 8 bits token-major: K and V change places
-        const uint64_t k_desc = E ? desc_k(uni(base) + kOffRing) : desc_mn(uni(base) + kOffRing);
+        // a BF16 page is channel-major, one in 8 bits token-major; keys in 8 bits stay codes, and the
+        // queries are two codes each, whose sum they are
+        const uint64_t k_desc = E ? desc_k(uni(base) + S::kOffKeys) : desc_mn(uni(base) + kOffRing);
         const uint64_t v_desc = E ? desc_mn(uni(base) + kOffRing) : desc_k(uni(base) + kOffRing);
         auto step_k = [](int ks) { return (uint64_t)((ks >> 2) * (kBox >> 4) + (ks & 3) * 2); };   // 16 along K, K-major
         auto step_mn = [](int ks) { return (uint64_t)(ks * 128); };                                // MN-major
@@ -694,32 +740,35 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
             // same: a warp that ran ahead of the ring could not tell a phase of a
             // slot's barrier from the one before the last.
             for (uint32_t u = u0; u != n_kv_ring; ++u) {
-              if (!wait(kv_full(u % kSlots), (u / kSlots) & 1)) break;
-              if (lane == 0) mbar_arrive(kv_empty(u % kSlots));
+              if (!wait(kv_full(u), turn_of(u) & 1)) break;
+              if (lane == 0) mbar_arrive(kv_empty(u));
             }
             continue;
           }
           // S of the K tile in slot s; by the elected lane
           auto qk = [&](uint32_t s) {
-            const uint64_t k = k_desc + (uint64_t)(s * (kSlot >> 4));
+            const uint64_t k = k_desc + (uint64_t)(s * ((E ? kRawTile : kSlot) >> 4));
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              mma_ss(t_s, q_desc + step_k(ks), k + (E ? step_k(ks) : step_mn(ks)), E ? kIdesc : kIdescMn, ks > 0);
+              if constexpr (E)
+                mma8_ss(t_s, q_desc + step_k(ks), k + (ks & 3) * 2, kIdesc8, ks > 0);
+              else
+                mma_ss(t_s, q_desc + step_k(ks), k + step_mn(ks), kIdescMn, ks > 0);
             tc_commit(s_full(g));
           };
-          if (!wait(kv_full(u0 % kSlots), (u0 / kSlots) & 1) || !wait(q_full(g), mma_items & 1)) break;
+          if (!wait(kv_full(u0), turn_of(u0) & 1) || !wait(q_full(g), mma_items & 1)) break;
           ++mma_items;
           tc_fence_after();
-          const uint32_t s0 = uni(u0 % kSlots);
+          const uint32_t s0 = uni(slot_of(u0));
           if (elected()) {
             qk(s0);
-            tc_commit(kv_empty(s0));
+            tc_commit(kv_empty(u0));
           }
           __syncwarp();
           for (int j = 0; j < n; ++j) {
             const uint32_t uv = u0 + 2 * j + 1, uk = uv + 1;
-            const uint32_t sv = uni(uv % kSlots), sk = uni(uk % kSlots);
-            if (!wait(kv_full(sv), (uv / kSlots) & 1)) break;
+            const uint32_t sv = uni(slot_of(uv)), sk = uni(slot_of(uk));
+            if (!wait(kv_full(uv), turn_of(uv) & 1)) break;
             const int tail = keys - j * kTileKeys;   // valid keys of the tile
             const int steps = uni(min(8, (tail + 15) >> 4));   // products of 16 keys that hold valid ones
             if (!E && tail < steps * 16) {   // (codes in 8 bits become numbers, whatever they are)
@@ -749,7 +798,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               fence_proxy_async();
               __syncwarp();
             }
-            if (j + 1 < n && !wait(kv_full(sk), (uk / kSlots) & 1)) break;
+            if (j + 1 < n && !wait(kv_full(uk), turn_of(uk) & 1)) break;
             if (!wait(p_full(g), mma_tiles & 1)) break;
             ++mma_tiles;
             // One group's block of products (this P V, the next Q K) at a time: mixed, both
@@ -780,10 +829,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
                   mma_ts(t_o, t_s + ks * 8, v + (E ? step_mn(ks) : step_k(ks)), E ? kIdescMn : kIdesc, more || ks > 0);
               }
               tc_commit(o_done(g));
-              tc_commit(kv_empty(sv));
+              tc_commit(kv_empty(uv));
               if (j + 1 < n) {
                 qk(sk);
-                tc_commit(kv_empty(sk));
+                tc_commit(kv_empty(uk));
               }
             }
             __syncwarp();
@@ -802,10 +851,12 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
       // ================= softmax: group g, one row a thread
       const int g = warp >> 2;
       const int r = (warp & 3) * 32 + lane;               // row of the group, tensor-memory lane
+      uint32_t skipped = 0;                               // E: tiles of keys that the group has no part in
       const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
       auto next_active = [&](int i) {   // the next item that this group has rows of, -1 behind the last
-        while (i >= 0 && (items[i].kind == kNothing || items[i].rows <= g * kGroupRows)) --i;
+        for (; i >= 0 && (items[i].kind == kNothing || items[i].rows <= g * kGroupRows); --i)
+          if (E && items[i].kind != kNothing) skipped += items[i].k1 - items[i].k0;
         return i;
       };
       // An item's queries on their way to shared memory, swizzled, 16 lanes a row; the
@@ -832,13 +883,48 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         }
         __syncwarp();
       };
+      // E: a row of 128 BF16 queries as two rows of 128 codes in its place, times the power of two that
+      // brings its largest value to 2^7..2^8: a value is the nearest code plus the nearest code of the rest, which
+      // holds all 8 bits of values down to 2^-10 of the largest, and is off by at most 2^-17 of that.
+      auto split_queries = [&](const Item&) {
+        __syncwarp();
+        const int part = lane & 15;
+        const uint32_t q = base + kOffQ + g * kQBytes;
+#pragma unroll 2
+        for (int x = 0; x < 16; ++x) {
+          const int rx = (warp & 3) * 32 + (lane >> 4) + 2 * x;
+          const uint4 v = lds16(q + (part >> 3) * kBox + rx * 128 + (((part & 7) ^ (rx & 7)) << 4));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t top = 0;   // largest magnitude, as BF16 bits
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int up = top == 0 ? 0 : min(max(7 + 127 - (int)(top >> 7), -100), 100);
+          const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) split_e4m3x4(w[2 * e], w[2 * e + 1], f, hi[e], lo[e]);
+          __syncwarp();       // both rows have been read
+          const uint32_t to = q + rx * 128 + (((part >> 1) ^ (rx & 7)) << 4) + 8 * (part & 1);
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(hi[0]), "r"(hi[1]) : "memory");
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to + kBox), "r"(lo[0]), "r"(lo[1]) : "memory");
+          if (part == 0) smem[S::kOffRowUp + g * kGroupRows + rx] = (uint8_t)(127 - up);
+        }
+        __syncwarp();
+      };
       auto queries_there = [&](const Item& it) {
         if (it.k0 == it.k1) return;
         copies_done();
+        if constexpr (E) split_queries(it);
         fence_proxy_async();
         mbar_arrive(q_full(g));
       };
       int i = next_active(n_items - 1);
+      if (E) {
+        n_keys += skipped;
+        skipped = 0;
+      }
       if (i >= 0) {
         load_queries(items[i]);
         queries_there(items[i]);
@@ -855,7 +941,8 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         if (n > 0) {
           // rows past the tile's last hold zero queries: whatever they sum up is not written
           const int seen = real ? visible(a, it.ctx, it.T, token) : 0x7fffffff;
-          const float sc = a.scale_log2;
+          float sc = a.scale_log2;
+          if constexpr (E) sc *= __uint_as_float((uint32_t)smem[S::kOffRowUp + g * kGroupRows + r] << 23);
           for (int j = 0;;) {
             const int j0 = j, j1 = min(n, j0 + kSumTiles);
             for (; j < j1; ++j) {
@@ -881,7 +968,15 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               // P against the running maximum as it stands, and the tile's maximum beside
               // it: the two do not wait for one another (1.36 us a tile of keys against 1.5 one
               // after the other).  Where the maximum has to move P is computed again.
-              const uint64_t sc2 = pair(sc, sc);
+              // E: with the scale of each block of 32 keys
+              float scb[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                scb[x] = sc;
+                if constexpr (E)
+                  scb[x] = fmaxf(sc * scale_of(smem[S::kOffKeyScale + (n_keys + j) % S::kKeyScales * kScaleBytes +
+                                                    4 * ((it.k0 + j) & 1) + x]), 1.17549435e-38f);   // -inf times it stays
+              }
               uint64_t sum[4];
               auto exps = [&](float ref) {
                 const uint64_t ref2 = pair(ref, ref);
@@ -890,6 +985,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                   uint32_t p[16];
+                  const uint64_t sc2 = pair(scb[x], scb[x]);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) {
                     float p0, p1;
@@ -903,13 +999,31 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
                 }
               };
               exps(m == -CUDART_INF_F ? 0.0f : -m);
-              float mx[8];
+              float top;
+              if constexpr (E) {
+                float mb[4];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) mx[x] = fmaxf(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+                for (int x = 0; x < 4; ++x) {
+                  const uint32_t* v = s + 32 * x;
+                  float m0 = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                  float m1 = fmaxf(__uint_as_float(v[2]), __uint_as_float(v[3]));
 #pragma unroll
-              for (int x = 8; x < 64; ++x)
-                mx[x & 7] = max3(mx[x & 7], __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
-              const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
+                  for (int e = 4; e < 32; e += 4) {
+                    m0 = max3(m0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    m1 = max3(m1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                  }
+                  mb[x] = fmaxf(m0, m1) * scb[x];
+                }
+                top = fmaxf(max3(mb[0], mb[1], mb[2]), mb[3]);
+              } else {
+                float mx[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) mx[x] = fmaxf(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+#pragma unroll
+                for (int x = 8; x < 64; ++x)
+                  mx[x & 7] = max3(mx[x & 7], __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+                top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
+              }
               if (__any_sync(0xffffffffu, top > m + kLazyLog2)) {
                 const float m_new = fmaxf(m, top);
                 const float f = m == -CUDART_INF_F ? 0.0f : ex2(m - m_new);
@@ -1051,6 +1165,10 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           }
         }
         tc_fence_before();   // O has been read before the next item's first product
+        if (E) {
+          n_keys += n + skipped;
+          skipped = 0;
+        }
       }
       if (failed && lane == 0) give_up();
       if (!list_done()) break;
@@ -1062,9 +1180,13 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
     copies_done();
     // the copies and products in flight end before the memory they use is given up
     if (warp == kTmaWarp && lane == 0) {
-      constexpr int kRing = E ? S::kRawSlots : kSlots;
-      for (uint32_t u = n_kv_ring > kRing ? n_kv_ring - kRing : 0; u < n_kv_ring; ++u)
-        if (!(a.inject && u == 1)) mbar_wait(E ? raw_full(u % kRing) : kv_full(u % kRing), (u / kRing) & 1, wait_ns);
+      constexpr uint32_t kRing = E ? 2 * S::kKeySlots : S::kSlots;
+      static_assert(S::kKeySlots == S::kRawSlots, "E: the last copies");
+      for (uint32_t u = n_kv_ring > kRing ? n_kv_ring - kRing : 0; u < n_kv_ring; ++u) {
+        if (a.inject && u == 1) continue;
+        if (E && (u & 1)) mbar_wait(raw_full((u >> 1) % S::kRawSlots), (u >> 1) / S::kRawSlots & 1, wait_ns);
+        else mbar_wait(kv_full(u), turn_of(u) & 1, wait_ns);
+      }
     }
     if (warp == kMmaWarp || warp == kMmaWarp1) {
       if (elected()) tc_commit(drained);
@@ -1230,7 +1352,6 @@ cudaError_t launch_chunk_attn_e4m3(ChunkArgs a, void* workspace, cudaStream_t s)
   CUtensorMap tk, tv;
   // a page is two tiles of 128 rows of 128 bytes
   if (!plane_map(&tk, a.k_codes, 2 * a.n_pool) || !plane_map(&tv, a.v_codes, 2 * a.n_pool)) return cudaErrorInvalidValue;
-  a.scale_log2 *= kE4m3Up;
   return launch_chunk<true>(a, tk, tv, workspace, s);
 }
 
