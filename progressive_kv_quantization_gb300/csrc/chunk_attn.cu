@@ -110,7 +110,7 @@ struct Layout {
   static constexpr int kRegsSoftmax = E ? 200 : 208, kRegsOther = E ? 64 : 80, kRegsConvert = 48;
   // Tiles through a ring, K and V in turn (BF16); E: keys as codes, values as codes and as BF16,
   // through a ring each, and the keys' scales, which the softmax reads behind the products
-  static constexpr int kSlots = 5, kKeySlots = 3, kRawSlots = 3, kValueSlots = 2, kKeyScales = 4;
+  static constexpr int kSlots = 5, kKeySlots = 2, kRawSlots = 2, kValueSlots = 2, kKeyScales = 4;
   static constexpr int kOffQ = 0;
   static constexpr int kOffRing = kOffQ + 2 * kQBytes;
   static constexpr int kOffKeys = kOffRing + (E ? kValueSlots : kSlots) * kSlot;
@@ -537,10 +537,15 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
   auto raw_empty = [&](int s) { return bars + 8 * (10 + S::kRawSlots + s); };
 
   if (tid == 0) {
-    for (uint32_t u = 0; u < (E ? 2 * S::kKeySlots : S::kSlots); ++u) {
-      if (E && (u & 1) && u / 2 >= S::kValueSlots) continue;
-      mbar_init(kv_full(u), E && (u & 1) ? 4 : 1);   // E: the converting warps
+    auto init_tile = [&](uint32_t u, int full) {
+      mbar_init(kv_full(u), full);
       mbar_init(kv_empty(u), 2);   // both groups
+    };
+    if (E) {
+      for (int s = 0; s < S::kKeySlots; ++s) init_tile(2 * s, 1);
+      for (int s = 0; s < S::kValueSlots; ++s) init_tile(2 * s + 1, 4);   // the converting warps
+    } else {
+      for (int s = 0; s < S::kSlots; ++s) init_tile(s, 1);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_full(g), kGroupRows);
