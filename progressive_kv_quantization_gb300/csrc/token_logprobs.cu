@@ -12,11 +12,13 @@
 // and are brought to the row's maximum at the end.
 //
 // The n most likely tokens (equal ones: the lowest first) as 64-bit keys: the float's bits in
-// an order of whole numbers, and under them the token's from behind.  While the logits go by,
-// a thread only notes its largest value and the piece that it is in.  The n-th largest of the
-// notes of 64 groups of 4 threads is a bound that at least n tokens of the CTA's part reach;
-// only threads whose own note reaches it (some n of 256) are gone through again, by
-// their whole warp, and the tokens that reach the bound, a few more than n, are ranked by counting.
+// an order of whole numbers, and under them the token's from behind.  While the first quarter
+// of a CTA's part goes by, a thread only notes its largest value and the piece that it is in.  The
+// n-th largest of the notes of 64 groups of 4 threads is a bound that at least n tokens
+// reach; the pieces of threads whose own note reaches it (some n of 256) are gone
+// through again, still in L2, and of the other three quarters what reaches the bound is kept as it
+// goes by: some 5 n tokens, which are ranked by counting.  (Going through the whole part again
+// at its end read lines of 16 bytes from DRAM: 1,000 rows of 128,256 took 114 us against 87.)
 //
 // Bound by the reads of the logits for many rows, by the chain (launch, one round trip
 // of loads, the reductions, the second look) for few.
@@ -35,10 +37,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;               // pieces of a thread read at once
 constexpr int kGroups = kThreads / 4;
 constexpr int kMaxTop = kLogprobsMaxTop;
 constexpr int kFound = 2048;            // tokens that reach the bound, at most
+constexpr int kKept = 512;              // pieces with such tokens, at most
 constexpr int kMaxCluster = 8;
 constexpr float kLag = 6.0f;            // of the reference behind the maximum
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -131,16 +133,23 @@ struct Found {
   Key best[kMaxTop];
 };
 
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads, 4)
 token_logprobs_kernel(const LogprobsArgs a) {
   using P = Piece<T>;
+  constexpr int kBatch = sizeof(T) == 2 && TOP ? 2 : 4;   // pieces of a thread read at once
   __shared__ Found s_found;
   __shared__ float s_part[kWarps][2];
   __shared__ Key s_group[TOP ? kGroups : 1];
   __shared__ Key s_keys[TOP ? kFound : 1];
   __shared__ Key s_bound;
-  __shared__ int s_count;
+  __shared__ int s_count, s_n_again, s_n_kept;
+  __shared__ uint4 s_kept[TOP ? kKept : 1];     // pieces that reach the bound, and which they are
+  __shared__ int s_kept_k[TOP ? kKept : 1];
+  __shared__ int s_again[TOP ? kThreads : 1];   // threads whose pieces are gone through again
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t row = blockIdx.x / C;
@@ -166,11 +175,31 @@ token_logprobs_kernel(const LogprobsArgs a) {
   Sums sums;
   float top = -CUDART_INF_F;
   int top_k = -1;   // the piece that it is in
-  auto take = [&](const P& p, int k, float m) {
-    if (TOP ? m > top || top_k < 0 : m > top) {
-      top = m;
-      top_k = k;
+  Key bound = 0;
+  float least = CUDART_INF_F;
+  auto look = [&](float v, int i) {
+    if (!(v >= least)) return;
+    const Key key = key_of(v, i);
+    if (key >= bound) {
+      const int at = atomicAdd(&s_count, 1);
+      if (at < kFound) s_keys[at] = key;
     }
+  };
+  auto look_at = [&](const P& p, int k) {
+#pragma unroll
+    for (int e = 0; e < P::kN; ++e) look(p.at(e), front + k * P::kN + e);
+  };
+  // a piece with a value that reaches the bound, for the end
+  auto keep = [&](const P& p, int k) {
+    const int at = atomicAdd(&s_n_kept, 1);
+    if (at < kKept) {
+      s_kept[at] = p.raw;
+      s_kept_k[at] = k;
+    }
+  };
+  auto take = [&](const P& p, int k, float m, auto notes) {
+    if (TOP && decltype(notes)::value && (m > top || top_k < 0)) top_k = k;
+    top = fmaxf(top, m);
 #pragma unroll
     for (int e = 0; e < P::kN; e += 2) sums.add(p.at(e), p.at(e + 1));
   };
@@ -180,41 +209,109 @@ token_logprobs_kernel(const LogprobsArgs a) {
     sums.follow(loose_x);
     sums.add(loose_x, -CUDART_INF_F);
   }
-  {
-    constexpr int kStep = kBatch * kThreads;
-    int k = k0 + tid;
+  // The bound of what was noted, and what reaches it.  Every thread comes here once; others' pieces
+  // are those up to `end`.
+  auto set_bound = [&](int end) {
+    // a thread's note: its largest value, and the last token of its piece
+    Key note = top_k < 0 ? 0 : key_of(top, front + top_k * P::kN + P::kN - 1);
+    note = max(note, __shfl_xor_sync(0xffffffffu, note, 1));
+    note = max(note, __shfl_xor_sync(0xffffffffu, note, 2));
+    if ((lane & 3) == 0) s_group[tid >> 2] = note;
+    if (tid == 0) s_count = s_n_again = s_n_kept = 0;
+    __syncthreads();
+    // the n-th largest, four threads a note; they differ from one another, but for those that are 0
+    const int i = tid >> 2;
+    const Key own = s_group[i];
+    int r = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / 4; ++j) {
+      const int at = 4 * j + (tid & 3);
+      const Key o = s_group[at];
+      r += o > own || (o == own && at < i);
+    }
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    r += __shfl_xor_sync(0xffffffffu, r, 2);
+    if ((tid & 3) == 0 && r == a.n_top - 1) s_bound = own;
+    __syncthreads();
+    bound = s_bound;
+    least = bound == 0 ? -CUDART_INF_F : unordered((uint32_t)(bound >> 32));
+    if (loose_at >= 0) look(loose_x, loose_at);
+    // a thread's best possible key: its value and the first token of the piece
+    if (top_k >= 0 && key_of(top, front + top_k * P::kN) >= bound) s_again[atomicAdd(&s_n_again, 1)] = tid;
+    __syncthreads();
+    // the pieces of such threads, by equally many threads each, kBatch of them on their way at once
+    const int each = s_n_again ? kThreads / s_n_again : 1, who = tid / each, step = each * kThreads;
+    if (who < s_n_again) {
+      for (int k = k0 + s_again[who] + (tid - who * each) * kThreads; k < end; k += kBatch * step) {
+        P p[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (k + u * step < end) p[u].raw = __ldg(body + k + u * step);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (k + u * step < end && p[u].largest() >= least) keep(p[u], k + u * step);
+      }
+    }
+  };
+  constexpr int kStep = kBatch * kThreads;
+  // whole batches from piece k on, the next one on its way
+  auto stream = [&](int k, int batches, auto notes) {
+    constexpr bool kNotes = decltype(notes)::value;
     P next[kBatch];
-    // whole batches, the next one on its way
-    const int whole = (k1 - k0) / kStep;
-    if (whole > 0) {
+    if (batches > 0) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) next[u].raw = __ldg(body + k + u * kThreads);
     }
-    for (int b = 0; b < whole; ++b, k += kStep) {
+    for (int b = 0; b < batches; ++b, k += kStep) {
       P cur[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) cur[u] = next[u];
-      if (b + 1 < whole) {
+      if (b + 1 < batches) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) next[u].raw = __ldg(body + k + kStep + u * kThreads);
       }
       float m[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) m[u] = cur[u].largest();
-      sums.follow(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+      sums.follow(kBatch == 2 ? fmaxf(m[0], m[1]) : fmaxf(fmaxf(m[0], m[1]), fmaxf(m[kBatch - 2], m[kBatch - 1])));
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) take(cur[u], k + u * kThreads, m[u]);
+      for (int u = 0; u < kBatch; ++u) take(cur[u], k + u * kThreads, m[u], notes);
+      if (TOP && !kNotes) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (m[u] >= least) keep(cur[u], k + u * kThreads);
+        __syncwarp();
+      }
     }
+  };
+  // fewer than kBatch pieces from piece k on
+  auto rest = [&](int k, auto notes) {
+    P p[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
-      if (k + u * kThreads < k1) next[u].raw = __ldg(body + k + u * kThreads);
+      if (k + u * kThreads < k1) p[u].raw = __ldg(body + k + u * kThreads);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       if (k + u * kThreads < k1) {
-        const float m = next[u].largest();
+        const float m = p[u].largest();
         sums.follow(m);
-        take(next[u], k + u * kThreads, m);
+        take(p[u], k + u * kThreads, m, notes);
+        if (TOP && !decltype(notes)::value && m >= least) keep(p[u], k + u * kThreads);
       }
+    __syncwarp();
+  };
+  const int whole = (k1 - k0) / kStep, first = whole >= 8 ? whole / 4 : whole;
+  if (!TOP) {
+    stream(k0 + tid, whole, No());
+    rest(k0 + tid + whole * kStep, No());
+  } else {
+    stream(k0 + tid, first, Yes());
+    if (first == whole) rest(k0 + tid + whole * kStep, Yes());
+    set_bound(first == whole ? k1 : k0 + first * kStep);
+    if (first < whole) {
+      stream(k0 + tid + first * kStep, whole - first, No());
+      rest(k0 + tid + whole * kStep, No());
+    }
   }
 
   // ---- the CTA's maximum and sums
@@ -222,14 +319,6 @@ token_logprobs_kernel(const LogprobsArgs a) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) cta_top = fmaxf(cta_top, __shfl_xor_sync(0xffffffffu, cta_top, o));
   if (lane == 0) s_part[warp][0] = cta_top;
-  if (TOP) {
-    // a thread's note: its largest value, and the last token of its piece
-    Key note = top_k < 0 ? 0 : key_of(top, front + top_k * P::kN + P::kN - 1);
-    note = max(note, __shfl_xor_sync(0xffffffffu, note, 1));
-    note = max(note, __shfl_xor_sync(0xffffffffu, note, 2));
-    if ((lane & 3) == 0) s_group[tid >> 2] = note;
-    if (tid == 0) s_count = 0;
-  }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) cta_top = fmaxf(cta_top, s_part[w][0]);
@@ -253,19 +342,6 @@ token_logprobs_kernel(const LogprobsArgs a) {
     s_sums[warp][0] = s;
     s_sums[warp][1] = t;
   }
-  if (TOP && warp == 0) {
-    // the n-th largest note; they differ from one another, but for those that are 0
-    const Key n0 = s_group[lane], n1 = s_group[lane + 32];
-    int r0 = 0, r1 = 0;
-#pragma unroll 8
-    for (int i = 0; i < kGroups; ++i) {
-      const Key o = s_group[i];
-      r0 += o > n0 || (o == n0 && i < lane);
-      r1 += o > n1 || (o == n1 && i < lane + 32);
-    }
-    if (r0 == a.n_top - 1) s_bound = n0;
-    if (r1 == a.n_top - 1) s_bound = n1;
-  }
   __syncthreads();
   if (tid == 0) {
     s = t = 0.0f;
@@ -281,34 +357,28 @@ token_logprobs_kernel(const LogprobsArgs a) {
 
   if (TOP) {
     // ---- the tokens that reach the bound
-    int n;
-    while (true) {
-      const Key bound = s_bound;
-      auto look = [&](float v, int i) {
-        const Key key = key_of(v, i);
-        if (key >= bound) {
-          const int at = atomicAdd(&s_count, 1);
-          if (at < kFound) s_keys[at] = key;
-        }
-      };
-      if (loose_at >= 0) look(loose_x, loose_at);
-      // a thread's best possible key: its value and the first token of the piece
-      unsigned who = __ballot_sync(0xffffffffu, top_k >= 0 && key_of(top, front + top_k * P::kN) >= bound);
-      while (who) {
-        const int l = __ffs(who) - 1;
-        who &= who - 1;
-        for (int k = k0 + 32 * warp + l + lane * kThreads; k < k1; k += 32 * kThreads) {
-          P p;
-          p.raw = __ldg(body + k);
-#pragma unroll
-          for (int e = 0; e < P::kN; ++e) look(p.at(e), front + k * P::kN + e);
-        }
+    const int kept = s_n_kept;
+    auto look_at_all = [&] {
+      for (int k = k0 + tid; k < k1; k += kThreads) {
+        P p;
+        p.raw = __ldg(body + k);
+        if (p.largest() >= least) look_at(p, k);
       }
-      __syncthreads();
-      n = s_count;
-      if (n <= kFound) break;
-      // Too many (values that rise within one thread's pieces): the n_top-th largest of those
-      // that found room is a higher bound.
+    };
+    if (kept <= kKept) {
+      for (int i = tid; i < kept; i += kThreads) {
+        P p;
+        p.raw = s_kept[i];
+        look_at(p, s_kept_k[i]);
+      }
+    } else {
+      look_at_all();
+    }
+    __syncthreads();
+    int n = s_count;
+    while (n > kFound) {
+      // Too many (values that rise, or stand close together): the n_top-th largest of those that
+      // found room is a higher bound, and everything is gone through again.
       Key higher = 0;
       for (int i = tid; i < kFound; i += kThreads) {
         int r = 0;
@@ -319,6 +389,12 @@ token_logprobs_kernel(const LogprobsArgs a) {
       if (tid == 0) s_count = 0;
       if (higher) s_bound = higher;
       __syncthreads();
+      bound = s_bound;
+      least = unordered((uint32_t)(bound >> 32));
+      if (loose_at >= 0) look(loose_x, loose_at);
+      look_at_all();
+      __syncthreads();
+      n = s_count;
     }
     // ranks; a CTA's part may hold fewer than n_top tokens
     if (tid < kMaxTop) s_found.best[tid] = 0;
