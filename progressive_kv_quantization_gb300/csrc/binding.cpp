@@ -14,6 +14,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/DimVector.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -97,7 +98,15 @@ class Call {
       Py_INCREF(o);
       return o;
     }
-    at::Tensor t = at::empty(shape.sizes, at::TensorOptions().dtype(type).device(device_));
+    // at::empty without its dispatch, which takes longer than the rest
+    c10::Allocator* const memory = c10::cuda::CUDACachingAllocator::get();
+    int64_t n = 1;
+    for (int64_t x : shape.sizes) n *= x;
+    const size_t bytes = (size_t)n * c10::elementSize(type);
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(c10::Storage::use_byte_size_t(), bytes, memory->allocate(bytes), memory, true),
+        c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape.sizes);
     *ptr = t.data_ptr();
     return THPVariable_Wrap(std::move(t));
   }

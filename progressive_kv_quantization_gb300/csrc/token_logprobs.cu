@@ -18,10 +18,15 @@
 // reach; the pieces of threads whose own note reaches it (some n of 256) are gone
 // through again, still in L2, and of the other three quarters what reaches the bound is kept as it
 // goes by: some 5 n tokens, which are ranked by counting.  (Going through the whole part again
-// at its end read lines of 16 bytes from DRAM: 1,000 rows of 128,256 took 114 us against 87.)
+// at its end read lines of 16 bytes from DRAM: 1,000 rows of 128,256 float32 took 114 us against 93.)
+// Parts of fewer than 8 batches a thread are still in L2 then, and noted as a whole.
 //
-// Bound by the reads of the logits for many rows, by the chain (launch, one round trip
-// of loads, the reductions, the second look) for few.
+// Bound by the reads of the logits for many rows: 2,047 rows of 128,256 BF16 take 82 us (6.4 TB/s,
+// 94% of a copy), with 20 alternatives 105 us; 1,000 rows of as many float32 79 and 93 us.  By the
+// chain (launch, one round trip of loads, the reductions, the bound, the ranks) for few: 64 rows of
+// 151,936 float32 10 us without alternatives, 16.5 us with 20 (39 MB, 5.7 us at a copy's rate).
+// Copies go into shared memory, three batches a thread deep: loads to registers held fewer (93 and
+// 119 us for the BF16 rows; 88 us for the float32 rows with alternatives).
 
 #include "f32x2.cuh"
 #include "lynx_internal.cuh"
@@ -40,7 +45,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = kThreads / 4;
 constexpr int kMaxTop = kLogprobsMaxTop;
 constexpr int kFound = 2048;            // tokens that reach the bound, at most
-constexpr int kKept = 512;              // pieces with such tokens, at most
+constexpr int kKept = 256;              // pieces with such tokens, at most
 constexpr int kMaxCluster = 8;
 constexpr float kLag = 6.0f;            // of the reference behind the maximum
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -74,6 +79,18 @@ __device__ __forceinline__ float unordered(uint32_t o) {
 using Key = unsigned long long;   // 0: none
 __device__ __forceinline__ Key key_of(float x, int token) {
   return (Key)ordered(x) << 32 | (0xFFFFFFFFu - (uint32_t)token);
+}
+
+// batches of pieces on their way to a thread
+template <bool TOP>
+struct Stream {
+  static constexpr int kBatch = TOP ? 3 : 4, kStages = 3;
+  static constexpr int kBytes = kStages * kBatch * kThreads * 16;
+};
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
 }
 
 template <typename T>
@@ -140,11 +157,12 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads, 4)
 token_logprobs_kernel(const LogprobsArgs a) {
   using P = Piece<T>;
-  constexpr int kBatch = sizeof(T) == 2 && TOP ? 2 : 4;   // pieces of a thread read at once
+  using S = Stream<TOP>;
+  constexpr int kBatch = S::kBatch, kStages = S::kStages;
+  extern __shared__ __align__(16) uint4 s_stage[];   // [stage][piece of a batch][thread]
   __shared__ Found s_found;
   __shared__ float s_part[kWarps][2];
   __shared__ Key s_group[TOP ? kGroups : 1];
-  __shared__ Key s_keys[TOP ? kFound : 1];
   __shared__ Key s_bound;
   __shared__ int s_count, s_n_again, s_n_kept;
   __shared__ uint4 s_kept[TOP ? kKept : 1];     // pieces that reach the bound, and which they are
@@ -177,6 +195,7 @@ token_logprobs_kernel(const LogprobsArgs a) {
   int top_k = -1;   // the piece that it is in
   Key bound = 0;
   float least = CUDART_INF_F;
+  Key* s_keys = reinterpret_cast<Key*>(s_stage);   // when all pieces have been read
   auto look = [&](float v, int i) {
     if (!(v >= least)) return;
     const Key key = key_of(v, i);
@@ -235,7 +254,6 @@ token_logprobs_kernel(const LogprobsArgs a) {
     __syncthreads();
     bound = s_bound;
     least = bound == 0 ? -CUDART_INF_F : unordered((uint32_t)(bound >> 32));
-    if (loose_at >= 0) look(loose_x, loose_at);
     // a thread's best possible key: its value and the first token of the piece
     if (top_k >= 0 && key_of(top, front + top_k * P::kN) >= bound) s_again[atomicAdd(&s_n_again, 1)] = tid;
     __syncthreads();
@@ -254,29 +272,43 @@ token_logprobs_kernel(const LogprobsArgs a) {
     }
   };
   constexpr int kStep = kBatch * kThreads;
-  // whole batches from piece k on, the next one on its way
-  auto stream = [&](int k, int batches, auto notes) {
-    constexpr bool kNotes = decltype(notes)::value;
-    P next[kBatch];
-    if (batches > 0) {
+  const int whole = (k1 - k0) / kStep;
+  // A thread's pieces come by asynchronous copies into places of its own, kStages - 1 batches
+  // ahead; behind the last whole batch is a part of one.
+  uint4* stage = s_stage + tid;
+  auto fetch = [&](int b) {
+    const int k = k0 + tid + b * kStep;
+    uint4* dst = stage + b % kStages * kStep;
+    if (b < whole) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) next[u].raw = __ldg(body + k + u * kThreads);
+      for (int u = 0; u < kBatch; ++u) copy_async16(dst + u * kThreads, body + k + u * kThreads);
+    } else if (b == whole) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (k + u * kThreads < k1) copy_async16(dst + u * kThreads, body + k + u * kThreads);
     }
-    for (int b = 0; b < batches; ++b, k += kStep) {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto arrived = [] { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); };
+  // batches b0 .. b1 - 1, whole ones
+  auto stream = [&](int b0, int b1, auto notes) {
+    for (int b = b0; b < b1; ++b) {
+      fetch(b + kStages - 1);
+      arrived();
       P cur[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) cur[u] = next[u];
-      if (b + 1 < batches) {
+      for (int u = 0; u < kBatch; ++u) cur[u].raw = stage[b % kStages * kStep + u * kThreads];
+      const int k = k0 + tid + b * kStep;
+      float m[kBatch], largest = -CUDART_INF_F;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) next[u].raw = __ldg(body + k + kStep + u * kThreads);
+      for (int u = 0; u < kBatch; ++u) {
+        m[u] = cur[u].largest();
+        largest = fmaxf(largest, m[u]);
       }
-      float m[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) m[u] = cur[u].largest();
-      sums.follow(kBatch == 2 ? fmaxf(m[0], m[1]) : fmaxf(fmaxf(m[0], m[1]), fmaxf(m[kBatch - 2], m[kBatch - 1])));
+      sums.follow(largest);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) take(cur[u], k + u * kThreads, m[u], notes);
-      if (TOP && !kNotes) {
+      if (TOP && !decltype(notes)::value) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
           if (m[u] >= least) keep(cur[u], k + u * kThreads);
@@ -284,33 +316,35 @@ token_logprobs_kernel(const LogprobsArgs a) {
       }
     }
   };
-  // fewer than kBatch pieces from piece k on
-  auto rest = [&](int k, auto notes) {
-    P p[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (k + u * kThreads < k1) p[u].raw = __ldg(body + k + u * kThreads);
+  auto rest = [&](auto notes) {
+    fetch(whole + kStages - 1);
+    arrived();
+    const int k = k0 + tid + whole * kStep;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       if (k + u * kThreads < k1) {
-        const float m = p[u].largest();
+        P p;
+        p.raw = stage[whole % kStages * kStep + u * kThreads];
+        const float m = p.largest();
         sums.follow(m);
-        take(p[u], k + u * kThreads, m, notes);
-        if (TOP && !decltype(notes)::value && m >= least) keep(p[u], k + u * kThreads);
+        take(p, k + u * kThreads, m, notes);
+        if (TOP && !decltype(notes)::value && m >= least) keep(p, k + u * kThreads);
       }
     __syncwarp();
   };
-  const int whole = (k1 - k0) / kStep, first = whole >= 8 ? whole / 4 : whole;
+#pragma unroll
+  for (int b = 0; b < kStages - 1; ++b) fetch(b);
   if (!TOP) {
-    stream(k0 + tid, whole, No());
-    rest(k0 + tid + whole * kStep, No());
+    stream(0, whole, No());
+    rest(No());
   } else {
-    stream(k0 + tid, first, Yes());
-    if (first == whole) rest(k0 + tid + whole * kStep, Yes());
+    const int first = whole >= 8 ? whole / 4 : whole;
+    stream(0, first, Yes());
+    if (first == whole) rest(Yes());
     set_bound(first == whole ? k1 : k0 + first * kStep);
     if (first < whole) {
-      stream(k0 + tid + first * kStep, whole - first, No());
-      rest(k0 + tid + whole * kStep, No());
+      stream(first, whole, No());
+      rest(No());
     }
   }
 
@@ -357,6 +391,7 @@ token_logprobs_kernel(const LogprobsArgs a) {
 
   if (TOP) {
     // ---- the tokens that reach the bound
+    static_assert(!TOP || S::kBytes >= kFound * (int)sizeof(Key), "s_keys");
     const int kept = s_n_kept;
     auto look_at_all = [&] {
       for (int k = k0 + tid; k < k1; k += kThreads) {
@@ -365,6 +400,7 @@ token_logprobs_kernel(const LogprobsArgs a) {
         if (p.largest() >= least) look_at(p, k);
       }
     };
+    if (loose_at >= 0) look(loose_x, loose_at);
     if (kept <= kKept) {
       for (int i = tid; i < kept; i += kThreads) {
         P p;
@@ -462,6 +498,16 @@ cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.n_rows * C));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Stream<TOP>::kBytes;
+  static bool configured[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<T, TOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Stream<TOP>::kBytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
