@@ -264,101 +264,111 @@ qkv_append_kernel(const AppendArgs a) {
     return;
   }
 
-  // ---- a KV head: keys and values to shared memory, then out by channel (E: by token)
-  uint4 xk[kSteps], xv[kSteps];
-#pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    xk[k] = head_at(row_hw + k * kHalfWarps, a.Hq + kv_head);
-    xv[k] = head_at(row_hw + k * kHalfWarps, a.Hq + a.Hkv + kv_head);
-  }
   if constexpr (E) {
+    // ---- a KV head into blocks of 32 tokens
     extern __shared__ __align__(16) float s_dyn[];
     float4* s_k = reinterpret_cast<float4*>(s_dyn);                        // [row][the lane's two fours][lane]
     uint4* s_v = reinterpret_cast<uint4*>(s_dyn + kRows8 * kH);            // [row][lane]
     __shared__ int64_t s_slot[2 * kTile];    // of the rows from row0 - 1 on; -1: not written
-    __shared__ uint32_t s_starts[2];         // rows that begin a run
     __shared__ uint32_t s_top[2][2 * kTile]; // at a run's first row: largest magnitude of keys and values, as bits
-    __shared__ int s_old[2][2 * kTile];      // and the scales that its block had, 0 if it begins the block
+    __shared__ int s_pos[2 * kTile], s_old[2 * kTile];
     if (tid < 2 * kTile) {
       const int64_t row = row0 - 1 + tid;
       int64_t slot = -1;
+      int p = -1;
       if (row >= 0 && row < a.n_rows) {
-        const int p = a.positions[row];
+        p = a.positions[row];
         slot = a.slots[row * a.Hkv + kv_head];
-        if (p < 0 || (a.rot > 0 && p >= a.max_pos)) slot = -1;
+        if (a.rot > 0 && p >= a.max_pos) {
+          if (tid > 0 && tid <= kTile) atomicExch(a.status, 4);
+          p = -1;
+        }
+        if (p < 0) slot = -1;
         if (slot >= a.n_pool * kP) {
           atomicExch(a.status, 5);
           slot = -1;
         }
       }
       s_slot[tid] = slot < 0 ? -1 : slot;
+      s_pos[tid] = p;
       s_top[0][tid] = s_top[1][tid] = 0u;
     }
     __syncthreads();
-    if (tid < 2 * kTile) {
-      const int64_t slot = s_slot[tid];
-      const bool starts = tid > 0 && slot >= 0 && (slot % kC == 0 || s_slot[tid - 1] != slot - 1);
-      const unsigned m = __ballot_sync(0xffffffffu, starts);
-      if (lane == 0) s_starts[tid >> 5] = m;
-      const uint8_t* old = a.scales + slot / kP * kScaleBytes + slot % kP / kC;
-      const bool behind = starts && tid <= kTile && slot % kC != 0;
-      s_old[0][tid] = behind ? min(max((int)old[0], kScaleLo), kScaleHi) : 0;
-      s_old[1][tid] = behind ? min(max((int)old[kChunks], kScaleLo), kScaleHi) : 0;
-    }
-    __syncthreads();
-    const unsigned long long starts = (unsigned long long)s_starts[1] << 32 | s_starts[0];
+    // rows that begin a run, as every warp sees them
+    auto begins = [&](int i) {
+      const int64_t slot = s_slot[i];
+      return i > 0 && slot >= 0 && (slot % kC == 0 || s_slot[i - 1] != slot - 1);
+    };
+    const unsigned starts0 = __ballot_sync(0xffffffffu, begins(lane)), starts1 = __ballot_sync(0xffffffffu, begins(lane + 32));
+    const unsigned long long starts = (unsigned long long)starts1 << 32 | starts0;
     // first row of row i's run, or 0 if that is none of the tile's
     auto run_of = [&](int i) {
       const int st = i < 2 * kTile && s_slot[i] >= 0 ? 63 - __clzll((long long)(starts & ((2ull << i) - 1))) : 0;
       return st > 0 && st <= kTile ? st : 0;
     };
-#pragma unroll
-    for (int k = 0; k < 2 * kSteps; ++k) {
-      const int i = 1 + k * kHalfWarps + hw, run = run_of(i);
-      if (!__any_sync(0xffffffffu, run > 0)) continue;
-      const int64_t row = row0 + i - 1;
-      uint4 xk_i, xv_i;
-      int p;
-      if (k < kSteps) {
-        xk_i = xk[k];
-        xv_i = xv[k];
-        p = pos[k];
-      } else {
-        xk_i = head_at(row, a.Hq + kv_head);
-        xv_i = head_at(row, a.Hq + a.Hkv + kv_head);
-        p = row < a.n_rows ? a.positions[row] : -1;
-      }
-      p = checked(p);
+    // The tile's runs, from the first one's first row on; 32 rows unless there are several
+    const unsigned own = (unsigned)(starts >> 1);
+    if (own == 0) return;
+    const int i0 = __ffs(own);
+    // Row i's key and value to shared memory, their largest magnitudes to its run.
+    auto prepare = [&](int i, int run, const uint4& xk_i, const uint4& xv_i) {
       float y[8];
-      norm_rotate<INTERLEAVED, WHOLE>(xk_i, turn_at(p), 8 * lane16 < a.rot, weight != nullptr, a.norm_eps, y);
-      uint32_t top_k = 0, top_v = 0;
+      norm_rotate<INTERLEAVED, WHOLE>(xk_i, turn_at(run ? s_pos[i] : -1), 8 * lane16 < a.rot, weight != nullptr, a.norm_eps, y);
       const uint32_t vw[4] = {xv_i.x, xv_i.y, xv_i.z, xv_i.w};
+      uint32_t mk = 0, mv = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top_k = max(top_k, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < 8; ++e) mk = max(mk, __float_as_uint(y[e]) & 0x7FFFFFFFu);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top_v = max(top_v, max(vw[e] & 0x7FFF0000u, vw[e] << 16 & 0x7FFF0000u));
+      for (int e = 0; e < 4; ++e) mv = max(mv, max(vw[e] & 0x7FFF0000u, vw[e] << 16 & 0x7FFF0000u));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) {
-        top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, o));
-        top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+        mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+        mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
       }
-      if (run > 0) {
-        s_k[(i - 1) * 32 + lane16] = make_float4(y[0], y[1], y[2], y[3]);
-        s_k[(i - 1) * 32 + 16 + lane16] = make_float4(y[4], y[5], y[6], y[7]);
-        s_v[(i - 1) * 16 + lane16] = xv_i;
-        if (lane16 == 0) {
-          atomicMax(&s_top[0][run], top_k);   // a maximum does not depend on the order
-          atomicMax(&s_top[1][run], top_v);
-        }
+      if (run == 0) return;
+      s_k[(i - 1) * 32 + lane16] = make_float4(y[0], y[1], y[2], y[3]);
+      s_k[(i - 1) * 32 + 16 + lane16] = make_float4(y[4], y[5], y[6], y[7]);
+      s_v[(i - 1) * 16 + lane16] = xv_i;
+      if (lane16 == 0) {
+        atomicMax(&s_top[0][run], mk);   // a maximum does not depend on the order
+        atomicMax(&s_top[1][run], mv);
       }
+    };
+    // the scales that a run's block had, 0 if the run begins the block: the keys' in the lower half
+    if (tid < 2 * kTile && run_of(tid) == tid && tid > 0) {
+      const int64_t first = s_slot[tid];
+      const uint8_t* s = a.scales + first / kP * kScaleBytes + first % kP / kC;
+      s_old[tid] = first % kC == 0 ? 0 : min(max((int)s[0], kScaleLo), kScaleHi) | min(max((int)s[kChunks], kScaleLo), kScaleHi) << 16;
+    }
+    {
+      uint4 xk[kSteps], xv[kSteps];
+      int run[kSteps];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int i = i0 + k * kHalfWarps + hw;
+        run[k] = run_of(i);
+        const int64_t row = run[k] ? row0 + i - 1 : a.n_rows;   // (none is read there)
+        xk[k] = head_at(row, a.Hq + kv_head);
+        xv[k] = head_at(row, a.Hq + a.Hkv + kv_head);
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+        if (__any_sync(0xffffffffu, run[k] > 0)) prepare(i0 + k * kHalfWarps + hw, run[k], xk[k], xv[k]);
+    }
+#pragma unroll 1
+    for (int i = i0 + kTile + hw; i - hw < 2 * kTile; i += kHalfWarps) {   // several runs
+      const int run = run_of(i);
+      if (!__any_sync(0xffffffffu, run > 0)) continue;
+      const int64_t row = run ? row0 + i - 1 : a.n_rows;
+      prepare(i, run, head_at(row, a.Hq + kv_head), head_at(row, a.Hq + a.Hkv + kv_head));
     }
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 2 * kSteps; ++k) {
-      const int i = 1 + k * kHalfWarps + hw, run = run_of(i);
+#pragma unroll 1
+    for (int i = i0 + hw; i < 2 * kTile; i += kHalfWarps) {
+      const int run = run_of(i);
       if (run == 0) continue;
       const int64_t slot = s_slot[i];
-      const int old_k = s_old[0][run], old_v = s_old[1][run];
+      const int old_k = s_old[run] & 0xFFFF, old_v = s_old[run] >> 16;
       const int sk = max(scale_byte(__uint_as_float(s_top[0][run])), old_k);
       const int sv = max(scale_byte(__uint_as_float(s_top[1][run])), old_v);
       const float fk = __uint_as_float((uint32_t)(254 - sk) << 23), fv = __uint_as_float((uint32_t)(254 - sv) << 23);
@@ -391,41 +401,48 @@ qkv_append_kernel(const AppendArgs a) {
         }
       }
     }
-    return;
-  }
-  const int64_t slot_row = row0 + lane;
-  const int slot_pos = slot_row < a.n_rows ? a.positions[slot_row] : -1;
-  int64_t slot = slot_row < a.n_rows ? a.slots[slot_row * a.Hkv + kv_head] : -1;
+  } else {
+    // ---- a KV head: keys and values to shared memory, then out by channel
+    uint4 xk[kSteps], xv[kSteps];
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
-    const int t = k * kHalfWarps + hw;
-    const uint4 r = finish(xk[k], turn_at(checked(pos[k])));
-    const uint4 v = xv[k];
-    uint32_t* dk = s_kv[0] + t * kPitch;
-    uint32_t* dv = s_kv[1] + t * kPitch;
-    dk[ca / 2] = r.x; dk[ca / 2 + 1] = r.y; dk[cb / 2] = r.z; dk[cb / 2 + 1] = r.w;
-    dv[ca / 2] = v.x; dv[ca / 2 + 1] = v.y; dv[cb / 2] = v.z; dv[cb / 2 + 1] = v.w;
-  }
-  __syncthreads();
-  // one token per lane, a pair of channels at a time
-  if (slot_pos < 0 || (a.rot > 0 && slot_pos >= a.max_pos)) slot = -1;
-  if (slot >= a.n_pool * kP) {
-    if (tid < 32) atomicExch(a.status, 5);
-    slot = -1;
-  }
-  if (slot >= 0) {
-    const int64_t at = (slot / kP) * kPageElems + slot % kP;
-    uint16_t* kd = a.k_pages + at;
-    uint16_t* vd = a.v_pages + at;
-    // the part's channel pairs
-    const int n_c2 = kH / 2 / a.kv_parts, c20 = (job - a.q_jobs) % a.kv_parts * n_c2;
+    for (int k = 0; k < kSteps; ++k) {
+      xk[k] = head_at(row_hw + k * kHalfWarps, a.Hq + kv_head);
+      xv[k] = head_at(row_hw + k * kHalfWarps, a.Hq + a.Hkv + kv_head);
+    }
+    const int64_t slot_row = row0 + lane;
+    const int slot_pos = slot_row < a.n_rows ? a.positions[slot_row] : -1;
+    int64_t slot = slot_row < a.n_rows ? a.slots[slot_row * a.Hkv + kv_head] : -1;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int t = k * kHalfWarps + hw;
+      const uint4 r = finish(xk[k], turn_at(checked(pos[k])));
+      const uint4 v = xv[k];
+      uint32_t* dk = s_kv[0] + t * kPitch;
+      uint32_t* dv = s_kv[1] + t * kPitch;
+      dk[ca / 2] = r.x; dk[ca / 2 + 1] = r.y; dk[cb / 2] = r.z; dk[cb / 2 + 1] = r.w;
+      dv[ca / 2] = v.x; dv[ca / 2 + 1] = v.y; dv[cb / 2] = v.z; dv[cb / 2 + 1] = v.w;
+    }
+    __syncthreads();
+    // one token per lane, a pair of channels at a time
+    if (slot_pos < 0 || (a.rot > 0 && slot_pos >= a.max_pos)) slot = -1;
+    if (slot >= a.n_pool * kP) {
+      if (tid < 32) atomicExch(a.status, 5);
+      slot = -1;
+    }
+    if (slot >= 0) {
+      const int64_t at = (slot / kP) * kPageElems + slot % kP;
+      uint16_t* kd = a.k_pages + at;
+      uint16_t* vd = a.v_pages + at;
+      // the part's channel pairs
+      const int n_c2 = kH / 2 / a.kv_parts, c20 = (job - a.q_jobs) % a.kv_parts * n_c2;
 #pragma unroll 4
-    for (int c2 = c20 + (tid >> 5); c2 < c20 + n_c2; c2 += kThreads / 32) {
-      const uint32_t kw = s_kv[0][lane * kPitch + c2], vw = s_kv[1][lane * kPitch + c2];
-      kd[(2 * c2) * kP] = (uint16_t)kw;
-      kd[(2 * c2 + 1) * kP] = (uint16_t)(kw >> 16);
-      vd[(2 * c2) * kP] = (uint16_t)vw;
-      vd[(2 * c2 + 1) * kP] = (uint16_t)(vw >> 16);
+      for (int c2 = c20 + (tid >> 5); c2 < c20 + n_c2; c2 += kThreads / 32) {
+        const uint32_t kw = s_kv[0][lane * kPitch + c2], vw = s_kv[1][lane * kPitch + c2];
+        kd[(2 * c2) * kP] = (uint16_t)kw;
+        kd[(2 * c2 + 1) * kP] = (uint16_t)(kw >> 16);
+        vd[(2 * c2) * kP] = (uint16_t)vw;
+        vd[(2 * c2 + 1) * kP] = (uint16_t)(vw >> 16);
+      }
     }
   }
 }
