@@ -29,8 +29,9 @@
 // Pages in 8 bits (lynx_qkv_append_e4m3).  A block of 32 tokens has one scale, so that its
 // new rows (a run: rows that follow one another in one block) are quantised together, and what
 // stands in front of them is rounded again where the scale grows.  A CTA takes the
-// runs that begin in its 32 rows, with up to 31 rows behind them: float32 keys and the values
-// wait in shared memory for the run's maximum, a page's token is then one 128-byte store.
+// runs that begin in its 32 rows, from the first one's first row on: 32 rows in registers, and where
+// there are several runs up to 31 more in shared memory, wait as float32 for the runs' maxima.  A page's
+// token is then one 128-byte store.
 // Powers of two as scales make the rounding that of E4M3 alone, and rounding a code
 // again under a larger one changes it only where it becomes subnormal.
 
@@ -49,7 +50,7 @@ constexpr int kHalfWarps = kThreads / 16;
 constexpr int kTile = 32;                  // rows per CTA
 constexpr int kBatch = 4;                  // query heads of a row read at once
 constexpr int kPitch = kH / 2 + 1;         // words per staged token: the reading lanes (one token each) hit all banks
-constexpr int kRows8 = 2 * kTile - 1;      // pages in 8 bits: rows that the runs of a tile reach
+constexpr int kRows8 = kTile - 1;          // pages in 8 bits: rows behind the first 32 that a tile's runs reach
 constexpr int kSmem8 = kRows8 * kH * 6;    // their keys (float32) and values (BF16)
 
 __device__ __forceinline__ void load4(const float* p, float* v) {
@@ -310,39 +311,46 @@ qkv_append_kernel(const AppendArgs a) {
     const unsigned own = (unsigned)(starts >> 1);
     if (own == 0) return;
     const int i0 = __ffs(own);
-    // Row i's key and value to shared memory, their largest magnitudes to its run.
-    auto prepare = [&](int i, int run, const uint4& xk_i, const uint4& xv_i) {
-      float y[8];
+    // a key's channels from the lane, and the largest magnitudes of both to the row's run
+    auto prepare = [&](int i, int run, const uint4& xk_i, const uint4& xv_i, float* y) {
       norm_rotate<INTERLEAVED, WHOLE>(xk_i, turn_at(run ? s_pos[i] : -1), 8 * lane16 < a.rot, weight != nullptr, a.norm_eps, y);
-      const uint32_t vw[4] = {xv_i.x, xv_i.y, xv_i.z, xv_i.w};
-      uint32_t mk = 0, mv = 0;
+      float mk = fmaxf(fabsf(y[0]), fabsf(y[1]));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mk = max(mk, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+      for (int e = 2; e < 8; ++e) mk = fmaxf(mk, fabsf(y[e]));
+      const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(&xv_i);
+      const __nv_bfloat162 v4 = __hmax2(__hmax2(__habs2(v2[0]), __habs2(v2[1])), __hmax2(__habs2(v2[2]), __habs2(v2[3])));
+      uint32_t top_k = __float_as_uint(mk), top_v = __float_as_uint(fmaxf(__low2float(v4), __high2float(v4)));
+      // a maximum does not depend on the order
+      if (__all_sync(0xffffffffu, run == __shfl_sync(0xffffffffu, run, 0))) {   // both rows of one run, as in a prompt
+        top_k = __reduce_max_sync(0xffffffffu, top_k);
+        top_v = __reduce_max_sync(0xffffffffu, top_v);
+        if (lane == 0 && run > 0) {
+          atomicMax(&s_top[0][run], top_k);
+          atomicMax(&s_top[1][run], top_v);
+        }
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mv = max(mv, max(vw[e] & 0x7FFF0000u, vw[e] << 16 & 0x7FFF0000u));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        mk = max(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-        mv = max(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-      }
-      if (run == 0) return;
-      s_k[(i - 1) * 32 + lane16] = make_float4(y[0], y[1], y[2], y[3]);
-      s_k[(i - 1) * 32 + 16 + lane16] = make_float4(y[4], y[5], y[6], y[7]);
-      s_v[(i - 1) * 16 + lane16] = xv_i;
-      if (lane16 == 0) {
-        atomicMax(&s_top[0][run], mk);   // a maximum does not depend on the order
-        atomicMax(&s_top[1][run], mv);
+        for (int o = 8; o > 0; o >>= 1) {
+          top_k = max(top_k, __shfl_xor_sync(0xffffffffu, top_k, o));
+          top_v = max(top_v, __shfl_xor_sync(0xffffffffu, top_v, o));
+        }
+        if (lane16 == 0 && run > 0) {
+          atomicMax(&s_top[0][run], top_k);
+          atomicMax(&s_top[1][run], top_v);
+        }
       }
     };
     // the scales that a run's block had, 0 if the run begins the block: the keys' in the lower half
-    if (tid < 2 * kTile && run_of(tid) == tid && tid > 0) {
+    if (tid > 0 && tid <= kTile && run_of(tid) == tid) {
       const int64_t first = s_slot[tid];
       const uint8_t* s = a.scales + first / kP * kScaleBytes + first % kP / kC;
       s_old[tid] = first % kC == 0 ? 0 : min(max((int)s[0], kScaleLo), kScaleHi) | min(max((int)s[kChunks], kScaleLo), kScaleHi) << 16;
     }
+    float y[kSteps][8];
+    uint4 xv[kSteps];
+    int run[kSteps];
     {
-      uint4 xk[kSteps], xv[kSteps];
-      int run[kSteps];
+      uint4 xk[kSteps];
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         const int i = i0 + k * kHalfWarps + hw;
@@ -353,35 +361,48 @@ qkv_append_kernel(const AppendArgs a) {
       }
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
-        if (__any_sync(0xffffffffu, run[k] > 0)) prepare(i0 + k * kHalfWarps + hw, run[k], xk[k], xv[k]);
+        if (__any_sync(0xffffffffu, run[k] > 0)) prepare(i0 + k * kHalfWarps + hw, run[k], xk[k], xv[k], y[k]);
     }
+    // rows behind the first 32, of several runs: their keys and values wait in shared memory
+    constexpr int kBehind = kTile;
 #pragma unroll 1
-    for (int i = i0 + kTile + hw; i - hw < 2 * kTile; i += kHalfWarps) {   // several runs
-      const int run = run_of(i);
-      if (!__any_sync(0xffffffffu, run > 0)) continue;
+    for (int i = i0 + kBehind + hw; i - hw < 2 * kTile; i += kHalfWarps) {
+      const int run = run_of(i), place = i - i0 - kBehind;
+      if (!__any_sync(0xffffffffu, run > 0)) break;
       const int64_t row = run ? row0 + i - 1 : a.n_rows;
-      prepare(i, run, head_at(row, a.Hq + kv_head), head_at(row, a.Hq + a.Hkv + kv_head));
+      const uint4 v = head_at(row, a.Hq + a.Hkv + kv_head);
+      float z[8];
+      prepare(i, run, head_at(row, a.Hq + kv_head), v, z);
+      if (run > 0) {
+        s_k[place * 32 + lane16] = make_float4(z[0], z[1], z[2], z[3]);
+        s_k[place * 32 + 16 + lane16] = make_float4(z[4], z[5], z[6], z[7]);
+        s_v[place * 16 + lane16] = v;
+      }
     }
     __syncthreads();
-#pragma unroll 1
-    for (int i = i0 + hw; i < 2 * kTile; i += kHalfWarps) {
-      const int run = run_of(i);
-      if (run == 0) continue;
+    auto write = [&](int i, int run, const float* y, const uint4& v) {
+      if (run == 0) return;
       const int64_t slot = s_slot[i];
       const int old_k = s_old[run] & 0xFFFF, old_v = s_old[run] >> 16;
       const int sk = max(scale_byte(__uint_as_float(s_top[0][run])), old_k);
       const int sv = max(scale_byte(__uint_as_float(s_top[1][run])), old_v);
       const float fk = __uint_as_float((uint32_t)(254 - sk) << 23), fv = __uint_as_float((uint32_t)(254 - sv) << 23);
-      const float4 k0 = s_k[(i - 1) * 32 + lane16], k1 = s_k[(i - 1) * 32 + 16 + lane16];
-      const uint4 v = s_v[(i - 1) * 16 + lane16];
-      auto half = [](uint32_t w, bool high) { return __uint_as_float(high ? w & 0xFFFF0000u : w << 16); };
+      auto low = [&](uint32_t w) { return __uint_as_float(w << 16) * fv; };
+      auto high = [&](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u) * fv; };
       uint8_t* kd = a.k_codes + slot * kH;
       uint8_t* vd = a.v_codes + slot * kH;
-      *reinterpret_cast<uint32_t*>(kd + ca) = e4m3x4(k0.x * fk, k0.y * fk, k0.z * fk, k0.w * fk);
-      *reinterpret_cast<uint32_t*>(kd + cb) = e4m3x4(k1.x * fk, k1.y * fk, k1.z * fk, k1.w * fk);
-      *reinterpret_cast<uint32_t*>(vd + ca) = e4m3x4(half(v.x, false) * fv, half(v.x, true) * fv, half(v.y, false) * fv, half(v.y, true) * fv);
-      *reinterpret_cast<uint32_t*>(vd + cb) = e4m3x4(half(v.z, false) * fv, half(v.z, true) * fv, half(v.w, false) * fv, half(v.w, true) * fv);
-      if (i != run) continue;
+      const uint2 kc = make_uint2(e4m3x4(y[0] * fk, y[1] * fk, y[2] * fk, y[3] * fk), e4m3x4(y[4] * fk, y[5] * fk, y[6] * fk, y[7] * fk));
+      const uint2 vc = make_uint2(e4m3x4(low(v.x), high(v.x), low(v.y), high(v.y)), e4m3x4(low(v.z), high(v.z), low(v.w), high(v.w)));
+      if (INTERLEAVED) {
+        *reinterpret_cast<uint2*>(kd + ca) = kc;
+        *reinterpret_cast<uint2*>(vd + ca) = vc;
+      } else {
+        *reinterpret_cast<uint32_t*>(kd + ca) = kc.x;
+        *reinterpret_cast<uint32_t*>(kd + cb) = kc.y;
+        *reinterpret_cast<uint32_t*>(vd + ca) = vc.x;
+        *reinterpret_cast<uint32_t*>(vd + cb) = vc.y;
+      }
+      if (i != run) return;
       // the block's scales, and what stands in front of the run under grown ones
       if (lane16 == 0) {
         uint8_t* s = a.scales + slot / kP * kScaleBytes + slot % kP / kC;
@@ -400,6 +421,16 @@ qkv_append_kernel(const AppendArgs a) {
           *d = make_uint2(rescaled(x.x, f), rescaled(x.y, f));
         }
       }
+    };
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) write(i0 + k * kHalfWarps + hw, run[k], y[k], xv[k]);
+#pragma unroll 1
+    for (int i = i0 + kBehind + hw; i < 2 * kTile; i += kHalfWarps) {
+      const int run = run_of(i), place = i - i0 - kBehind;
+      if (run == 0) break;
+      const float4 k0 = s_k[place * 32 + lane16], k1 = s_k[place * 32 + 16 + lane16];
+      const float z[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+      write(i, run, z, s_v[place * 16 + lane16]);
     }
   } else {
     // ---- a KV head: keys and values to shared memory, then out by channel
