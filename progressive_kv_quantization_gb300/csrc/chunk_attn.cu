@@ -286,11 +286,19 @@ __device__ __forceinline__ void sts16(uint32_t addr, const uint32_t* v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
 }
-// Two E4M3 codes, each in the upper byte of 16 bits, as BF16 numbers times `f2`: exponent
-// and mantissa go to the places that BF16 has for them, where they stand for
-// code * 2^-120, subnormal codes among them; exact.  (A NaN code counts as 480.)
+// bytes of x picked by four hexadecimal digits; 8 more: the byte's sign, eight times
+template <uint32_t kDigits>
+__device__ __forceinline__ uint32_t sign_extended(uint32_t x) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(d) : "r"(x), "n"(kDigits));
+  return d;
+}
+// Two E4M3 codes as BF16 numbers times `f2`, from each code with its sign in the eight bits
+// above it: four places up, and the sign's copies masked out but for the topmost, exponent and
+// mantissa stand where BF16 has them, as code * 2^-120, subnormal codes among them; exact.
+// (A NaN code counts as 480.)
 __device__ __forceinline__ uint32_t bf16x2_of_e4m3(uint32_t codes, uint32_t f2) {
-  const uint32_t x = ((codes >> 4) & 0x07F007F0u) | (codes & 0x80008000u);
+  const uint32_t x = (codes << 4) & 0x87F087F0u;
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(f2));
   return d;
@@ -626,7 +634,7 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           // 2^(s - 127 - 64) and the 2^120 between an E4M3 code and the same bits as BF16
           const uint32_t f = (uint32_t)(min(max(byte, kScaleLo), kScaleHi) + 56) << 7, f2 = f | f << 16;
           const uint32_t src = base + S::kOffRaw + rs * kRawTile + row, dst = base + kOffRing + s * kSlot + row;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < 4; ++x) {      // 8 tokens
 #pragma unroll
             for (int h = 0; h < 2; ++h) {    // 64 channels
@@ -635,8 +643,8 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               uint32_t o[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                o[2 * e] = bf16x2_of_e4m3(__byte_perm(w[e], 0u, 0x1404u), f2);
-                o[2 * e + 1] = bf16x2_of_e4m3(__byte_perm(w[e], 0u, 0x3424u), f2);
+                o[2 * e] = bf16x2_of_e4m3(sign_extended<0x9180>(w[e]), f2);
+                o[2 * e + 1] = bf16x2_of_e4m3(sign_extended<0xB3A2>(w[e]), f2);
               }
               const uint32_t to = dst + h * kBox + x * 8 * kH;
               sts16(to + (((2 * part) ^ tok) << 4), o);
