@@ -153,8 +153,10 @@ struct Walk {
   __device__ explicit Walk(const DecodeE4m3Args& args) : a(args) {
     const int lane = threadIdx.x & 31;
     const long long M = (long long)a.Hkv * a.n_tiles;
-    long long sum = 0;
-    for (int i = lane; i < a.B; i += 32) {
+    load(lane);   // of the first 32 requests, a lane each
+    const int first_ctx = ctx, first_units = units;
+    long long sum = lane < a.B ? units + kItemCost : 0;
+    for (int i = lane + 32; i < a.B; i += 32) {
       load(i);
       sum += units + kItemCost;
     }
@@ -164,7 +166,8 @@ struct Walk {
     const int grid = (int)gridDim.x;
     const int n = W >= (long long)grid * kMinCost ? grid : max(1, (int)W / kMinCost);
     const int i = min((int)blockIdx.x + (lane & 1), n);
-    const long long at = i == 0 ? 0 : W * i / n;
+    // W i / n; short lines without a 64-bit division
+    const long long at = W < 0x7fffffff / kMaxCtas ? (int)W * i / n : W * i / n;
     x = __shfl_sync(0xffffffffu, at, 0);
     x1 = __shfl_sync(0xffffffffu, at, 1);
     b = a.B;
@@ -172,7 +175,12 @@ struct Walk {
     if (x >= x1) return;
     long long before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-      load(b0 + lane);
+      if (b0 == 0) {
+        ctx = first_ctx;
+        units = first_units;
+      } else {
+        load(b0 + lane);
+      }
       const long long len = b0 + lane < a.B ? (units + kItemCost) * M : 0;
       long long end = len;
 #pragma unroll
@@ -186,14 +194,15 @@ struct Walk {
         const int l = __ffs(in) - 1;
         b = b0 + l;
         before = __shfl_sync(0xffffffffu, end - len, l);
+        ctx = __shfl_sync(0xffffffffu, ctx, l);
+        units = __shfl_sync(0xffffffffu, units, l);
         break;
       }
       before = __shfl_sync(0xffffffffu, end, 31);
     }
-    load(b);
     const long long rem = x - before;
     const int L = units + kItemCost;
-    j = (int)(rem / L);
+    j = rem <= 0x7fffffff ? (int)rem / L : (int)(rem / L);
     off = (int)(rem - (long long)j * L);
   }
   __device__ bool next(Part& p) {
