@@ -5,26 +5,27 @@
 //   x = code 2^(s - 127) with one s for 32 tokens of a head's keys, one for its values
 //   S = Q K^T,  p = 2^(c S - m),  O = (sum p V) / (sum p),  lse = (m + log2 sum p) ln 2
 //
-// A CTA takes 8 or 16 query rows (NT tiles of 8) of a request and KV head and goes
-// through the keys in units of half a page (128 tokens), K and V tile (16 KB each) one
-// behind the other through a ring that one lane fills by TMA; each of four warps owns a block of
-// 32 tokens of every unit, with a softmax of its own, and the four are joined at the
-// end.  Two CTAs an SM: what one waits for (a join, an item's first copy) the other
-// covers.
+// A CTA takes 8, 16 or 24 query rows (NT tiles of 8) of a request and KV head and goes
+// through the keys in units of half a page (128 tokens; a page for 24 rows), K and V tile one
+// behind the other through a ring that one lane fills by TMA.  Each of four (eight) warps owns a
+// block of 32 tokens of every unit, with a softmax of its own, and they are joined at the end.  Two
+// CTAs an SM (one): what one waits for (a join, an item's first copy) the other covers.
 //
-//   K side  S[16 rows x 32 tokens] as f16 m16n8k16, query rows as M.  A lane reads 16
-//           codes of a token at once; a k-step takes 4 of them, so that channels come
-//           in the order (64 j + 16 t + 4 w ..) and the query fragments with them.
-//           The token of column n of a tile of 8 is (n >> 1) + 4 (n & 1): lanes that
-//           read together then hit rows that differ in bit 2, whose 16-byte pieces the
-//           128-byte swizzle of the copy keeps in other banks.
+//   K side  f16 m16n8k16.  A lane reads 16 codes of a token at once; a k-step takes 4 of them, so
+//           that channels come in the order (64 j + 16 t + 4 w ..) and the query fragments with
+//           them.  The token of place n of 8 is (n >> 1) + 4 (n & 1): lanes that read together
+//           then hit rows that differ in bit 2, whose 16-byte pieces the 128-byte swizzle of the
+//           copy keeps in other banks.  Up to 8 rows: S = Q K^T, query rows as M (half of it
+//           empty), and P stands as the V side wants it.  More rows: S^T = K Q^T, half the products a
+//           row, and P is transposed 8 x 8 at a time (one tile of 8 rows that way: 159 us for the
+//           48 requests below against 155).
 //   V side  U[16 channels x 8 rows] = V P^T, channels as M.  A lane reads 16 channels of
 //           four tokens, 8 at a time, and interleaves two tokens' bytes (prmt); a code pair
 //           becomes an FP16 pair in one instruction.  Lane group g holds channels 16 c(g) .. + 15,
 //           c(g) = (g >> 1) + 4 (g & 1), for the banks' sake again.
 //
 // Numbers.  Codes are exact in FP16.  A query row is scaled by a power of two to a
-// largest value of 2^14..2^15, which leaves BF16's 8 bits exact down to 2^-29 of it.  p is
+// largest value of 2^14..2^15, which leaves BF16's 8 bits exact down to 2^-30 of it.  p is
 // split into two FP16 numbers (2^10 p, so that what is below 2^-35 is lost), 22 bits;
 // products sum in float32.  A block's scales are factors of its scores' (warp-wide) and of
 // its U, which is added to O in float32: the tensor core's accumulators, which cut off and
@@ -35,6 +36,13 @@
 // begins or ends inside an item leaves O, m and l in the workspace, and
 // decode_e4m3_join adds up what belongs together; ragged batches and one long
 // context fill the machine alike, and nothing depends on timing.
+//
+// What bounds it (GB300, 128 channels).  Up to 8 rows: memory.  48 requests of up to 16,383 keys, 32 / 8
+// heads: 155 us, 6.5 TB/s of codes and scales (95% of a copy); 4 of 131,071, 64 / 8: 83 us (90%, of
+// which some 8 us are the start, the last units and the join).  One request of 983 keys: 8.0 us, the two
+// launches and one unit's chain.  More rows: latency, at two warps a scheduler that the registers of
+// O leave; 5 tokens of 8 requests up to 32,000 keys, 16 / 4 heads (20 rows): 60 us against 26 of
+// memory, tensor pipe 41% busy, an instruction every 6.3 clocks of a warp.
 //
 // A warp that has given up a wait goes on through the items without waiting or
 // reading, because the others meet it at the joins.
@@ -488,6 +496,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
             const float ks = scale_of(s_scale[s_k * kScaleBytes + block]);
             __syncwarp();
             if (lane == 0) mbar_arrive(empty(s_k));
+            __syncwarp();
             const float f = fmaxf(sc[0][0] * ks, 1.17549435e-38f);   // not 0: a masked score times it is -inf
             const bool whole = pos + 32 <= common;
             float top = -CUDART_INF_F;
@@ -535,6 +544,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
               if (jj == 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty(s_k));
+                __syncwarp();
               }
 #pragma unroll
               for (int h = 0; h < 2; ++h) {   // two k-steps
@@ -599,6 +609,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
         } else {
           __syncwarp();
           if (lane == 0) mbar_arrive(empty(s_k));
+          __syncwarp();
         }
 
         if (!mbar_wait(full(s_v), ((n_tiles + 1) / kSlots) & 1, a.wait_ns)) failed = true;
@@ -648,6 +659,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
             if (h == 1) {
               __syncwarp();
               if (lane == 0) mbar_arrive(empty(s_v));
+              __syncwarp();
             }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
@@ -695,6 +707,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
         } else {
           __syncwarp();
           if (lane == 0) mbar_arrive(empty(s_v));
+          __syncwarp();
         }
       }
 
