@@ -60,6 +60,23 @@
 //
 // Keys past ctx_len in the last page take no part: their scores are replaced, and
 // their V rows are zeroed in shared memory (0 x NaN would be NaN).
+//
+// Pages in 8 bits (lynx_chunk_attn_e4m3; E in the code).  A page is token-major, so that a K half
+// page is the K-major operand of S = Q K^T as codes (kind::f8f6f4), and a V half page as BF16 the
+// MN-major operand of O += P V.
+//   Queries   A row of 128 BF16 values is scaled by a power of two to a largest value of 2^7..2^8 and held
+//             as two codes a value, the nearest one and that of the rest, 8 bits in all: S is the sum of
+//             two products at twice BF16's rate, and 256 bytes a row stay 256.
+//   Scales    of the keys' blocks of 32 tokens are factors of the scores in the softmax (its
+//             maximum is taken over each block's scores first, then over the blocks).
+//   Values    A fourth warpgroup turns V tiles of codes into BF16 tiles, the block's scale and
+//             2^-64 in them: shifted by four places a code's bits are a BF16 number, 2^-120 times the
+//             value, so that one multiplication is left (four operations for two values).
+// K as BF16 too cost 1,774 us at the end of 131,072 keys; as codes 1,449, with two slots of each
+// kind 1,431, and with the conversion's loop rolled 1,405 (215 us for the six requests above;
+// unrolled it took the issue slots of one group's softmax, and the groups fell out of step: 1,440
+// and 248).  What bounds it: the tensor core at the power cap as over BF16 pages (1,345 us); below
+// the cap the issue slots that softmax and conversion share (50% busy, tensor pipe 62%).
 
 #include "e4m3.cuh"
 #include "lynx_internal.cuh"

@@ -24,7 +24,6 @@
 // interleaved 124 us (81%).  Some thousand rows, all in L2: latency at 32 warps an SM (64
 // registers; 5.2 TB/s for 4,096 rows of 16 + 4 heads).  A decode step of 64 rows (2.8 us):
 // the launch, the position and then the cosines at it.
-
 //
 // Pages in 8 bits (lynx_qkv_append_e4m3).  A block of 32 tokens has one scale, so that its
 // new rows (a run: rows that follow one another in one block) are quantised together, and what
@@ -33,7 +32,10 @@
 // there are several runs up to 31 more in shared memory, wait as float32 for the runs' maxima.  A page's
 // token is then one 128-byte store.
 // Powers of two as scales make the rounding that of E4M3 alone, and rounding a code
-// again under a larger one changes it only where it becomes subnormal.
+// again under a larger one changes it only where it becomes subnormal.  27,292 rows of 32 + 8
+// heads, half rotated: 122 us, 5.1 TB/s (75% of a copy), bound by instructions (issue slots 74%
+// busy): 145 us with the rows put through shared memory between the two barriers.
+// 3,689 rows of 16 + 4: 11.0 us, 64 rows of 32 + 8: 4.2 us.
 
 #include "e4m3.cuh"
 #include "f32x2.cuh"
