@@ -476,12 +476,14 @@ token_logprobs_kernel(const LogprobsArgs a) {
       const Key* keys = C > 1 ? s_keys : s_found.best;
       for (int i = tid; i < n; i += kThreads) {
         const Key own = keys[i];
-        if (own == 0) continue;
         int r = 0;
         for (int j = 0; j < n; ++j) r += keys[j] > own;
+        if (own == 0)
+          for (int j = 0; j < i; ++j) r += keys[j] == 0;
         if (r < a.n_top) {
-          a.top_ids[row * a.n_top + r] = (int32_t)(0xFFFFFFFFu - (uint32_t)own);
-          a.top_logprobs[row * a.n_top + r] = logprob(unordered((uint32_t)(own >> 32)));
+          // none are left only where NaN is not among them: any id, NaN
+          a.top_ids[row * a.n_top + r] = own == 0 ? r : (int32_t)(0xFFFFFFFFu - (uint32_t)own);
+          a.top_logprobs[row * a.n_top + r] = own == 0 ? CUDART_NAN_F : logprob(unordered((uint32_t)(own >> 32)));
         }
       }
     }

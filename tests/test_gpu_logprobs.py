@@ -127,6 +127,22 @@ def test_a_row_with_nan_or_infinity_is_nan(cuda_device, bad):
     assert ((ids >= 0) & (ids < 40000)).all()
 
 
+@pytest.mark.parametrize("V", [40, 3000, 200000])
+def test_rows_with_too_few_numbers(cuda_device, V):
+    """Fewer values than alternatives that are not NaN: every output is written all the same."""
+    x = torch.full((4, V), math.nan, device="cuda")
+    x[1, 7] = 1.0
+    x[2, V - 5:] = torch.arange(5.0, device="cuda")
+    x[3] = torch.randn(V, device="cuda")
+    tokens = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out = dict(logprob=torch.zeros(4, device="cuda"), entropy=torch.zeros(4, device="cuda"),
+               top_ids=torch.full((4, 20), -7, dtype=torch.int32, device="cuda"), top_logprobs=torch.zeros(4, 20, device="cuda"))
+    L.lynx_token_logprobs(x, tokens, 20, **out)
+    assert out["top_logprobs"][:3].isnan().all() and out["entropy"][:3].isnan().all() and out["logprob"][:3].isnan().all()
+    assert ((out["top_ids"] >= 0) & (out["top_ids"] < V)).all()
+    check(x[3:], tokens[3:], 20, [t[3:] for t in out.values()])
+
+
 def test_one_token_with_almost_all_weight(cuda_device):
     """Log probabilities near 0 keep their relative precision, down to what float32's sum holds."""
     x, tokens = logits(3, 30000, torch.float32, 5, size=1.0)
