@@ -412,21 +412,19 @@ token_logprobs_kernel(const LogprobsArgs a) {
     }
     __syncthreads();
     int n = s_count;
-    while (n > kFound) {
-      // Too many (values that rise, or stand close together): the n_top-th largest of those that
-      // found room is a higher bound, and everything is gone through again.
-      Key higher = 0;
-      for (int i = tid; i < kFound; i += kThreads) {
-        int r = 0;
-        for (int j = 0; j < kFound; ++j) r += s_keys[j] > s_keys[i];
-        if (r == a.n_top - 1) higher = s_keys[i];
-      }
+    // Too many (values that rise, or stand close together): a bound between the last one, which
+    // more than kFound tokens reach, and one that fewer than n_top reach, by halving.  Keys differ,
+    // so that one with a count in between is found in at most 64 steps, whatever the row.
+    // (lo is not 0: that needs a part of fewer tokens.)
+    Key lo = bound, hi = ~0ull;
+    if (n > kFound) hi = key_of(cta_top, 0) + 1;
+    while (n > kFound || (n < a.n_top && lo != bound)) {
+      if (n > kFound) lo = bound; else hi = bound;
+      bound = lo + (hi - lo) / 2;
+      least = unordered((uint32_t)(bound >> 32));
       __syncthreads();
       if (tid == 0) s_count = 0;
-      if (higher) s_bound = higher;
       __syncthreads();
-      bound = s_bound;
-      least = unordered((uint32_t)(bound >> 32));
       if (loose_at >= 0) look(loose_x, loose_at);
       look_at_all();
       __syncthreads();

@@ -143,6 +143,18 @@ def test_rows_with_too_few_numbers(cuda_device, V):
     check(x[3:], tokens[3:], 20, [t[3:] for t in out.values()])
 
 
+@pytest.mark.parametrize("N,V", [(1, 1 << 22), (2, 151936), (700, 70001)])
+def test_rising_values(cuda_device, N, V):
+    """The bound from the front of a row holds nothing back behind it."""
+    x = (torch.arange(V, device="cuda", dtype=torch.float32) * 2.0 ** -12).expand(N, V).contiguous()
+    x[-1] = x[-1].flip(0)
+    tokens = torch.full((N,), V - 1, dtype=torch.int32, device="cuda")
+    for n_top in (1, 32):
+        got = L.lynx_token_logprobs(x, tokens, n_top)
+        rows = sorted({0, N - 1})
+        check(x[rows], tokens[rows], n_top, [t[rows] for t in got])
+
+
 def test_one_token_with_almost_all_weight(cuda_device):
     """Log probabilities near 0 keep their relative precision, down to what float32's sum holds."""
     x, tokens = logits(3, 30000, torch.float32, 5, size=1.0)
