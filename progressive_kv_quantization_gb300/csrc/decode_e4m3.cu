@@ -530,6 +530,9 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
                 l_run[0][0] += v;
               }
           } else {
+            // The scales belong to the slot as the codes do: they are read before it is given back, since
+            // the next tile's may land there from then on.
+            const float ks = scale_of(s_scale[s_k * kScaleBytes + block]);
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -541,7 +544,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
               uint4 x[2][2];
 #pragma unroll
               for (int i = 0; i < 4; ++i) x[i >> 1][i & 1] = lds16(tile + i * 8 * kH + (jj ? k_piece1 : k_piece0));
-              if (jj == 1) {
+              if (jj == 1) {   // the last reads of the slot are behind
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty(s_k));
                 __syncwarp();
@@ -564,7 +567,6 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
                   }
               }
             }
-            const float ks = scale_of(s_scale[s_k * kScaleBytes + block]);
             const bool whole = pos + 32 <= common;
             float f[NT][2], top[NT][2];
 #pragma unroll

@@ -72,3 +72,27 @@ def decode_bound(q, k, v, scale):
     """How far an output may be off, for probabilities of 22 bits: twice the scores' error
     (in p and in the sum), the exponential's 2^-21 and the sums' roundings."""
     return (2 * score_error(q, k, scale) + 2.0 ** -18) * float(np.abs(v).max(initial=0.0))
+
+
+def attention_and_bounds(q, k, v, scale, seen):
+    """One KV head, row by row: (out, lse, how far each output may be off, how far each lse).
+
+    Row r's scores are off by e_r at most: score_error's 16 steps of 2^-23, of that row's own
+    scale |q| |k| over the keys that it sees.  A probability, relative to itself, by e_r, by 2^-19 of the exponent's
+    argument (rounded once, in 32..64 where it is largest) and by 2^-21 of the exponential, 2^-18 in
+    all with the float32 sums behind them; and by 2^-35 of the largest one, since it is held as two
+    FP16 numbers of 2^10 p whose steps end at 2^-24 (half a step each).  So with sum p = 1
+        |out error| <= 2 (e_r + 2^-18) sum p |v| + 2 * 2^-35 max p sum |v|
+    (the factors 2: once for the sum of p v, once for the sum of p)."""
+    out, lse = e4m3.attention(q, k, v, scale, seen)
+    off_o, off_l = np.zeros_like(out), np.zeros_like(lse)
+    size = np.abs(v)
+    for r in range(q.shape[0]):
+        n = min(max(int(seen[r]), 0), k.shape[0])
+        if n == 0:
+            continue
+        p = np.exp(scale * (k[:n] @ q[r]) - lse[r])
+        e = 16 * 2.0 ** -23 * scale * float((np.abs(k[:n]) @ np.abs(q[r])).max()) + 2.0 ** -18
+        off_o[r] = 2 * e * (p @ size[:n]) + 2.0 ** -34 * p.max() * size[:n].sum(0)
+        off_l[r] = e + 2.0 ** -22 * abs(lse[r])
+    return out, lse, off_o, off_l
