@@ -576,7 +576,9 @@ int lynx_token_logprobs(const void* logits, int64_t row_stride, int logit_dtype,
 
 /* lynx_qkv_append into pages in 8 bits; arguments and errors as there, with the
  * scales of the pools.  The new rows of one block of 32 tokens must follow one another, in
- * the order of their tokens and without a gap (as lynx_assign_pages gives them).  Of a block
+ * the order of their tokens and without a gap (as lynx_assign_pages gives them).  A row among
+ * them that is refused, or has no position or slot, only leaves its own place as it is: the
+ * code there stays, under the block's new scale.  Of a block
  * that rows are written to, with x the float32 keys (behind norm and rotation) or
  * values of those rows:
  *   s' = the smallest byte in 74..198 with max |x| <= 448 * 2^(s' - 127) (198 if none), but no

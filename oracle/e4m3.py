@@ -71,7 +71,9 @@ def dequantise_pages(codes, scales):
 def append(x, slots, codes, scales):
     """Rows x float64 [n, heads, 128] written to slots [n, heads] (negative: not written) of
     codes [pool, 256, 128] and scales [pool, 8]; returns new arrays and, for each code, the
-    value that it stands for before it is rounded (the codes' own where nothing was written)."""
+    value that it stands for before it is rounded (the codes' own where nothing was written).
+    A row that is not written, where a block's rows go on behind it one row a token, leaves
+    them one run."""
     codes, scales = codes.copy(), scales.copy()
     wanted = decode(codes)
     for h in range(x.shape[1]):
@@ -83,21 +85,25 @@ def append(x, slots, codes, scales):
                 continue
             page, first = divmod(slot, PAGE)
             block, at = divmod(first, BLOCK)
-            n = 1   # the rows behind it that go on in its block
-            while r + n < x.shape[0] and at + n < BLOCK and int(slots[r + n, h]) == slot + n:
-                n += 1
+            run = [0]   # the rows behind it that go on in its block
+            for n in range(1, min(BLOCK - at, x.shape[0] - r)):
+                if int(slots[r + n, h]) == slot + n:
+                    run.append(n)
+                elif slots[r + n, h] >= 0:
+                    break
+            run = np.array(run)
             was = min(max(int(scales[page, block]), SCALE_LO), SCALE_HI)
-            s = scale_byte(np.abs(x[r:r + n, h]).max())
+            s = scale_byte(np.abs(x[r + run, h]).max())
             if at > 0:
                 s = max(s, was)
                 old = slice(block * BLOCK, first)
                 wanted[page, old] = decode(codes[page, old]) * 2.0 ** (was - s)
                 codes[page, old] = encode(wanted[page, old])
-            new = x[r:r + n, h] * 2.0 ** (127 - s)
-            wanted[page, first:first + n] = np.clip(new, -TOP, TOP)
-            codes[page, first:first + n] = encode(np.clip(new, -TOP, TOP))
+            new = x[r + run, h] * 2.0 ** (127 - s)
+            wanted[page, first + run] = np.clip(new, -TOP, TOP)
+            codes[page, first + run] = encode(np.clip(new, -TOP, TOP))
             scales[page, block] = s
-            r += n
+            r += int(run[-1]) + 1
     return codes, scales, wanted
 
 

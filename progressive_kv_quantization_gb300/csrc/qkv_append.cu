@@ -26,8 +26,9 @@
 // the launch, the position and then the cosines at it.
 //
 // Pages in 8 bits (lynx_qkv_append_e4m3).  A block of 32 tokens has one scale, so that its
-// new rows (a run: rows that follow one another in one block) are quantised together, and what
-// stands in front of them is rounded again where the scale grows.  A CTA takes the
+// new rows (a run: rows that follow one another in one block, whether or not all of them are
+// written) are quantised together, and what stands in front of them is rounded again where the
+// scale grows.  A CTA takes the
 // runs that begin in its 32 rows, from the first one's first row on: 32 rows in registers, and where
 // there are several runs up to 31 more in shared memory, wait as float32 for the runs' maxima.  A page's
 // token is then one 128-byte store.
@@ -272,18 +273,20 @@ qkv_append_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) float s_dyn[];
     float4* s_k = reinterpret_cast<float4*>(s_dyn);                        // [row][the lane's two fours][lane]
     uint4* s_v = reinterpret_cast<uint4*>(s_dyn + kRows8 * kH);            // [row][lane]
-    __shared__ int64_t s_slot[2 * kTile];    // of the rows from row0 - 1 on; -1: not written
+    __shared__ int64_t s_slots[3 * kTile - 1];
+    int64_t* const s_slot = s_slots + kTile - 1;   // [i]: of row row0 - 1 + i, from i = -31 on; -1: not written
     __shared__ uint32_t s_top[2][2 * kTile]; // at a run's first row: largest magnitude of keys and values, as bits
     __shared__ int s_pos[2 * kTile], s_old[2 * kTile];
-    if (tid < 2 * kTile) {
-      const int64_t row = row0 - 1 + tid;
-      int64_t slot = -1;
+    if (tid < 3 * kTile - 1) {
+      const int i = tid - (kTile - 1);
+      const int64_t row = row0 - 1 + i;
+      int64_t slot = row < 0 ? INT64_MAX : -1;   // (nothing goes on from in front of the first row)
       int p = -1;
       if (row >= 0 && row < a.n_rows) {
         p = a.positions[row];
         slot = a.slots[row * a.Hkv + kv_head];
         if (a.rot > 0 && p >= a.max_pos) {
-          if (tid > 0 && tid <= kTile) atomicExch(a.status, 4);
+          if (i > 0 && i <= kTile) atomicExch(a.status, 4);
           p = -1;
         }
         if (p < 0) slot = -1;
@@ -292,18 +295,29 @@ qkv_append_kernel(const AppendArgs a) {
           slot = -1;
         }
       }
-      s_slot[tid] = slot < 0 ? -1 : slot;
-      s_pos[tid] = p;
-      s_top[0][tid] = s_top[1][tid] = 0u;
+      s_slot[i] = slot < 0 ? -1 : slot;
+      if (i >= 0) {
+        s_pos[i] = p;
+        s_top[0][i] = s_top[1][i] = 0u;
+      }
     }
     __syncthreads();
-    // rows that begin a run, as every warp sees them
-    auto begins = [&](int i) {
-      const int64_t slot = s_slot[i];
-      return i > 0 && slot >= 0 && (slot % kC == 0 || s_slot[i - 1] != slot - 1);
-    };
-    const unsigned starts0 = __ballot_sync(0xffffffffu, begins(lane)), starts1 = __ballot_sync(0xffffffffu, begins(lane + 32));
-    const unsigned long long starts = (unsigned long long)starts1 << 32 | starts0;
+    // Rows that begin a run, as every warp sees them.  One that is not written does not end it: with
+    // two runs in one block, each would take the scale that the block had before the call, and both
+    // would set it.
+    unsigned long long starts = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = 32 * x + lane;
+      const int64_t slot = s_slot[i], before = s_slot[i - 1];
+      bool first = i > 0 && slot >= 0 && (slot % kC == 0 || before != slot - 1);
+      if (__any_sync(0xffffffffu, first && before < 0)) {   // is there one of the block in front of such rows?
+#pragma unroll 1
+        for (int d = 2; first && d <= (int)(slot % kC) && s_slot[i - d + 1] < 0; ++d) first = s_slot[i - d] != slot - d;
+        __syncwarp();
+      }
+      starts |= (unsigned long long)__ballot_sync(0xffffffffu, first) << (32 * x);
+    }
     // first row of row i's run, or 0 if that is none of the tile's
     auto run_of = [&](int i) {
       const int st = i < 2 * kTile && s_slot[i] >= 0 ? 63 - __clzll((long long)(starts & ((2ull << i) - 1))) : 0;
@@ -313,6 +327,9 @@ qkv_append_kernel(const AppendArgs a) {
     const unsigned own = (unsigned)(starts >> 1);
     if (own == 0) return;
     const int i0 = __ffs(own);
+    // and up to 31 rows behind the last one's first, or the next tile's first run
+    const unsigned next = (unsigned)(starts >> 33);
+    const int i1 = min(32 - __clz(own) + kTile - 1, next ? 32 + __ffs(next) - 1 : 2 * kTile - 1);
     // a key's channels from the lane, and the largest magnitudes of both to the row's run
     auto prepare = [&](int i, int run, const uint4& xk_i, const uint4& xv_i, float* y) {
       norm_rotate<INTERLEAVED, WHOLE>(xk_i, turn_at(run ? s_pos[i] : -1), 8 * lane16 < a.rot, weight != nullptr, a.norm_eps, y);
@@ -368,9 +385,9 @@ qkv_append_kernel(const AppendArgs a) {
     // rows behind the first 32, of several runs: their keys and values wait in shared memory
     constexpr int kBehind = kTile;
 #pragma unroll 1
-    for (int i = i0 + kBehind + hw; i - hw < 2 * kTile; i += kHalfWarps) {
+    for (int i = i0 + kBehind + hw; i - hw <= i1; i += kHalfWarps) {
       const int run = run_of(i), place = i - i0 - kBehind;
-      if (!__any_sync(0xffffffffu, run > 0)) break;
+      if (!__any_sync(0xffffffffu, run > 0)) continue;
       const int64_t row = run ? row0 + i - 1 : a.n_rows;
       const uint4 v = head_at(row, a.Hq + a.Hkv + kv_head);
       float z[8];
@@ -427,9 +444,9 @@ qkv_append_kernel(const AppendArgs a) {
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) write(i0 + k * kHalfWarps + hw, run[k], y[k], xv[k]);
 #pragma unroll 1
-    for (int i = i0 + kBehind + hw; i < 2 * kTile; i += kHalfWarps) {
+    for (int i = i0 + kBehind + hw; i <= i1; i += kHalfWarps) {
       const int run = run_of(i), place = i - i0 - kBehind;
-      if (run == 0) break;
+      if (run == 0) continue;
       const float4 k0 = s_k[place * 32 + lane16], k1 = s_k[place * 32 + 16 + lane16];
       const float z[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
       write(i, run, z, s_v[place * 16 + lane16]);
