@@ -608,7 +608,8 @@ int lynx_decode_attn_e4m3(const void* q_bf16, int B, int T, int Hq, int Hkv, int
  * arguments, workspace (lynx_chunk_attn_workspace_size), rounding and errors as
  * lynx_chunk_attn_bf16 over the BF16 pages that the codes stand for, but a query row is held
  * as sums of two E4M3 codes: its values down to 2^-9 of the largest exactly, smaller ones to
- * 2^-17 of it.  sm_scale <= 2^20. */
+ * 2^-17 of it (of 2^-119 where all are smaller); one with an infinity is NaN.  sm_scale <= 2^20,
+ * and scores (sm_scale times the products) up to 2^30. */
 int lynx_chunk_attn_e4m3(const void* q_bf16, int64_t n_rows, int64_t row_stride, const int32_t* cu_q, int B, int Hq,
                          int Hkv, int head_dim, const void* k_pages, const void* v_pages, const uint8_t* scales,
                          int64_t n_pool_pages, const int32_t* page_table, int max_pages, const int32_t* ctx_len,

@@ -914,8 +914,9 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
         __syncwarp();
       };
       // E: a row of 128 BF16 queries as two rows of 128 codes in its place, times the power of two that
-      // brings its largest value to 2^7..2^8: a value is the nearest code plus the nearest code of the rest, which
-      // holds all 8 bits of values down to 2^-10 of the largest, and is off by at most 2^-17 of that.
+      // brings its largest value to 2^7..2^8 (at most 2^126, below which scores vanish): a value is the nearest
+      // code plus the nearest code of the rest, which holds all 8 bits of values down to 2^-9 of the largest, and is
+      // off by at most 2^-17 of that.  Codes have no infinity: a row with one is NaN.
       auto split_queries = [&](const Item&) {
         __syncwarp();
         const int part = lane & 15;
@@ -930,11 +931,14 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int up = top == 0 ? 0 : min(max(7 + 127 - (int)(top >> 7), -100), 100);
+          const int up = top == 0 ? 0 : min(max(7 + 127 - (int)(top >> 7), -120), 126);
           const float f = __uint_as_float((uint32_t)(127 + up) << 23);
           uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) split_e4m3x4(w[2 * e], w[2 * e + 1], f, hi[e], lo[e]);
+          for (int e = 0; e < 2; ++e) {
+            split_e4m3x4(w[2 * e], w[2 * e + 1], f, hi[e], lo[e]);
+            if (top >= 0x7F80u) hi[e] = 0x7F7F7F7Fu;
+          }
           __syncwarp();       // both rows have been read
           const uint32_t to = q + rx * 128 + (((part >> 1) ^ (rx & 7)) << 4) + 8 * (part & 1);
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(hi[0]), "r"(hi[1]) : "memory");
@@ -1004,8 +1008,8 @@ chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tm_k, c
               for (int x = 0; x < 4; ++x) {
                 scb[x] = sc;
                 if constexpr (E)
-                  scb[x] = fmaxf(sc * scale_of(smem[S::kOffKeyScale + (n_keys + j) % S::kKeyScales * kScaleBytes +
-                                                    4 * ((it.k0 + j) & 1) + x]), 1.17549435e-38f);   // -inf times it stays
+                  scb[x] = clamped(sc * scale_of(smem[S::kOffKeyScale + (n_keys + j) % S::kKeyScales * kScaleBytes +
+                                                      4 * ((it.k0 + j) & 1) + x]));
               }
               uint64_t sum[4];
               auto exps = [&](float ref) {

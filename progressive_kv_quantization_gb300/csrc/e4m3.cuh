@@ -20,6 +20,9 @@ __device__ __forceinline__ float scale_of(int byte) {
   return __uint_as_float((uint32_t)min(max(byte, kScaleLo), kScaleHi) << 23);
 }
 
+// a factor of scores as a positive finite number: -inf (a masked score) times it is -inf, and 0 is 0
+__device__ __forceinline__ float clamped(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 3.402823466e38f); }
+
 // the smallest scale byte with top <= 448 * 2^(s - 127); top = 1.m * 2^e is at most
 // 1.75 * 2^(8 + s - 127) from s = e + 119 on, or from the one behind it for 1.m > 1.75
 __device__ __forceinline__ int scale_byte(float top) {
