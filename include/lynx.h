@@ -595,7 +595,9 @@ int lynx_qkv_append_e4m3(const void* qkv_bf16, int64_t n_rows, int64_t row_strid
 
 /* Decode / verification attention over pages in 8 bits: arguments as
  * lynx_decode_attn_bf16, but only q, the pools, scales, out and the workspace need 16-byte
- * alignment.  Scores and sums in float32, the probabilities held in 22 bits.
+ * alignment.  Scores and sums in float32, the probabilities held in 22 bits and to 2^-35 of a
+ * row's largest.  A query row with an infinity is NaN.  Scores (sm_scale times the products) up
+ * to 2^23.
  *   workspace   device scratch of lynx_decode_attn_e4m3_workspace_size() bytes,
  *               clobbered.  Calls that may overlap need one each.
  * out and lse must not share memory with q.  Limits as lynx_decode_attn. */

@@ -429,9 +429,10 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
           }
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^(14 - exponent of the largest); the scale and its inverse stay normal numbers
-          const int up = top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 7), -100), 100);
-          const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+          // 2^(14 - exponent of the largest); the scale and its inverse stay normal numbers.  A row with
+          // an infinity is NaN (it would be nothing but weights of 0 where all its scores are -inf).
+          const int up = top == 0 ? 0 : min(max(14 + 127 - (int)(top >> 7), -113), 126);
+          const float f = top >= 0x7F80u ? CUDART_NAN_F : __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {   // 8 channels: two k-steps
             const uint4 h = make_uint4(scaled_half2(x[i].x, f), scaled_half2(x[i].y, f), scaled_half2(x[i].z, f), scaled_half2(x[i].w, f));
@@ -497,7 +498,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
             __syncwarp();
             if (lane == 0) mbar_arrive(empty(s_k));
             __syncwarp();
-            const float f = fmaxf(sc[0][0] * ks, 1.17549435e-38f);   // not 0: a masked score times it is -inf
+            const float f = clamped(sc[0][0] * ks);
             const bool whole = pos + 32 <= common;
             float top = -CUDART_INF_F;
 #pragma unroll
@@ -573,7 +574,7 @@ decode_e4m3_kernel(const DecodeE4m3Args a, const __grid_constant__ CUtensorMap t
             for (int nr = 0; nr < NT; ++nr)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                f[nr][e] = fmaxf(sc[nr][e] * ks, 1.17549435e-38f);   // not 0: a masked score times it is -inf
+                f[nr][e] = clamped(sc[nr][e] * ks);
                 if (!whole) {
                   const int seen = s_seen[8 * nr + 2 * t + e] - pos - n_of;
 #pragma unroll

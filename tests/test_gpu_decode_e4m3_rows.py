@@ -41,3 +41,58 @@ def test_blocks_of_very_different_scales(Hq, Hkv, T, causal):
         out, lse = run(cache, q, lens, causal)
         check_rows(cache, q, lens, causal, out, lse)
     L.lynx_device_status()
+
+
+@pytest.mark.parametrize("Hq,T", [(8, 1), (4, 4), (8, 3), (5, 9)])
+@pytest.mark.parametrize("scale,low,high", [(2.0 ** -120, 100, 127), (2.0 ** -100, 60, 127), (2.0 ** 100, -126, -90), (1.0, -60, 20)])
+def test_rows_of_all_sizes_over_one_key(Hq, T, scale, low, high):
+    """One key: the lse is the score, the output the value; sizes from BF16's smallest normal to its largest number.
+
+    Scores below 2^23: the maximum is a score rounded once, off by 2^-24 of it, and with a lead of 2^5 over the running
+    one p 2^10 has to stay below FP16's 65,504."""
+    cache = Cache([1] * 20, 1, seed=23)
+    rng = np.random.default_rng(24)
+    q = rng.uniform(0.5, 1.0, (20, T, Hq, 128)) * rng.choice([-1, 1], (20, T, Hq, 128))
+    q = q * np.exp2(rng.integers(low, high + 1, (20, T, Hq, 1)).astype(float))
+    q[3::4] *= np.exp2(-rng.integers(0, 24, (5, T, Hq, 128)).astype(float))
+    q[1, 0, 0] = 0
+    q = np.where(np.abs(q) < 2.0 ** -126, 0.0, q)
+    q = queries_of(q)
+    out, lse = run(cache, q, [1] * 20, False, sm_scale=scale)
+    L.lynx_device_status()
+    held = 0
+    for b in range(20):
+        k, v = cache.values(b, 0)
+        rows = q[b].reshape(-1, 128)
+        fits = np.abs(scale * rows @ k[0]) < 2.0 ** 23
+        held += fits.mean() / 20
+        ro, rl, off_o, off_l = attention_and_bounds(rows[fits], k, v, scale, [1] * int(fits.sum()))
+        o, l = (t[b].double().cpu().numpy() for t in (out, lse))
+        assert np.all(np.abs(o.reshape(-1, 128)[fits] - ro) <= off_o)
+        assert np.all(np.abs(l.reshape(-1)[fits] - rl) <= off_l)
+    assert held > 0.5
+
+
+def queries_of(x):
+    return torch.from_numpy(x.astype(np.float32)).bfloat16().double().numpy()
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("Hq,T,n", [(4, 1, 1), (4, 2, 300), (6, 4, 9000), (8, 3, 2)])
+def test_a_row_that_is_not_finite_is_nan(Hq, T, n, bad):
+    """Over few keys and many, and nothing but that row; without a key it is 0."""
+    cache = Cache([n], 1, seed=25)
+    q = queries((1, T, Hq, 128), 26)
+    with np.errstate(invalid="ignore"):
+        sick = q.copy()
+        sick[0, T - 1, 1, 77] = bad
+        sick[0, 0, Hq - 1, 3] = bad
+    out, lse = run(cache, sick, [n], True)
+    L.lynx_device_status()
+    for t, h in ((T - 1, 1), (0, Hq - 1)):
+        if n - T + t + 1 > 0:
+            assert out[0, t, h].isnan().all() and lse[0, t, h].isnan()
+        else:
+            assert (out[0, t, h] == 0).all() and lse[0, t, h] == -math.inf
+        out[0, t, h], lse[0, t, h] = (x[0, t, h] for x in run(cache, q, [n], True))
+    check_rows(cache, q, [n], True, out, lse)
