@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from e4m3_testutil import Cache, attention_and_bounds
+from oracle import e4m3
 from progressive_kv_quantization_gb300 import lynx as L
 from test_gpu_decode_e4m3 import queries, run
 
@@ -96,3 +97,35 @@ def test_a_row_that_is_not_finite_is_nan(Hq, T, n, bad):
             assert (out[0, t, h] == 0).all() and lse[0, t, h] == -math.inf
         out[0, t, h], lse[0, t, h] = (x[0, t, h] for x in run(cache, q, [n], True))
     check_rows(cache, q, [n], True, out, lse)
+
+
+@pytest.mark.parametrize("scale", [0.02, 0.04, 0.07, 0.1, 0.2])
+@pytest.mark.parametrize("T", [1, 3, 5])
+def test_sums_over_long_contexts_do_not_drift(T, scale):
+    """131,072 keys that one CTA sums by itself, all but the first page's the same, so that the roundings go
+    one way.  In each 32 keys of the first page one has the lead, and the others' p is no round number.
+
+    A row's sum gets one addition a unit of 128 keys, 1,024 in all, each off by 2^-24 of the sum so far
+    at most, half of that over all: 2^-15; O's the same.  And what attention_and_bounds counts for the
+    scores (of 16 |q| |k| 2^-23) and the exponentials (2^-18)."""
+    n, B, Hkv, G = 131072, 304, 2, 4         # two items a CTA of two an SM
+    codes = np.full((3, 256, 128), 0x38, dtype=np.uint8)           # keys of ones
+    codes[1, ::32] = 0x39                                          # and of 1.125
+    rng = np.random.default_rng(27)
+    values = rng.integers(0x30, 0x48, (3, 256, 128), dtype=np.uint8)   # 0.5 .. 3.75
+    scales = np.full((3, 2, 8), 127, dtype=np.uint8)
+    table = torch.full((B, Hkv, n // 256), 2, dtype=torch.int32, device="cuda")
+    table[:, :, 0] = 1
+    up = lambda a: torch.from_numpy(a).cuda()
+    q = torch.full((B, T, G * Hkv, 128), 0.125, dtype=torch.bfloat16, device="cuda")
+    out, lse = L.lynx_decode_attn_e4m3(q, up(codes).view(torch.float8_e4m3fn), up(values).view(torch.float8_e4m3fn), up(scales),
+                                       table, torch.full((B,), n, dtype=torch.int32, device="cuda"), Hkv, sm_scale=scale)
+    L.lynx_device_status()
+    scale = float(np.float32(scale))
+    w = np.where(np.arange(256) % 32 == 0, np.exp(scale * 18.0), np.exp(scale * 16.0))[:, None]
+    first, other = e4m3.decode(values[1]), e4m3.decode(values[2])
+    total = w.sum() + (n - 256) * math.exp(scale * 16.0)
+    want = ((w * first).sum(0) + math.exp(scale * 16.0) * (n // 256 - 1) * other.sum(0)) / total
+    e = 16 * 2.0 ** -23 * scale * 18.0 + 2.0 ** -18
+    assert np.abs(lse.double().cpu().numpy() - math.log(total)).max() <= e + 2.0 ** -15 + 2.0 ** -22 * math.log(total)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= (2 * e + 2.0 ** -14) * want)
