@@ -9,7 +9,11 @@
 // A thread-block cluster takes a row, each CTA a contiguous part of it, a thread
 // every 256th piece of 16 bytes.  s and t are kept against a reference that follows
 // the thread's maximum at a distance of at most 6 (so that both are scaled again on few pieces),
-// and are brought to the row's maximum at the end.
+// and are brought to the row's maximum at the end.  A thread may have 65,536 terms, whose roundings
+// go one way where they are alike (1.2e-4 of s for 4,194,304 flat logits, 4.5e-4 for four times as many):
+// a batch's 12 to 32 are summed first, and the running sums keep what each addition lost.  (2,047 rows of
+// 128,256 BF16 with 20 alternatives 109 us against 105, the others 1% at most; behind every fourth or eighth
+// batch only, or with the running sums in shared memory, 111 to 118.)
 //
 // The n most likely tokens (equal ones: the lowest first) as 64-bit keys: the float's bits in
 // an order of whole numbers, and under them the token's from behind.  While the first quarter
@@ -21,10 +25,10 @@
 // at its end read lines of 16 bytes from DRAM: 1,000 rows of 128,256 float32 took 114 us against 93.)
 // Parts of fewer than 8 batches a thread are still in L2 then, and noted as a whole.
 //
-// Bound by the reads of the logits for many rows: 2,047 rows of 128,256 BF16 take 82 us (6.4 TB/s,
-// 94% of a copy), with 20 alternatives 105 us; 1,000 rows of as many float32 79 and 93 us.  By the
+// Bound by the reads of the logits for many rows: 2,047 rows of 128,256 BF16 take 83 us (6.35 TB/s,
+// 93% of a copy), with 20 alternatives 109 us; 1,000 rows of as many float32 80 and 94 us.  By the
 // chain (launch, one round trip of loads, the reductions, the bound, the ranks) for few: 64 rows of
-// 151,936 float32 10 us without alternatives, 16.5 us with 20 (39 MB, 5.7 us at a copy's rate).
+// 151,936 float32 10.4 us without alternatives, 16.8 us with 20 (39 MB, 5.7 us at a copy's rate).
 // Copies go into shared memory, three batches a thread deep: loads to registers held fewer (93 and
 // 119 us for the BF16 rows; 88 us for the float32 rows with alternatives).
 
@@ -110,10 +114,12 @@ struct Piece {   // 16 bytes of a row
   }
 };
 
-// sums against the reference `ref` (natural units)
+// sums against the reference `ref` (natural units): a batch's by themselves, and the running ones with
+// what their roundings lost, to be taken off
 struct Sums {
   float ref = -3.402823466e38f;
-  uint64_t s = 0, t = 0;   // pairs
+  float s = 0.0f, s_lost = 0.0f, t = 0.0f, t_lost = 0.0f;
+  uint64_t s2 = 0, t2 = 0;   // of the batch, pairs
 
   // to a reference `to` >= ref, of one value each
   static __device__ __forceinline__ void move(float from, float to, float& s, float& t) {
@@ -121,15 +127,11 @@ struct Sums {
     t = f * fmaf(d, s, t);
     s *= f;
   }
+  // in front of a batch
   __device__ __forceinline__ void follow(float largest) {
     if (largest > ref + kLag) {
-      float s0, s1, t0, t1;
-      unpair(s, s0, s1);
-      unpair(t, t0, t1);
-      move(ref, largest, s0, t0);
-      move(ref, largest, s1, t1);
-      s = pair(s0, s1);
-      t = pair(t0, t1);
+      move(ref, largest, s, t);
+      move(ref, largest, s_lost, t_lost);
       ref = largest;
     }
   }
@@ -139,8 +141,21 @@ struct Sums {
     d0 = max_nan(d0, kLeast);   // of a logit of -inf; NaN stays
     d1 = max_nan(d1, kLeast);
     const uint64_t e = pair(ex2(d0), ex2(d1));
-    s = add2(s, e);
-    t = fma2(e, pair(d0, d1), t);
+    s2 = add2(s2, e);
+    t2 = fma2(e, pair(d0, d1), t2);
+  }
+  static __device__ __forceinline__ void put(uint64_t more, float& sum, float& lost) {
+    float m0, m1;
+    unpair(more, m0, m1);
+    const float m = __fadd_rn(__fadd_rn(m0, m1), -lost), next = __fadd_rn(sum, m);
+    lost = __fadd_rn(__fadd_rn(next, -sum), -m);
+    sum = next;
+  }
+  // behind a batch
+  __device__ __forceinline__ void flush() {
+    put(s2, s, s_lost);
+    put(t2, t, t_lost);
+    s2 = t2 = 0;
   }
 };
 
@@ -227,6 +242,7 @@ token_logprobs_kernel(const LogprobsArgs a) {
     loose_x = value(loose_at);
     sums.follow(loose_x);
     sums.add(loose_x, -CUDART_INF_F);
+    sums.flush();
   }
   // The bound of what was noted, and what reaches it.  Every thread comes here once; others' pieces
   // are those up to `end`.
@@ -308,6 +324,7 @@ token_logprobs_kernel(const LogprobsArgs a) {
       sums.follow(largest);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) take(cur[u], k + u * kThreads, m[u], notes);
+      sums.flush();
       if (TOP && !decltype(notes)::value) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
@@ -328,6 +345,7 @@ token_logprobs_kernel(const LogprobsArgs a) {
         const float m = p.largest();
         sums.follow(m);
         take(p, k + u * kThreads, m, notes);
+        sums.flush();
         if (TOP && !decltype(notes)::value && m >= least) keep(p, k + u * kThreads);
       }
     __syncwarp();
@@ -356,16 +374,9 @@ token_logprobs_kernel(const LogprobsArgs a) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) cta_top = fmaxf(cta_top, s_part[w][0]);
-  float s, t;
-  {
-    float s1, t1;
-    unpair(sums.s, s, s1);
-    unpair(sums.t, t, t1);
-    s += s1;
-    t += t1;
-    // cta_top is below the reference only where nothing was added
-    Sums::move(sums.ref, fmaxf(cta_top, sums.ref), s, t);
-  }
+  float s = sums.s, t = sums.t;
+  // cta_top is below the reference only where nothing was added
+  Sums::move(sums.ref, fmaxf(cta_top, sums.ref), s, t);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
