@@ -11,6 +11,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/core/DimVector.h>
 #include <ATen/ops/empty.h>
@@ -97,6 +98,12 @@ class Call {
       *ptr = at(o, type, shape, name);
       Py_INCREF(o);
       return o;
+    }
+    const at::Context& torch_state = at::globalContext();
+    if (torch_state.deterministicAlgorithms() && torch_state.deterministicFillUninitializedMemory()) {
+      at::Tensor filled = at::empty(shape.sizes, at::TensorOptions().dtype(type).device(device_));
+      *ptr = filled.data_ptr();
+      return THPVariable_Wrap(std::move(filled));
     }
     // at::empty without its dispatch, which takes longer than the rest
     c10::Allocator* const memory = c10::cuda::CUDACachingAllocator::get();
