@@ -2,6 +2,8 @@
 off (no GPU code here)."""
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
 from oracle import e4m3
@@ -96,3 +98,46 @@ def attention_and_bounds(q, k, v, scale, seen):
         off_o[r] = 2 * e * (p @ size[:n]) + 2.0 ** -34 * p.max() * size[:n].sum(0)
         off_l[r] = e + 2.0 ** -22 * abs(lse[r])
     return out, lse, off_o, off_l
+
+
+def far_key_case():
+    """One key's score stands 20 above those of 20,000 equal ones, whose values are 2^12 times as large:
+    (cache, queries [1, 1, 4, 128], scale).  Products and sums of the scores are exact."""
+    n, far = 20001, 700
+    cache = Cache([n], 1, seed=11)
+    rng = np.random.default_rng(12)
+    cache.codes[0][:] = 0x38                                           # keys of ones
+    cache.codes[0][cache.table[0, 0, far // 256], far % 256] = 0x40    # twos
+    cache.codes[1][:] = rng.integers(0x30, 0x48, cache.codes[1].shape, dtype=np.uint8)   # 0.5 .. 3.75
+    cache.scales[0][:] = 127
+    cache.scales[1][:] = 127 + 12
+    cache.scales[1][cache.table[0, 0, far // 256], far % 256 // 32] = 127
+    cache.codes[0][cache.table[0, 0, n // 256], n % 256:] = NAN_CODE
+    return cache, np.full((1, 1, 4, 128), 0.125), 1.25
+
+
+def equal_keys_case(rows):
+    """2,000 keys, all but one in 32 of the first page alike, a little below those: their p is no round
+    number, and its rounding to FP16 the same for all: (cache, queries [1, 1, rows, 128], scale)."""
+    cache = Cache([2000], 1, seed=13, poison=False)
+    rng = np.random.default_rng(14)
+    cache.codes[0][:] = 0x38
+    cache.codes[0][cache.table[0, 0, 0], ::32] = 0x39                  # 1.125
+    cache.codes[1][:] = rng.integers(0x30, 0x48, cache.codes[1].shape, dtype=np.uint8)
+    for s in cache.scales:
+        s[:] = 127
+    return cache, np.full((1, 1, rows, 128), 0.125), 0.1
+
+
+def small_channels_case():
+    """Channel c of the queries is 2^-(c mod 17) of the usual size, and the keys' 2^(c mod 17) times: all count
+    alike.  (cache, queries [1, 1, 8, 128], scale)"""
+    cache = Cache([777], 1, seed=15)
+    rng = np.random.default_rng(16)
+    size = np.exp2(np.arange(128) % 17)
+    x = rng.standard_normal(cache.codes[0].shape) * size
+    cache.codes[0], cache.scales[0] = e4m3.quantise_pages(x)
+    last = cache.table[0, 0, 3]
+    cache.codes[0][last, 777 % 256:] = NAN_CODE
+    q = rng.uniform(0.5, 1.5, (1, 1, 8, 128)) * rng.choice([-1, 1], (1, 1, 8, 128))
+    return cache, to_bf16(q / size), 1 / math.sqrt(128)

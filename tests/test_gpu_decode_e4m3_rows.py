@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from e4m3_testutil import Cache, attention_and_bounds
+from e4m3_testutil import Cache, attention_and_bounds, equal_keys_case, far_key_case, small_channels_case
 from oracle import e4m3
 from progressive_kv_quantization_gb300 import lynx as L
 from test_gpu_decode_e4m3 import queries, run
@@ -129,3 +129,41 @@ def test_sums_over_long_contexts_do_not_drift(T, scale):
     e = 16 * 2.0 ** -23 * scale * 18.0 + 2.0 ** -18
     assert np.abs(lse.double().cpu().numpy() - math.log(total)).max() <= e + 2.0 ** -15 + 2.0 ** -22 * math.log(total)
     assert np.all(np.abs(out.double().cpu().numpy() - want) <= (2 * e + 2.0 ** -14) * want)
+
+
+def test_the_keys_far_below_the_largest_count():
+    cache, q, scale = far_key_case()
+    out, lse = run(cache, q, [20001], False, sm_scale=scale)
+    check_rows(cache, q, [20001], False, out, lse, scale)
+
+
+@pytest.mark.parametrize("rows", [4, 12, 20])
+def test_both_halves_of_a_probability_count(rows):
+    cache, q, scale = equal_keys_case(rows)
+    out, lse = run(cache, q, [2000], False, sm_scale=scale)
+    check_rows(cache, q, [2000], False, out, lse, float(np.float32(scale)))
+
+
+def test_small_channels_count():
+    cache, q, scale = small_channels_case()
+    out, lse = run(cache, q, [777], False, sm_scale=scale)
+    check_rows(cache, q, [777], False, out, lse, scale)
+
+
+@pytest.mark.parametrize("key_size", [-8, 0, 8, 30, 60])
+@pytest.mark.parametrize("Hq", [8, 14, 22])
+def test_rows_of_other_sizes_in_one_tile(Hq, key_size):
+    """Keys of the size that makes the scores of some of the rows ordinary ones."""
+    cache = Cache([777], 1, seed=9)
+    cache.scales[0][:] = np.clip(cache.scales[0].astype(int) + key_size, 0, 255)
+    q = queries((1, 1, Hq, 128), 10) * np.resize(2.0 ** np.array([0, 8, -8, -30, -60, -4, -1, -28]), Hq)[:, None]
+    q[0, 0, 7] = 0.0
+    rows = np.log2(np.abs(q[0, 0]).max(-1), where=q[0, 0].any(-1), out=np.full(Hq, -99.0)) + key_size < 5
+    out, lse = run(cache, q, [777], False)
+    k, v = cache.values(0, 0)
+    ro, rl, off_o, off_l = attention_and_bounds(q[0, 0], k, v, SCALE, [777] * Hq)
+    o, l = out[0, 0].double().cpu().numpy(), lse[0, 0].double().cpu().numpy()
+    # larger scores than some hundreds make one key of them all, which a rounding of the scores decides
+    assert np.all((np.abs(o - ro) <= off_o)[rows]) and np.all((np.abs(l - rl) <= off_l)[rows])
+    fits = np.abs(SCALE * q[0, 0] @ k.T).max(-1) < 2.0 ** 23
+    assert np.isfinite(o[fits]).all() and np.all((np.abs(l - rl) <= off_l)[fits])
