@@ -587,7 +587,8 @@ int lynx_token_logprobs(const void* logits, int64_t row_stride, int logit_dtype,
  *   codes in front of the rows become code * 2^(s - s'), rounded again (which changes a value
  *   only where it becomes a subnormal code)
  * so that a block's first token forgets what the page held before, and drafts that are
- * taken back leave at most a larger scale behind.  Codes behind the rows stay as they are. */
+ * taken back leave at most a larger scale behind.  NaN does not count for a scale and becomes a NaN
+ * code, which no token that attention sees may have.  Codes behind the rows stay as they are. */
 int lynx_qkv_append_e4m3(const void* qkv_bf16, int64_t n_rows, int64_t row_stride, int Hq, int Hkv, int head_dim,
                          const float* q_weight, const float* k_weight, float norm_eps, const float* cos_sin, int max_pos,
                          int rot_dim, int interleaved, const int32_t* positions, const int64_t* slots, void* q_out,

@@ -338,7 +338,8 @@ qkv_append_kernel(const AppendArgs a) {
       for (int e = 2; e < 8; ++e) mk = fmaxf(mk, fabsf(y[e]));
       const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(&xv_i);
       const __nv_bfloat162 v4 = __hmax2(__hmax2(__habs2(v2[0]), __habs2(v2[1])), __hmax2(__habs2(v2[2]), __habs2(v2[3])));
-      uint32_t top_k = __float_as_uint(mk), top_v = __float_as_uint(fmaxf(__low2float(v4), __high2float(v4)));
+      // (a maximum of nothing but NaN counts as 0: the block's other tokens keep their scale)
+      uint32_t top_k = __float_as_uint(fmaxf(mk, 0.0f)), top_v = __float_as_uint(fmaxf(fmaxf(__low2float(v4), __high2float(v4)), 0.0f));
       // a maximum does not depend on the order
       if (__all_sync(0xffffffffu, run == __shfl_sync(0xffffffffu, run, 0))) {   // both rows of one run, as in a prompt
         top_k = __reduce_max_sync(0xffffffffu, top_k);
