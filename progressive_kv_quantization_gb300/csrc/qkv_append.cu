@@ -34,9 +34,10 @@
 // token is then one 128-byte store.
 // Powers of two as scales make the rounding that of E4M3 alone, and rounding a code
 // again under a larger one changes it only where it becomes subnormal.  27,292 rows of 32 + 8
-// heads, half rotated: 122 us, 5.1 TB/s (75% of a copy), bound by instructions (issue slots 74%
+// heads, half rotated: 121 us, 5.2 TB/s (76% of a copy), bound by instructions (issue slots 74%
 // busy): 145 us with the rows put through shared memory between the two barriers.
-// 3,689 rows of 16 + 4: 11.0 us, 64 rows of 32 + 8: 4.2 us.
+// 3,689 rows of 16 + 4: 11.0 to 13.7 us, 64 rows of 32 + 8: 4.4 us, and where every block's scale grows
+// 10 and 15 us with 15 and 31 tokens in front of each row.
 
 #include "e4m3.cuh"
 #include "f32x2.cuh"

@@ -10,7 +10,7 @@
 // every 256th piece of 16 bytes.  s and t are kept against a reference that follows
 // the thread's maximum at a distance of at most 6 (so that both are scaled again on few pieces),
 // and are brought to the row's maximum at the end.  A thread may have 65,536 terms, whose roundings
-// go one way where they are alike (1.2e-4 of s for 4,194,304 flat logits, 4.5e-4 for four times as many):
+// go one way where they are alike (4e-5 of s for 1,048,576 flat logits, 4.9e-4 for sixteen times as many):
 // a batch's 12 to 32 are summed first, and the running sums keep what each addition lost.  (2,047 rows of
 // 128,256 BF16 with 20 alternatives 109 us against 105, the others 1% at most; behind every fourth or eighth
 // batch only, or with the running sums in shared memory, 111 to 118.)
